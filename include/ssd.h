@@ -69,7 +69,8 @@ enum ssd_status_code {
   SSD_ERR_TIMEOUT = 5      /* reserved, never returned: expired device waits raise SSD_FAULT_TIMEOUT */
 };
 
-enum ssd_dtype { SSD_DTYPE_F32 = 0, SSD_DTYPE_BF16 = 1 };
+/* SSD_DTYPE_NVFP4 is the element type of a 4-bit cache; the ssd_kv4_* and page calls take it. */
+enum ssd_dtype { SSD_DTYPE_F32 = 0, SSD_DTYPE_BF16 = 1, SSD_DTYPE_NVFP4 = 2 };
 
 /* Device status word bits (ssd_status). */
 enum ssd_device_fault {
@@ -79,7 +80,9 @@ enum ssd_device_fault {
   SSD_FAULT_KMAX = 8u,     /* a requested K larger than k_max (output truncated to k_max) */
   SSD_FAULT_UNION = 16u,   /* a block union larger than umax (output truncated) */
   SSD_FAULT_TIMEOUT = 32u, /* a bounded wait inside a kernel expired; that block's outputs are invalid */
-  SSD_FAULT_VALUE = 64u    /* a score that must be >= 0 (top-p selection) was negative or NaN */
+  SSD_FAULT_VALUE = 64u,   /* a score that must be >= 0 (top-p selection) was negative or NaN; a row
+                              quantised into a 4-bit cache held an infinity or NaN */
+  SSD_FAULT_NOPAGE = 128u  /* the pool has too few free pages (ssd_kv_reserve: nothing was changed) */
 };
 
 /*
@@ -363,6 +366,57 @@ int ssd_block_sparse_attn(const ssd_paged_kv *kv, const void *q, int h_q, int n_
  */
 int ssd_combine(const float *o_parts, const float *lse_parts, int n_rows, int n_splits, int d,
                 float *out, float *lse, ssd_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * 4-bit paged KV cache (NVFP4).  An ssd_paged_kv with dtype SSD_DTYPE_NVFP4; its pool is bytes:
+ *   pool  device, [num_pages][2][h_kv] blocks of page_size * (d / 2 + d / 16) bytes, index 0 = K,
+ *         1 = V, 16-byte aligned.  A block holds its tokens' codes (d / 2 bytes each, element 2i in the
+ *         low nibble of byte i), then their scales (d / 16 bytes each).  page_size is at least 8.
+ * Elements 16 j .. 16 j + 15 of a row share scale j.  A code is e2m1 (bit 3: sign; magnitudes 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6), a scale e4m3; the element stands for code * scale * k_scale (V: v_scale).  k_scale and
+ * v_scale are host constants of a cache, powers of two between 2^-32 and 2^32, and go to every call.
+ * Scale bytes of appended tokens must not be NaN codes (ssd_kv4_append writes none); what lies behind a
+ * request's last token may be anything.
+ *
+ * ssd_kv4_append: quantises row j (0 <= j < counts[b], or < n_new when counts is NULL) of request b into
+ *   position seq_lens[b] + j: per 16 elements x (after division by k_scale / v_scale) the scale is
+ *   e4m3(max |x| / 6) and a code e2m1(x / scale), both to nearest with ties to even, saturating; a group
+ *   whose scale is 0 holds zeros.  NaN is stored as 0 and an infinity as the largest value, and either
+ *   raises SSD_FAULT_VALUE.  seq_lens is only read (ssd_kv_advance moves it).
+ *   k_new, v_new  device [batch][n_new][h_kv][d] of `dtype` (SSD_DTYPE_BF16 or SSD_DTYPE_F32), 16-byte
+ *                 aligned.  counts: device int32 [batch] or NULL.
+ *   A request whose count lies outside [0, n_new] or whose new positions would pass max_seq_len
+ *   (SSD_FAULT_SEQLEN) or use a page id outside the pool (SSD_FAULT_PAGE) is skipped as a whole.
+ * ssd_kv4_read: the values of the tokens first[b] + j, 0 <= j < counts[b] (NULL: n), into row j of
+ *   k, v (device [batch][n][h_kv][d] of `dtype`, exact in both types); rows from counts[b] on are zeros.
+ *   Positions are not tied to seq_lens, so what was appended can be read before the lengths advance.
+ *   Ranges outside [0, max_seq_len] (SSD_FAULT_SEQLEN) and pages outside the pool (SSD_FAULT_PAGE)
+ *   read as zeros.
+ */
+int ssd_kv4_append(const ssd_paged_kv *kv, const void *k_new, const void *v_new, int dtype, int n_new,
+                   const int32_t *counts, float k_scale, float v_scale, ssd_stream_t stream);
+int ssd_kv4_read(const ssd_paged_kv *kv, const int32_t *first, const int32_t *counts, int n, float k_scale,
+                 float v_scale, int dtype, void *k, void *v, ssd_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Attention over a 4-bit cache.  ssd_kv4_verify_attn is ssd_verify_attn (n_cand candidates at the end of
+ * each request, causal among themselves; n_cand = 1 is plain decoding) and ssd_kv4_draft_attn is
+ * ssd_draft_attn over the values the cache holds, with the same shapes, masks, list and fault rules
+ * (a candidate that sees no token, an empty list: out = 0, lse = -inf), except:
+ *   q    device of q_dtype, 16-byte aligned; out device of out_dtype, 16-byte aligned (each
+ *        SSD_DTYPE_BF16 or SSD_DTYPE_F32).  Products and sums are held in fp32; probabilities are
+ *        carried in f16 (2^-12 relative) for a bf16 out and in 22 bits for an fp32 out or q.
+ *   scores  as in ssd_verify_attn, or NULL.
+ *   workspace  device, >= the matching query's bytes, 256-byte aligned.
+ */
+size_t ssd_kv4_verify_workspace_bytes(const ssd_paged_kv *kv, int h_q, int n_cand);
+int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_dtype, int h_q, int n_cand, float scale,
+                        float k_scale, float v_scale, void *out, int out_dtype, float *lse, float *scores,
+                        int64_t scores_stride, void *workspace, size_t workspace_bytes, ssd_stream_t stream);
+size_t ssd_kv4_draft_workspace_bytes(const ssd_paged_kv *kv, int h_q, int k_max);
+int ssd_kv4_draft_attn(const ssd_paged_kv *kv, const void *q, int q_dtype, int h_q, const int32_t *idx, int k_max,
+                       const int32_t *cnt, float scale, float k_scale, float v_scale, void *out, int out_dtype,
+                       float *lse, void *workspace, size_t workspace_bytes, ssd_stream_t stream);
 
 #ifdef __cplusplus
 }

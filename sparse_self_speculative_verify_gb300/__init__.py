@@ -6,15 +6,17 @@ verify/draft launch and the block-granular variant, as CUDA kernels behind the C
 of one speculative round together; ``workloads`` draws the seeded synthetic inputs.
 """
 
-from .binding import (KVCache, LibraryNotBuilt, SSDError, Workspace, ssd_block_sparse_attn, ssd_block_union,
+from .binding import (KV4Cache, KVCache, LibraryNotBuilt, SSDError, Workspace, ssd_block_sparse_attn, ssd_block_union,
                       ssd_combine, ssd_draft_attn, ssd_draft_attn_packed, ssd_draft_attn_static,
-                      ssd_draft_pack_bytes, ssd_kv_advance, ssd_kv_append,
+                      ssd_draft_pack_bytes, ssd_kv4_append, ssd_kv4_draft_attn, ssd_kv4_read, ssd_kv4_verify_attn,
+                      ssd_kv_advance, ssd_kv_append,
                       ssd_phase_assign, ssd_phase_fill, ssd_select_topk, ssd_select_topp, ssd_status, ssd_unified_attn,
                       ssd_verify_attn, ssd_verify_select, ssd_version)
 from .round import SpecRound
 
-__all__ = ["KVCache", "LibraryNotBuilt", "SSDError", "Workspace", "SpecRound", "ssd_block_sparse_attn",
+__all__ = ["KV4Cache", "KVCache", "LibraryNotBuilt", "SSDError", "Workspace", "SpecRound", "ssd_block_sparse_attn",
            "ssd_block_union", "ssd_combine", "ssd_draft_attn", "ssd_draft_attn_packed", "ssd_draft_attn_static",
-           "ssd_draft_pack_bytes", "ssd_kv_advance",
+           "ssd_draft_pack_bytes", "ssd_kv4_append", "ssd_kv4_draft_attn", "ssd_kv4_read", "ssd_kv4_verify_attn",
+           "ssd_kv_advance",
            "ssd_kv_append", "ssd_phase_assign", "ssd_phase_fill", "ssd_select_topk", "ssd_select_topp",
            "ssd_status", "ssd_unified_attn", "ssd_verify_attn", "ssd_verify_select", "ssd_version"]

@@ -10,6 +10,7 @@ PyTorch supplies device memory (outputs and zero-initialised workspaces) and str
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -21,8 +22,9 @@ import torch
 from . import build as _build
 
 SSD_OK, SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_WORKSPACE, SSD_ERR_CUDA, SSD_ERR_TIMEOUT = range(6)
-SSD_DTYPE_F32, SSD_DTYPE_BF16 = 0, 1
-FAULT_PAGE, FAULT_SEQLEN, FAULT_INDEX, FAULT_KMAX, FAULT_UNION, FAULT_TIMEOUT, FAULT_VALUE = 1, 2, 4, 8, 16, 32, 64
+SSD_DTYPE_F32, SSD_DTYPE_BF16, SSD_DTYPE_NVFP4 = 0, 1, 2
+FAULT_PAGE, FAULT_SEQLEN, FAULT_INDEX, FAULT_KMAX, FAULT_UNION, FAULT_TIMEOUT, FAULT_VALUE, FAULT_NOPAGE = \
+    1, 2, 4, 8, 16, 32, 64, 128
 
 EXPORTED = ["ssd_last_error", "ssd_version", "ssd_status", "ssd_verify_workspace_bytes", "ssd_verify_attn",
             "ssd_verify_select", "ssd_verify_select_packed",
@@ -30,7 +32,9 @@ EXPORTED = ["ssd_last_error", "ssd_version", "ssd_status", "ssd_verify_workspace
             "ssd_draft_pack_bytes", "ssd_draft_attn_packed",
             "ssd_unified_workspace_bytes", "ssd_kv_append", "ssd_kv_advance", "ssd_phase_assign", "ssd_phase_fill",
             "ssd_unified_attn", "ssd_block_union", "ssd_block_sparse_workspace_bytes", "ssd_block_sparse_attn",
-            "ssd_combine"]
+            "ssd_combine",
+            "ssd_kv4_append", "ssd_kv4_read", "ssd_kv4_verify_workspace_bytes", "ssd_kv4_verify_attn",
+            "ssd_kv4_draft_workspace_bytes", "ssd_kv4_draft_attn"]
 
 
 class LibraryNotBuilt(RuntimeError):
@@ -96,6 +100,12 @@ def load(path: Optional[str] = None, as_default: bool = False):
             "ssd_block_sparse_workspace_bytes": ([KV, I, I, I], S),
             "ssd_block_sparse_attn": ([KV, P, I, I, P, P, P, I, I, F, P, P, P, S, P], I),
             "ssd_combine": ([P, P, I, I, I, P, P, P], I),
+            "ssd_kv4_append": ([KV, P, P, I, I, P, F, F, P], I),
+            "ssd_kv4_read": ([KV, P, P, I, F, F, I, P, P, P], I),
+            "ssd_kv4_verify_workspace_bytes": ([KV, I, I], S),
+            "ssd_kv4_verify_attn": ([KV, P, I, I, I, F, F, F, P, I, P, P, I64, P, S, P], I),
+            "ssd_kv4_draft_workspace_bytes": ([KV, I, I], S),
+            "ssd_kv4_draft_attn": ([KV, P, I, I, P, I, P, F, F, F, P, I, P, P, S, P], I),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -577,3 +587,208 @@ def ssd_combine(o_parts: torch.Tensor, lse_parts: torch.Tensor, *, out=None, lse
         lse = torch.empty((R,), dtype=torch.float32, device=dev)
     _check(_lib().ssd_combine(_ptr(o_parts), _ptr(lse_parts), R, S, d, _ptr(out), _ptr(lse), _stream(stream)))
     return out, lse
+
+
+# ------------------------------------------------------------------------------------------------
+# 4-bit paged cache (NVFP4).
+# ------------------------------------------------------------------------------------------------
+
+
+@dataclass
+class KV4Cache:
+    """A 4-bit paged cache: pool uint8 [num_pages, 2, h_kv, page_size, d / 2 + d / 16] (the shape sizes a
+    page's blocks; inside one, all tokens' codes come before their scales), page_table [B, max_pages]
+    int32, seq_lens [B] int32, max_seq_len (host int, >= every seq_len), and the power-of-two factors that
+    stored K and V values are multiplied with.  ``pool_shape`` gives the shape to allocate."""
+    pool: torch.Tensor
+    page_table: torch.Tensor
+    seq_lens: torch.Tensor
+    max_seq_len: int
+    k_scale: float = 1.0
+    v_scale: float = 1.0
+
+    def __post_init__(self):
+        _need(self.pool, "pool", torch.uint8)
+        _need(self.page_table, "page_table", torch.int32, self.pool.device)
+        _need(self.seq_lens, "seq_lens", torch.int32, self.pool.device)
+        if self.pool.dim() != 5 or self.pool.shape[1] != 2 or self.pool.shape[4] not in (36, 72):
+            raise ValueError("pool must be [num_pages, 2, h_kv, page_size, d / 2 + d / 16] with d 64 or 128")
+        if self.seq_lens.dim() != 1 or self.page_table.dim() != 2 or self.page_table.shape[0] != self.seq_lens.shape[0]:
+            raise ValueError("page_table must be [batch, max_pages] and seq_lens [batch]")
+        self._struct = PagedKVStruct(
+            self.pool.data_ptr(), SSD_DTYPE_NVFP4, self.pool.shape[0], self.pool.shape[3], self.pool.shape[2], self.d,
+            self.page_table.data_ptr(), self.page_table.shape[1], self.seq_lens.data_ptr(), self.seq_lens.shape[0],
+            int(self.max_seq_len))
+
+    @staticmethod
+    def pool_shape(num_pages: int, h_kv: int, page_size: int, d: int):
+        return (num_pages, 2, h_kv, page_size, d // 2 + d // 16)
+
+    @property
+    def h_kv(self) -> int:
+        return self.pool.shape[2]
+
+    @property
+    def d(self) -> int:
+        return self.pool.shape[4] * 16 // 9
+
+    @property
+    def batch(self) -> int:
+        return self.seq_lens.shape[0]
+
+    @property
+    def device(self):
+        return self.pool.device
+
+    def ref(self):
+        return ctypes.byref(self._struct)
+
+
+_TYPES = {torch.float32: SSD_DTYPE_F32, torch.bfloat16: SSD_DTYPE_BF16}
+
+
+@contextlib.contextmanager
+def _scope(device, stream):
+    """The caches' device and the call's stream current, for allocations as for launches."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _typed(t: torch.Tensor, name: str, device, shape=None) -> int:
+    _need(t, name, None, device)
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be bf16 or fp32, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return _TYPES[t.dtype]
+
+
+def _shaped(t: Optional[torch.Tensor], name: str, dtype, device, shape):
+    if t is None:
+        return None
+    _need(t, name, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _is_kv4(kv):
+    if not isinstance(kv, KV4Cache):
+        raise TypeError(f"kv must be a KV4Cache, got {type(kv).__name__}")
+
+
+def _stream_ws(device, name: str, nbytes: int, workspace: Optional[Workspace]):
+    """Workspace of a call on the current stream: the caller's, or one kept for (device, stream), so that
+    calls on different streams never share one; a call under stream capture without a workspace takes a
+    zero-filled buffer of its graph's own memory.  A caller's workspace is sized before a capture that uses
+    it and must outlive the graph."""
+    if workspace is not None:
+        return _ws(device, name, nbytes, workspace)
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.zeros(int(nbytes) + 256, dtype=torch.uint8, device=device)
+        return ctypes.c_void_p(Workspace.aligned(buf)), int(nbytes)
+    return _ws(device, f"{name}@{torch.cuda.current_stream().cuda_stream:x}", nbytes, None)
+
+
+def ssd_kv4_append(kv: KV4Cache, k_new: torch.Tensor, v_new: torch.Tensor, counts: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """Quantises rows k_new / v_new [B, n_new, h_kv, d] (bf16 or fp32) into positions seq_lens[b] + j of every
+    request, j < counts[b] (int32 [B]; None: all n_new); kv.pool is modified in place, kv.seq_lens is not."""
+    _is_kv4(kv)
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4 or k_new.shape[0] != kv.batch or \
+            k_new.shape[2] != kv.h_kv or k_new.shape[3] != kv.d:
+        raise ValueError("k_new and v_new must both be [batch, n_new, h_kv, d]")
+    dt = _typed(k_new, "k_new", kv.device)
+    _shaped(v_new, "v_new", k_new.dtype, kv.device, k_new.shape)
+    _shaped(counts, "counts", torch.int32, kv.device, (kv.batch,))
+    with _scope(kv.device, stream):
+        _check(_lib().ssd_kv4_append(kv.ref(), _ptr(k_new), _ptr(v_new), dt, k_new.shape[1], _ptr(counts),
+                                     float(kv.k_scale), float(kv.v_scale), _stream()))
+
+
+def ssd_kv4_read(kv: KV4Cache, first: torch.Tensor, n: int, counts: Optional[torch.Tensor] = None, *, k=None, v=None,
+                 dtype=torch.bfloat16, stream=None):
+    """The values of the tokens first[b] + j, j < counts[b] (None: n), as k, v [B, n, h_kv, d] of `dtype` (bf16 or
+    fp32; both exact); rows from counts[b] on are zeros."""
+    _is_kv4(kv)
+    dev, shape = kv.device, (kv.batch, int(n), kv.h_kv, kv.d)
+    _shaped(first, "first", torch.int32, dev, (kv.batch,))
+    _shaped(counts, "counts", torch.int32, dev, (kv.batch,))
+    with _scope(dev, stream):
+        if k is None:
+            k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=dev)
+        if v is None:
+            v = torch.empty(shape, dtype=k.dtype, device=dev)
+        dt = _typed(k, "k", dev, shape)
+        _shaped(v, "v", k.dtype, dev, shape)
+        _check(_lib().ssd_kv4_read(kv.ref(), _ptr(first), _ptr(counts), int(n), float(kv.k_scale), float(kv.v_scale), dt,
+                                   _ptr(k), _ptr(v), _stream()))
+    return k, v
+
+
+def ssd_kv4_verify_attn(kv: KV4Cache, q: torch.Tensor, n_cand: int, scale: float, *, out=None, lse=None,
+                        scores: Optional[torch.Tensor] = None, want_scores: bool = True, want_lse: bool = True,
+                        out_dtype=torch.float32, workspace: Optional[Workspace] = None, stream=None) -> dict:
+    """Verify attention over a 4-bit cache, with the tokens' criticality on request (n_cand = 1: plain
+    decoding).  q [B, n_cand, h_q, d] bf16 or fp32; out fp32 or bf16 (`out_dtype` where it is not given)."""
+    _is_kv4(kv)
+    dev = kv.device
+    qt = _typed(q, "q", dev)
+    if q.dim() != 4 or q.shape[0] != kv.batch or q.shape[1] != n_cand or q.shape[3] != kv.d:
+        raise ValueError("q must be [batch, n_cand, h_q, d]")
+    B, nc, h_q, d = q.shape
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((B, nc, h_q, d), dtype=out_dtype, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty((B, nc, h_q), dtype=torch.float32, device=dev)
+        if scores is None and want_scores:
+            scores = torch.zeros((B, kv.h_kv, max(kv.max_seq_len, 1)), dtype=torch.float32, device=dev)
+        ot = _typed(out, "out", dev, (B, nc, h_q, d))
+        _shaped(lse, "lse", torch.float32, dev, (B, nc, h_q))
+        if scores is not None:
+            _shaped(scores, "scores", torch.float32, dev, (B, kv.h_kv, scores.shape[-1] if scores.dim() else 0))
+        L = _lib()
+        need = L.ssd_kv4_verify_workspace_bytes(kv.ref(), h_q, n_cand)
+        wsp, avail = _stream_ws(dev, "kv4", need, workspace)
+        _check(L.ssd_kv4_verify_attn(kv.ref(), _ptr(q), qt, h_q, n_cand, float(scale), float(kv.k_scale),
+                                     float(kv.v_scale), _ptr(out), ot, _ptr(lse), _ptr(scores),
+                                     scores.shape[-1] if scores is not None else 0, wsp, avail, _stream()))
+    return {"out": out, "lse": lse, "scores": scores}
+
+
+def ssd_kv4_draft_attn(kv: KV4Cache, q: torch.Tensor, idx: torch.Tensor, cnt: torch.Tensor, scale: float, *, out=None,
+                       lse=None, want_lse: bool = True, out_dtype=torch.float32,
+                       workspace: Optional[Workspace] = None, stream=None) -> dict:
+    """Single-query attention over the selected tokens of a 4-bit cache.  q [B, h_q, d] bf16 or fp32;
+    idx [B, h_kv, k_max] and cnt [B, h_kv] int32; out fp32 or bf16 (`out_dtype` where it is not given)."""
+    _is_kv4(kv)
+    dev = kv.device
+    qt = _typed(q, "q", dev)
+    if q.dim() != 3 or q.shape[0] != kv.batch or q.shape[2] != kv.d:
+        raise ValueError("q must be [batch, h_q, d]")
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 3:
+        raise ValueError("idx must be [batch, h_kv, k_max]")
+    B, h_q, d = q.shape
+    k_max = idx.shape[2]
+    _shaped(idx, "idx", torch.int32, dev, (B, kv.h_kv, k_max))
+    _need(cnt, "cnt", torch.int32, dev)
+    _shaped(cnt, "cnt", torch.int32, dev, (B, kv.h_kv))
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((B, h_q, d), dtype=out_dtype, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty((B, h_q), dtype=torch.float32, device=dev)
+        ot = _typed(out, "out", dev, (B, h_q, d))
+        _shaped(lse, "lse", torch.float32, dev, (B, h_q))
+        L = _lib()
+        need = L.ssd_kv4_draft_workspace_bytes(kv.ref(), h_q, k_max)
+        wsp, avail = _stream_ws(dev, "kv4", need, workspace)
+        _check(L.ssd_kv4_draft_attn(kv.ref(), _ptr(q), qt, h_q, _ptr(idx), k_max, _ptr(cnt), float(scale),
+                                    float(kv.k_scale), float(kv.v_scale), _ptr(out), ot, _ptr(lse), wsp, avail,
+                                    _stream()))
+    return {"out": out, "lse": lse}
