@@ -418,6 +418,54 @@ int ssd_kv4_draft_attn(const ssd_paged_kv *kv, const void *q, int q_dtype, int h
                        const int32_t *cnt, float scale, float k_scale, float v_scale, void *out, int out_dtype,
                        float *lse, void *workspace, size_t workspace_bytes, ssd_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Pages of a cache: sharing, taking, giving back, compacting (SpecSA "branch handling": branches of a
+ * request share the KV of their common tokens; SparseSpec §4.1: the selected tokens are the ones kept).
+ * For caches of every dtype.  Next to the cache the caller keeps
+ *   page_refs  device int32 [num_pages]: how many page-table entries (rows of the batch) hold each page;
+ *              0 = free.  Free entries of the page table are negative.
+ * These calls write the page table, the lengths, page_refs and the pool (the struct's const qualifiers
+ * notwithstanding) on the device and in stream order; nothing is read back.  A free page is always the
+ * one with the lowest index, so results do not depend on timing.
+ *
+ * ssd_kv_fork: for n pairs, row dst[i] comes to share the pages of row src[i]'s tokens (counts go up, no
+ *   K / V moves) and takes its length.  dst's row must hold no page.  src, dst: device int32 [n].  A pair is
+ *   skipped when a row is out of range, when its src is any pair's dst or when its dst is an earlier pair's
+ *   (SSD_FAULT_INDEX), when a page of src is not held or dst's row is not empty (SSD_FAULT_PAGE), or when
+ *   src's length is out of range (SSD_FAULT_SEQLEN).
+ * ssd_kv_reserve: makes room for counts[b] tokens behind every request (device int32 [batch], 0 = none):
+ *   afterwards the pages of positions seq_lens[b] .. seq_lens[b] + counts[b] - 1 are held by row b alone.
+ *   Missing pages are taken from the free ones in the order of rows and positions.  A page held with other
+ *   rows is replaced by a free one, and the live tokens of its slots (below seq_lens[b]) are copied; when
+ *   all of a page's holders ask for room in it, the lowest row keeps it.  Call it before appending.
+ *   If the free pages do not suffice, nothing is changed at all and SSD_FAULT_NOPAGE is raised.  A request
+ *   with a count or end out of range (SSD_FAULT_SEQLEN) or whose affected entries name pages outside the
+ *   pool or not held (SSD_FAULT_PAGE) is skipped; the others are served.
+ *   workspace: device, >= ssd_kv_reserve_workspace_bytes(kv) bytes, 256-byte aligned.
+ * ssd_kv_release: row b gives back the pages behind its first keep[b] tokens (device int32 [batch]; 0: all
+ *   of them, negative: the row is left alone), and its length becomes min(length, keep[b]).  Entries that
+ *   name pages outside the pool or not held are cleared and raise SSD_FAULT_PAGE.
+ * ssd_kv_compact: for n pairs, the listed tokens of row src[i] of kv go to positions 0 .. of row dst[i] of
+ *   the cache `to` (same dtype, h_kv and d; the page size may differ; it may be kv itself), whose length
+ *   becomes the count.  idx: device int32 [n][h_kv][k_max], cnt: device int32 [n][h_kv], the same for every head
+ *   of a pair.  Token order is the list's.  dst's pages must be reserved beforehand; slots behind the last
+ *   token stay as they are.  to_refs: page_refs of `to`, or NULL; with it, rows go only into pages held once.
+ *   A pair is skipped when a row is out of range, when its dst is an earlier pair's or, within one cache,
+ *   any pair's src (SSD_FAULT_INDEX), when its counts differ or lie outside [0, k_max] (SSD_FAULT_KMAX), or
+ *   when src's length or the count does not fit (SSD_FAULT_SEQLEN).  An entry outside [0, length of src)
+ *   (SSD_FAULT_INDEX) or in a page outside the pool (SSD_FAULT_PAGE) stores zeros; a destination page that
+ *   is outside the pool or shared (SSD_FAULT_PAGE) is not written.  Two caches over one pool must not
+ *   share pages between rows read and rows written.
+ */
+int ssd_kv_fork(const ssd_paged_kv *kv, int32_t *page_refs, const int32_t *src, const int32_t *dst, int n,
+                ssd_stream_t stream);
+size_t ssd_kv_reserve_workspace_bytes(const ssd_paged_kv *kv);
+int ssd_kv_reserve(const ssd_paged_kv *kv, int32_t *page_refs, const int32_t *counts, void *workspace,
+                   size_t workspace_bytes, ssd_stream_t stream);
+int ssd_kv_release(const ssd_paged_kv *kv, int32_t *page_refs, const int32_t *keep, ssd_stream_t stream);
+int ssd_kv_compact(const ssd_paged_kv *kv, const ssd_paged_kv *to, const int32_t *to_refs, const int32_t *src,
+                   const int32_t *dst, int n, const int32_t *idx, int k_max, const int32_t *cnt, ssd_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

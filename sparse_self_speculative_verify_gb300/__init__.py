@@ -6,17 +6,17 @@ verify/draft launch and the block-granular variant, as CUDA kernels behind the C
 of one speculative round together; ``workloads`` draws the seeded synthetic inputs.
 """
 
-from .binding import (KV4Cache, KVCache, LibraryNotBuilt, SSDError, Workspace, ssd_block_sparse_attn, ssd_block_union,
-                      ssd_combine, ssd_draft_attn, ssd_draft_attn_packed, ssd_draft_attn_static,
+from .binding import (KV4Cache, KVCache, LibraryNotBuilt, PagePool, SSDError, Workspace, ssd_block_sparse_attn,
+                      ssd_block_union, ssd_combine, ssd_draft_attn, ssd_draft_attn_packed, ssd_draft_attn_static,
                       ssd_draft_pack_bytes, ssd_kv4_append, ssd_kv4_draft_attn, ssd_kv4_read, ssd_kv4_verify_attn,
-                      ssd_kv_advance, ssd_kv_append,
-                      ssd_phase_assign, ssd_phase_fill, ssd_select_topk, ssd_select_topp, ssd_status, ssd_unified_attn,
-                      ssd_verify_attn, ssd_verify_select, ssd_version)
+                      ssd_kv_advance, ssd_kv_append, ssd_kv_compact, ssd_kv_fork, ssd_kv_release, ssd_kv_reserve,
+                      ssd_phase_assign, ssd_phase_fill, ssd_select_topk, ssd_select_topp, ssd_status,
+                      ssd_unified_attn, ssd_verify_attn, ssd_verify_select, ssd_version)
 from .round import SpecRound
 
-__all__ = ["KV4Cache", "KVCache", "LibraryNotBuilt", "SSDError", "Workspace", "SpecRound", "ssd_block_sparse_attn",
-           "ssd_block_union", "ssd_combine", "ssd_draft_attn", "ssd_draft_attn_packed", "ssd_draft_attn_static",
-           "ssd_draft_pack_bytes", "ssd_kv4_append", "ssd_kv4_draft_attn", "ssd_kv4_read", "ssd_kv4_verify_attn",
-           "ssd_kv_advance",
-           "ssd_kv_append", "ssd_phase_assign", "ssd_phase_fill", "ssd_select_topk", "ssd_select_topp",
-           "ssd_status", "ssd_unified_attn", "ssd_verify_attn", "ssd_verify_select", "ssd_version"]
+__all__ = ["KV4Cache", "KVCache", "LibraryNotBuilt", "PagePool", "SSDError", "SpecRound", "Workspace",
+           "ssd_block_sparse_attn", "ssd_block_union", "ssd_combine", "ssd_draft_attn", "ssd_draft_attn_packed",
+           "ssd_draft_attn_static", "ssd_draft_pack_bytes", "ssd_kv4_append", "ssd_kv4_draft_attn", "ssd_kv4_read",
+           "ssd_kv4_verify_attn", "ssd_kv_advance", "ssd_kv_append", "ssd_kv_compact", "ssd_kv_fork",
+           "ssd_kv_release", "ssd_kv_reserve", "ssd_phase_assign", "ssd_phase_fill", "ssd_select_topk",
+           "ssd_select_topp", "ssd_status", "ssd_unified_attn", "ssd_verify_attn", "ssd_verify_select", "ssd_version"]

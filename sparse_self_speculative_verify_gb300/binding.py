@@ -34,7 +34,8 @@ EXPORTED = ["ssd_last_error", "ssd_version", "ssd_status", "ssd_verify_workspace
             "ssd_unified_attn", "ssd_block_union", "ssd_block_sparse_workspace_bytes", "ssd_block_sparse_attn",
             "ssd_combine",
             "ssd_kv4_append", "ssd_kv4_read", "ssd_kv4_verify_workspace_bytes", "ssd_kv4_verify_attn",
-            "ssd_kv4_draft_workspace_bytes", "ssd_kv4_draft_attn"]
+            "ssd_kv4_draft_workspace_bytes", "ssd_kv4_draft_attn",
+            "ssd_kv_fork", "ssd_kv_reserve_workspace_bytes", "ssd_kv_reserve", "ssd_kv_release", "ssd_kv_compact"]
 
 
 class LibraryNotBuilt(RuntimeError):
@@ -105,6 +106,11 @@ def load(path: Optional[str] = None, as_default: bool = False):
             "ssd_kv4_verify_workspace_bytes": ([KV, I, I], S),
             "ssd_kv4_verify_attn": ([KV, P, I, I, I, F, F, F, P, I, P, P, I64, P, S, P], I),
             "ssd_kv4_draft_workspace_bytes": ([KV, I, I], S),
+            "ssd_kv_fork": ([KV, P, P, P, I, P], I),
+            "ssd_kv_reserve_workspace_bytes": ([KV], S),
+            "ssd_kv_reserve": ([KV, P, P, P, S, P], I),
+            "ssd_kv_release": ([KV, P, P, P], I),
+            "ssd_kv_compact": ([KV, KV, P, P, P, I, P, I, P, P], I),
             "ssd_kv4_draft_attn": ([KV, P, I, I, P, I, P, F, F, F, P, I, P, P, S, P], I),
         }
         for name, (args, res) in sig.items():
@@ -647,15 +653,14 @@ class KV4Cache:
 _TYPES = {torch.float32: SSD_DTYPE_F32, torch.bfloat16: SSD_DTYPE_BF16}
 
 
-@contextlib.contextmanager
+_HERE = contextlib.nullcontext()
+
+
 def _scope(device, stream):
     """The caches' device and the call's stream current, for allocations as for launches."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
+    if stream is None:
+        return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return torch.cuda.stream(stream)  # switches to the stream's device as well
 
 
 def _typed(t: torch.Tensor, name: str, device, shape=None) -> int:
@@ -792,3 +797,100 @@ def ssd_kv4_draft_attn(kv: KV4Cache, q: torch.Tensor, idx: torch.Tensor, cnt: to
                                     float(kv.k_scale), float(kv.v_scale), _ptr(out), ot, _ptr(lse), wsp, avail,
                                     _stream()))
     return {"out": out, "lse": lse}
+
+
+# ------------------------------------------------------------------------------------------------
+# Pages of a cache: sharing, taking, giving back, compacting.
+# ------------------------------------------------------------------------------------------------
+
+
+@dataclass
+class PagePool:
+    """Reference counts of a pool's pages: refs int32 [num_pages], how many page-table entries hold each page
+    (0 = free)."""
+    refs: torch.Tensor
+
+    def __post_init__(self):
+        _need(self.refs, "refs", torch.int32)
+        if self.refs.dim() != 1:
+            raise ValueError("refs must be [num_pages]")
+
+    @classmethod
+    def from_table(cls, page_table: torch.Tensor, num_pages: int) -> "PagePool":
+        """The counts of the pages a page table holds (entries >= 0)."""
+        held = page_table.reshape(-1)
+        held = held[held >= 0].to(torch.int64)
+        refs = torch.zeros((num_pages,), dtype=torch.int32, device=page_table.device)
+        return cls(refs.scatter_add_(0, held, torch.ones_like(held, dtype=torch.int32)))
+
+
+def _pages_of(kv, pages: PagePool):
+    if not isinstance(kv, (KVCache, KV4Cache)):
+        raise TypeError(f"kv must be a KVCache or a KV4Cache, got {type(kv).__name__}")
+    if not isinstance(pages, PagePool):
+        raise TypeError(f"pages must be a PagePool, got {type(pages).__name__}")
+    return _ptr(_shaped(pages.refs, "pages.refs", torch.int32, kv.device, (kv.pool.shape[0],)))
+
+
+def _rows(t: torch.Tensor, name: str, device, n: Optional[int] = None):
+    _need(t, name, torch.int32, device)
+    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be [{'n' if n is None else n}]")
+    return t
+
+
+def ssd_kv_fork(kv, pages: PagePool, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Row dst[i] (empty before) shares the pages of row src[i] and takes its length; src, dst int32 [n].
+    kv.page_table, kv.seq_lens and pages.refs are modified in place; no K / V moves."""
+    refs = _pages_of(kv, pages)
+    _rows(src, "src", kv.device)
+    _rows(dst, "dst", kv.device, src.shape[0])
+    with _scope(kv.device, stream):
+        _check(_lib().ssd_kv_fork(kv.ref(), refs, _ptr(src), _ptr(dst), src.shape[0], _stream()))
+
+
+def ssd_kv_reserve(kv, pages: PagePool, counts: torch.Tensor, *, workspace: Optional[Workspace] = None,
+                   stream=None) -> None:
+    """Pages of its own for the next counts[b] tokens of every request (int32 [B]); what a request shares there is
+    copied.  All or nothing: with too few free pages the status reports FAULT_NOPAGE and nothing changes."""
+    refs = _pages_of(kv, pages)
+    _rows(counts, "counts", kv.device, kv.batch)
+    with _scope(kv.device, stream):
+        L = _lib()
+        wsp, avail = _stream_ws(kv.device, "pages", L.ssd_kv_reserve_workspace_bytes(kv.ref()), workspace)
+        _check(L.ssd_kv_reserve(kv.ref(), refs, _ptr(counts), wsp, avail, _stream()))
+
+
+def ssd_kv_release(kv, pages: PagePool, keep: torch.Tensor, stream=None) -> None:
+    """Row b gives back the pages behind its first keep[b] tokens (int32 [B]; 0: all, negative: none) and its
+    length becomes min(length, keep[b])."""
+    refs = _pages_of(kv, pages)
+    _rows(keep, "keep", kv.device, kv.batch)
+    with _scope(kv.device, stream):
+        _check(_lib().ssd_kv_release(kv.ref(), refs, _ptr(keep), _stream()))
+
+
+def ssd_kv_compact(kv, to, src: torch.Tensor, dst: torch.Tensor, idx: torch.Tensor, cnt: torch.Tensor,
+                   pages: Optional[PagePool] = None, stream=None) -> None:
+    """The listed tokens idx [n, h_kv, k_max] (cnt [n, h_kv] of them, the same for every head) of row src[i] of `kv`
+    go to positions 0 .. of row dst[i] of `to`, whose length becomes the count.  dst's pages are reserved
+    beforehand; with `pages` (the PagePool of `to`) shared ones are left alone and reported."""
+    dev = kv.device
+    if not isinstance(kv, (KVCache, KV4Cache)) or type(to) is not type(kv):
+        raise TypeError("kv and to must both be a KVCache or both a KV4Cache")
+    refs = None if pages is None else _pages_of(to, pages)
+    if to.device != dev:
+        raise ValueError(f"to is on {to.device}, expected {dev}")
+    if isinstance(kv, KV4Cache) and (kv.k_scale, kv.v_scale) != (to.k_scale, to.v_scale):
+        raise ValueError("the two caches differ in k_scale or v_scale")
+    _rows(src, "src", dev)
+    n = src.shape[0]
+    _rows(dst, "dst", dev, n)
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 3:
+        raise ValueError("idx must be [n, h_kv, k_max]")
+    _need(cnt, "cnt", torch.int32, dev)
+    _shaped(idx, "idx", torch.int32, dev, (n, kv.h_kv, idx.shape[2]))
+    _shaped(cnt, "cnt", torch.int32, dev, (n, kv.h_kv))
+    with _scope(dev, stream):
+        _check(_lib().ssd_kv_compact(kv.ref(), to.ref(), refs, _ptr(src), _ptr(dst), n, _ptr(idx), idx.shape[2], _ptr(cnt),
+                                     _stream()))

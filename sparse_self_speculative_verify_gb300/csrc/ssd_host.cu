@@ -1,13 +1,9 @@
 // ssd_host.cu -- error reporting, the device status word and argument validation.
-#include <math.h>
 #include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
 
-#include <initializer_list>
-
 #include "ssd_host.h"
-#include "ssd_kv4.cuh"
 
 namespace ssd {
 
@@ -74,29 +70,12 @@ int sm_count() {
   return s_sm_count[dev];
 }
 
-int validate_kv(const ssd_paged_kv *kv, KVView *v, const char *who) { return validate_cache(kv, v, who, kCache16Or32); }
-
-int kv4_scales_ok(float k_scale, float v_scale, const char *who) {
-  for (float s : {k_scale, v_scale}) {
-    int e = 0;
-    if (!(s > 0.f) || frexpf(s, &e) != 0.5f || e < -31 || e > 33)
-      return fail(SSD_ERR_INVALID_ARG, "%s: k_scale and v_scale must be powers of two between 2^-32 and 2^32", who);
-  }
-  return SSD_OK;
-}
-
-int validate_cache(const ssd_paged_kv *kv, KVView *v, const char *who, unsigned kinds) {
+int validate_kv(const ssd_paged_kv *kv, KVView *v, const char *who) {
   if (!kv) return fail(SSD_ERR_INVALID_ARG, "%s: kv is NULL", who);
   if (!kv->pool || !kv->page_table || !kv->seq_lens)
     return fail(SSD_ERR_INVALID_ARG, "%s: pool, page_table and seq_lens must be non-NULL", who);
-  const unsigned kind = kv->dtype == SSD_DTYPE_NVFP4 ? kCacheNvfp4
-                        : kv->dtype == SSD_DTYPE_BF16 || kv->dtype == SSD_DTYPE_F32 ? kCache16Or32 : 0u;
-  if (!(kind & kinds))
-    return fail(SSD_ERR_UNSUPPORTED, "%s: dtype %d (expected %s)", who, kv->dtype,
-                kinds == kCache16Or32 ? "SSD_DTYPE_F32 or SSD_DTYPE_BF16"
-                : kinds == kCacheNvfp4 ? "SSD_DTYPE_NVFP4" : "SSD_DTYPE_F32, SSD_DTYPE_BF16 or SSD_DTYPE_NVFP4");
-  if (kind == kCacheNvfp4 && kv->page_size < kKv4MinPage)
-    return fail(SSD_ERR_UNSUPPORTED, "%s: page_size %d of a 4-bit cache is below %d", who, kv->page_size, kKv4MinPage);
+  if (kv->dtype != SSD_DTYPE_BF16 && kv->dtype != SSD_DTYPE_F32)
+    return fail(SSD_ERR_UNSUPPORTED, "%s: dtype %d (expected SSD_DTYPE_BF16 or SSD_DTYPE_F32)", who, kv->dtype);
   if (kv->d != 64 && kv->d != 128) return fail(SSD_ERR_UNSUPPORTED, "%s: head dim %d (64 or 128)", who, kv->d);
   if (kv->page_size <= 0 || (kv->page_size & (kv->page_size - 1)))
     return fail(SSD_ERR_UNSUPPORTED, "%s: page_size %d is not a power of two", who, kv->page_size);

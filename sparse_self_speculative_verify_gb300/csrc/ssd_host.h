@@ -19,13 +19,8 @@ int check_launch(const char *what);
 unsigned *device_status();
 // Number of SMs of the current device (cached).
 int sm_count();
-// Validates the cache description and fills `v`.  `kinds` lists the accepted element types as bits;
-// validate_kv takes the 16- and 32-bit ones.
-constexpr unsigned kCache16Or32 = 1u, kCacheNvfp4 = 2u;
-int validate_cache(const ssd_paged_kv *kv, KVView *v, const char *who, unsigned kinds);
+// Validates the cache description; fills `v`.  `need_mask` lists the accepted dtypes as bits.
 int validate_kv(const ssd_paged_kv *kv, KVView *v, const char *who);
-// A 4-bit cache's k_scale and v_scale: powers of two, so that applying them never rounds.
-int kv4_scales_ok(float k_scale, float v_scale, const char *who);
 
 // Whether kernels are launched with programmatic stream serialization (programmatic dependent
 // launch): on unless the environment variable SSD_PDL is "0" when the library first launches.

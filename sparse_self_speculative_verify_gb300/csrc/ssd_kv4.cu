@@ -3,6 +3,7 @@
 
 #include <initializer_list>
 
+#include "ssd_cache.h"
 #include "ssd_kv4_attn.cuh"
 
 namespace ssd {
@@ -78,8 +79,6 @@ static int kv4_prepare(const Kv4Call &c, int max_tokens, Kv4AttnArgs *a, Kv4Layo
     return fail(SSD_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", who, c.workspace_bytes, lay->total);
   if (reinterpret_cast<uintptr_t>(c.workspace) & 255u)
     return fail(SSD_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
-  if (c.kv->batch == 0) return SSD_OK;
-  if (!(a->status = device_status())) return SSD_ERR_CUDA;
   char *ws = static_cast<char *>(c.workspace);
   a->q = c.q, a->out = c.out, a->lse = c.lse;
   a->q_f32 = c.q_dtype == SSD_DTYPE_F32, a->out_f32 = c.out_dtype == SSD_DTYPE_F32;
@@ -121,6 +120,7 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
   if (scores && scores_stride < kv->max_seq_len)
     return fail(SSD_ERR_INVALID_ARG, "%s: scores_stride %lld < max_seq_len %d", who, (long long)scores_stride, kv->max_seq_len);
   if (kv->batch == 0) return SSD_OK;
+  if (!(a.status = device_status())) return SSD_ERR_CUDA;
   if (scores && !a.lse) a.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + lay.lse);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int nt = kv4_nt(a.R), grid = kv4_grid(a.n_units, kv->max_seq_len, kv4_blocks_per_sm(nt));
@@ -152,6 +152,7 @@ extern "C" int ssd_kv4_draft_attn(const ssd_paged_kv *kv, const void *q, int q_d
   if (!cnt || (!idx && k_max > 0)) return fail(SSD_ERR_INVALID_ARG, "%s: idx and cnt must be non-NULL", who);
   if (a.G > 16) return fail(SSD_ERR_UNSUPPORTED, "%s: group size %d > 16", who, a.G);
   if (kv->batch == 0) return SSD_OK;
+  if (!(a.status = device_status())) return SSD_ERR_CUDA;
   a.idx = idx, a.cnt = cnt, a.k_max = k_max;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int nt = kv4_nt(a.R), grid = kv4_grid(a.n_units, k_max, kv4_blocks_per_sm(nt));

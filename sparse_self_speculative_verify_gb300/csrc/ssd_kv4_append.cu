@@ -4,7 +4,7 @@
 // exact):  s = e4m3(max |x| / 6),  code_i = e2m1(x_i / s), both to nearest with ties to even and
 // saturating; s = 0 stores zeros.  SparseSpec §2.3 / SpecSA "branch handling": the candidates of a round
 // are appended at the request's end, as ssd_kv_append does for 16- and 32-bit caches.
-#include "ssd_host.h"
+#include "ssd_cache.h"
 #include "ssd_kv4.cuh"
 
 namespace ssd {

@@ -1,0 +1,508 @@
+// ssd_pages.cu -- pages of a paged cache shared, taken, given back and compacted on the device.
+//
+// The only state beside a cache's page table and lengths is one reference count per page: a page is free
+// when its count is 0, and taking a page always takes the lowest free index, so the outcome of every call
+// is a function of its inputs.  The calls move whole rows of bytes and work on 16-, 32- and 4-bit caches.
+//
+// SpecSA ("SpecSA：融合推测解码与稀疏注意力的高效LLM推理框架"), "branch handling": branches of a request
+// share the KV of their common tokens.  SparseSpec §4.1: the tokens a verify selects are the ones kept.
+#include "ssd_cache.h"
+#include "ssd_kv4.cuh"
+
+namespace ssd {
+
+// A row of bytes per (page, K|V, head, token): `wide` bytes at slot * wide of the block and, for a 4-bit
+// cache, `thin` bytes behind all the wide parts.
+struct RowShape {
+  int wide, thin;
+};
+static RowShape row_shape(const ssd_paged_kv *kv) {
+  if (kv->dtype == SSD_DTYPE_NVFP4) return {kv4_code_bytes(kv->d), kv4_scale_bytes(kv->d)};
+  return {kv->d * (kv->dtype == SSD_DTYPE_BF16 ? 2 : 4), 0};
+}
+
+// ---- fork -----------------------------------------------------------------------------------
+constexpr int kForkThreads = 256;
+
+// One block per pair.  dst's row becomes a copy of the first ceil(L / page_size) entries of src's.  Pairs
+// of one call must not touch each other's rows: whatever a pair reads no other pair writes.
+__global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(KVView kv, int32_t *table, int32_t *seq_lens, int32_t *refs,
+                                                               const int32_t *src, const int32_t *dst, int n,
+                                                               unsigned *status) {
+  const int i = blockIdx.x, tid = threadIdx.x;
+  pdl_trigger();
+  pdl_wait();
+  const int s = src[i], d = dst[i];
+  bool ok = s >= 0 && s < kv.batch && d >= 0 && d < kv.batch;
+  for (int j = tid; j < n && ok; j += kForkThreads) ok = dst[j] != s && !(j < i && dst[j] == d);
+  if (!__syncthreads_and(ok)) {
+    if (tid == 0) atomicOr(status, (unsigned)SSD_FAULT_INDEX);
+    return;
+  }
+  const int L = seq_lens[s];
+  if (L < 0 || L > kv.max_seq_len) {
+    if (tid == 0) atomicOr(status, (unsigned)SSD_FAULT_SEQLEN);
+    return;
+  }
+  const int np = (L + kv.page_size - 1) >> kv.log2_ps;
+  const int32_t *from = table + (int64_t)s * kv.max_pages;
+  int32_t *to = table + (int64_t)d * kv.max_pages;
+  // Every page of src held by somebody, and dst's row empty.
+  for (int j = tid; j < kv.max_pages; j += kForkThreads) {
+    ok &= to[j] < 0;
+    if (j < np) {
+      const int32_t p = from[j];
+      ok &= p >= 0 && (int64_t)p < kv.num_pages && refs[p] > 0;
+    }
+  }
+  if (!__syncthreads_and(ok)) {
+    if (tid == 0) atomicOr(status, (unsigned)SSD_FAULT_PAGE);
+    return;
+  }
+  for (int j = tid; j < np; j += kForkThreads) {
+    const int32_t p = from[j];
+    to[j] = p;
+    atomicAdd(refs + p, 1);
+  }
+  if (tid == 0) seq_lens[d] = L;
+}
+
+// ---- release --------------------------------------------------------------------------------
+constexpr int kReleaseThreads = 256;
+
+// One block per request: entries behind the kept tokens leave the row, and their pages lose a holder.
+__global__ void __launch_bounds__(kReleaseThreads) kv_release_kernel(KVView kv, int32_t *table, int32_t *seq_lens,
+                                                                     int32_t *refs, const int32_t *keep, unsigned *status) {
+  const int b = blockIdx.x, tid = threadIdx.x;
+  pdl_trigger();
+  pdl_wait();
+  const int k = keep[b];
+  if (k < 0) return;
+  int32_t *row = table + (int64_t)b * kv.max_pages;
+  for (int64_t j = ((int64_t)k + kv.page_size - 1) / kv.page_size + tid; j < kv.max_pages; j += kReleaseThreads) {
+    const int32_t p = row[j];
+    if (p < 0) continue;
+    row[j] = -1;
+    // A count never goes below 0, whatever the table says.
+    if ((int64_t)p >= kv.num_pages) {
+      atomicOr(status, (unsigned)SSD_FAULT_PAGE);
+    } else if (atomicSub(refs + p, 1) <= 0) {
+      atomicAdd(refs + p, 1);
+      atomicOr(status, (unsigned)SSD_FAULT_PAGE);
+    }
+  }
+  if (tid == 0) {
+    const int L = seq_lens[b];
+    if (L < 0 || L > kv.max_seq_len)
+      atomicOr(status, (unsigned)SSD_FAULT_SEQLEN);
+    else if (k < L)
+      seq_lens[b] = k;
+  }
+}
+
+// ---- reserve --------------------------------------------------------------------------------
+constexpr int kResThreads = 1024;
+constexpr int kResLanes = 8;  // lanes per request
+
+// Per page of the pool, valid for the pages that requests of the call hold and ask for.
+struct PageAsk {
+  int refs;    // its count before the call
+  int asked;   // requests of the call that hold it and want to write it
+  int lowest;  // the first of them
+  int pad;
+};
+struct ReserveArgs {
+  KVView kv;
+  int32_t *table;
+  int32_t *refs;
+  const int32_t *counts;
+  PageAsk *ask;     // [num_pages]
+  int32_t *take;    // [batch]: pages each request needs (-1: request skipped), then their exclusive sums
+  int32_t *fresh;   // [num_pages]: the free pages handed out, ascending
+  int4 *copies;     // [batch]: {old page, new page, live slots, 0}; slots 0: nothing to copy
+  unsigned *status;
+};
+
+// One block.  A request needs a page for every page index that its tokens L .. L + n - 1 touch: where it has
+// none, and where it holds one together with others.  If all holders of a page ask, the first of them keeps
+// it.  Phases, with the whole block in step: what is asked of every page; how many new pages a request
+// needs; the first free pages of the pool; hand them out.  If they do not suffice nothing is changed.
+__global__ void __launch_bounds__(kResThreads) kv_reserve_kernel(ReserveArgs a) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int grp = tid / kResLanes, gl = tid % kResLanes;
+  constexpr int kGroups = kResThreads / kResLanes;
+  const unsigned gmask = 0xffu << (lane & ~(kResLanes - 1));
+  __shared__ int s_warp[33];
+  pdl_wait();
+  const KVView &kv = a.kv;
+  const int ps = kv.page_size;
+
+  // Requests in order: whether a request can be served at all, and its pages' counts before the call.
+  for (int b = grp; b < kv.batch; b += kGroups) {
+    const int L = kv.seq_lens[b], n = a.counts[b];
+    bool len_ok = L >= 0 && n >= 0 && (int64_t)L + n <= kv.max_seq_len;
+    bool page_ok = true;
+    if (len_ok && n > 0) {
+      const int32_t *row = a.table + (int64_t)b * kv.max_pages;
+      const int j0 = L >> kv.log2_ps, j1 = (L + n + ps - 1) >> kv.log2_ps;
+      for (int j = j0 + gl; j < j1; j += kResLanes) {
+        const int32_t p = row[j];
+        if (p < 0) {
+          page_ok &= !(j == j0 && (L & (ps - 1)));  // the page of live tokens is missing
+          continue;
+        }
+        if ((int64_t)p >= kv.num_pages) {
+          page_ok = false;
+          continue;
+        }
+        const int rc = a.refs[p];
+        page_ok &= rc > 0;
+        a.ask[p] = PageAsk{rc, 0, 0x7fffffff, 0};
+      }
+    }
+    page_ok = __all_sync(gmask, page_ok);
+    if (gl == 0) {
+      if (!len_ok) atomicOr(a.status, (unsigned)SSD_FAULT_SEQLEN);
+      if (!page_ok) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
+      a.take[b] = len_ok && page_ok ? 0 : -1;
+    }
+  }
+  __syncthreads();
+  // Who asks for a page that it shares.
+  for (int b = grp; b < kv.batch; b += kGroups) {
+    if (a.take[b] < 0 || a.counts[b] == 0) continue;
+    const int L = kv.seq_lens[b], n = a.counts[b];
+    const int32_t *row = a.table + (int64_t)b * kv.max_pages;
+    for (int j = (L >> kv.log2_ps) + gl; j < (L + n + ps - 1) >> kv.log2_ps; j += kResLanes) {
+      const int32_t p = row[j];
+      if (p < 0 || a.ask[p].refs == 1) continue;
+      atomicAdd(&a.ask[p].asked, 1);
+      atomicMin(&a.ask[p].lowest, b);
+    }
+  }
+  __syncthreads();
+  // Pages to take, per request.
+  auto takes = [&](int b, int32_t p) {
+    if (p < 0) return true;
+    const PageAsk k = a.ask[p];
+    return !(k.refs == 1 || (k.asked == k.refs && k.lowest == b));
+  };
+  for (int b = grp; b < kv.batch; b += kGroups) {
+    int c = 0;
+    if (a.take[b] >= 0 && a.counts[b] > 0) {
+      const int L = kv.seq_lens[b], n = a.counts[b];
+      const int32_t *row = a.table + (int64_t)b * kv.max_pages;
+      for (int j = (L >> kv.log2_ps) + gl; j < (L + n + ps - 1) >> kv.log2_ps; j += kResLanes) c += takes(b, row[j]);
+    }
+#pragma unroll
+    for (int o = kResLanes / 2; o; o >>= 1) c += __shfl_xor_sync(gmask, c, o);
+    if (gl == 0 && a.take[b] >= 0) a.take[b] = c;
+  }
+  __syncthreads();
+  // Exclusive sums over the requests, in their order (skipped requests keep -1), through `copies.w`.
+  int total = 0;
+  for (int b0 = 0; b0 < kv.batch; b0 += kResThreads) {
+    const int b = b0 + tid;
+    const int v = b < kv.batch ? max(a.take[b], 0) : 0;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+      int w = s_warp[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+      }
+      s_warp[lane] = w;
+    }
+    __syncthreads();
+    const int base = total + (warp ? s_warp[warp - 1] : 0);
+    if (b < kv.batch) a.copies[b] = make_int4(0, 0, 0, base + inc - v);
+    total += s_warp[31];
+    __syncthreads();
+  }
+  // The first `total` free pages.
+  int found = 0;
+  for (int64_t p0 = 0; p0 < kv.num_pages && found < total; p0 += kResThreads * 4) {
+    const int64_t p = p0 + tid * 4;
+    int v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = p + k < kv.num_pages ? (a.refs[p + k] == 0) : 0;
+    const int mine = v[0] + v[1] + v[2] + v[3];
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+      int w = s_warp[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+      }
+      s_warp[lane] = w;
+    }
+    __syncthreads();
+    int at = found + (warp ? s_warp[warp - 1] : 0) + inc - mine;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (v[k] && at < total) a.fresh[at++] = (int32_t)(p + k);
+    found += s_warp[31];
+    __syncthreads();
+  }
+  if (found < total) {
+    if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_NOPAGE);
+    return;
+  }
+  for (int b = grp; b < kv.batch; b += kGroups) {
+    if (a.take[b] <= 0) continue;
+    const int L = kv.seq_lens[b], n = a.counts[b];
+    int32_t *row = a.table + (int64_t)b * kv.max_pages;
+    int at = a.copies[b].w;
+    const int j0 = L >> kv.log2_ps, j1 = (L + n + ps - 1) >> kv.log2_ps;
+    for (int jb = j0; jb < j1; jb += kResLanes) {
+      const int j = jb + gl;
+      const int32_t p = j < j1 ? row[j] : -1;
+      const bool t = j < j1 && takes(b, p);
+      const unsigned m = __ballot_sync(gmask, t) & gmask;
+      if (t) {
+        const int32_t f = a.fresh[at + __popc(m & ((1u << lane) - 1))];
+        row[j] = f;
+        a.refs[f] = 1;
+        if (p >= 0) {
+          atomicSub(a.refs + p, 1);
+          if (j == j0 && (L & (ps - 1))) a.copies[b] = make_int4(p, f, L & (ps - 1), 0);
+        }
+      }
+      at += __popc(m);
+    }
+  }
+}
+
+constexpr int kMoveThreads = 128;
+
+// The live slots of shared last pages into the pages that replace them.  Block (x, b): K or V of a head.
+__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(char *pool, const int4 *copies, int page_size, int h_kv,
+                                                               RowShape rs) {
+  pdl_trigger();
+  pdl_wait();
+  const int4 c = copies[blockIdx.y];
+  if (c.z == 0) return;
+  const int64_t block_bytes = (int64_t)page_size * (rs.wide + rs.thin);
+  const int64_t part = blockIdx.x;
+  const char *src = pool + ((int64_t)c.x * 2 * h_kv + part) * block_bytes;
+  char *dst = pool + ((int64_t)c.y * 2 * h_kv + part) * block_bytes;
+  for (int e = threadIdx.x; e < c.z * rs.wide / 16; e += kMoveThreads)
+    reinterpret_cast<uint4 *>(dst)[e] = reinterpret_cast<const uint4 *>(src)[e];
+  const int thin0 = page_size * rs.wide;
+  for (int e = threadIdx.x; e < c.z * rs.thin / 4; e += kMoveThreads)
+    reinterpret_cast<uint32_t *>(dst + thin0)[e] = reinterpret_cast<const uint32_t *>(src + thin0)[e];
+}
+
+// ---- compact --------------------------------------------------------------------------------
+constexpr int kCompactThreads = 256;
+constexpr int kCompactTokens = 128;  // list entries per block
+
+struct CompactArgs {
+  KVView from, to;
+  char *to_pool;
+  int32_t *to_lens;
+  const int32_t *to_refs;
+  const int32_t *src, *dst, *idx, *cnt;
+  int n, k_max;
+  bool same;  // one cache
+  RowShape rs;
+  unsigned *status;
+};
+
+// Block (x, g, i): list entries [x * kCompactTokens, ...) of head g of pair i.  Addresses first, one entry
+// per thread, then 16-byte pieces of the rows.
+__global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactArgs a) {
+  const int i = blockIdx.z, g = blockIdx.y, j0 = blockIdx.x * kCompactTokens, tid = threadIdx.x;
+  const int h = a.from.h_kv;
+  __shared__ int64_t s_from[kCompactTokens], s_to[kCompactTokens];  // K block of the entry, or -1
+  __shared__ int s_slots[kCompactTokens];
+  pdl_trigger();
+  pdl_wait();
+  const int s = a.src[i], d = a.dst[i];
+  bool ok = s >= 0 && s < a.from.batch && d >= 0 && d < a.to.batch;
+  for (int j = tid; j < a.n && ok; j += kCompactThreads) ok = !(j < i && a.dst[j] == d) && !(a.same && a.src[j] == d);
+  if (!__syncthreads_and(ok)) {
+    if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
+    return;
+  }
+  const int count = a.cnt[(int64_t)i * h];
+  for (int j = tid; j < h; j += kCompactThreads) ok &= a.cnt[(int64_t)i * h + j] == count;
+  ok &= count >= 0 && count <= a.k_max;
+  if (!__syncthreads_and(ok)) {
+    if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_KMAX);
+    return;
+  }
+  const int L = a.from.seq_lens[s];
+  if (L < 0 || L > a.from.max_seq_len || count > a.to.max_seq_len) {
+    if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_SEQLEN);
+    return;
+  }
+  if (tid == 0 && j0 == 0 && g == 0) a.to_lens[d] = count;
+  const int nj = min(kCompactTokens, count - j0);
+  const int64_t fb = (int64_t)a.from.page_size * (a.rs.wide + a.rs.thin), tb = (int64_t)a.to.page_size * (a.rs.wide + a.rs.thin);
+  if (tid < nj) {
+    const int j = j0 + tid, t = a.idx[((int64_t)i * h + g) * a.k_max + j];
+    int64_t f = -1, to = -1;
+    if (t < 0 || t >= L) {
+      atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
+    } else {
+      const int32_t p = __ldg(a.from.page_table + (int64_t)s * a.from.max_pages + (t >> a.from.log2_ps));
+      if (p < 0 || (int64_t)p >= a.from.num_pages)
+        atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
+      else
+        f = ((int64_t)p * 2 * h + g) * fb;
+    }
+    const int32_t p = __ldg(a.to.page_table + (int64_t)d * a.to.max_pages + (j >> a.to.log2_ps));
+    if (p < 0 || (int64_t)p >= a.to.num_pages || (a.to_refs && a.to_refs[p] != 1))
+      atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
+    else
+      to = ((int64_t)p * 2 * h + g) * tb;
+    s_from[tid] = f, s_to[tid] = to;
+    s_slots[tid] = t & (a.from.page_size - 1);
+  }
+  __syncthreads();
+  const char *from = static_cast<const char *>(a.from.pool);
+  const int cpr = a.rs.wide / 16;
+  const int pieces = nj * 2 * cpr;
+  for (int e = tid; e < pieces; e += kCompactThreads) {
+    const int c = e % cpr, which = (e / cpr) & 1, j = e / (2 * cpr);
+    if (s_to[j] < 0) continue;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (s_from[j] >= 0) v = __ldg(reinterpret_cast<const uint4 *>(from + s_from[j] + which * h * fb + s_slots[j] * a.rs.wide) + c);
+    reinterpret_cast<uint4 *>(a.to_pool + s_to[j] + which * h * tb + (int64_t)((j0 + j) & (a.to.page_size - 1)) * a.rs.wide)[c] = v;
+  }
+  if (a.rs.thin) {
+    const int tpr = a.rs.thin / 4;
+    for (int e = tid; e < nj * 2 * tpr; e += kCompactThreads) {
+      const int c = e % tpr, which = (e / tpr) & 1, j = e / (2 * tpr);
+      if (s_to[j] < 0) continue;
+      uint32_t v = 0;
+      if (s_from[j] >= 0)
+        v = __ldg(reinterpret_cast<const uint32_t *>(from + s_from[j] + which * h * fb + a.from.page_size * a.rs.wide + s_slots[j] * a.rs.thin) + c);
+      reinterpret_cast<uint32_t *>(a.to_pool + s_to[j] + which * h * tb + a.to.page_size * a.rs.wide +
+                                   ((j0 + j) & (a.to.page_size - 1)) * a.rs.thin)[c] = v;
+    }
+  }
+}
+
+static int page_checks(const ssd_paged_kv *kv, KVView *v, const int32_t *refs, const char *who) {
+  int rc = validate_cache(kv, v, who, kCache16Or32 | kCacheNvfp4);
+  if (rc) return rc;
+  if (!refs) return fail(SSD_ERR_INVALID_ARG, "%s: page_refs must be non-NULL", who);
+  if (kv->num_pages > 0x7fffffff) return fail(SSD_ERR_UNSUPPORTED, "%s: num_pages above 2^31 - 1", who);
+  return SSD_OK;
+}
+
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" int ssd_kv_fork(const ssd_paged_kv *kv, int32_t *page_refs, const int32_t *src, const int32_t *dst, int n,
+                           ssd_stream_t stream) {
+  const char *who = "ssd_kv_fork";
+  KVView v;
+  int rc = page_checks(kv, &v, page_refs, who);
+  if (rc) return rc;
+  if (n < 0) return fail(SSD_ERR_INVALID_ARG, "%s: n %d < 0", who, n);
+  if (n == 0) return SSD_OK;
+  if (!src || !dst) return fail(SSD_ERR_INVALID_ARG, "%s: src and dst must be non-NULL", who);
+  unsigned *status = device_status();
+  if (!status) return SSD_ERR_CUDA;
+  return launch(kv_fork_kernel, dim3(n), dim3(kForkThreads), 0, reinterpret_cast<cudaStream_t>(stream), "kv_fork_kernel", v,
+                const_cast<int32_t *>(kv->page_table), const_cast<int32_t *>(kv->seq_lens), page_refs, src, dst, n, status);
+}
+
+extern "C" int ssd_kv_release(const ssd_paged_kv *kv, int32_t *page_refs, const int32_t *keep, ssd_stream_t stream) {
+  const char *who = "ssd_kv_release";
+  KVView v;
+  int rc = page_checks(kv, &v, page_refs, who);
+  if (rc) return rc;
+  if (kv->batch == 0) return SSD_OK;
+  if (!keep) return fail(SSD_ERR_INVALID_ARG, "%s: keep must be non-NULL", who);
+  unsigned *status = device_status();
+  if (!status) return SSD_ERR_CUDA;
+  return launch(kv_release_kernel, dim3(kv->batch), dim3(kReleaseThreads), 0, reinterpret_cast<cudaStream_t>(stream),
+                "kv_release_kernel", v, const_cast<int32_t *>(kv->page_table), const_cast<int32_t *>(kv->seq_lens), page_refs,
+                keep, status);
+}
+
+static size_t reserve_layout(const ssd_paged_kv *kv, ReserveArgs *a, void *ws) {
+  Carver c(ws);
+  c.off = kCounterBytes;
+  PageAsk *ask = c.take<PageAsk>((size_t)kv->num_pages);
+  int32_t *fresh = c.take<int32_t>((size_t)kv->num_pages);
+  int4 *copies = c.take<int4>((size_t)kv->batch);
+  int32_t *take = c.take<int32_t>((size_t)kv->batch);
+  if (a) a->ask = ask, a->fresh = fresh, a->copies = copies, a->take = take;
+  return c.off;
+}
+
+extern "C" size_t ssd_kv_reserve_workspace_bytes(const ssd_paged_kv *kv) {
+  if (!kv || kv->num_pages <= 0 || kv->batch < 0) return 0;
+  return reserve_layout(kv, nullptr, nullptr);
+}
+
+extern "C" int ssd_kv_reserve(const ssd_paged_kv *kv, int32_t *page_refs, const int32_t *counts, void *workspace,
+                              size_t workspace_bytes, ssd_stream_t stream) {
+  const char *who = "ssd_kv_reserve";
+  ReserveArgs a{};
+  int rc = page_checks(kv, &a.kv, page_refs, who);
+  if (rc) return rc;
+  if (kv->batch > 65535) return fail(SSD_ERR_UNSUPPORTED, "%s: batch above 65535", who);
+  if (!counts && kv->batch > 0) return fail(SSD_ERR_INVALID_ARG, "%s: counts must be non-NULL", who);
+  const size_t need = ssd_kv_reserve_workspace_bytes(kv);
+  if (!workspace || workspace_bytes < need)
+    return fail(SSD_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", who, workspace_bytes, need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(SSD_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
+  if (kv->batch == 0) return SSD_OK;
+  if (!(a.status = device_status())) return SSD_ERR_CUDA;
+  reserve_layout(kv, &a, workspace);
+  a.table = const_cast<int32_t *>(kv->page_table);
+  a.refs = page_refs;
+  a.counts = counts;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if ((rc = launch(kv_reserve_kernel, dim3(1), dim3(kResThreads), 0, st, "kv_reserve_kernel", a))) return rc;
+  return launch(kv_move_kernel, dim3(2 * kv->h_kv, kv->batch), dim3(kMoveThreads), 0, st, "kv_move_kernel",
+                static_cast<char *>(const_cast<void *>(kv->pool)), a.copies, kv->page_size, kv->h_kv, row_shape(kv));
+}
+
+extern "C" int ssd_kv_compact(const ssd_paged_kv *kv, const ssd_paged_kv *to, const int32_t *to_refs, const int32_t *src,
+                              const int32_t *dst, int n, const int32_t *idx, int k_max, const int32_t *cnt,
+                              ssd_stream_t stream) {
+  const char *who = "ssd_kv_compact";
+  CompactArgs a{};
+  int rc = validate_cache(kv, &a.from, who, kCache16Or32 | kCacheNvfp4);
+  if (rc || (rc = validate_cache(to, &a.to, who, kCache16Or32 | kCacheNvfp4))) return rc;
+  if (kv->dtype != to->dtype || kv->h_kv != to->h_kv || kv->d != to->d)
+    return fail(SSD_ERR_INVALID_ARG, "%s: the two caches differ in dtype, h_kv or d", who);
+  if (n < 0 || k_max < 0) return fail(SSD_ERR_INVALID_ARG, "%s: n and k_max must be >= 0", who);
+  if (n > 65535 || kv->h_kv > 65535) return fail(SSD_ERR_UNSUPPORTED, "%s: n or h_kv above 65535", who);
+  if (n == 0) return SSD_OK;
+  if (!src || !dst || !cnt || (!idx && k_max > 0)) return fail(SSD_ERR_INVALID_ARG, "%s: src, dst, idx and cnt must be non-NULL", who);
+  if (!(a.status = device_status())) return SSD_ERR_CUDA;
+  a.to_pool = static_cast<char *>(const_cast<void *>(to->pool));
+  a.to_lens = const_cast<int32_t *>(to->seq_lens);
+  a.to_refs = to_refs;
+  a.src = src, a.dst = dst, a.idx = idx, a.cnt = cnt, a.n = n, a.k_max = k_max;
+  a.same = kv->page_table == to->page_table;
+  a.rs = row_shape(kv);
+  return launch(kv_compact_kernel, dim3(cdiv(k_max > 0 ? k_max : 1, kCompactTokens), kv->h_kv, n), dim3(kCompactThreads), 0,
+                reinterpret_cast<cudaStream_t>(stream), "kv_compact_kernel", a);
+}
