@@ -663,11 +663,15 @@ def _scope(device, stream):
     return torch.cuda.stream(stream)  # switches to the stream's device as well
 
 
+def _raw_stream(device) -> int:
+    return torch.cuda.current_stream(device.index).cuda_stream
+
+
 def _typed(t: torch.Tensor, name: str, device, shape=None) -> int:
     _need(t, name, None, device)
     if t.dtype not in _TYPES:
         raise TypeError(f"{name} must be bf16 or fp32, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     return _TYPES[t.dtype]
 
@@ -676,7 +680,7 @@ def _shaped(t: Optional[torch.Tensor], name: str, dtype, device, shape):
     if t is None:
         return None
     _need(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -696,7 +700,7 @@ def _stream_ws(device, name: str, nbytes: int, workspace: Optional[Workspace]):
     if torch.cuda.is_current_stream_capturing():
         buf = torch.zeros(int(nbytes) + 256, dtype=torch.uint8, device=device)
         return ctypes.c_void_p(Workspace.aligned(buf)), int(nbytes)
-    return _ws(device, f"{name}@{torch.cuda.current_stream().cuda_stream:x}", nbytes, None)
+    return _ws(device, (name, _raw_stream(device)), nbytes, None)
 
 
 def ssd_kv4_append(kv: KV4Cache, k_new: torch.Tensor, v_new: torch.Tensor, counts: Optional[torch.Tensor] = None,
@@ -712,7 +716,7 @@ def ssd_kv4_append(kv: KV4Cache, k_new: torch.Tensor, v_new: torch.Tensor, count
     _shaped(counts, "counts", torch.int32, kv.device, (kv.batch,))
     with _scope(kv.device, stream):
         _check(_lib().ssd_kv4_append(kv.ref(), _ptr(k_new), _ptr(v_new), dt, k_new.shape[1], _ptr(counts),
-                                     float(kv.k_scale), float(kv.v_scale), _stream()))
+                                     float(kv.k_scale), float(kv.v_scale), _raw_stream(kv.device)))
 
 
 def ssd_kv4_read(kv: KV4Cache, first: torch.Tensor, n: int, counts: Optional[torch.Tensor] = None, *, k=None, v=None,
@@ -731,7 +735,7 @@ def ssd_kv4_read(kv: KV4Cache, first: torch.Tensor, n: int, counts: Optional[tor
         dt = _typed(k, "k", dev, shape)
         _shaped(v, "v", k.dtype, dev, shape)
         _check(_lib().ssd_kv4_read(kv.ref(), _ptr(first), _ptr(counts), int(n), float(kv.k_scale), float(kv.v_scale), dt,
-                                   _ptr(k), _ptr(v), _stream()))
+                                   _ptr(k), _ptr(v), _raw_stream(dev)))
     return k, v
 
 
@@ -762,7 +766,7 @@ def ssd_kv4_verify_attn(kv: KV4Cache, q: torch.Tensor, n_cand: int, scale: float
         wsp, avail = _stream_ws(dev, "kv4", need, workspace)
         _check(L.ssd_kv4_verify_attn(kv.ref(), _ptr(q), qt, h_q, n_cand, float(scale), float(kv.k_scale),
                                      float(kv.v_scale), _ptr(out), ot, _ptr(lse), _ptr(scores),
-                                     scores.shape[-1] if scores is not None else 0, wsp, avail, _stream()))
+                                     scores.shape[-1] if scores is not None else 0, wsp, avail, _raw_stream(dev)))
     return {"out": out, "lse": lse, "scores": scores}
 
 
@@ -795,7 +799,7 @@ def ssd_kv4_draft_attn(kv: KV4Cache, q: torch.Tensor, idx: torch.Tensor, cnt: to
         wsp, avail = _stream_ws(dev, "kv4", need, workspace)
         _check(L.ssd_kv4_draft_attn(kv.ref(), _ptr(q), qt, h_q, _ptr(idx), k_max, _ptr(cnt), float(scale),
                                     float(kv.k_scale), float(kv.v_scale), _ptr(out), ot, _ptr(lse), wsp, avail,
-                                    _stream()))
+                                    _raw_stream(dev)))
     return {"out": out, "lse": lse}
 
 
@@ -846,7 +850,7 @@ def ssd_kv_fork(kv, pages: PagePool, src: torch.Tensor, dst: torch.Tensor, strea
     _rows(src, "src", kv.device)
     _rows(dst, "dst", kv.device, src.shape[0])
     with _scope(kv.device, stream):
-        _check(_lib().ssd_kv_fork(kv.ref(), refs, _ptr(src), _ptr(dst), src.shape[0], _stream()))
+        _check(_lib().ssd_kv_fork(kv.ref(), refs, _ptr(src), _ptr(dst), src.shape[0], _raw_stream(kv.device)))
 
 
 def ssd_kv_reserve(kv, pages: PagePool, counts: torch.Tensor, *, workspace: Optional[Workspace] = None,
@@ -858,7 +862,7 @@ def ssd_kv_reserve(kv, pages: PagePool, counts: torch.Tensor, *, workspace: Opti
     with _scope(kv.device, stream):
         L = _lib()
         wsp, avail = _stream_ws(kv.device, "pages", L.ssd_kv_reserve_workspace_bytes(kv.ref()), workspace)
-        _check(L.ssd_kv_reserve(kv.ref(), refs, _ptr(counts), wsp, avail, _stream()))
+        _check(L.ssd_kv_reserve(kv.ref(), refs, _ptr(counts), wsp, avail, _raw_stream(kv.device)))
 
 
 def ssd_kv_release(kv, pages: PagePool, keep: torch.Tensor, stream=None) -> None:
@@ -867,7 +871,7 @@ def ssd_kv_release(kv, pages: PagePool, keep: torch.Tensor, stream=None) -> None
     refs = _pages_of(kv, pages)
     _rows(keep, "keep", kv.device, kv.batch)
     with _scope(kv.device, stream):
-        _check(_lib().ssd_kv_release(kv.ref(), refs, _ptr(keep), _stream()))
+        _check(_lib().ssd_kv_release(kv.ref(), refs, _ptr(keep), _raw_stream(kv.device)))
 
 
 def ssd_kv_compact(kv, to, src: torch.Tensor, dst: torch.Tensor, idx: torch.Tensor, cnt: torch.Tensor,
@@ -893,4 +897,4 @@ def ssd_kv_compact(kv, to, src: torch.Tensor, dst: torch.Tensor, idx: torch.Tens
     _shaped(cnt, "cnt", torch.int32, dev, (n, kv.h_kv))
     with _scope(dev, stream):
         _check(_lib().ssd_kv_compact(kv.ref(), to.ref(), refs, _ptr(src), _ptr(dst), n, _ptr(idx), idx.shape[2], _ptr(cnt),
-                                     _stream()))
+                                     _raw_stream(dev)))

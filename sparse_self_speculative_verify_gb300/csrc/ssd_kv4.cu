@@ -23,7 +23,7 @@ static int kv4_chunks(int R) { return cdiv(R, 8 * kv4_nt(R)); }
 // there are not eight tiles for each.
 static int64_t kv4_grid_bound(int64_t units, int max_tokens) {
   const int64_t tiles = units * (max_tokens > 0 ? cdiv(max_tokens, kKv4Tile) : 1);
-  const int64_t blocks = cdiv64(tiles, kKv4Warps);
+  const int64_t blocks = cdiv64(tiles, 8);
   return blocks > kKv4MaxBlocks ? kKv4MaxBlocks : blocks;
 }
 
@@ -73,6 +73,8 @@ static int kv4_prepare(const Kv4Call &c, int max_tokens, Kv4AttnArgs *a, Kv4Layo
   if (R > kMaxRows) return fail(SSD_ERR_UNSUPPORTED, "%s: %lld query rows per KV head (at most %d)", who, (long long)R, kMaxRows);
   if (!isfinite(c.scale)) return fail(SSD_ERR_INVALID_ARG, "%s: scale is not finite", who);
   if ((rc = kv4_scales_ok(c.k_scale, c.v_scale, who))) return rc;
+  if ((int64_t)c.kv->page_size * c.kv->h_kv * kv4_row_bytes(c.kv->d) >= (int64_t)1 << 30)
+    return fail(SSD_ERR_UNSUPPORTED, "%s: a page of 2 GB or more", who);
   if ((int64_t)c.kv->batch * c.kv->h_kv > 65535) return fail(SSD_ERR_UNSUPPORTED, "%s: batch*h_kv above 65535", who);
   *lay = kv4_layout(c.kv, c.h_q, c.n_rows, max_tokens);
   if (!c.workspace || c.workspace_bytes < lay->total)
@@ -98,7 +100,9 @@ static int kv4_grid(int64_t units, int max_tokens, int blocks_per_sm) {
   return (int)(bound < dev ? bound : dev);
 }
 
-static int kv4_blocks_per_sm(int nt) { return nt == 1 ? Kv4Tune<1>::kBlocks : Kv4Tune<2>::kBlocks; }
+static int kv4_blocks_per_sm(int nt) {
+  return nt == 1 ? Kv4Tune<1>::kBlocks : nt == 2 ? Kv4Tune<2>::kBlocks : nt == 3 ? Kv4Tune<3>::kBlocks : Kv4Tune<4>::kBlocks;
+}
 
 }  // namespace ssd
 
@@ -131,7 +135,7 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
   a.scores_stride = scores_stride;
   a.n_chunk = 1;
   a.n_units = kv->batch * kv->h_kv;
-  const int cgrid = kv4_grid(a.n_units, kv->max_seq_len, 2);
+  const int cgrid = kv4_grid(a.n_units, kv->max_seq_len, kKv4CritBlocks);
   return kv->d == 128 ? kv4_crit_d128(a, nt, cgrid, st) : kv4_crit_d64(a, nt, cgrid, st);
 }
 
