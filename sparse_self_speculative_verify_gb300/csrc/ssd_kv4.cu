@@ -4,26 +4,26 @@
 #include <initializer_list>
 
 #include "ssd_cache.h"
-#include "ssd_kv4_attn.cuh"
+#include "ssd_kv4_tc.cuh"
 
 namespace ssd {
 
 int kv4_dense_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
-int kv4_dense_d128(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
+int kv4_tc_attn(const Kv4AttnArgs &a, int rows, int grid, cudaStream_t st);
+int kv4_tc_crit(const Kv4AttnArgs &a, int np, int grid, cudaStream_t st);
 int kv4_list_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
 int kv4_list_d128(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
 int kv4_crit_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
-int kv4_crit_d128(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
 
-// Rows of a pass in steps of 8, and the passes: up to 32 rows go in one.
+// Query rows padded to what a pass takes, and the passes: up to 32 rows go in one.
 static int kv4_nt(int R) { return R > 8 * kKv4MaxNT ? kKv4MaxNT : cdiv(R, 8); }
-static int kv4_chunks(int R) { return cdiv(R, 8 * kv4_nt(R)); }
+static int kv4_np(int R) { return R <= 16 ? 16 : 32; }
+static int kv4_chunks(int R) { return cdiv(R, 32); }
 
-// Blocks of a launch over `units` units of at most `max_tokens` tokens: the device's, or fewer when
-// there are not eight tiles for each.
-static int64_t kv4_grid_bound(int64_t units, int max_tokens) {
+// Blocks of a launch over `units` units of at most `max_tokens` tokens, `tile` of which a block takes at least.
+static int64_t kv4_grid_bound(int64_t units, int max_tokens, int tile) {
   const int64_t tiles = units * (max_tokens > 0 ? cdiv(max_tokens, kKv4Tile) : 1);
-  const int64_t blocks = cdiv64(tiles, 8);
+  const int64_t blocks = cdiv64(tiles * kKv4Tile, tile);
   return blocks > kKv4MaxBlocks ? kKv4MaxBlocks : blocks;
 }
 
@@ -31,8 +31,8 @@ struct Kv4Layout {
   size_t o, ml, lse, total;
 };
 static Kv4Layout kv4_layout(const ssd_paged_kv *kv, int h_q, int n_rows, int max_tokens) {
-  const int R = h_q / kv->h_kv * n_rows, rows = 8 * kv4_nt(R);
-  const size_t slots = 2 * (size_t)kv4_grid_bound((int64_t)kv->batch * kv->h_kv * kv4_chunks(R), max_tokens);
+  const int R = h_q / kv->h_kv * n_rows, rows = kv4_np(R);
+  const size_t slots = 2 * (size_t)kv4_grid_bound((int64_t)kv->batch * kv->h_kv * kv4_chunks(R), max_tokens, kKv4Tile);
   Kv4Layout y{};
   y.o = kCounterBytes;
   y.ml = y.o + align256(slots * rows * kv->d * sizeof(float));
@@ -95,8 +95,8 @@ static int kv4_prepare(const Kv4Call &c, int max_tokens, Kv4AttnArgs *a, Kv4Layo
   return SSD_OK;
 }
 
-static int kv4_grid(int64_t units, int max_tokens, int blocks_per_sm) {
-  const int64_t bound = kv4_grid_bound(units, max_tokens), dev = (int64_t)sm_count() * blocks_per_sm;
+static int kv4_grid(int64_t units, int max_tokens, int tile, int blocks_per_sm) {
+  const int64_t bound = kv4_grid_bound(units, cdiv(max_tokens, tile) * tile, tile), dev = (int64_t)sm_count() * blocks_per_sm;
   return (int)(bound < dev ? bound : dev);
 }
 
@@ -127,16 +127,21 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
   if (!(a.status = device_status())) return SSD_ERR_CUDA;
   if (scores && !a.lse) a.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + lay.lse);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int nt = kv4_nt(a.R), grid = kv4_grid(a.n_units, kv->max_seq_len, kv4_blocks_per_sm(nt));
-  rc = kv->d == 128 ? kv4_dense_d128(a, nt, grid, st) : kv4_dense_d64(a, nt, grid, st);
+  // d = 128 runs on tcgen05; at d = 64 V^T would fill half the rows of its M = 128, and the mma.sync kernel runs.
+  const int nt = kv4_nt(a.R);
+  if (kv->d == 128)
+    rc = kv4_tc_attn(a, a.R > 32 ? 32 : a.R, kv4_grid(a.n_units, kv->max_seq_len, kKv4TcTile, 2), st);
+  else
+    rc = kv4_dense_d64(a, nt, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(nt)), st);
   if (rc || !scores) return rc;
   a.lse_in = a.lse;
   a.scores = scores;
   a.scores_stride = scores_stride;
   a.n_chunk = 1;
   a.n_units = kv->batch * kv->h_kv;
-  const int cgrid = kv4_grid(a.n_units, kv->max_seq_len, kKv4CritBlocks);
-  return kv->d == 128 ? kv4_crit_d128(a, nt, cgrid, st) : kv4_crit_d64(a, nt, cgrid, st);
+  if (kv->d == 128)
+    return kv4_tc_crit(a, a.R <= 32 ? kv4_np(a.R) : 64, kv4_grid(a.n_units, kv->max_seq_len, kKv4TcTile, kKv4CritTcBlocks), st);
+  return kv4_crit_d64(a, nt, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kKv4CritBlocks), st);
 }
 
 extern "C" size_t ssd_kv4_draft_workspace_bytes(const ssd_paged_kv *kv, int h_q, int k_max) {
@@ -159,6 +164,6 @@ extern "C" int ssd_kv4_draft_attn(const ssd_paged_kv *kv, const void *q, int q_d
   if (!(a.status = device_status())) return SSD_ERR_CUDA;
   a.idx = idx, a.cnt = cnt, a.k_max = k_max;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int nt = kv4_nt(a.R), grid = kv4_grid(a.n_units, k_max, kv4_blocks_per_sm(nt));
+  const int nt = kv4_nt(a.R), grid = kv4_grid(a.n_units, k_max, kKv4Tile * 4, kv4_blocks_per_sm(nt));
   return kv->d == 128 ? kv4_list_d128(a, nt, grid, st) : kv4_list_d64(a, nt, grid, st);
 }

@@ -99,7 +99,7 @@ __device__ __forceinline__ bool pair_any(int id, bool v) {
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
 
 // Tiles of a unit; a unit without tokens has one empty tile, whose rows come out as 0 and -inf.
-template <bool LIST>
+template <bool LIST, int TILE = kKv4Tile>
 __device__ __forceinline__ int kv4_tiles(const Kv4AttnArgs &a, int u) {
   int n;
   if (LIST) {
@@ -109,7 +109,7 @@ __device__ __forceinline__ int kv4_tiles(const Kv4AttnArgs &a, int u) {
     n = a.kv.seq_lens[u / (a.kv.h_kv * a.n_chunk)];
     n = n < 0 ? 0 : (n > a.kv.max_seq_len ? a.kv.max_seq_len : n);
   }
-  return n > 0 ? cdiv(n, kKv4Tile) : 1;
+  return n > 0 ? cdiv(n, TILE) : 1;
 }
 
 // Position of this block in the list of all units' tiles: the tiles are dealt out in equal contiguous
@@ -118,13 +118,13 @@ struct Kv4Range {
   int64_t x, x1, per;  // next tile, end, tiles per block
   int u, off;          // unit and tile inside it of x
 };
-template <bool LIST, int NW>
+template <bool LIST, int NW, int TILE = kKv4Tile, int MIN = NW>
 __device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int64_t *s_scan /* [NW + 2] */) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per_thread = cdiv(a.n_units, NW * 32);
   const int u0 = min(a.n_units, tid * per_thread), u1 = min(a.n_units, u0 + per_thread);
   int64_t sum = 0;
-  for (int u = u0; u < u1; ++u) sum += kv4_tiles<LIST>(a, u);
+  for (int u = u0; u < u1; ++u) sum += kv4_tiles<LIST, TILE>(a, u);
   int64_t inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -141,7 +141,7 @@ __device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int
     total += v;
   }
   int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < NW) per = NW;  // a tile for every warp before another block is used
+  if (per < MIN) per = MIN;  // MIN = NW: a tile for every warp before another block is used
   const int64_t x0 = per * blockIdx.x;
   if (x0 >= total) return false;
   const int64_t excl = base + inc - sum;
@@ -149,7 +149,7 @@ __device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int
     int64_t e = excl;
     int u = u0;
     for (;; ++u) {
-      const int n = kv4_tiles<LIST>(a, u);
+      const int n = kv4_tiles<LIST, TILE>(a, u);
       if (x0 < e + n) break;
       e += n;
     }

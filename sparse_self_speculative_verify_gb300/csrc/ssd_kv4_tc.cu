@@ -1,0 +1,46 @@
+// ssd_kv4_tc.cu -- launches of the tcgen05 kernels over a 4-bit cache (d = 128).
+#include "ssd_host.h"
+#include "ssd_kv4_tc.cuh"
+
+namespace ssd {
+
+template <int NP, int CW, int QS, int PS>
+static int launch_tc(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
+  constexpr auto kernel = kv4_tc_kernel<NP, CW, QS, PS>;
+  constexpr int smem = Kv4TcCfg<NP, QS>::kSmem;
+  int rc = ensure_smem<kernel>(smem);
+  if (rc) return rc;
+  return launch(kernel, dim3(grid), dim3(kKv4TcWarps * 32), smem, st, "kv4_tc_kernel", a);
+}
+
+template <int NP, int CW>
+static int launch_types(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
+  return a.q_f32 ? launch_tc<NP, CW, 2, 2>(a, grid, st) : a.out_f32 ? launch_tc<NP, CW, 1, 2>(a, grid, st) : launch_tc<NP, CW, 1, 1>(a, grid, st);
+}
+
+template <int NP, int QS>
+static int launch_crit(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
+  constexpr auto kernel = kv4_crit_tc_kernel<NP, QS, kKv4CritTcBlocks>;
+  constexpr int smem = Kv4CritCfg<NP, QS>::kSmem;
+  int rc = ensure_smem<kernel>(smem);
+  if (rc) return rc;
+  return launch(kernel, dim3(grid), dim3(kKv4CritTcWarps * 32), smem, st, "kv4_crit_tc_kernel", a);
+}
+
+// rows: of a pass (at most 32).
+int kv4_tc_attn(const Kv4AttnArgs &a, int rows, int grid, cudaStream_t st) {
+  return rows <= 8    ? launch_types<16, 4>(a, grid, st)
+         : rows <= 16 ? launch_types<16, 8>(a, grid, st)
+         : rows <= 24 ? launch_types<32, 12>(a, grid, st)
+                      : launch_types<32, 16>(a, grid, st);
+}
+
+int kv4_tc_crit(const Kv4AttnArgs &a, int np, int grid, cudaStream_t st) {
+  switch (np) {
+    case 16: return a.q_f32 ? launch_crit<16, 2>(a, grid, st) : launch_crit<16, 1>(a, grid, st);
+    case 32: return a.q_f32 ? launch_crit<32, 2>(a, grid, st) : launch_crit<32, 1>(a, grid, st);
+    default: return a.q_f32 ? launch_crit<64, 2>(a, grid, st) : launch_crit<64, 1>(a, grid, st);
+  }
+}
+
+}  // namespace ssd
