@@ -9,6 +9,7 @@
 namespace ssd {
 
 int kv4_dense_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
+int kv4_dense_d128(const Kv4AttnArgs &a, int grid, cudaStream_t st);
 int kv4_tc_attn(const Kv4AttnArgs &a, int rows, int grid, cudaStream_t st);
 int kv4_tc_crit(const Kv4AttnArgs &a, int np, int grid, cudaStream_t st);
 int kv4_list_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
@@ -127,9 +128,11 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
   if (!(a.status = device_status())) return SSD_ERR_CUDA;
   if (scores && !a.lse) a.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + lay.lse);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // d = 128 runs on tcgen05; at d = 64 V^T would fill half the rows of its M = 128, and the mma.sync kernel runs.
+  // d = 128 runs on tcgen05 from 9 rows on; at d = 64 V^T would fill half the rows of its M = 128.
   const int nt = kv4_nt(a.R);
-  if (kv->d == 128)
+  if (kv->d == 128 && a.R <= 8)
+    rc = kv4_dense_d128(a, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(nt)), st);
+  else if (kv->d == 128)
     rc = kv4_tc_attn(a, a.R > 32 ? 32 : a.R, kv4_grid(a.n_units, kv->max_seq_len, kKv4TcTile, 2), st);
   else
     rc = kv4_dense_d64(a, nt, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(nt)), st);

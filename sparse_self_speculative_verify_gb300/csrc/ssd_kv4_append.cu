@@ -18,52 +18,145 @@ struct Kv4RowsArgs {
   void *k_out, *v_out;      // read
   const int32_t *first;     // read: first token of each request
   const int32_t *counts;    // rows of each request, or NULL: n for all
-  int n, d, gpb;            // gpb: groups of 16 per block
+  int n, d;
+  int tokens;               // tokens per block
   float k_mul, v_mul;       // append: 1 / scale, read: scale
   unsigned *status;
 };
 
-// 16 elements from global memory as fp32.
-template <typename T>
-__device__ __forceinline__ void load_group(const T *p, float (&x)[16]);
-template <>
-__device__ __forceinline__ void load_group<float>(const float *p, float (&x)[16]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float4 v = __ldg(reinterpret_cast<const float4 *>(p) + k);
-    x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
+// 32 bytes from and to global memory: in one access where the base is 32-byte aligned (torch's allocations are; the
+// calls ask for 16).
+__device__ __forceinline__ void load32(const void *p, bool wide, uint4 &x, uint4 &y) {
+  if (wide) {
+    asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                 : "l"(p));
+  } else {
+    x = __ldg(static_cast<const uint4 *>(p));
+    y = __ldg(static_cast<const uint4 *>(p) + 1);
   }
 }
-template <>
-__device__ __forceinline__ void load_group<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[16]) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + k);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[8 * k + 2 * i] = bf16_lo(w[i]), x[8 * k + 2 * i + 1] = bf16_hi(w[i]);
+__device__ __forceinline__ void store32(void *p, bool wide, const uint4 &x, const uint4 &y) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y),
+                 "r"(y.z), "r"(y.w)
+                 : "memory");
+  } else {
+    static_cast<uint4 *>(p)[0] = x;
+    static_cast<uint4 *>(p)[1] = y;
   }
 }
 
-// Division by the group's scale.  fp32 inputs take the IEEE division.  bf16 inputs (8 significant
-// bits) take the product with the rounded reciprocal, off by less than 2^-22 relative, rounded to 17
-// significant bits: x / s is either one of e2m1's ties (3 significant bits, times s's 4: 7 bits, so the
-// rounding restores it exactly) or at least 2^-8 relative away from every tie, so the code is that of
-// the exact quotient.
+// 16 elements as loaded.
 template <typename T>
-__device__ __forceinline__ float scaled(float x, float s, float r);
+struct Raw;
 template <>
-__device__ __forceinline__ float scaled<float>(float x, float s, float r) { return __fdiv_rn(x, s); }
+struct Raw<float> {
+  uint4 v[4];
+  __device__ __forceinline__ void load(const float *p, bool wide) {
+    load32(p, wide, v[0], v[1]);
+    load32(p + 8, wide, v[2], v[3]);
+  }
+  __device__ __forceinline__ void get(float (&x)[16]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[4 * k] = __uint_as_float(v[k].x), x[4 * k + 1] = __uint_as_float(v[k].y);
+      x[4 * k + 2] = __uint_as_float(v[k].z), x[4 * k + 3] = __uint_as_float(v[k].w);
+    }
+  }
+  // Largest magnitude; infinity or NaN when an element is.
+  __device__ __forceinline__ float amax() const {
+    float x[16], m = 0.f;
+    get(x);
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) odd |= isnan(x[i]), m = fmaxf(m, fabsf(x[i]));
+    return odd ? NAN : m;
+  }
+};
 template <>
-__device__ __forceinline__ float scaled<__nv_bfloat16>(float x, float s, float r) {
-  return __uint_as_float((__float_as_uint(x * r) + 0x40u) & ~0x7fu);
+struct Raw<__nv_bfloat16> {
+  uint4 v[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool wide) { load32(p, wide, v[0], v[1]); }
+  __device__ __forceinline__ void get(float (&x)[16]) const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[8 * k + 2 * i] = bf16_lo(w[i]), x[8 * k + 2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+  __device__ __forceinline__ float amax() const {  // pairs; max.NaN keeps a NaN
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+    }
+    const float lo = bf16_lo(m), hi = bf16_hi(m);
+    return isnan(lo) || isnan(hi) ? NAN : fmaxf(lo, hi);
+  }
+};
+
+// Eight values over the group's scale s (r = 1 / s, rounded) as codes.  fp32 inputs take the IEEE division.
+// bf16 inputs (8 significant bits) take x r, off by less than 2^-22 relative, rounded to a multiple of 2^-10
+// by adding and taking away 1.5 * 2^13: x / s is either one of e2m1's ties (multiples of 1/4, with s's 4 bits
+// at most 7 significant bits, so the rounding restores it exactly) or at least 2^-8 relative, so 2^-10,
+// away from every tie, and the code is that of the exact quotient.  (Above 8 the spacing is wider, but
+// everything there is 6.)
+template <typename T>
+__device__ __forceinline__ uint32_t codes_of(const float *x, float s, float r);
+template <>
+__device__ __forceinline__ uint32_t codes_of<float>(const float *x, float s, float r) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+  return f32_to_e2m1(y);
+}
+template <>
+__device__ __forceinline__ uint32_t codes_of<__nv_bfloat16>(const float *x, float s, float r) {
+  constexpr float C = 12288.f;
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = copysignf(__fadd_rn(__fmaf_rn(x[i], r, C), -C), x[i]);
+  return f32_to_e2m1(y);
 }
 
-// One group of 16 elements per thread and step; consecutive threads take consecutive groups of a row,
-// then the next head, K before V of a token.  blockIdx.y is the request; a request is appended whole or
-// not at all, so every block first looks at all the page ids its request needs.
+// Quantises one group of K or V into codes (two words) and its scale byte.
 template <typename T>
-__global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4RowsArgs a) {
+__device__ __forceinline__ bool quantise(const Raw<T> &raw, float mul, uint2 &codes, uint32_t &sc) {
+  float x[16];
+  raw.get(x);
+  float amax = raw.amax();
+  const bool bad = !isfinite(amax);
+  if (bad) {  // NaN counts as 0
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (isnan(x[i])) x[i] = 0.f;
+      amax = fmaxf(amax, fabsf(x[i]));
+    }
+  }
+  sc = f32_to_e4m3(__fdiv_rn(amax * mul, 6.f));
+  const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(sc) & 0xffffu)));
+  const float r = __frcp_rn(s);
+  if (mul != 1.f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] *= mul;
+  }
+  codes = s > 0.f ? make_uint2(codes_of<T>(x, s, r), codes_of<T>(x + 8, s, r)) : make_uint2(0, 0);
+  return bad;
+}
+
+// One group of 16 elements per thread and step, of K and of V; consecutive threads take consecutive groups of a
+// row, then the next head, then the next token.  blockIdx.y is the request; a request is appended whole or not
+// at all, so every block first looks at all the page ids its request needs.
+//
+// Bound: 2.56 bytes per bf16 element against about 8 instructions; at the first version's 13 (an element's NaN
+// looked at on its own, 64-bit index divisions) issue bound it, 62 us for 168 MB of input.
+template <typename T>
+__global__ void __launch_bounds__(kKv4Threads, sizeof(T) == 2 ? 5 : 4) kv4_append_kernel(Kv4RowsArgs a) {
   const int b = blockIdx.y, tid = threadIdx.x;
   pdl_trigger();
   pdl_wait();
@@ -73,10 +166,8 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4RowsArgs a) 
     if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_SEQLEN);
     return;
   }
-  const int gpr = a.d / kKv4Group;                      // groups per row
-  const int64_t total = (int64_t)n * a.kv.h_kv * gpr;   // of K, and of V
-  const int64_t e0 = (int64_t)blockIdx.x * a.gpb;
-  if (e0 >= total) return;
+  const int j0 = blockIdx.x * a.tokens, nt = min(a.tokens, n - j0);
+  if (nt <= 0) return;
   const int32_t *table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
   bool ok = true;
   for (int j = (L >> a.kv.log2_ps) + tid; j <= (L + n - 1) >> a.kv.log2_ps; j += kKv4Threads) {
@@ -87,53 +178,51 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4RowsArgs a) 
     if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
     return;
   }
-  const int64_t e1 = min(total, e0 + a.gpb);
+  const int log2_gpr = a.d == 128 ? 3 : 2;
+  const unsigned per_token = (unsigned)a.kv.h_kv << log2_gpr, total = nt * per_token;
   const int cb = kv4_code_bytes(a.d), sb = kv4_scale_bytes(a.d);
-  const int64_t block_bytes = (int64_t)a.kv.page_size * (cb + sb);
+  const int64_t block_bytes = (int64_t)a.kv.page_size * (cb + sb), v_off = a.kv.h_kv * block_bytes;
+  const int64_t src0 = ((int64_t)b * a.n + j0) * a.kv.h_kv * a.d;
+  const T *kin = static_cast<const T *>(a.k_in) + src0, *vin = static_cast<const T *>(a.v_in) + src0;
   bool bad = false;
-  for (int64_t e = e0 + tid; e < e1; e += kKv4Threads) {
-    const int c = (int)(e % gpr);
-    const int64_t row = e / gpr;
-    const int g = (int)(row % a.kv.h_kv);
-    const int j = (int)(row / a.kv.h_kv);
-    const int t = L + j, slot = t & (a.kv.page_size - 1);
+  auto store = [&](unsigned e, const Raw<T> &k, const Raw<T> &v) {
+    const unsigned jt = e / per_token, in = e - jt * per_token;
+    const int g = in >> log2_gpr, c = in & ((1 << log2_gpr) - 1);
+    const int t = L + j0 + (int)jt, slot = t & (a.kv.page_size - 1);
     const int32_t p = __ldg(table + (t >> a.kv.log2_ps));
-    const int64_t src = (((int64_t)b * a.n + j) * a.kv.h_kv + g) * a.d + c * kKv4Group;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      float x[16];
-      load_group(static_cast<const T *>(which ? a.v_in : a.k_in) + src, x);
-      const float mul = which ? a.v_mul : a.k_mul;
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        bad |= !isfinite(x[i]);
-        x[i] = isnan(x[i]) ? 0.f : x[i] * mul;
-        amax = fmaxf(amax, fabsf(x[i]));
-      }
-      const uint32_t sc = f32_to_e4m3(__fdiv_rn(amax, 6.f));
-      const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(sc) & 0xffffu)));
-      const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = s > 0.f ? scaled<T>(x[i], s, r) : 0.f;
-      char *blk = a.pool + (((int64_t)p * 2 + which) * a.kv.h_kv + g) * block_bytes;
-      *reinterpret_cast<uint2 *>(blk + slot * cb + c * 8) = make_uint2(f32_to_e2m1(x), f32_to_e2m1(x + 8));
-      blk[a.kv.page_size * cb + slot * sb + c] = (char)sc;
-    }
+    char *blk = a.pool + ((int64_t)p * 2 * a.kv.h_kv + g) * block_bytes;
+    char *to = blk + slot * cb + c * 8, *ts = blk + a.kv.page_size * cb + slot * sb + c;
+    uint2 w;
+    uint32_t sc;
+    bad |= quantise<T>(k, a.k_mul, w, sc);
+    *reinterpret_cast<uint2 *>(to) = w;
+    *ts = (char)sc;
+    bad |= quantise<T>(v, a.v_mul, w, sc);
+    *reinterpret_cast<uint2 *>(to + v_off) = w;
+    ts[v_off] = (char)sc;
+  };
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.k_in) | reinterpret_cast<uintptr_t>(a.v_in)) & 31) == 0;
+#pragma unroll 1
+  for (unsigned e = tid; e < total; e += kKv4Threads) {
+    Raw<T> k, v;
+    k.load(kin + (int64_t)e * 16, wide), v.load(vin + (int64_t)e * 16, wide);
+    store(e, k, v);
   }
   if (bad) atomicOr(a.status, (unsigned)SSD_FAULT_VALUE);
 }
 
-__device__ __forceinline__ void store_group(float *p, const float (&x)[16]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    reinterpret_cast<float4 *>(p)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+__device__ __forceinline__ uint4 bits4(float a, float b, float c, float d) {
+  return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
 }
-__device__ __forceinline__ void store_group(__nv_bfloat16 *p, const float (&x)[16]) {
+__device__ __forceinline__ void store_group(float *p, const float (&x)[16], bool wide) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    reinterpret_cast<uint4 *>(p)[k] = make_uint4(pack_bf16(x[8 * k], x[8 * k + 1]), pack_bf16(x[8 * k + 2], x[8 * k + 3]),
-                                                 pack_bf16(x[8 * k + 4], x[8 * k + 5]), pack_bf16(x[8 * k + 6], x[8 * k + 7]));
+  for (int k = 0; k < 16; k += 8) store32(p + k, wide, bits4(x[k], x[k + 1], x[k + 2], x[k + 3]), bits4(x[k + 4], x[k + 5], x[k + 6], x[k + 7]));
+}
+__device__ __forceinline__ void store_group(__nv_bfloat16 *p, const float (&x)[16], bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = pack_bf16(x[2 * k], x[2 * k + 1]);
+  store32(p, wide, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
 }
 
 // The reverse: rows first[b] + j, j < counts[b], as T; rows from counts[b] on are zeros.  The values are
@@ -149,40 +238,52 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4RowsArgs a) {
     if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_SEQLEN);
     n = 0;
   }
-  const int gpr = a.d / kKv4Group;
-  const int64_t total = (int64_t)a.n * a.kv.h_kv * gpr;
-  const int64_t e0 = (int64_t)blockIdx.x * a.gpb, e1 = min(total, e0 + a.gpb);
+  const int j0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - j0), live = min(nt, n - j0);
+  const int log2_gpr = a.d == 128 ? 3 : 2;
+  const unsigned per_token = (unsigned)a.kv.h_kv << log2_gpr, total = nt * per_token;
   const int32_t *table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
   const int cb = kv4_code_bytes(a.d), sb = kv4_scale_bytes(a.d);
-  const int64_t block_bytes = (int64_t)a.kv.page_size * (cb + sb);
-  for (int64_t e = e0 + tid; e < e1; e += kKv4Threads) {
-    const int c = (int)(e % gpr);
-    const int64_t row = e / gpr;
-    const int g = (int)(row % a.kv.h_kv);
-    const int j = (int)(row / a.kv.h_kv);
-    const int t = f0 + j, slot = t & (a.kv.page_size - 1);
-    int32_t p = -1;
-    if (j < n) {
-      p = __ldg(table + (t >> a.kv.log2_ps));
-      if (p < 0 || (int64_t)p >= a.kv.num_pages) {
-        atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
-        p = -1;
+  const int64_t block_bytes = (int64_t)a.kv.page_size * (cb + sb), v_off = a.kv.h_kv * block_bytes;
+  const int64_t dst0 = ((int64_t)b * a.n + j0) * a.kv.h_kv * a.d;
+  T *ko = static_cast<T *>(a.k_out) + dst0, *vo = static_cast<T *>(a.v_out) + dst0;
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.v_out)) & 31) == 0;
+  constexpr int U = 2;  // groups in flight per thread
+  for (unsigned e0 = tid; e0 < total; e0 += U * kKv4Threads) {
+    uint2 w[U][2];
+    uint32_t sc[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const unsigned e = e0 + u * kKv4Threads, jt = e / per_token, in = e - jt * per_token;
+      w[u][0] = w[u][1] = make_uint2(0, 0), sc[u][0] = sc[u][1] = 0;
+      if (e < total && (int)jt < live) {
+        const int g = in >> log2_gpr, c = in & ((1 << log2_gpr) - 1);
+        const int t = f0 + j0 + (int)jt, slot = t & (a.kv.page_size - 1);
+        const int32_t p = __ldg(table + (t >> a.kv.log2_ps));
+        if (p < 0 || (int64_t)p >= a.kv.num_pages) {
+          atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
+        } else {
+          const char *blk = a.pool + ((int64_t)p * 2 * a.kv.h_kv + g) * block_bytes;
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            w[u][which] = *reinterpret_cast<const uint2 *>(blk + which * v_off + slot * cb + c * 8);
+            sc[u][which] = (unsigned char)blk[which * v_off + a.kv.page_size * cb + slot * sb + c];
+          }
+        }
       }
     }
-    const int64_t dst = (((int64_t)b * a.n + j) * a.kv.h_kv + g) * a.d + c * kKv4Group;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      float x[16];
-      if (p >= 0) {
-        const char *blk = a.pool + (((int64_t)p * 2 + which) * a.kv.h_kv + g) * block_bytes;
-        const uint2 w = *reinterpret_cast<const uint2 *>(blk + slot * cb + c * 8);
-        const uint32_t sc = (unsigned char)blk[a.kv.page_size * cb + slot * sb + c];
-        const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(sc) & 0xffffu))) *
+    for (int u = 0; u < U; ++u) {
+      const unsigned e = e0 + u * kKv4Threads;
+      if (e >= total) break;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(sc[u][which]) & 0xffffu))) *
                         (which ? a.v_mul : a.k_mul);
+        float x[16];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t h[4];
-          e2m1_to_f16x2(k ? w.y : w.x, h);
+          e2m1_to_f16x2(k ? w[u][which].y : w[u][which].x, h);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
@@ -190,20 +291,22 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4RowsArgs a) {
             x[8 * k + 2 * i + 1] = v.y * s;
           }
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+        store_group((which ? vo : ko) + (int64_t)e * 16, x, wide);
       }
-      store_group(static_cast<T *>(which ? a.v_out : a.k_out) + dst, x);
     }
   }
 }
 
-// Groups per block: whole multiples of the block's threads, few enough that the grid covers the SMs.
-static int groups_per_block(int64_t total, int batch) {
-  const int64_t per_sm = total * batch / ((int64_t)sm_count() * 8 * kKv4Threads);
-  const int64_t steps = per_sm < 1 ? 1 : (per_sm > 8 ? 8 : per_sm);
-  return (int)steps * kKv4Threads;
+// Tokens per block: enough groups for the threads, more (up to eight steps each) while the grid still covers the
+// SMs eight times.
+static int tokens_per_block(const ssd_paged_kv *kv, int n) {
+  const int64_t per_token = (int64_t)kv->h_kv * (kv->d / kKv4Group);
+  int64_t steps = per_token * n * kv->batch / ((int64_t)sm_count() * 8 * kKv4Threads);
+  steps = steps < 1 ? 1 : (steps > 8 ? 8 : steps);
+  int64_t t = steps * kKv4Threads / per_token;
+  const int64_t least = cdiv64(n, 65535 * 16);  // grid.x stays far below its limit
+  t = t < least ? least : t;
+  return (int)(t < 1 ? 1 : t);
 }
 
 static int rows_checks(const ssd_paged_kv *kv, KVView *v, const void *k, const void *vv, int dtype, int n, float k_scale,
@@ -235,9 +338,8 @@ extern "C" int ssd_kv4_append(const ssd_paged_kv *kv, const void *k_new, const v
   a.pool = static_cast<char *>(const_cast<void *>(kv->pool));
   a.k_in = k_new, a.v_in = v_new, a.counts = counts, a.n = n_new, a.d = kv->d;
   a.k_mul = 1.f / k_scale, a.v_mul = 1.f / v_scale;
-  const int64_t total = (int64_t)n_new * kv->h_kv * (kv->d / kKv4Group);
-  a.gpb = groups_per_block(total, kv->batch);
-  const dim3 grid((unsigned)cdiv64(total, a.gpb), kv->batch), block(kKv4Threads);
+  a.tokens = tokens_per_block(kv, n_new);
+  const dim3 grid(cdiv(n_new, a.tokens), kv->batch), block(kKv4Threads);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == SSD_DTYPE_BF16) return launch(kv4_append_kernel<__nv_bfloat16>, grid, block, 0, st, "kv4_append_kernel", a);
   return launch(kv4_append_kernel<float>, grid, block, 0, st, "kv4_append_kernel", a);
@@ -254,9 +356,8 @@ extern "C" int ssd_kv4_read(const ssd_paged_kv *kv, const int32_t *first, const 
   a.pool = static_cast<char *>(const_cast<void *>(kv->pool));
   a.k_out = k, a.v_out = v, a.first = first, a.counts = counts, a.n = n, a.d = kv->d;
   a.k_mul = k_scale, a.v_mul = v_scale;
-  const int64_t total = (int64_t)n * kv->h_kv * (kv->d / kKv4Group);
-  a.gpb = groups_per_block(total, kv->batch);
-  const dim3 grid((unsigned)cdiv64(total, a.gpb), kv->batch), block(kKv4Threads);
+  a.tokens = tokens_per_block(kv, n);
+  const dim3 grid(cdiv(n, a.tokens), kv->batch), block(kKv4Threads);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == SSD_DTYPE_BF16) return launch(kv4_read_kernel<__nv_bfloat16>, grid, block, 0, st, "kv4_read_kernel", a);
   return launch(kv4_read_kernel<float>, grid, block, 0, st, "kv4_read_kernel", a);

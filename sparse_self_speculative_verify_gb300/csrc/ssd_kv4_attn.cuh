@@ -12,16 +12,17 @@
 // Bound: 9 bits per (K, V) element pair stored, 144 bytes per token of a head at d = 128, so HBM bounds
 // small R; the f16 tensor-core rate of mma.sync (1024 multiply-adds per clock and SM) bounds R > 20.
 //
-// Layout of the work.  Two warps take a tile of 32 tokens and compute, on the tensor cores,
-//   S^T [16 tokens each x 8 NT rows] = K Q^T   and   O^T [d / 2 each x 8 NT rows] += V^T P^T,
+// Layout of the work.  A warp takes tiles of 32 tokens and computes, on the tensor cores,
+//   S^T [32 tokens x 8 NT rows] = K Q^T   and   O^T [d x 8 NT rows] += V^T P^T,
 // so that the cache is the A operand of both products and the few query rows the narrow N side (M = 16
-// rows of queries would be mostly padding).  The halves of P pass between the two warps through shared
-// memory; splitting d halves the registers of the O accumulators (with a whole tile per warp, NT = 3 had 8
-// warps on an SM and 432 us for 8 x 131072 tokens).  Codes go from shared memory to A fragments in
-// registers: pairs of codes are converted to f16 and multiplied by their scale (exact, see ssd_kv4.cuh).
-// Which d a lane's fragment column stands for is free for K as long as Q is laid out alike, and for V it
-// only permutes the output rows, so a lane reads consecutive bytes of both.  P^T is S^T's fragment
-// transposed (movmatrix).
+// rows of queries would be mostly padding).  Codes go from shared memory to A fragments in registers: pairs
+// of codes are converted to f16 and multiplied by their scale (exact, see ssd_kv4.cuh).  Which d a lane's
+// fragment column stands for is free for K as long as Q is laid out alike, and for V it only permutes the
+// output rows, so a lane reads consecutive bytes of both.  P^T is S^T's fragment transposed (movmatrix).
+//
+// What bounds it: instructions, about 600 per tile of a head at d = 128 and up to 8 rows, 256 of them the
+// conversions (HBM delivers a tile in 195 clocks an SM).  With more rows the O accumulators leave room for
+// few warps, and the kernel of ssd_kv4_tc.cuh takes over at d = 128.
 #pragma once
 
 #include "ssd_kv4.cuh"
@@ -63,40 +64,26 @@ struct Kv4AttnArgs {
 // reads touch every bank once.
 __device__ __forceinline__ int kv4_sigma(int k) { return k ^ (((k >> 1) ^ (k >> 2)) & 1); }
 
-// What a warp keeps of a tile: K of its 16 tokens, V of its half of d for all 32, and their scales.
+// A tile in shared memory: codes of K and of V, scales of K and of V.
 template <int D>
 struct Kv4Smem {
   static constexpr int kCb = kv4_code_bytes(D), kSb = kv4_scale_bytes(D);
-  static constexpr int kV = 16 * kCb;                   // offsets: K codes at 0, V codes,
-  static constexpr int kKs = kV + kKv4Tile * kCb / 2;   // K scales,
-  static constexpr int kVs = kKs + 16 * kSb;            // V scales
+  static constexpr int kV = kKv4Tile * kCb, kKs = 2 * kV, kVs = kKs + kKv4Tile * kSb;  // offsets
   static constexpr int kStage = kVs + kKv4Tile * kSb;
-  // Criticality pass: K of 32 tokens, two halves of codes and then the scales.
-  static constexpr int kCritStage = kKv4Tile * (kCb + kSb);
-  // Byte of piece c (16 bytes) of token t in a half's K codes: at d = 128 a 128-byte line holds two tokens,
-  // and odd lines have their pieces permuted, against bank conflicts.
-  static __device__ __forceinline__ int k_piece(int t, int c) {
+  // Criticality pass: K alone.
+  static constexpr int kCritScales = kV, kCritStage = kV + kKv4Tile * kSb;
+  // Byte of 16-byte piece c of token t's codes: at d = 128 a 128-byte line holds two tokens, and odd lines have
+  // their pieces permuted, against bank conflicts.
+  static __device__ __forceinline__ int piece(int t, int c) {
     return D == 128 ? (t >> 1) * 128 + ((((t & 1) * 4 + c) ^ ((t >> 1 & 1) * 2)) << 4) : t * 32 + c * 16;
   }
 };
 
-template <int D, int NT, int QS, int PS, int NW, int NST>
+template <int D, int NT, int QS, int NW, int NST>
 constexpr int kv4_smem_bytes() {
-  // ring, query fragments, exchanged probabilities, per-row logit factors, the warps' maxima and sums
-  return NW * NST * Kv4Smem<D>::kStage + NT * 8 * D * 2 * QS + NW * 2 * PS * NT * 256 + NT * 8 * 4 + 2 * NW * NT * 8 * 4;
+  // ring, query fragments, per-row logit factors, the warps' references and sums
+  return NW * NST * Kv4Smem<D>::kStage + NT * 8 * D * 2 * QS + NT * 8 * 4 + 2 * NW * NT * 8 * 4;
 }
-
-// Or over the 64 threads of barrier `id`; also orders their shared-memory accesses.
-__device__ __forceinline__ bool pair_any(int id, bool v) {
-  int r;
-  asm volatile(
-      "{ .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n selp.s32 %0, 1, 0, q; }\n"
-      : "=r"(r)
-      : "r"((int)v), "r"(id)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
 
 // Tiles of a unit; a unit without tokens has one empty tile, whose rows come out as 0 and -inf.
 template <bool LIST, int TILE = kKv4Tile>
@@ -162,11 +149,12 @@ __device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int
   return true;
 }
 
-// Loads of one warp's part of a tile, by 16-byte cp.async, one group per tile.  (A page's rows of one head are
-// 1152 bytes at page size 16 and d = 128: bulk copies of that size took about 200 clocks each to issue.)
+// Loads of one warp's tiles into its ring, by 16-byte cp.async, one group per tile.  (A page's rows of one head
+// are 1152 bytes at page size 16 and d = 128: bulk copies of that size took about 200 clocks each to issue.)
 template <int D>
 struct Kv4Loader {
   using S = Kv4Smem<D>;
+  static constexpr int CPR = S::kCb / 16;  // 16-byte pieces of a row's codes
   const Kv4AttnArgs &a;
   const char *head;     // the head's K block of page 0
   const int32_t *table, *list;
@@ -174,11 +162,14 @@ struct Kv4Loader {
   int log2_cs;          // log2 of the tokens of a page inside a tile
   uint32_t page_bytes;  // of all heads' K and V blocks
   uint32_t v_off;       // from a head's K block to its V block
+  uint32_t lane_to;     // this lane's piece of the first rows, in a tile
 
   __device__ __forceinline__ Kv4Loader(const Kv4AttnArgs &args) : a(args) {
+    const int lane = threadIdx.x & 31;
     log2_cs = min(a.kv.log2_ps, 5);
     v_off = (uint32_t)a.kv.h_kv * a.kv.page_size * (S::kCb + S::kSb);
     page_bytes = 2 * v_off;
+    lane_to = S::piece(lane / CPR, lane % CPR);
   }
   __device__ __forceinline__ void unit(int b, int g, int len, int count, const int32_t *lst) {
     table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
@@ -195,156 +186,128 @@ struct Kv4Loader {
     const int at = tile * kKv4Tile + (lane << log2_cs);
     return lane < (kKv4Tile >> log2_cs) && at < n ? __ldg(table + (at >> a.kv.log2_ps)) : 0;
   }
-  // Pointer to the K block of the page of tile token tok, and the token's slot in it.
-  __device__ __forceinline__ const char *page_of(int32_t pid, int tok) const {
-    return head + (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, pid, tok >> log2_cs) * page_bytes;
-  }
-  __device__ __forceinline__ uint32_t slot_of(int t) const { return t & (a.kv.page_size - 1); }
-
-  __device__ __forceinline__ void k_codes(int t0, int32_t pid, int half, uint32_t dst, int lane) const {
-    constexpr int CPR = S::kCb / 16;  // 16-byte pieces of a row's codes
+  // The codes of G consecutive tokens of a page are G * kCb consecutive bytes.
+  template <int G, bool K_ONLY>
+  __device__ __forceinline__ void codes(int t0, int32_t pid, uint32_t dst, int lane) const {
+    constexpr int R = 32 / CPR;  // rows that a warp copies at once
 #pragma unroll
-    for (int i = 0; i < CPR / 2; ++i) {
-      const int t = (i * 32 + lane) / CPR, c = lane % CPR;
-      const char *src = page_of(pid, half * 16 + t) + slot_of(t0 + half * 16 + t) * S::kCb + c * 16;
-      cp_async16(dst + S::k_piece(t, c), src, 16);
+    for (int i = 0; i < kKv4Tile / G; ++i) {
+      const int32_t p = __shfl_sync(0xffffffffu, pid, (G * i) >> log2_cs);
+      const char *src = head + (uint64_t)(uint32_t)p * page_bytes + ((t0 + G * i) & (a.kv.page_size - 1)) * S::kCb + lane * 16;
+#pragma unroll
+      for (int k = 0; k < G; k += R) {
+        if (G < R && lane >= G * CPR) break;
+        const uint32_t to = dst + lane_to + (G * i + k) * S::kCb;
+        cp_async16(to, src + k * S::kCb, 16);
+        if (!K_ONLY) cp_async16(to + S::kV, src + v_off + k * S::kCb, 16);
+      }
     }
   }
-  // Pages outside the pool: their tokens' scales become 0, and so their rows.
-  __device__ __forceinline__ void blank(unsigned bad, int first, int count, uint32_t scales, int lane) const {
-    if (lane < count && (bad >> ((first + lane) >> log2_cs) & 1))
-#pragma unroll
-      for (int k = 0; k < S::kSb; k += 4)
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(scales + lane * S::kSb + k), "r"(0) : "memory");
-  }
-  __device__ __forceinline__ void load(int tile, int32_t pid, int half, uint32_t dst, int lane) const {
+  template <bool K_ONLY>
+  __device__ __forceinline__ void load(int tile, int32_t pid, uint32_t dst, int lane) const {
+    constexpr int scales = K_ONLY ? S::kCritScales : S::kKs;
     const int t0 = tile * kKv4Tile;
     const bool ok = in_pool(pid);
     const unsigned bad = __ballot_sync(0xffffffffu, !ok);
     if (!ok) pid = 0;
-    k_codes(t0, pid, half, dst, lane);
-    constexpr int VPR = S::kCb / 32;  // pieces of half a row
-#pragma unroll
-    for (int i = 0; i < VPR; ++i) {
-      const int t = (i * 32 + lane) / VPR, c = lane % VPR;
-      const char *src = page_of(pid, t) + v_off + slot_of(t0 + t) * S::kCb + (half * VPR + c) * 16;
-      cp_async16(dst + S::kV + (i * 32 + lane) * 16, src, 16);
-    }
-    // Scales: TPC tokens to a piece, K's of the warp's 16 tokens and V's of all.
-    constexpr int TPC = 16 / S::kSb, NK = 16 / TPC, NV = 32 / TPC;
-    const int which = lane >= NK, t = which ? (lane - NK) * TPC : half * 16 + lane * TPC;
-    const char *src = page_of(pid, t & 31) + which * v_off + (uint32_t)a.kv.page_size * S::kCb + slot_of(t0 + t) * S::kSb;
-    if (lane < NK + NV) cp_async16(dst + S::kKs + lane * 16, src, 16);
+    if (log2_cs >= 4)
+      codes<16, K_ONLY>(t0, pid, dst, lane);
+    else
+      codes<8, K_ONLY>(t0, pid, dst, lane);
+    // Scales: TPC tokens to a piece; the first lanes K's, the next V's.
+    constexpr int TPC = 16 / S::kSb, N = kKv4Tile / TPC;
+    const int which = lane / N, t = lane % N * TPC;
+    const int32_t p = __shfl_sync(0xffffffffu, pid, t >> log2_cs);
+    const char *src = head + (uint64_t)(uint32_t)p * page_bytes + which * v_off + (uint32_t)a.kv.page_size * S::kCb +
+                      ((t0 + t) & (a.kv.page_size - 1)) * S::kSb;
+    if (which < (K_ONLY ? 1 : 2)) cp_async16(dst + scales + lane * 16, src, 16);
     if (bad) {
+      // Pages outside the pool: scales of 0 make their rows zeros.
       if (!ok) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
       cp_async_commit();
       cp_async_wait<0>();
       __syncwarp();
-      blank(bad, half * 16, 16, dst + S::kKs, lane);
-      blank(bad, 0, 32, dst + S::kVs, lane);
-      __syncwarp();
-    }
-  }
-  __device__ __forceinline__ void load_k(int tile, int32_t pid, uint32_t dst, int lane) const {
-    const int t0 = tile * kKv4Tile;
-    const bool ok = in_pool(pid);
-    const unsigned bad = __ballot_sync(0xffffffffu, !ok);
-    if (!ok) pid = 0;
-    k_codes(t0, pid, 0, dst, lane);
-    k_codes(t0, pid, 1, dst + 16 * S::kCb, lane);
-    constexpr int TPC = 16 / S::kSb;
-    const int t = lane * TPC;
-    const char *src = page_of(pid, t & 31) + (uint32_t)a.kv.page_size * S::kCb + slot_of(t0 + t) * S::kSb;
-    if (t < 32) cp_async16(dst + 32 * S::kCb + lane * 16, src, 16);
-    if (bad) {
-      cp_async_commit();
-      cp_async_wait<0>();
-      __syncwarp();
-      blank(bad, 0, 32, dst + 32 * S::kCb, lane);
+      if (bad >> (lane >> log2_cs) & 1)
+        for (int k = 0; k < (K_ONLY ? 1 : 2) * kKv4Tile * S::kSb; k += kKv4Tile * S::kSb)
+          for (int j = 0; j < S::kSb; j += 4)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + scales + k + lane * S::kSb + j), "r"(0) : "memory");
       __syncwarp();
     }
   }
 
-  // List tiles: each lane resolves one entry (both warps resolve all), then pieces of the rows go out.  An
-  // entry that is not there reads as zeros.
+  // List tiles: each lane resolves one entry, then pieces of the rows go out.  An entry that is not there reads
+  // as zeros.
   __device__ __forceinline__ int32_t peek_list(int tile, int lane) const {
     return tile * kKv4Tile + lane < n ? __ldg(list + tile * kKv4Tile + lane) : -1;
   }
-  __device__ __forceinline__ void load_list(int tile, int32_t token, int half, uint32_t dst, int lane) const {
-    const char *codes = nullptr, *scales = head;  // the entry's row of the head's K block
+  __device__ __forceinline__ void load_list(int tile, int32_t token, uint32_t dst, int lane) const {
+    const char *row = nullptr, *scales = head;  // the entry's codes and scales in the head's K block
     if (tile * kKv4Tile + lane < n) {
       if (token < 0 || token >= L) {
         atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
       } else {
         const int32_t p = __ldg(table + (token >> a.kv.log2_ps));
         if (in_pool(p)) {
-          const char *page = head + (uint64_t)(uint32_t)p * page_bytes;
-          codes = page + slot_of(token) * S::kCb;
-          scales = page + (uint32_t)a.kv.page_size * S::kCb + slot_of(token) * S::kSb;
+          const int slot = token & (a.kv.page_size - 1);
+          row = head + (uint64_t)(uint32_t)p * page_bytes + slot * S::kCb;
+          scales = head + (uint64_t)(uint32_t)p * page_bytes + (uint32_t)a.kv.page_size * S::kCb + slot * S::kSb;
         } else {
           atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
         }
       }
     }
-    auto row = [&](int t) {
-      return reinterpret_cast<const char *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(codes), t));
-    };
-    constexpr int CPR = S::kCb / 16, VPR = CPR / 2;
 #pragma unroll
-    for (int i = 0; i < CPR / 2; ++i) {
-      const int t = (i * 32 + lane) / CPR, c = lane % CPR;
-      const char *r = row(half * 16 + t);
-      cp_async16(dst + S::k_piece(t, c), r ? r + c * 16 : head, r ? 16 : 0);
+    for (int i = 0; i < CPR; ++i) {
+      constexpr int R = 32 / CPR;
+      const char *rw =
+          reinterpret_cast<const char *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), i * R + lane / CPR));
+      const char *src = rw ? rw + lane % CPR * 16 : head;
+      const int nb = rw ? 16 : 0;
+      const uint32_t to = dst + lane_to + i * R * S::kCb;
+      cp_async16(to, src, nb);
+      cp_async16(to + S::kV, src + (rw ? v_off : 0), nb);
     }
-#pragma unroll
-    for (int i = 0; i < VPR; ++i) {
-      const int t = (i * 32 + lane) / VPR, c = lane % VPR;
-      const char *r = row(t);
-      cp_async16(dst + S::kV + (i * 32 + lane) * 16, r ? r + v_off + (half * VPR + c) * 16 : head, r ? 16 : 0);
-    }
-    const int nb = codes ? S::kSb : 0;
-    if ((lane >> 4) == half)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst + S::kKs + (lane & 15) * S::kSb), "l"(scales), "n"(S::kSb),
-                   "r"(nb)
-                   : "memory");
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst + S::kVs + lane * S::kSb), "l"(scales + (codes ? v_off : 0)),
+    const int nb = row ? S::kSb : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst + S::kKs + lane * S::kSb), "l"(scales), "n"(S::kSb), "r"(nb)
+                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst + S::kVs + lane * S::kSb), "l"(scales + (row ? v_off : 0)),
                  "n"(S::kSb), "r"(nb)
                  : "memory");
   }
 };
 
-// S^T of HS halves of 16 tokens: c[h][nt] holds rows (tokens) sigma(r) and 8 + sigma(r) of half h, columns (query
-// rows) 8 nt + 2c, + 1 for lane 4r + c.  `codes`, `scales`: the halves' K.
-template <int D, int NT, int QS, int HS>
-__device__ __forceinline__ void kv4_qk(float (&c)[HS][NT][4], const char *codes, const char *scales, const char *qf, int lane) {
+// S^T of a tile: c[h][nt] holds rows (tokens) 16 h + sigma(r) and + 8, columns (query rows) 8 nt + 2c, + 1 for
+// lane 4r + c.  `codes`, `scales`: the tile's K.
+template <int D, int NT, int QS>
+__device__ __forceinline__ void kv4_qk(float (&c)[2][NT][4], const char *codes, const char *scales, const char *qf, int lane) {
   using S = Kv4Smem<D>;
   const int r = lane >> 2, col = lane & 3, tok = kv4_sigma(r);
   constexpr int W = D / 32;  // words of a lane's share of a row
-  uint32_t w[2 * HS][W], sc[2 * HS];
+  uint32_t w[4][W], sc[4];
 #pragma unroll
-  for (int k = 0; k < 2 * HS; ++k) {
-    const char *ka = codes + (k >> 1) * 16 * S::kCb, *sa = scales + (8 * k + tok) * S::kSb;
+  for (int k = 0; k < 4; ++k) {
+    const char *sa = scales + (8 * k + tok) * S::kSb;
     if (D == 128) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(ka + S::k_piece(8 * (k & 1) + tok, col));
+      const uint4 v = *reinterpret_cast<const uint4 *>(codes + S::piece(tok, col) + 8 * k * S::kCb);
       w[k][0] = v.x, w[k][1] = v.y, w[k][W - 2] = v.z, w[k][W - 1] = v.w;
       sc[k] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(sa + col * 2));  // the lane's two groups
     } else {
-      const uint2 v = *reinterpret_cast<const uint2 *>(ka + (8 * (k & 1) + tok) * S::kCb + col * 8);
+      const uint2 v = *reinterpret_cast<const uint2 *>(codes + (8 * k + tok) * S::kCb + col * 8);
       w[k][0] = v.x, w[k][1] = v.y;
       sc[k] = e4m3x2_to_f16x2(*reinterpret_cast<const uint8_t *>(sa + col) * 0x101u);  // its one group, twice
     }
   }
 #pragma unroll
-  for (int h = 0; h < HS; ++h)
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int k = 0; k < 4; ++k) c[h][nt][k] = 0.f;
 #pragma unroll
   for (int x = 0; x < W; ++x) {
-    uint32_t f[2 * HS][4];
+    uint32_t f[4][4];
 #pragma unroll
-    for (int k = 0; k < 2 * HS; ++k) {
+    for (int k = 0; k < 4; ++k) {
       e2m1_to_f16x2(w[k][x], f[k]);
       const uint32_t s = D == 128 ? __byte_perm(sc[k], 0, x < W / 2 ? 0x1010 : 0x3232) : sc[k];
 #pragma unroll
@@ -358,7 +321,7 @@ __device__ __forceinline__ void kv4_qk(float (&c)[HS][NT][4], const char *codes,
         for (int nt = 0; nt < NT; ++nt) {
           const uint2 q = reinterpret_cast<const uint2 *>(qf)[((qs * NT + nt) * (D / 16) + 2 * x + y) * 32 + lane];
 #pragma unroll
-          for (int h = 0; h < HS; ++h)
+          for (int h = 0; h < 2; ++h)
             mma_f16(c[h][nt], f[2 * h][2 * y], f[2 * h + 1][2 * y], f[2 * h][2 * y + 1], f[2 * h + 1][2 * y + 1], q.x, q.y);
         }
   }
@@ -433,20 +396,17 @@ __device__ __forceinline__ void kv4_write4(const Kv4AttnArgs &a, int64_t elem, c
 template <int D, int NT, int QS, int PS, int NW, int NST, int BPS, bool LIST>
 __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
   using S = Kv4Smem<D>;
-  constexpr int NP = NW / 2;     // pairs
-  constexpr int MT = D / 32;     // fragments of 16 d a warp has
+  constexpr int MT = D / 16;  // fragments of 16 d
   constexpr int ROWS = NT * 8;
-  constexpr int PIECES = D / 8;  // 16-byte pieces of a warp's half row of O
+  constexpr int PIECES = D / 4;  // 16-byte pieces of a row of O
   extern __shared__ __align__(128) char smem[];
   char *ring = smem;
   char *qf = ring + NW * NST * S::kStage;
-  char *xchg = qf + ROWS * D * 2 * QS;
-  float *s_sl = reinterpret_cast<float *>(xchg + NW * 2 * PS * NT * 256);
+  float *s_sl = reinterpret_cast<float *>(qf + ROWS * D * 2 * QS);
   float *s_m = s_sl + ROWS, *s_l = s_m + NW * ROWS;
   __shared__ int64_t s_scan[NW + 2];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, col = lane & 3;
-  const int pair = warp >> 1, half = warp & 1;
   pdl_wait();
   Kv4Range rg;
   if (!kv4_range<LIST, NW>(a, rg, s_scan)) return;
@@ -458,12 +418,8 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
   }
   const char *my_tiles = ring + warp * NST * S::kStage;
   const uint32_t my_ring = smem_u32(my_tiles);
-  // Probabilities on their way to the other warp: [parity][PS][NT][lane] of two registers.
-  uint2 *give = reinterpret_cast<uint2 *>(xchg + warp * 2 * PS * NT * 256);
-  const uint2 *take = reinterpret_cast<const uint2 *>(xchg + (warp ^ 1) * 2 * PS * NT * 256);
   Kv4Loader<D> ld(a);
   int issued = 0, used = 0;  // the warp's ring positions
-  int parity = 0;
 
   while (rg.x < rg.x1) {
     const int u = rg.u, b = u / (a.kv.h_kv * a.n_chunk), g = (u / a.n_chunk) % a.kv.h_kv, r0 = (u % a.n_chunk) * ROWS;
@@ -475,19 +431,19 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
     ld.unit(b, g, L, count, LIST ? a.idx + (int64_t)u * a.k_max : nullptr);
     Kv4Queries<D, NT, QS, NW> qs;
     qs.fetch(a, b, g, r0, rows);
-    int next = seg0 + pair;
+    int next = seg0 + warp;
     auto peek = [&](int tile) { return LIST ? ld.peek_list(tile, lane) : ld.peek(tile, lane); };
     int32_t seen = next < seg1 ? peek(next) : -1;
     auto issue = [&]() {
       if (next < seg1) {
         const int32_t now = seen;
-        if (next + NP < seg1) seen = peek(next + NP);
+        if (next + NW < seg1) seen = peek(next + NW);
         if (LIST)
-          ld.load_list(next, now, half, my_ring + issued * S::kStage, lane);
+          ld.load_list(next, now, my_ring + issued * S::kStage, lane);
         else
-          ld.load(next, now, half, my_ring + issued * S::kStage, lane);
+          ld.template load<false>(next, now, my_ring + issued * S::kStage, lane);
         issued = issued + 1 == NST ? 0 : issued + 1;
-        next += NP;
+        next += NW;
       }
       cp_async_commit();
     };
@@ -507,83 +463,59 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.f;
 
-    for (int tile = seg0 + pair; tile < seg1; tile += NP) {
+    for (int tile = seg0 + warp; tile < seg1; tile += NW) {
       cp_async_wait<NST - 1>();
       __syncwarp();
       const char *st = my_tiles + used * S::kStage;
       const int t0 = tile * kKv4Tile;
       const bool edge = LIST ? t0 + kKv4Tile > count : t0 + kKv4Tile > L - a.n_c + 1;
-      float c[1][NT][4];
-      kv4_qk<D, NT, QS, 1>(c, st, st + S::kKs, qf, lane);
+      float c[2][NT][4], x[2][NT][4];
+      kv4_qk<D, NT, QS>(c, st, st + S::kKs, qf, lane);
       // x = logit (log2) - reference; -inf where a row does not see the token.
-      float x[NT][4], ls[NT][2];
-      uint32_t p[NT][2], pl[NT][2];
-      auto visible = [&](int nt, int k) {
+      auto visible = [&](int h, int nt, int k) {
         const int lim = LIST ? count : min(L, L - a.n_c + 1 + (r0 + 8 * nt + 2 * col + (k & 1)) / a.G);
-        return t0 + 16 * half + (k >> 1) * 8 + kv4_sigma(r) < lim;
+        return t0 + 16 * h + (k >> 1) * 8 + kv4_sigma(r) < lim;
       };
       auto logits = [&]() {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[nt][k] = fmaf(c[0][nt][k], sl[nt][k & 1], -m[nt][k & 1]);
-        if (edge) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (!visible(nt, k)) x[nt][k] = -INFINITY;
-        }
-      };
-      // Probabilities of the warp's tokens: B fragments, kept and handed to the other warp.
-      auto probs = [&]() {
+            for (int k = 0; k < 4; ++k) x[h][nt][k] = fmaf(c[h][nt][k], sl[nt][k & 1], -m[nt][k & 1]);
+        if (edge) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float e[4];
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) e[k] = fast_exp2(x[nt][k]);
-          ls[nt][0] = e[0] + e[2], ls[nt][1] = e[1] + e[3];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const __half2 hi = __floats2half2_rn(e[2 * k], e[2 * k + 1]);
-            p[nt][k] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&hi));
-            if (PS == 2) {
-              const float2 back = __half22float2(hi);
-              pl[nt][k] = movmatrix_trans(pack_half(e[2 * k] - back.x, e[2 * k + 1] - back.y));
-            }
-          }
-          give[((parity * PS) * NT + nt) * 32 + lane] = make_uint2(p[nt][0], p[nt][1]);
-          if (PS == 2) give[((parity * PS + 1) * NT + nt) * 32 + lane] = make_uint2(pl[nt][0], pl[nt][1]);
+              for (int k = 0; k < 4; ++k)
+                if (!visible(h, nt, k)) x[h][nt][k] = -INFINITY;
         }
       };
       logits();
       float top = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top = fmaxf(top, x[nt][k]);
-      probs();
-      if (pair_any(1 + pair, top > kKv4Slack)) {
-        // Both warps move to the references of the tile's 32 tokens and take the probabilities again.
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = fmaxf(top, x[h][nt][k]);
+      if (__any_sync(0xffffffffu, top > kKv4Slack)) {
+        // The references move to the tile's largest logits; O and the sums follow.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float mx = -INFINITY;
 #pragma unroll
-            for (int j = k; j < 4; j += 2)
-              if (!edge || visible(nt, j)) mx = fmaxf(mx, c[0][nt][j] * sl[nt][k]);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = k; j < 4; j += 2)
+                if (!edge || visible(h, nt, j)) mx = fmaxf(mx, c[h][nt][j] * sl[nt][k]);
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-            if (r == 0) s_m[warp * ROWS + 8 * nt + 2 * col + k] = mx;
-          }
-        pair_sync(1 + pair);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int q = 8 * nt + 2 * col + k;
-            const float mx = fmaxf(fmaxf(s_m[warp * ROWS + q], s_m[(warp ^ 1) * ROWS + q]), m[nt][k] + kKv4Lift);
+            mx = fmaxf(mx, m[nt][k] + kKv4Lift);
             const float f = fast_exp2(m[nt][k] + kKv4Lift - mx);
             m[nt][k] = mx - kKv4Lift;
             l[nt][k] *= f;
@@ -591,73 +523,81 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
             for (int i = 0; i < MT; ++i) o[i][nt][k] *= f, o[i][nt][k + 2] *= f;
           }
         logits();
-        probs();
-        pair_sync(1 + pair);
       }
+      uint32_t p[2][NT][2], pl[2][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) l[nt][0] += ls[nt][0], l[nt][1] += ls[nt][1];
-
-      // O^T += V^T P^T, 16 tokens a step: the warp's own, then the other's.  A lane reads its d / 16 elements of
-      // four tokens and pairs the codes of two tokens in a byte, so that each conversion gives a fragment
-      // register.
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h == 1) {
+        for (int nt = 0; nt < NT; ++nt) {
+          float e[4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 v = take[((parity * PS) * NT + nt) * 32 + lane];
-            p[nt][0] = v.x, p[nt][1] = v.y;
+          for (int k = 0; k < 4; ++k) {
+            e[k] = fast_exp2(x[h][nt][k]);
+            l[nt][k & 1] += e[k];
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const __half2 hi = __floats2half2_rn(e[2 * k], e[2 * k + 1]);
+            p[h][nt][k] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&hi));
             if (PS == 2) {
-              const uint2 y = take[((parity * PS + 1) * NT + nt) * 32 + lane];
-              pl[nt][0] = y.x, pl[nt][1] = y.y;
+              const float2 back = __half22float2(hi);
+              pl[h][nt][k] = movmatrix_trans(pack_half(e[2 * k] - back.x, e[2 * k + 1] - back.y));
             }
           }
         }
-        const int th = 16 * (h ^ half);  // first of the 16 tokens
-        uint32_t w[4], sc[2];
+      // O^T += V^T P^T, 16 tokens a step.  A lane reads its d / 8 elements of four tokens and pairs the codes of two
+      // tokens in a byte, so that each conversion gives a fragment register.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        constexpr int W = D / 64;
+        uint32_t w[4][W], sc[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int ta = th + 8 * k + kv4_sigma(2 * col), tb = ta ^ 1;
-          const char *cb = st + S::kV, *sb = st + S::kVs + (D == 128 ? 4 * half + (r >> 1) : 2 * half + (r >> 2));
-          if (D == 128) {
-            w[2 * k] = *reinterpret_cast<const uint32_t *>(cb + ta * 32 + r * 4);
-            w[2 * k + 1] = *reinterpret_cast<const uint32_t *>(cb + tb * 32 + r * 4);
+          const int g8 = 16 * h + 8 * k, ta = kv4_sigma(2 * col), tb = ta ^ 1;  // the eight tokens, the lane's two
+          const char *vb = st + S::kV + g8 * S::kCb;
+          if (W == 2) {
+            const uint2 va = *reinterpret_cast<const uint2 *>(vb + S::piece(ta, r >> 1) + (r & 1) * 8);
+            const uint2 vc = *reinterpret_cast<const uint2 *>(vb + S::piece(tb, r >> 1) + (r & 1) * 8);
+            w[2 * k][0] = va.x, w[2 * k][W - 1] = va.y;
+            w[2 * k + 1][0] = vc.x, w[2 * k + 1][W - 1] = vc.y;
           } else {
-            w[2 * k] = *reinterpret_cast<const uint16_t *>(cb + ta * 16 + r * 2);
-            w[2 * k + 1] = *reinterpret_cast<const uint16_t *>(cb + tb * 16 + r * 2);
+            w[2 * k][0] = *reinterpret_cast<const uint32_t *>(vb + ta * S::kCb + r * 4);
+            w[2 * k + 1][0] = *reinterpret_cast<const uint32_t *>(vb + tb * S::kCb + r * 4);
           }
+          const char *sb = st + S::kVs + g8 * S::kSb + (D == 128 ? r : r >> 1);
           uint32_t sa = *reinterpret_cast<const uint8_t *>(sb + ta * S::kSb), sbb = *reinterpret_cast<const uint8_t *>(sb + tb * S::kSb);
           if (edge) {  // tokens past the end: whatever their slots hold counts as 0
-            if (t0 + ta >= count) sa = 0;
-            if (t0 + tb >= count) sbb = 0;
+            if (t0 + g8 + ta >= count) sa = 0;
+            if (t0 + g8 + tb >= count) sbb = 0;
           }
           sc[k] = e4m3x2_to_f16x2(sa | (sbb << 8));
         }
-        uint32_t f[4][4];
-        e2m1_to_f16x2((w[0] & 0x0f0f0f0fu) | ((w[1] << 4) & 0xf0f0f0f0u), f[0]);
-        e2m1_to_f16x2(((w[0] >> 4) & 0x0f0f0f0fu) | (w[1] & 0xf0f0f0f0u), f[1]);
-        e2m1_to_f16x2((w[2] & 0x0f0f0f0fu) | ((w[3] << 4) & 0xf0f0f0f0u), f[2]);
-        e2m1_to_f16x2(((w[2] >> 4) & 0x0f0f0f0fu) | (w[3] & 0xf0f0f0f0u), f[3]);
 #pragma unroll
-        for (int y = 0; y < MT; ++y) {
-          const uint32_t a0 = mul_f16x2(f[0][y], sc[0]), a1 = mul_f16x2(f[1][y], sc[0]), a2 = mul_f16x2(f[2][y], sc[1]),
-                         a3 = mul_f16x2(f[3][y], sc[1]);
+        for (int y = 0; y < W; ++y) {
+          uint32_t f[4][4];
+          e2m1_to_f16x2((w[0][y] & 0x0f0f0f0fu) | ((w[1][y] << 4) & 0xf0f0f0f0u), f[0]);
+          e2m1_to_f16x2(((w[0][y] >> 4) & 0x0f0f0f0fu) | (w[1][y] & 0xf0f0f0f0u), f[1]);
+          e2m1_to_f16x2((w[2][y] & 0x0f0f0f0fu) | ((w[3][y] << 4) & 0xf0f0f0f0u), f[2]);
+          e2m1_to_f16x2(((w[2][y] >> 4) & 0x0f0f0f0fu) | (w[3][y] & 0xf0f0f0f0u), f[3]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(o[y][nt], a0, a1, a2, a3, p[nt][0], p[nt][1]);
-            if (PS == 2) mma_f16(o[y][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+          for (int z = 0; z < 4; ++z) {
+            const uint32_t a0 = mul_f16x2(f[0][z], sc[0]), a1 = mul_f16x2(f[1][z], sc[0]), a2 = mul_f16x2(f[2][z], sc[1]),
+                           a3 = mul_f16x2(f[3][z], sc[1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(o[4 * y + z][nt], a0, a1, a2, a3, p[h][nt][0], p[h][nt][1]);
+              if (PS == 2) mma_f16(o[4 * y + z][nt], a0, a1, a2, a3, pl[h][nt][0], pl[h][nt][1]);
+            }
           }
         }
       }
       __syncwarp();
-      parity ^= 1;
       used = used + 1 == NST ? 0 : used + 1;
       issue();
     }
     if (rg.x + (seg1 - seg0) >= rg.x1) pdl_trigger();
 
     // Sums of the lanes of a query row, then of the warps: the ring is free now and takes their O.
-    __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -667,21 +607,21 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
         if (r == 0) s_m[warp * ROWS + 8 * nt + 2 * col + k] = m[nt][k], s_l[warp * ROWS + 8 * nt + 2 * col + k] = l[nt][k];
       }
     __syncthreads();
-    const int np = min(NP, seg1 - seg0);           // pairs that had a tile
-    float *acc = reinterpret_cast<float *>(ring);  // [warp][row][d / 2], 16-byte pieces of a row permuted
-    if (pair < np) {
+    const int nw = min(NW, seg1 - seg0);           // warps that had a tile
+    float *acc = reinterpret_cast<float *>(ring);  // [warp][row][d], 16-byte pieces of a row permuted
+    if (warp < nw) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int q = 8 * nt + 2 * col + k;
           float M = -1e30f;
-          for (int w = 0; w < np; ++w) M = fmaxf(M, s_m[2 * w * ROWS + q]);
+          for (int w = 0; w < nw; ++w) M = fmaxf(M, s_m[w * ROWS + q]);
           const float f = fast_exp2(m[nt][k] - M);
           float4 *dst = reinterpret_cast<float4 *>(acc) + (warp * ROWS + q) * PIECES;
 #pragma unroll
           for (int i = 0; i < MT; i += 2)
-            dst[(D == 128 ? (2 * r + i / 2) ^ ((col & 1) | (col >> 1) << 2) : r ^ (col << 1))] =
+            dst[(r * (MT / 2) + i / 2) ^ (r >> 1) ^ col] =
                 make_float4(o[i][nt][k] * f, o[i][nt][k + 2] * f, o[i + 1][nt][k] * f, o[i + 1][nt][k + 2] * f);
         }
     }
@@ -690,16 +630,14 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
     const int blk0 = (int)(ua / rg.per), blk1 = (int)((ua + n_tiles - 1) / rg.per);
     const bool whole = blk0 == blk1;
     const int64_t slot = (int64_t)blockIdx.x * 2 + (rg.x == rg.per * blockIdx.x ? 0 : 1);
-    for (int e = tid; e < rows * (D / 4); e += NW * 32) {
-      const int q = e / (D / 4), piece = e % (D / 4), hd = piece / PIECES, c4 = (q >> 1) & 3;
-      const int at = (piece % PIECES) ^ (D == 128 ? (c4 & 1) | (c4 >> 1) << 2 : c4 << 1);
+    for (int e = tid; e < rows * PIECES; e += NW * 32) {
+      const int q = e / PIECES, piece = e % PIECES, rr = piece / (MT / 2);
       float M = -1e30f, Z = 0.f;
-      for (int w = 0; w < np; ++w) M = fmaxf(M, s_m[2 * w * ROWS + q]);
-      for (int w = 0; w < np; ++w)
-        Z += (s_l[2 * w * ROWS + q] + s_l[(2 * w + 1) * ROWS + q]) * fast_exp2(s_m[2 * w * ROWS + q] - M);
+      for (int w = 0; w < nw; ++w) M = fmaxf(M, s_m[w * ROWS + q]);
+      for (int w = 0; w < nw; ++w) Z += s_l[w * ROWS + q] * fast_exp2(s_m[w * ROWS + q] - M);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < np; ++w) {
-        const float4 y = reinterpret_cast<const float4 *>(acc)[((2 * w + hd) * ROWS + q) * PIECES + at];
+      for (int w = 0; w < nw; ++w) {
+        const float4 y = reinterpret_cast<const float4 *>(acc)[(w * ROWS + q) * PIECES + (piece ^ (rr >> 1) ^ ((q >> 1) & 3))];
         v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
       }
       if (whole) {
@@ -811,7 +749,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
       if (next < seg1) {
         const int32_t now = seen;
         if (next + NW < seg1) seen = ld.peek(next + NW, lane);
-        ld.load_k(next, now, my_ring + issued * S::kCritStage, lane);
+        ld.template load<true>(next, now, my_ring + issued * S::kCritStage, lane);
         issued = issued + 1 == NST ? 0 : issued + 1;
         next += NW;
       }
@@ -843,7 +781,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int ch = 0; ch < n_chunk; ++ch) {
         float c[2][NT][4];
-        kv4_qk<D, NT, QS, 2>(c, kt, kt + 32 * S::kCb, qf + ch * ROWS * D * 2 * QS, lane);
+        kv4_qk<D, NT, QS>(c, kt, kt + S::kCritScales, qf + ch * ROWS * D * 2 * QS, lane);
         const float *fac = s_sl + ch * ROWS + 2 * col, *off = s_lse + ch * ROWS + 2 * col;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -903,17 +841,16 @@ namespace ssd {
 template <int NT>
 struct Kv4Tune {
   static constexpr int kWarps = 8;
-  static constexpr int kBlocks = NT <= 3 ? 2 : 1;
-  static constexpr int kStages = NT <= 2 ? 4 : 4;
+  static constexpr int kBlocks = NT == 1 ? 2 : 1;
+  static constexpr int kStages = NT <= 2 ? 3 : 4;
 };
 constexpr int kKv4CritWarps = 8, kKv4CritBlocks = 2, kKv4CritStages = 4;
 
 template <int D, int NT, int QS, int PS, bool LIST>
 int kv4_launch_attn(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
   constexpr int NST = Kv4Tune<NT>::kStages, BPS = Kv4Tune<NT>::kBlocks, NW = Kv4Tune<NT>::kWarps;
-  constexpr int ring = NW * NST * Kv4Smem<D>::kStage;
-  static_assert(ring >= NW * NT * 8 * D * 2, "the ring holds the warps' O");
-  constexpr int smem = kv4_smem_bytes<D, NT, QS, PS, NW, NST>();
+  static_assert(NST * Kv4Smem<D>::kStage >= NT * 8 * D * 4, "the ring holds the warps' O");
+  constexpr int smem = kv4_smem_bytes<D, NT, QS, NW, NST>();
   constexpr auto kernel = kv4_attn_kernel<D, NT, QS, PS, NW, NST, BPS, LIST>;
   int rc = ensure_smem<kernel>(smem);
   if (rc) return rc;

@@ -9,6 +9,8 @@
 #include "ssd_cache.h"
 #include "ssd_kv4.cuh"
 
+#include <type_traits>
+
 namespace ssd {
 
 // A row of bytes per (page, K|V, head, token): `wide` bytes at slot * wide of the block and, for a 4-bit
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kReleaseThreads) kv_release_kernel(KVView kv, 
 
 // ---- reserve --------------------------------------------------------------------------------
 constexpr int kResThreads = 1024;
-constexpr int kResLanes = 8;  // lanes per request
+constexpr int kResFew = 4;  // up to so many affected pages a request has a thread, above a warp
 
 // Per page of the pool, valid for the pages that requests of the call hold and ask for.
 struct PageAsk {
@@ -117,176 +119,186 @@ struct ReserveArgs {
   int32_t *refs;
   const int32_t *counts;
   PageAsk *ask;     // [num_pages]
-  int32_t *take;    // [batch]: pages each request needs (-1: request skipped), then their exclusive sums
+  int4 *row;        // [batch]: {first affected page index, their number (-1: request skipped), pages to take, sum of those before}
   int32_t *fresh;   // [num_pages]: the free pages handed out, ascending
   int4 *copies;     // [batch]: {old page, new page, live slots, 0}; slots 0: nothing to copy
   unsigned *status;
 };
 
+// Inclusive sum of v over the block's threads in order; s_warp: 33 ints.  total: the block's.
+__device__ __forceinline__ int block_scan(int v, int *s_warp, int &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  const int base = warp ? s_warp[warp - 1] : 0;
+  total = s_warp[31];
+  __syncthreads();
+  return base + inc;
+}
+
 // One block.  A request needs a page for every page index that its tokens L .. L + n - 1 touch: where it has
 // none, and where it holds one together with others.  If all holders of a page ask, the first of them keeps
 // it.  Phases, with the whole block in step: what is asked of every page; how many new pages a request
 // needs; the first free pages of the pool; hand them out.  If they do not suffice nothing is changed.
-__global__ void __launch_bounds__(kResThreads) kv_reserve_kernel(ReserveArgs a) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int grp = tid / kResLanes, gl = tid % kResLanes;
-  constexpr int kGroups = kResThreads / kResLanes;
-  const unsigned gmask = 0xffu << (lane & ~(kResLanes - 1));
-  __shared__ int s_warp[33];
-  pdl_wait();
+// LPR lanes share a request: bound by the latency of a dozen dependent loads, so a thread per request
+// (all requests at once) where they need a page or two, a warp for long prompts.
+template <int LPR>
+__device__ __forceinline__ void reserve_rows(const ReserveArgs &a, int *s_warp) {
+  const int tid = threadIdx.x, gl = tid % LPR, grp = tid / LPR;
+  constexpr int kGroups = kResThreads / LPR;
   const KVView &kv = a.kv;
-  const int ps = kv.page_size;
-
-  // Requests in order: whether a request can be served at all, and its pages' counts before the call.
+  const unsigned gmask = LPR == 32 ? 0xffffffffu : 1u << (tid & 31);
+  // Whether a request can be served at all, and its pages' counts before the call.
   for (int b = grp; b < kv.batch; b += kGroups) {
-    const int L = kv.seq_lens[b], n = a.counts[b];
-    bool len_ok = L >= 0 && n >= 0 && (int64_t)L + n <= kv.max_seq_len;
-    bool page_ok = true;
-    if (len_ok && n > 0) {
-      const int32_t *row = a.table + (int64_t)b * kv.max_pages;
-      const int j0 = L >> kv.log2_ps, j1 = (L + n + ps - 1) >> kv.log2_ps;
-      for (int j = j0 + gl; j < j1; j += kResLanes) {
-        const int32_t p = row[j];
-        if (p < 0) {
-          page_ok &= !(j == j0 && (L & (ps - 1)));  // the page of live tokens is missing
-          continue;
-        }
-        if ((int64_t)p >= kv.num_pages) {
-          page_ok = false;
-          continue;
-        }
+    const int4 r = a.row[b];
+    const int32_t *row = a.table + (int64_t)b * kv.max_pages;
+    bool ok = true;
+    for (int i = gl; i < r.y; i += LPR) {
+      const int32_t p = row[r.x + i];
+      if (p < 0) {
+        ok &= !(i == 0 && r.z);  // the page of live tokens is missing
+      } else if ((int64_t)p >= kv.num_pages) {
+        ok = false;
+      } else {
         const int rc = a.refs[p];
-        page_ok &= rc > 0;
+        ok &= rc > 0;
         a.ask[p] = PageAsk{rc, 0, 0x7fffffff, 0};
       }
     }
-    page_ok = __all_sync(gmask, page_ok);
-    if (gl == 0) {
-      if (!len_ok) atomicOr(a.status, (unsigned)SSD_FAULT_SEQLEN);
-      if (!page_ok) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
-      a.take[b] = len_ok && page_ok ? 0 : -1;
+    if (LPR > 1) ok = __all_sync(gmask, ok);
+    if (!ok && gl == 0) {
+      atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
+      a.row[b].y = -1;
     }
   }
   __syncthreads();
   // Who asks for a page that it shares.
   for (int b = grp; b < kv.batch; b += kGroups) {
-    if (a.take[b] < 0 || a.counts[b] == 0) continue;
-    const int L = kv.seq_lens[b], n = a.counts[b];
+    const int4 r = a.row[b];
     const int32_t *row = a.table + (int64_t)b * kv.max_pages;
-    for (int j = (L >> kv.log2_ps) + gl; j < (L + n + ps - 1) >> kv.log2_ps; j += kResLanes) {
-      const int32_t p = row[j];
+    for (int i = gl; i < r.y; i += LPR) {
+      const int32_t p = row[r.x + i];
       if (p < 0 || a.ask[p].refs == 1) continue;
       atomicAdd(&a.ask[p].asked, 1);
       atomicMin(&a.ask[p].lowest, b);
     }
   }
   __syncthreads();
-  // Pages to take, per request.
   auto takes = [&](int b, int32_t p) {
     if (p < 0) return true;
     const PageAsk k = a.ask[p];
     return !(k.refs == 1 || (k.asked == k.refs && k.lowest == b));
   };
   for (int b = grp; b < kv.batch; b += kGroups) {
+    const int4 r = a.row[b];
+    const int32_t *row = a.table + (int64_t)b * kv.max_pages;
     int c = 0;
-    if (a.take[b] >= 0 && a.counts[b] > 0) {
-      const int L = kv.seq_lens[b], n = a.counts[b];
-      const int32_t *row = a.table + (int64_t)b * kv.max_pages;
-      for (int j = (L >> kv.log2_ps) + gl; j < (L + n + ps - 1) >> kv.log2_ps; j += kResLanes) c += takes(b, row[j]);
+    for (int i = gl; i < r.y; i += LPR) c += takes(b, row[r.x + i]);
+    if (LPR > 1) c = __reduce_add_sync(gmask, c);
+    if (gl == 0) {
+      a.row[b].z = c;
+      a.copies[b] = make_int4(0, 0, 0, 0);
     }
-#pragma unroll
-    for (int o = kResLanes / 2; o; o >>= 1) c += __shfl_xor_sync(gmask, c, o);
-    if (gl == 0 && a.take[b] >= 0) a.take[b] = c;
   }
   __syncthreads();
-  // Exclusive sums over the requests, in their order (skipped requests keep -1), through `copies.w`.
+  // Sums over the requests, in their order.
   int total = 0;
   for (int b0 = 0; b0 < kv.batch; b0 += kResThreads) {
-    const int b = b0 + tid;
-    const int v = b < kv.batch ? max(a.take[b], 0) : 0;
-    int inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    if (warp == 0) {
-      int w = s_warp[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-      }
-      s_warp[lane] = w;
-    }
-    __syncthreads();
-    const int base = total + (warp ? s_warp[warp - 1] : 0);
-    if (b < kv.batch) a.copies[b] = make_int4(0, 0, 0, base + inc - v);
-    total += s_warp[31];
-    __syncthreads();
+    const int b = b0 + tid, v = b < kv.batch ? a.row[b].z : 0;
+    int part;
+    const int inc = block_scan(v, s_warp, part);
+    if (b < kv.batch) a.row[b].w = total + inc - v;
+    total += part;
   }
-  // The first `total` free pages.
+  // The first `total` free pages, 16 counts a thread and step.
   int found = 0;
-  for (int64_t p0 = 0; p0 < kv.num_pages && found < total; p0 += kResThreads * 4) {
-    const int64_t p = p0 + tid * 4;
-    int v[4];
+  const bool vec = (reinterpret_cast<uintptr_t>(a.refs) & 15) == 0;
+  for (int64_t p0 = 0; p0 < kv.num_pages && found < total; p0 += kResThreads * 16) {
+    const int64_t p = p0 + tid * 16;
+    unsigned free = 0;
+    if (vec && p + 16 <= kv.num_pages) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = p + k < kv.num_pages ? (a.refs[p + k] == 0) : 0;
-    const int mine = v[0] + v[1] + v[2] + v[3];
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    if (warp == 0) {
-      int w = s_warp[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
+      for (int k = 0; k < 4; ++k) {
+        const int4 v = *reinterpret_cast<const int4 *>(a.refs + p + 4 * k);
+        free |= (unsigned)((v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3) << (4 * k);
       }
-      s_warp[lane] = w;
+    } else {
+      for (int k = 0; k < 16; ++k)
+        if (p + k < kv.num_pages && a.refs[p + k] == 0) free |= 1u << k;
     }
-    __syncthreads();
-    int at = found + (warp ? s_warp[warp - 1] : 0) + inc - mine;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (v[k] && at < total) a.fresh[at++] = (int32_t)(p + k);
-    found += s_warp[31];
-    __syncthreads();
+    const int mine = __popc(free);
+    int part;
+    int at = found + block_scan(mine, s_warp, part) - mine;
+    for (; free && at < total; free &= free - 1) a.fresh[at++] = (int32_t)(p + __ffs(free) - 1);
+    found += part;
   }
+  __syncthreads();
   if (found < total) {
     if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_NOPAGE);
     return;
   }
   for (int b = grp; b < kv.batch; b += kGroups) {
-    if (a.take[b] <= 0) continue;
-    const int L = kv.seq_lens[b], n = a.counts[b];
+    const int4 r = a.row[b];
+    if (r.z == 0) continue;
     int32_t *row = a.table + (int64_t)b * kv.max_pages;
-    int at = a.copies[b].w;
-    const int j0 = L >> kv.log2_ps, j1 = (L + n + ps - 1) >> kv.log2_ps;
-    for (int jb = j0; jb < j1; jb += kResLanes) {
-      const int j = jb + gl;
-      const int32_t p = j < j1 ? row[j] : -1;
-      const bool t = j < j1 && takes(b, p);
-      const unsigned m = __ballot_sync(gmask, t) & gmask;
+    const int live = kv.seq_lens[b] & (kv.page_size - 1);
+    int at = r.w;
+    for (int i0 = 0; i0 < r.y; i0 += LPR) {
+      const int i = i0 + gl;
+      const int32_t p = i < r.y ? row[r.x + i] : -1;
+      const bool t = i < r.y && takes(b, p);
+      const unsigned m = LPR > 1 ? __ballot_sync(gmask, t) : (unsigned)t;
       if (t) {
-        const int32_t f = a.fresh[at + __popc(m & ((1u << lane) - 1))];
-        row[j] = f;
+        const int32_t f = a.fresh[at + (LPR > 1 ? __popc(m & ((1u << gl) - 1)) : 0)];
+        row[r.x + i] = f;
         a.refs[f] = 1;
         if (p >= 0) {
           atomicSub(a.refs + p, 1);
-          if (j == j0 && (L & (ps - 1))) a.copies[b] = make_int4(p, f, L & (ps - 1), 0);
+          if (i == 0 && live) a.copies[b] = make_int4(p, f, live, 0);
         }
       }
       at += __popc(m);
     }
   }
+}
+
+__global__ void __launch_bounds__(kResThreads) kv_reserve_kernel(ReserveArgs a) {
+  __shared__ int s_warp[33];
+  pdl_wait();
+  bool many = false;
+  for (int b = threadIdx.x; b < a.kv.batch; b += kResThreads) {
+    const int L = a.kv.seq_lens[b], n = a.counts[b];
+    int4 r = make_int4(0, 0, 0, 0);
+    if (L < 0 || n < 0 || (int64_t)L + n > a.kv.max_seq_len) {
+      atomicOr(a.status, (unsigned)SSD_FAULT_SEQLEN);
+    } else if (n > 0) {
+      r.x = L >> a.kv.log2_ps;
+      r.y = ((L + n - 1) >> a.kv.log2_ps) + 1 - r.x;
+      r.z = L & (a.kv.page_size - 1);
+    }
+    many |= r.y > kResFew;
+    a.row[b] = r;
+  }
+  if (__syncthreads_or(many))
+    reserve_rows<32>(a, s_warp);
+  else
+    reserve_rows<1>(a, s_warp);
 }
 
 constexpr int kMoveThreads = 128;
@@ -377,28 +389,32 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactArgs
     s_slots[tid] = t & (a.from.page_size - 1);
   }
   __syncthreads();
+  // Pieces of 16 bytes, four loads on their way per thread; then a 4-bit cache's scales in words.
   const char *from = static_cast<const char *>(a.from.pool);
-  const int cpr = a.rs.wide / 16;
-  const int pieces = nj * 2 * cpr;
-  for (int e = tid; e < pieces; e += kCompactThreads) {
-    const int c = e % cpr, which = (e / cpr) & 1, j = e / (2 * cpr);
-    if (s_to[j] < 0) continue;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (s_from[j] >= 0) v = __ldg(reinterpret_cast<const uint4 *>(from + s_from[j] + which * h * fb + s_slots[j] * a.rs.wide) + c);
-    reinterpret_cast<uint4 *>(a.to_pool + s_to[j] + which * h * tb + (int64_t)((j0 + j) & (a.to.page_size - 1)) * a.rs.wide)[c] = v;
-  }
-  if (a.rs.thin) {
-    const int tpr = a.rs.thin / 4;
-    for (int e = tid; e < nj * 2 * tpr; e += kCompactThreads) {
-      const int c = e % tpr, which = (e / tpr) & 1, j = e / (2 * tpr);
-      if (s_to[j] < 0) continue;
-      uint32_t v = 0;
-      if (s_from[j] >= 0)
-        v = __ldg(reinterpret_cast<const uint32_t *>(from + s_from[j] + which * h * fb + a.from.page_size * a.rs.wide + s_slots[j] * a.rs.thin) + c);
-      reinterpret_cast<uint32_t *>(a.to_pool + s_to[j] + which * h * tb + a.to.page_size * a.rs.wide +
-                                   ((j0 + j) & (a.to.page_size - 1)) * a.rs.thin)[c] = v;
+  const int64_t fv = h * fb, tv = h * tb;
+  auto copy = [&](auto *tag, int width, int at_from, int at_to) {
+    using V = typename std::remove_pointer<decltype(tag)>::type;
+    const int sh = 31 - __clz(width / (int)sizeof(V));  // log2 of the pieces of a row (widths are powers of two)
+    const int total = nj << (sh + 1);
+    constexpr int U = 4;
+    for (int e0 = tid; e0 < total; e0 += U * kCompactThreads) {
+      V v[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int e = e0 + k * kCompactThreads, c = e & ((1 << sh) - 1), which = (e >> sh) & 1, j = e >> (sh + 1);
+        v[k] = V{};
+        if (e < total && s_from[j] >= 0) v[k] = __ldg(reinterpret_cast<const V *>(from + s_from[j] + (which ? fv : 0) + at_from + s_slots[j] * width) + c);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int e = e0 + k * kCompactThreads, c = e & ((1 << sh) - 1), which = (e >> sh) & 1, j = e >> (sh + 1);
+        if (e < total && s_to[j] >= 0)
+          reinterpret_cast<V *>(a.to_pool + s_to[j] + (which ? tv : 0) + at_to + ((j0 + j) & (a.to.page_size - 1)) * width)[c] = v[k];
+      }
     }
-  }
+  };
+  copy(static_cast<uint4 *>(nullptr), a.rs.wide, 0, 0);
+  if (a.rs.thin) copy(static_cast<uint32_t *>(nullptr), a.rs.thin, a.from.page_size * a.rs.wide, a.to.page_size * a.rs.wide);
 }
 
 static int page_checks(const ssd_paged_kv *kv, KVView *v, const int32_t *refs, const char *who) {
@@ -448,8 +464,8 @@ static size_t reserve_layout(const ssd_paged_kv *kv, ReserveArgs *a, void *ws) {
   PageAsk *ask = c.take<PageAsk>((size_t)kv->num_pages);
   int32_t *fresh = c.take<int32_t>((size_t)kv->num_pages);
   int4 *copies = c.take<int4>((size_t)kv->batch);
-  int32_t *take = c.take<int32_t>((size_t)kv->batch);
-  if (a) a->ask = ask, a->fresh = fresh, a->copies = copies, a->take = take;
+  int4 *row = c.take<int4>((size_t)kv->batch);
+  if (a) a->ask = ask, a->fresh = fresh, a->copies = copies, a->row = row;
   return c.off;
 }
 
