@@ -11,7 +11,7 @@ namespace ssd {
 int kv4_dense_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
 int kv4_dense_d128(const Kv4AttnArgs &a, int grid, cudaStream_t st);
 int kv4_tc_attn(const Kv4AttnArgs &a, int rows, int grid, cudaStream_t st);
-int kv4_tc_crit(const Kv4AttnArgs &a, int np, int grid, cudaStream_t st);
+int kv4_tc_crit(const Kv4AttnArgs &a, int grid, cudaStream_t st);
 int kv4_list_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
 int kv4_list_d128(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
 int kv4_crit_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
@@ -143,7 +143,7 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
   a.n_chunk = 1;
   a.n_units = kv->batch * kv->h_kv;
   if (kv->d == 128)
-    return kv4_tc_crit(a, a.R <= 32 ? kv4_np(a.R) : 64, kv4_grid(a.n_units, kv->max_seq_len, kKv4TcTile, kKv4CritTcBlocks), st);
+    return kv4_tc_crit(a, kv4_grid(a.n_units, kv->max_seq_len, kKv4TcTile, kKv4CritTcBlocks), st);
   return kv4_crit_d64(a, nt, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kKv4CritBlocks), st);
 }
 

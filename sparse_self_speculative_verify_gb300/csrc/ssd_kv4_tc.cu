@@ -18,13 +18,21 @@ static int launch_types(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
   return a.q_f32 ? launch_tc<NP, CW, 2, 2>(a, grid, st) : a.out_f32 ? launch_tc<NP, CW, 1, 2>(a, grid, st) : launch_tc<NP, CW, 1, 1>(a, grid, st);
 }
 
-template <int NP, int QS>
+template <int NP, int CR, int QS>
 static int launch_crit(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
-  constexpr auto kernel = kv4_crit_tc_kernel<NP, QS, kKv4CritTcBlocks>;
+  constexpr int BPS = QS == 2 && NP == 64 ? 2 : NP == 64 ? 3 : kKv4CritTcBlocks;
+  constexpr auto kernel = kv4_crit_tc_kernel<NP, CR, QS, BPS>;
   constexpr int smem = Kv4CritCfg<NP, QS>::kSmem;
+  static_assert(smem * BPS <= 227 * 1024, "the blocks of an SM fit");
   int rc = ensure_smem<kernel>(smem);
   if (rc) return rc;
-  return launch(kernel, dim3(grid), dim3(kKv4CritTcWarps * 32), smem, st, "kv4_crit_tc_kernel", a);
+  const int most = sm_count() * BPS;
+  return launch(kernel, dim3(grid < most ? grid : most), dim3(kKv4CritTcWarps * 32), smem, st, "kv4_crit_tc_kernel", a);
+}
+
+template <int NP, int CR>
+static int launch_crit_types(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
+  return a.q_f32 ? launch_crit<NP, CR, 2>(a, grid, st) : launch_crit<NP, CR, 1>(a, grid, st);
 }
 
 // rows: of a pass (at most 32).
@@ -35,12 +43,14 @@ int kv4_tc_attn(const Kv4AttnArgs &a, int rows, int grid, cudaStream_t st) {
                       : launch_types<32, 16>(a, grid, st);
 }
 
-int kv4_tc_crit(const Kv4AttnArgs &a, int np, int grid, cudaStream_t st) {
-  switch (np) {
-    case 16: return a.q_f32 ? launch_crit<16, 2>(a, grid, st) : launch_crit<16, 1>(a, grid, st);
-    case 32: return a.q_f32 ? launch_crit<32, 2>(a, grid, st) : launch_crit<32, 1>(a, grid, st);
-    default: return a.q_f32 ? launch_crit<64, 2>(a, grid, st) : launch_crit<64, 1>(a, grid, st);
-  }
+// All rows (up to 64) at once.
+int kv4_tc_crit(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
+  return a.R <= 8    ? launch_crit_types<16, 8>(a, grid, st)
+         : a.R <= 16 ? launch_crit_types<16, 16>(a, grid, st)
+         : a.R <= 24 ? launch_crit_types<32, 24>(a, grid, st)
+         : a.R <= 32 ? launch_crit_types<32, 32>(a, grid, st)
+         : a.R <= 48 ? launch_crit_types<64, 48>(a, grid, st)
+                     : launch_crit_types<64, 64>(a, grid, st);
 }
 
 }  // namespace ssd

@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
 // ---- criticality ------------------------------------------------------------------------------
 constexpr int kKv4CritTcWarps = 6;  // 0-3: K and the sums, 4: MMA issue, 5: raw tiles
 constexpr int kKv4CritTcStages = 4;
-constexpr int kKv4CritTcBlocks = 3;  // per SM
+constexpr int kKv4CritTcBlocks = 4;  // per SM
 
 template <int NP, int QS>
 struct Kv4CritCfg {
@@ -713,13 +713,18 @@ struct Kv4CritCfg {
   static constexpr int kQBytes = NP * 256;
   static constexpr int kMisc = kQ + QS * kQBytes;
   static constexpr int kSmem = kMisc + 2 * NP * 4 + 16 * 8 + 64 + 1024;
+  // tensor memory: K, S^T of two tiles (of one, where the rows are many)
+  static constexpr int kBufs = NP <= 32 ? 2 : 1;
   static constexpr int kTmem = 128, kColS = 64;
+  static_assert(kColS + kBufs * NP <= kTmem, "tensor memory");
 };
 
 // A second pass over K alone recomputes the logits of all rows and sums exp(x - lse) per token.  (Keeping them from
 // the first pass would cost 2 R bytes per token each way, more than K's 72 for R > 18, and a rounding to
 // f16.)
-template <int NP, int QS, int BPS>
+//
+// CR: columns that hold rows (the MMA takes NP).  Four blocks share an SM.
+template <int NP, int CR, int QS, int BPS>
 __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(Kv4AttnArgs a) {
   using C = Kv4CritCfg<NP, QS>;
   using namespace sm100;
@@ -728,7 +733,7 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
   const uint32_t sbase = smem_u32(sm);
   float *s_sl = reinterpret_cast<float *>(sm + C::kMisc), *s_lse = s_sl + NP;
   const uint32_t bars = smem_u32(s_lse + NP);
-  const uint32_t b_raw = bars, b_free = bars + 8 * kKv4CritTcStages, b_k = b_free + 8 * kKv4CritTcStages, b_s = b_k + 8, b_drain = b_s + 8;
+  const uint32_t b_raw = bars, b_free = bars + 8 * kKv4CritTcStages, b_k = b_free + 8 * kKv4CritTcStages, b_s = b_k + 8, b_drain = b_s + 16;
   __shared__ int64_t s_scan[kKv4CritTcWarps + 2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -736,7 +741,7 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kKv4CritTcStages; ++i) mbar_init(b_raw + 8 * i, 32), mbar_init(b_free + 8 * i, 4);
-    mbar_init(b_k, 128), mbar_init(b_s, 1), mbar_init(b_drain, 1);
+    mbar_init(b_k, 4), mbar_init(b_s, 1), mbar_init(b_s + 8, 1), mbar_init(b_drain, 1);
     mbar_init_fence();
   }
   if (warp == 4) {
@@ -788,9 +793,9 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
         for (int q = 0; q < QS; ++q)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ts(tmu + C::kColS, tmu + 8 * kk, qd + (uint64_t)((q * C::kQBytes + (kk >> 2) * (NP * 128) + (kk & 3) * 32) >> 4), id_qk,
+            mma_f16_ts(tmu + C::kColS + n % C::kBufs * NP, tmu + 8 * kk, qd + (uint64_t)((q * C::kQBytes + (kk >> 2) * (NP * 128) + (kk & 3) * 32) >> 4), id_qk,
                        q + kk > 0 ? 1u : 0u);
-        mma_commit(b_s);
+        mma_commit(b_s + 8 * (n % C::kBufs));
       }
       __syncwarp();
     }
@@ -808,9 +813,8 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
       kv4_convert_k<4>(sm + st * C::kStage, sm + st * C::kStage + kKv4TcTile * 64, tw, 0, tm + lanes);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(b_k);
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_free + 8 * st);
+      if (lane == 0) mbar_arrive(b_k), mbar_arrive(b_free + 8 * st);
     };
     for (; rg.x < rg.x1;) {
       const int b = rg.u / a.kv.h_kv, g = rg.u % a.kv.h_kv, t1 = seg_end(kv4_tiles<false, kKv4TcTile>(a, rg.u));
@@ -832,29 +836,47 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
       for (int t = rg.off; t < t1; ++t, ++n) {
         const int tok = t * kKv4TcTile + tw;
         const bool edge = (t + 1) * kKv4TcTile > L - a.n_c + 1;
-        const int first = tok < L ? max(0, (tok - (L - a.n_c)) * a.G) : NP;
-        wait(b_s, n);
+        wait(b_s + 8 * (n % C::kBufs), n / C::kBufs);
         tc_fence_after();
-        float x[NP];
+        const uint32_t s_at = tm + lanes + C::kColS + n % C::kBufs * NP;
+        float x[C::kBufs == 1 ? CR : 4];
+        if (C::kBufs == 1) {  // the one buffer is read before the next tile's K is announced
 #pragma unroll
-        for (int c = 0; c < NP; c += 16) tmem_ld16(tm + lanes + C::kColS + c, x + c);
-        tmem_ld_wait();
-        if (t + 1 < t1) {
+          for (int c = 0; c < CR; c += 4) tmem_ld4(s_at + c, x + (C::kBufs == 1 ? c : 0));
+          tmem_ld_wait();
           tc_fence_before();
-          convert(n + 1);
         }
+        if (t + 1 < t1) convert(n + 1);
+        int first = 0;
+        if (edge) first = tok < L ? (tok - (L - a.n_c)) * a.G : NP;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < NP; q += 4) {
-          const float4 sl = *reinterpret_cast<const float4 *>(s_sl + q), ls = *reinterpret_cast<const float4 *>(s_lse + q);
-          float y[4] = {fmaf(x[q], sl.x, -ls.x), fmaf(x[q + 1], sl.y, -ls.y), fmaf(x[q + 2], sl.z, -ls.z), fmaf(x[q + 3], sl.w, -ls.w)};
+        for (int c = 0; c < CR; c += 8) {
+          constexpr int W = 8;
+          float v[W];
+          if (C::kBufs == 1) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (edge && q + k < first) y[k] = -INFINITY;
-            sum[k] += fast_exp2(y[k]);
+            for (int k = 0; k < W; ++k) v[k] = x[C::kBufs == 1 ? c + k : 0];
+          } else {
+            tmem_ld8(s_at + c, v);
+            tmem_ld_wait();
           }
+#pragma unroll
+          for (int q = 0; q < W; q += 4) {
+            const float4 sl = *reinterpret_cast<const float4 *>(s_sl + c + q), ls = *reinterpret_cast<const float4 *>(s_lse + c + q);
+            v[q] = fmaf(v[q], sl.x, -ls.x), v[q + 1] = fmaf(v[q + 1], sl.y, -ls.y);
+            v[q + 2] = fmaf(v[q + 2], sl.z, -ls.z), v[q + 3] = fmaf(v[q + 3], sl.w, -ls.w);
+          }
+          if (edge) {
+#pragma unroll
+            for (int q = 0; q < W; ++q)
+              if (c + q < first) v[q] = -INFINITY;
+          }
+#pragma unroll
+          for (int q = 0; q < W; ++q) sum[q & 3] += fast_exp2(v[q]);
         }
         if (tok < L) a.scores[(int64_t)rg.u * a.scores_stride + tok] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc_fence_before();
       }
       named_sync(1, 128);
       rg.x += t1 - rg.off, rg.u += 1, rg.off = 0;
