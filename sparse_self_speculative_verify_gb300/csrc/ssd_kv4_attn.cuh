@@ -56,6 +56,7 @@ struct Kv4AttnArgs {
   int64_t scores_stride;
   const float *lse_in;    // criticality pass
   int n_units;            // batch * h_kv * n_chunk
+  int whole_units;        // blocks take whole units (short ones: see kv4_range)
   unsigned *status;
 };
 
@@ -79,10 +80,15 @@ struct Kv4Smem {
   }
 };
 
+// Whether the warps' O have a place of their own at a segment's end, so that the next segment's tiles are on their
+// way meanwhile; otherwise they go to the ring.
+constexpr bool kv4_ahead(int nt) { return nt == 1; }
+
 template <int D, int NT, int QS, int NW, int NST>
 constexpr int kv4_smem_bytes() {
-  // ring, query fragments, per-row logit factors, the warps' references and sums
-  return NW * NST * Kv4Smem<D>::kStage + NT * 8 * D * 2 * QS + NT * 8 * 4 + 2 * NW * NT * 8 * 4;
+  // ring, the warps' O, query fragments, per-row logit factors, the warps' references and sums
+  return NW * NST * Kv4Smem<D>::kStage + (kv4_ahead(NT) ? NW * NT * 8 * D * 4 : 0) + NT * 8 * D * 2 * QS + NT * 8 * 4 +
+         2 * NW * NT * 8 * 4;
 }
 
 // Tiles of a unit; a unit without tokens has one empty tile, whose rows come out as 0 and -inf.
@@ -99,8 +105,9 @@ __device__ __forceinline__ int kv4_tiles(const Kv4AttnArgs &a, int u) {
   return n > 0 ? cdiv(n, TILE) : 1;
 }
 
-// Position of this block in the list of all units' tiles: the tiles are dealt out in equal contiguous
-// ranges, whatever the lengths.  Returns false when the block has none.
+// Position of this block in the list of all units' tiles: the tiles are dealt out in equal contiguous ranges,
+// whatever the lengths.  Short units (up to four tiles a warp) are dealt out whole instead: a part of one costs
+// more to join (about 4 us) than to compute.  Returns false when the block has none.
 struct Kv4Range {
   int64_t x, x1, per;  // next tile, end, tiles per block
   int u, off;          // unit and tile inside it of x
@@ -108,6 +115,13 @@ struct Kv4Range {
 template <bool LIST, int NW, int TILE = kKv4Tile, int MIN = NW>
 __device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int64_t *s_scan /* [NW + 2] */) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (a.whole_units) {
+    const int units = cdiv(a.n_units, (int)gridDim.x);
+    r.u = (int)blockIdx.x * units, r.off = 0;
+    r.x = r.x1 = 0, r.per = (int64_t)1 << 40;  // more than there are tiles
+    for (int u = r.u; u < min(a.n_units, r.u + units); ++u) r.x1 += kv4_tiles<LIST, TILE>(a, u);
+    return r.x1 > 0;
+  }
   const int per_thread = cdiv(a.n_units, NW * 32);
   const int u0 = min(a.n_units, tid * per_thread), u1 = min(a.n_units, u0 + per_thread);
   int64_t sum = 0;
@@ -391,6 +405,79 @@ __device__ __forceinline__ void kv4_write4(const Kv4AttnArgs &a, int64_t elem, c
     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + elem) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
+// Counts a block in, after a barrier of the threads that wrote its part: releases those writes, and lets the last
+// block's threads (after a barrier) see the others'.
+__device__ __forceinline__ unsigned kv4_arrive(unsigned *counter) {
+  unsigned old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
+}
+
+// Joins the `parts` partial results of a unit's pass, in the blocks' order: part k lies in rows row_of_part(k) .. of
+// part_o / part_ml.  NT threads (whole warps), `sync` their barrier; s_M, s_F, s_L: `rows` floats each.  Several loads
+// are kept on their way: a part's load behind the last one's took 0.7 us each.
+template <int D, int NT, typename PartRow, typename OutRow, typename Sync>
+__device__ __forceinline__ void kv4_join(const Kv4AttnArgs &a, int parts, int rows, int tid, float *s_M, float *s_F, float *s_L,
+                                         PartRow part, OutRow row_of, Sync sync) {
+  const int lane = tid & 31, warp = tid >> 5;
+  const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
+  constexpr int U = 4;  // rows of a warp at once
+  for (int q0 = warp; q0 < rows; q0 += U * (NT / 32)) {
+    float2 v[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int q = q0 + j * (NT / 32);
+      v[j] = q < rows && lane < parts ? __ldcg(ml + part(lane) + q) : make_float2(-1e30f, 0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int q = q0 + j * (NT / 32);
+      if (q >= rows) break;
+      float M = v[j].x;
+      for (int k = lane + 32; k < parts; k += 32) M = fmaxf(M, __ldcg(ml + part(k) + q).x);
+      M = warp_max(M);
+      float Z = v[j].y * fast_exp2(v[j].x - M);
+      for (int k = lane + 32; k < parts; k += 32) {
+        const float2 w = __ldcg(ml + part(k) + q);
+        Z += w.y * fast_exp2(w.x - M);
+      }
+      Z = warp_sum(Z);
+      if (lane == 0) {
+        s_M[q] = M;
+        s_F[q] = Z == 0.f ? 0.f : a.v_scale / Z;
+        s_L[q] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
+      }
+    }
+  }
+  sync();
+  for (int e = tid; e < rows * (D / 4); e += NT) {
+    const int q = e / (D / 4), piece = e % (D / 4);
+    const float M = s_M[q];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < parts; k0 += 8) {
+      float4 y[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        y[j] = make_float4(0.f, 0.f, 0.f, 0.f), w[j] = -INFINITY;
+        if (k0 + j < parts) {
+          const int64_t at = part(k0 + j) + q;
+          y[j] = __ldcg(reinterpret_cast<const float4 *>(a.part_o) + at * (D / 4) + piece);
+          w[j] = __ldcg(ml + at).x;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = fast_exp2(w[j] - M);
+        acc.x = fmaf(y[j].x, f, acc.x), acc.y = fmaf(y[j].y, f, acc.y), acc.z = fmaf(y[j].z, f, acc.z), acc.w = fmaf(y[j].w, f, acc.w);
+      }
+    }
+    const float f = s_F[q];
+    kv4_write4(a, row_of(q) * D + piece * 4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+    if (piece == 0 && a.lse) a.lse[row_of(q)] = s_L[q];
+  }
+}
+
 // PS = 2 carries a probability as the sum of two f16 (22 bits) for fp32 outputs; PS = 1 rounds it to f16
 // (2^-12 relative) for bf16 outputs, whose own rounding is 2^-9.
 template <int D, int NT, int QS, int PS, int NW, int NST, int BPS, bool LIST>
@@ -399,13 +486,16 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
   constexpr int MT = D / 16;  // fragments of 16 d
   constexpr int ROWS = NT * 8;
   constexpr int PIECES = D / 4;  // 16-byte pieces of a row of O
+  constexpr bool AHEAD = kv4_ahead(NT);
   extern __shared__ __align__(128) char smem[];
   char *ring = smem;
-  char *qf = ring + NW * NST * S::kStage;
+  char *qf = ring + NW * NST * S::kStage + (AHEAD ? NW * ROWS * D * 4 : 0);
   float *s_sl = reinterpret_cast<float *>(qf + ROWS * D * 2 * QS);
   float *s_m = s_sl + ROWS, *s_l = s_m + NW * ROWS;
+  float *acc = reinterpret_cast<float *>(AHEAD ? ring + NW * NST * S::kStage : ring);  // [warp][row][d], pieces of a row permuted
   __shared__ int64_t s_scan[NW + 2];
   __shared__ int s_last;
+  __shared__ float s_join[3 * ROWS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, col = lane & 3;
   pdl_wait();
   Kv4Range rg;
@@ -419,36 +509,57 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
   const char *my_tiles = ring + warp * NST * S::kStage;
   const uint32_t my_ring = smem_u32(my_tiles);
   Kv4Loader<D> ld(a);
+  Kv4Queries<D, NT, QS, NW> qs;
   int issued = 0, used = 0;  // the warp's ring positions
-
-  while (rg.x < rg.x1) {
-    const int u = rg.u, b = u / (a.kv.h_kv * a.n_chunk), g = (u / a.n_chunk) % a.kv.h_kv, r0 = (u % a.n_chunk) * ROWS;
-    const int rows = min(ROWS, a.R - r0);
-    const int n_tiles = kv4_tiles<LIST>(a, u);
-    const int seg0 = rg.off, seg1 = seg0 + (int)min((int64_t)(n_tiles - rg.off), rg.x1 - rg.x);
-    const int L = min(max(a.kv.seq_lens[b], 0), a.kv.max_seq_len);
-    const int count = LIST ? min(max(a.cnt[u], 0), a.k_max) : L;
-    ld.unit(b, g, L, count, LIST ? a.idx + (int64_t)u * a.k_max : nullptr);
-    Kv4Queries<D, NT, QS, NW> qs;
-    qs.fetch(a, b, g, r0, rows);
-    int next = seg0 + warp;
-    auto peek = [&](int tile) { return LIST ? ld.peek_list(tile, lane) : ld.peek(tile, lane); };
-    int32_t seen = next < seg1 ? peek(next) : -1;
-    auto issue = [&]() {
-      if (next < seg1) {
-        const int32_t now = seen;
-        if (next + NW < seg1) seen = peek(next + NW);
-        if (LIST)
-          ld.load_list(next, now, my_ring + issued * S::kStage, lane);
-        else
-          ld.template load<false>(next, now, my_ring + issued * S::kStage, lane);
-        issued = issued + 1 == NST ? 0 : issued + 1;
-        next += NW;
-      }
-      cp_async_commit();
-    };
+  int next = 0, end = 0;     // the warp's next tile to load, and the end of its segment
+  int32_t seen = -1;
+  auto peek = [&](int tile) { return LIST ? ld.peek_list(tile, lane) : ld.peek(tile, lane); };
+  auto issue = [&](bool look) {
+    if (next < end) {
+      const int32_t now = seen;
+      if (look && next + NW < end) seen = peek(next + NW);
+      if (LIST)
+        ld.load_list(next, now, my_ring + issued * S::kStage, lane);
+      else
+        ld.template load<false>(next, now, my_ring + issued * S::kStage, lane);
+      issued = issued + 1 == NST ? 0 : issued + 1;
+      next += NW;
+    }
+    cp_async_commit();
+  };
+  // The segment at rg: its queries and first tiles on their way.
+  struct Seg {
+    int u, b, g, r0, rows, n_tiles, t0, t1, L, count;
+  };
+  auto begin = [&]() {
+    Seg s;
+    s.u = rg.u, s.b = s.u / (a.kv.h_kv * a.n_chunk), s.g = (s.u / a.n_chunk) % a.kv.h_kv, s.r0 = (s.u % a.n_chunk) * ROWS;
+    s.rows = min(ROWS, a.R - s.r0);
+    s.n_tiles = kv4_tiles<LIST>(a, s.u);
+    s.t0 = rg.off, s.t1 = s.t0 + (int)min((int64_t)(s.n_tiles - rg.off), rg.x1 - rg.x);
+    s.L = min(max(a.kv.seq_lens[s.b], 0), a.kv.max_seq_len);
+    s.count = LIST ? min(max(a.cnt[s.u], 0), a.k_max) : s.L;
+    ld.unit(s.b, s.g, s.L, s.count, LIST ? a.idx + (int64_t)s.u * a.k_max : nullptr);
+    qs.fetch(a, s.b, s.g, s.r0, s.rows);
+    next = s.t0 + warp, end = s.t1;
+    // The first tiles' pages at once, then their loads.
+    int32_t first[NST];
+#pragma unroll
+    for (int k = 0; k < NST; ++k) first[k] = next + k * NW < end ? peek(next + k * NW) : -1;
 #pragma unroll 1
-    for (int s = 0; s < NST; ++s) issue();
+    for (int k = 0; k < NST; ++k) {
+      seen = first[0];
+#pragma unroll
+      for (int j = 0; j + 1 < NST; ++j) first[j] = first[j + 1];
+      issue(k + 1 == NST);
+    }
+    return s;
+  };
+
+  Seg sg = begin();
+  for (;;) {
+    const int b = sg.b, g = sg.g, r0 = sg.r0, rows = sg.rows, n_tiles = sg.n_tiles, seg0 = sg.t0, seg1 = sg.t1, L = sg.L, count = sg.count;
+    const int64_t seg_x = rg.x, ua = rg.x - rg.off;  // the unit's tiles are ua .. ua + n_tiles - 1 of all
     qs.store(a, qf, s_sl);
     __syncthreads();
     float sl[NT][2], m[NT][2], l[NT][2], o[MT][NT][4];
@@ -593,11 +704,14 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
       }
       __syncwarp();
       used = used + 1 == NST ? 0 : used + 1;
-      issue();
+      issue(true);
     }
-    if (rg.x + (seg1 - seg0) >= rg.x1) pdl_trigger();
+    rg.x += seg1 - seg0, rg.u = sg.u + 1, rg.off = 0;
+    const bool more = rg.x < rg.x1;
+    if (!more) pdl_trigger();
+    if (AHEAD && more) sg = begin();
 
-    // Sums of the lanes of a query row, then of the warps: the ring is free now and takes their O.
+    // Sums of the lanes of a query row, then of the warps.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -608,7 +722,6 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
       }
     __syncthreads();
     const int nw = min(NW, seg1 - seg0);           // warps that had a tile
-    float *acc = reinterpret_cast<float *>(ring);  // [warp][row][d], 16-byte pieces of a row permuted
     if (warp < nw) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -626,10 +739,13 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
         }
     }
     __syncthreads();
-    const int64_t ua = rg.x - rg.off;  // the unit's tiles are ua .. ua + n_tiles - 1 of all
     const int blk0 = (int)(ua / rg.per), blk1 = (int)((ua + n_tiles - 1) / rg.per);
     const bool whole = blk0 == blk1;
-    const int64_t slot = (int64_t)blockIdx.x * 2 + (rg.x == rg.per * blockIdx.x ? 0 : 1);
+    const int64_t slot = (int64_t)blockIdx.x * 2 + (seg_x == rg.per * blockIdx.x ? 0 : 1);
+    auto row_of = [&](int q) {
+      const int rr = r0 + q;
+      return ((int64_t)b * a.n_c + rr / a.G) * a.h_q + g * a.G + rr % a.G;
+    };
     for (int e = tid; e < rows * PIECES; e += NW * 32) {
       const int q = e / PIECES, piece = e % PIECES, rr = piece / (MT / 2);
       float M = -1e30f, Z = 0.f;
@@ -641,8 +757,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
         v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
       }
       if (whole) {
-        const int gr_row = r0 + q;
-        const int64_t row = ((int64_t)b * a.n_c + gr_row / a.G) * a.h_q + g * a.G + gr_row % a.G;
+        const int64_t row = row_of(q);
         const float f = Z == 0.f ? 0.f : a.v_scale / Z;
         kv4_write4(a, row * D + piece * 4, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
         if (piece == 0 && a.lse) a.lse[row] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
@@ -652,62 +767,24 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
       }
     }
     if (!whole) {
-      // The last block of the unit to arrive joins the partial results, in the blocks' order.
-      __threadfence();
+      // The last block of the unit to arrive joins the partial results.
       __syncthreads();
       if (tid == 0) {
-        const unsigned n = (unsigned)(blk1 - blk0 + 1);
-        const unsigned old = atomicAdd(a.counters + blk0, 1u);
-        s_last = old == n - 1;
+        s_last = kv4_arrive(a.counters + blk0) == (unsigned)(blk1 - blk0);
         if (s_last) a.counters[blk0] = 0;
       }
       __syncthreads();
       if (s_last) {
-        __threadfence();
-        const int n = blk1 - blk0 + 1;
         // Only the first block can hold the unit's start behind another unit's tiles.
         const int64_t slot0 = (int64_t)blk0 * 2 + (ua == rg.per * blk0 ? 0 : 1);
-        const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
-        auto part = [&](int k) { return (k ? (int64_t)(blk0 + k) * 2 : slot0) * ROWS; };
-        // A warp per row: the largest reference, the sum, and what they make of the output and lse.
-        for (int q = warp; q < rows; q += NW) {
-          float M = -1e30f, Z = 0.f;
-          for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(ml + part(k) + q).x);
-          M = warp_max(M);
-          for (int k = lane; k < n; k += 32) {
-            const float2 w = __ldcg(ml + part(k) + q);
-            Z += w.y * fast_exp2(w.x - M);
-          }
-          Z = warp_sum(Z);
-          if (lane == 0) {
-            s_m[q] = M;
-            s_l[q] = Z == 0.f ? 0.f : a.v_scale / Z;
-            s_sl[q] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
-          }
-        }
-        __syncthreads();
-        for (int e = tid; e < rows * (D / 4); e += NW * 32) {
-          const int q = e / (D / 4), piece = e % (D / 4);
-          const float M = s_m[q];
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int k = 0; k < n; ++k) {
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o) + (part(k) + q) * (D / 4) + piece);
-            const float f = fast_exp2(__ldcg(ml + part(k) + q).x - M);
-            v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
-          }
-          const int gr_row = r0 + q;
-          const int64_t row = ((int64_t)b * a.n_c + gr_row / a.G) * a.h_q + g * a.G + gr_row % a.G;
-          const float f = s_l[q];
-          kv4_write4(a, row * D + piece * 4, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-          if (piece == 0 && a.lse) a.lse[row] = s_sl[q];
-        }
+        kv4_join<D, NW * 32>(
+            a, blk1 - blk0 + 1, rows, tid, s_join, s_join + ROWS, s_join + 2 * ROWS,
+            [&](int k) { return (k ? (int64_t)(blk0 + k) * 2 : slot0) * ROWS; }, row_of, [] { __syncthreads(); });
       }
     }
+    if (!more) break;
     __syncthreads();
-    rg.x += seg1 - seg0;
-    rg.u = u + 1;
-    rg.off = 0;
+    if (!AHEAD) sg = begin();
   }
 }
 
@@ -842,14 +919,14 @@ template <int NT>
 struct Kv4Tune {
   static constexpr int kWarps = 8;
   static constexpr int kBlocks = NT == 1 ? 2 : 1;
-  static constexpr int kStages = NT <= 2 ? 3 : 4;
+  static constexpr int kStages = NT == 1 ? 2 : NT == 2 ? 3 : 4;
 };
 constexpr int kKv4CritWarps = 8, kKv4CritBlocks = 2, kKv4CritStages = 4;
 
 template <int D, int NT, int QS, int PS, bool LIST>
 int kv4_launch_attn(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
   constexpr int NST = Kv4Tune<NT>::kStages, BPS = Kv4Tune<NT>::kBlocks, NW = Kv4Tune<NT>::kWarps;
-  static_assert(NST * Kv4Smem<D>::kStage >= NT * 8 * D * 4, "the ring holds the warps' O");
+  static_assert(kv4_ahead(NT) || NST * Kv4Smem<D>::kStage >= NT * 8 * D * 4, "the ring holds the warps' O");
   constexpr int smem = kv4_smem_bytes<D, NT, QS, NW, NST>();
   constexpr auto kernel = kv4_attn_kernel<D, NT, QS, PS, NW, NST, BPS, LIST>;
   int rc = ensure_smem<kernel>(smem);

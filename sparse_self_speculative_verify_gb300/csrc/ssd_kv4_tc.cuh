@@ -644,51 +644,18 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
       tc_fence_before();
       arrive(b_lfree);
       if (!whole) {
-        // The last block of the unit to arrive joins the partial results, in the blocks' order.
-        __threadfence();
+        // The last block of the unit to arrive joins the partial results.
         named_sync(2, 128);
         if (tw == 0) {
-          const unsigned parts = (unsigned)(blk1 - blk0 + 1);
-          const unsigned old = atomicAdd(a.counters + blk0, 1u);
-          s_last = old == parts - 1;
+          s_last = kv4_arrive(a.counters + blk0) == (unsigned)(blk1 - blk0);
           if (s_last) a.counters[blk0] = 0;
         }
         named_sync(2, 128);
         if (s_last) {
-          __threadfence();
-          const int parts = blk1 - blk0 + 1;
           const int64_t slot0 = (int64_t)blk0 * 2 + (ua == rg.per * blk0 ? 0 : 1);
-          const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
-          auto part = [&](int k) { return (k ? (int64_t)(blk0 + k) * 2 : slot0) * NP; };
-          for (int q = w; q < s.rows; q += 4) {
-            float M = -1e30f, Z = 0.f;
-            for (int k = lane; k < parts; k += 32) M = fmaxf(M, __ldcg(ml + part(k) + q).x);
-            M = warp_max(M);
-            for (int k = lane; k < parts; k += 32) {
-              const float2 v = __ldcg(ml + part(k) + q);
-              Z += v.y * fast_exp2(v.x - M);
-            }
-            Z = warp_sum(Z);
-            if (lane == 0) {
-              s_jm[q] = M;
-              s_jf[q] = Z == 0.f ? 0.f : a.v_scale / Z;
-              s_jl[q] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
-            }
-          }
-          named_sync(2, 128);
-          for (int e = tw; e < s.rows * 32; e += 128) {
-            const int q = e / 32, piece = e % 32;
-            const float M = s_jm[q], f = s_jf[q];
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int k = 0; k < parts; ++k) {
-              const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o) + (part(k) + q) * 32 + piece);
-              const float c = fast_exp2(__ldcg(ml + part(k) + q).x - M);
-              v.x = fmaf(y.x, c, v.x), v.y = fmaf(y.y, c, v.y), v.z = fmaf(y.z, c, v.z), v.w = fmaf(y.w, c, v.w);
-            }
-            kv4_write4(a, row_of(q) * 128 + piece * 4, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-            if (piece == 0 && a.lse) a.lse[row_of(q)] = s_jl[q];
-          }
+          kv4_join<128, 128>(
+              a, blk1 - blk0 + 1, s.rows, tw, s_jm, s_jf, s_jl, [&](int k) { return (k ? (int64_t)(blk0 + k) * 2 : slot0) * NP; }, row_of,
+              [] { named_sync(2, 128); });
         }
         named_sync(2, 128);
       }
