@@ -206,6 +206,9 @@ class KVCache:
         return cls(w.pool, w.page_table, w.seq_lens, w.max_seq_len)
 
 
+COUNTER_BYTES = 1 << 18  # the counter area at a workspace's start
+
+
 class Workspace:
     """Zero-initialised device scratch buffers, grown on demand, one per (device, name).  The
     library keeps its counters in a fixed area at the start of a workspace and returns them to zero
@@ -693,12 +696,13 @@ def _is_kv4(kv):
 def _stream_ws(device, name: str, nbytes: int, workspace: Optional[Workspace]):
     """Workspace of a call on the current stream: the caller's, or one kept for (device, stream), so that
     calls on different streams never share one; a call under stream capture without a workspace takes a
-    zero-filled buffer of its graph's own memory.  A caller's workspace is sized before a capture that uses
+    buffer of its graph's own memory, whose counters a node of the graph clears.  A caller's workspace is sized before a capture that uses
     it and must outlive the graph."""
     if workspace is not None:
         return _ws(device, name, nbytes, workspace)
     if torch.cuda.is_current_stream_capturing():
-        buf = torch.zeros(int(nbytes) + 256, dtype=torch.uint8, device=device)
+        buf = torch.empty(int(nbytes) + 256, dtype=torch.uint8, device=device)
+        buf[:COUNTER_BYTES + 256].zero_()
         return ctypes.c_void_p(Workspace.aligned(buf)), int(nbytes)
     return _ws(device, (name, _raw_stream(device)), nbytes, None)
 

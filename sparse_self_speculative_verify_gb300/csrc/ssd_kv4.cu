@@ -96,13 +96,7 @@ static int kv4_prepare(const Kv4Call &c, int max_tokens, Kv4AttnArgs *a, Kv4Layo
   return SSD_OK;
 }
 
-static int kv4_grid(Kv4AttnArgs *a, int64_t units, int max_tokens, int tile, int most, int blocks_per_sm) {
-  // Short units (at most `most` loads of `tile` tokens) go to blocks whole, see kv4_range.
-  a->whole_units = cdiv(max_tokens, tile) <= most;
-  if (a->whole_units) {
-    const int64_t dev = (int64_t)sm_count() * blocks_per_sm;
-    return (int)(units < dev ? units : dev);
-  }
+static int kv4_grid(int64_t units, int max_tokens, int tile, int blocks_per_sm) {
   const int64_t bound = kv4_grid_bound(units, cdiv(max_tokens, tile) * tile, tile), dev = (int64_t)sm_count() * blocks_per_sm;
   return (int)(bound < dev ? bound : dev);
 }
@@ -137,11 +131,11 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
   // d = 128 runs on tcgen05 from 9 rows on; at d = 64 V^T would fill half the rows of its M = 128.
   const int nt = kv4_nt(a.R);
   if (kv->d == 128 && a.R <= 8)
-    rc = kv4_dense_d128(a, kv4_grid(&a, a.n_units, kv->max_seq_len, kKv4Tile * 4, 8, kv4_blocks_per_sm(nt)), st);
+    rc = kv4_dense_d128(a, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(nt)), st);
   else if (kv->d == 128)
-    rc = kv4_tc_attn(a, a.R > 32 ? 32 : a.R, kv4_grid(&a, a.n_units, kv->max_seq_len, kKv4TcTile, 4, 2), st);
+    rc = kv4_tc_attn(a, a.R > 32 ? 32 : a.R, kv4_grid(a.n_units, kv->max_seq_len, kKv4TcTile, 2), st);
   else
-    rc = kv4_dense_d64(a, nt, kv4_grid(&a, a.n_units, kv->max_seq_len, kKv4Tile * 4, 8, kv4_blocks_per_sm(nt)), st);
+    rc = kv4_dense_d64(a, nt, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(nt)), st);
   if (rc || !scores) return rc;
   a.lse_in = a.lse;
   a.scores = scores;
@@ -149,8 +143,8 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
   a.n_chunk = 1;
   a.n_units = kv->batch * kv->h_kv;
   if (kv->d == 128)
-    return kv4_tc_crit(a, kv4_grid(&a, a.n_units, kv->max_seq_len, kKv4TcTile, 0, kKv4CritTcBlocks), st);
-  return kv4_crit_d64(a, nt, kv4_grid(&a, a.n_units, kv->max_seq_len, kKv4Tile * 4, 0, kKv4CritBlocks), st);
+    return kv4_tc_crit(a, kv4_grid(a.n_units, kv->max_seq_len, kKv4TcTile, kKv4CritTcBlocks), st);
+  return kv4_crit_d64(a, nt, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kKv4CritBlocks), st);
 }
 
 extern "C" size_t ssd_kv4_draft_workspace_bytes(const ssd_paged_kv *kv, int h_q, int k_max) {
@@ -173,6 +167,6 @@ extern "C" int ssd_kv4_draft_attn(const ssd_paged_kv *kv, const void *q, int q_d
   if (!(a.status = device_status())) return SSD_ERR_CUDA;
   a.idx = idx, a.cnt = cnt, a.k_max = k_max;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int nt = kv4_nt(a.R), grid = kv4_grid(&a, a.n_units, k_max, kKv4Tile * 4, 8, kv4_blocks_per_sm(nt));
+  const int nt = kv4_nt(a.R), grid = kv4_grid(a.n_units, k_max, kKv4Tile * 4, kv4_blocks_per_sm(nt));
   return kv->d == 128 ? kv4_list_d128(a, nt, grid, st) : kv4_list_d64(a, nt, grid, st);
 }

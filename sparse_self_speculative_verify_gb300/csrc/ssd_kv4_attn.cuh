@@ -56,7 +56,6 @@ struct Kv4AttnArgs {
   int64_t scores_stride;
   const float *lse_in;    // criticality pass
   int n_units;            // batch * h_kv * n_chunk
-  int whole_units;        // blocks take whole units (short ones: see kv4_range)
   unsigned *status;
 };
 
@@ -105,27 +104,41 @@ __device__ __forceinline__ int kv4_tiles(const Kv4AttnArgs &a, int u) {
   return n > 0 ? cdiv(n, TILE) : 1;
 }
 
-// Position of this block in the list of all units' tiles: the tiles are dealt out in equal contiguous ranges,
-// whatever the lengths.  Short units (up to four tiles a warp) are dealt out whole instead: a part of one costs
-// more to join (about 4 us) than to compute.  Returns false when the block has none.
+// Dealing out the units' tiles to blocks.  All units stand in one line, each with a lead before its own tiles:
+// about what starting, merging and writing a unit costs, in tiles.  Blocks take equal contiguous stretches of the
+// line.  A boundary inside a lead, or at most `snap` tiles from a unit's start or end, moves there: a unit cut in
+// two costs a join as well.  (Without leads, a block whose stretch held many short units ran twice as long as the
+// others: 128 requests of 1 to 2048 tokens, 8 heads of 128, one query row a head: 143 us against 85 with them; the
+// same with 5 candidates: 292 against 148.)
+template <int TILE>
+constexpr int kKv4Lead = TILE == kKv4Tile ? 16 : 6;  // 4 us of a block's time
+template <int TILE>
+__device__ __forceinline__ int64_t kv4_snap(int64_t per) {
+  return TILE == kKv4Tile ? min(max(per / 4, (int64_t)4), (int64_t)20) : 0;  // tcgen05's tiles are 128 tokens
+}
 struct Kv4Range {
-  int64_t x, x1, per;  // next tile, end, tiles per block
-  int u, off;          // unit and tile inside it of x
+  int64_t x, x1, per, snap;  // place of the unit u in the line, the block's end, a stretch's length
+  int u, off;                // next unit, and its first tile of this block
 };
-template <bool LIST, int NW, int TILE = kKv4Tile, int MIN = NW>
-__device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int64_t *s_scan /* [NW + 2] */) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (a.whole_units) {
-    const int units = cdiv(a.n_units, (int)gridDim.x);
-    r.u = (int)blockIdx.x * units, r.off = 0;
-    r.x = r.x1 = 0, r.per = (int64_t)1 << 40;  // more than there are tiles
-    for (int u = r.u; u < min(a.n_units, r.u + units); ++u) r.x1 += kv4_tiles<LIST, TILE>(a, u);
-    return r.x1 > 0;
+// Blocks that hold parts of the unit of n tiles at place x: `first` and `more` blocks after it.  The unit's start
+// is stored in the first one's second slot, other parts in their block's first one.
+struct Kv4Parts {
+  int first, more;
+  __device__ __forceinline__ Kv4Parts(const Kv4Range &r, int64_t x, int lead, int n) {
+    first = (int)((x + lead + r.snap) / r.per);
+    more = max(0, (int)((x + lead + n - r.snap + r.per - 1) / r.per) - 1 - first);
   }
+  __device__ __forceinline__ int64_t slot(int k) const { return k ? (int64_t)(first + k) * 2 : (int64_t)first * 2 + 1; }
+};
+// Returns false when the block has no tile.
+template <bool LIST, int NW, int TILE = kKv4Tile, int MIN = NW>
+__device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int64_t *s_scan /* [NW + 4] */) {
+  constexpr int LEAD = kKv4Lead<TILE>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per_thread = cdiv(a.n_units, NW * 32);
   const int u0 = min(a.n_units, tid * per_thread), u1 = min(a.n_units, u0 + per_thread);
   int64_t sum = 0;
-  for (int u = u0; u < u1; ++u) sum += kv4_tiles<LIST, TILE>(a, u);
+  for (int u = u0; u < u1; ++u) sum += kv4_tiles<LIST, TILE>(a, u) + LEAD;
   int64_t inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -143,24 +156,40 @@ __device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int
   }
   int64_t per = (total + gridDim.x - 1) / gridDim.x;
   if (per < MIN) per = MIN;  // MIN = NW: a tile for every warp before another block is used
-  const int64_t x0 = per * blockIdx.x;
-  if (x0 >= total) return false;
+  r.per = per, r.snap = kv4_snap<TILE>(per);
   const int64_t excl = base + inc - sum;
-  if (x0 >= excl && x0 < excl + sum) {
-    int64_t e = excl;
-    int u = u0;
-    for (;; ++u) {
-      const int n = kv4_tiles<LIST, TILE>(a, u);
-      if (x0 < e + n) break;
-      e += n;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t y = per * ((int64_t)blockIdx.x + k);
+    if (y >= total && tid == 0) s_scan[NW + 2 * k] = total;
+    if (y >= excl && y < excl + sum) {
+      int64_t e = excl;
+      int u = u0, n;
+      for (;; ++u) {
+        n = kv4_tiles<LIST, TILE>(a, u) + LEAD;
+        if (y < e + n) break;
+        e += n;
+      }
+      const bool down = y - e <= LEAD + r.snap, up = !down && e + n - y <= r.snap;
+      s_scan[NW + 2 * k] = down ? e : up ? e + n : y;
+      if (k == 0) s_scan[NW + 1] = (int64_t)(u + up) << 32 | (uint32_t)(down || up ? 0 : (int)(y - e) - LEAD);
     }
-    s_scan[NW] = u;
-    s_scan[NW + 1] = x0 - e;
   }
   __syncthreads();
-  r.x = x0, r.x1 = min(total, x0 + per), r.per = per;
-  r.u = (int)s_scan[NW], r.off = (int)s_scan[NW + 1];
+  r.x = s_scan[NW], r.x1 = s_scan[NW + 2];
+  if (r.x >= r.x1) return false;
+  r.u = (int)(s_scan[NW + 1] >> 32), r.off = (int)(uint32_t)s_scan[NW + 1];
+  if (r.off) r.x -= r.off + LEAD;
   return true;
+}
+// End of the block's tiles of the unit at r, which has n; and the step to the next unit.
+template <int TILE = kKv4Tile>
+__device__ __forceinline__ int kv4_range_end(const Kv4Range &r, int n) {
+  return (int)min((int64_t)n, r.x1 - r.x - kKv4Lead<TILE>);
+}
+template <int TILE = kKv4Tile>
+__device__ __forceinline__ void kv4_range_next(Kv4Range &r, int n) {
+  r.x += n + kKv4Lead<TILE>, r.u += 1, r.off = 0;
 }
 
 // Loads of one warp's tiles into its ring, by 16-byte cp.async, one group per tile.  (A page's rows of one head
@@ -493,7 +522,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
   float *s_sl = reinterpret_cast<float *>(qf + ROWS * D * 2 * QS);
   float *s_m = s_sl + ROWS, *s_l = s_m + NW * ROWS;
   float *acc = reinterpret_cast<float *>(AHEAD ? ring + NW * NST * S::kStage : ring);  // [warp][row][d], pieces of a row permuted
-  __shared__ int64_t s_scan[NW + 2];
+  __shared__ int64_t s_scan[NW + 4];
   __shared__ int s_last;
   __shared__ float s_join[3 * ROWS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, col = lane & 3;
@@ -536,7 +565,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
     s.u = rg.u, s.b = s.u / (a.kv.h_kv * a.n_chunk), s.g = (s.u / a.n_chunk) % a.kv.h_kv, s.r0 = (s.u % a.n_chunk) * ROWS;
     s.rows = min(ROWS, a.R - s.r0);
     s.n_tiles = kv4_tiles<LIST>(a, s.u);
-    s.t0 = rg.off, s.t1 = s.t0 + (int)min((int64_t)(s.n_tiles - rg.off), rg.x1 - rg.x);
+    s.t0 = rg.off, s.t1 = kv4_range_end(rg, s.n_tiles);
     s.L = min(max(a.kv.seq_lens[s.b], 0), a.kv.max_seq_len);
     s.count = LIST ? min(max(a.cnt[s.u], 0), a.k_max) : s.L;
     ld.unit(s.b, s.g, s.L, s.count, LIST ? a.idx + (int64_t)s.u * a.k_max : nullptr);
@@ -559,7 +588,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
   Seg sg = begin();
   for (;;) {
     const int b = sg.b, g = sg.g, r0 = sg.r0, rows = sg.rows, n_tiles = sg.n_tiles, seg0 = sg.t0, seg1 = sg.t1, L = sg.L, count = sg.count;
-    const int64_t seg_x = rg.x, ua = rg.x - rg.off;  // the unit's tiles are ua .. ua + n_tiles - 1 of all
+    const int64_t place = rg.x;
     qs.store(a, qf, s_sl);
     __syncthreads();
     float sl[NT][2], m[NT][2], l[NT][2], o[MT][NT][4];
@@ -706,7 +735,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
       used = used + 1 == NST ? 0 : used + 1;
       issue(true);
     }
-    rg.x += seg1 - seg0, rg.u = sg.u + 1, rg.off = 0;
+    kv4_range_next(rg, n_tiles);
     const bool more = rg.x < rg.x1;
     if (!more) pdl_trigger();
     if (AHEAD && more) sg = begin();
@@ -739,9 +768,9 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
         }
     }
     __syncthreads();
-    const int blk0 = (int)(ua / rg.per), blk1 = (int)((ua + n_tiles - 1) / rg.per);
-    const bool whole = blk0 == blk1;
-    const int64_t slot = (int64_t)blockIdx.x * 2 + (seg_x == rg.per * blockIdx.x ? 0 : 1);
+    const Kv4Parts parts(rg, place, kKv4Lead<kKv4Tile>, n_tiles);
+    const bool whole = parts.more == 0;
+    const int64_t slot = parts.slot((int)blockIdx.x - parts.first);
     auto row_of = [&](int q) {
       const int rr = r0 + q;
       return ((int64_t)b * a.n_c + rr / a.G) * a.h_q + g * a.G + rr % a.G;
@@ -770,17 +799,14 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
       // The last block of the unit to arrive joins the partial results.
       __syncthreads();
       if (tid == 0) {
-        s_last = kv4_arrive(a.counters + blk0) == (unsigned)(blk1 - blk0);
-        if (s_last) a.counters[blk0] = 0;
+        s_last = kv4_arrive(a.counters + parts.first) == (unsigned)parts.more;
+        if (s_last) a.counters[parts.first] = 0;
       }
       __syncthreads();
-      if (s_last) {
-        // Only the first block can hold the unit's start behind another unit's tiles.
-        const int64_t slot0 = (int64_t)blk0 * 2 + (ua == rg.per * blk0 ? 0 : 1);
+      if (s_last)
         kv4_join<D, NW * 32>(
-            a, blk1 - blk0 + 1, rows, tid, s_join, s_join + ROWS, s_join + 2 * ROWS,
-            [&](int k) { return (k ? (int64_t)(blk0 + k) * 2 : slot0) * ROWS; }, row_of, [] { __syncthreads(); });
-      }
+            a, parts.more + 1, rows, tid, s_join, s_join + ROWS, s_join + 2 * ROWS,
+            [&](int k) { return parts.slot(k) * ROWS; }, row_of, [] { __syncthreads(); });
     }
     if (!more) break;
     __syncthreads();
@@ -800,7 +826,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
   char *qf = ring + NW * NST * S::kCritStage;
   float *s_sl = reinterpret_cast<float *>(qf + 2 * ROWS * D * 2 * QS);  // two chunks of rows at most
   float *s_lse = s_sl + 2 * ROWS;
-  __shared__ int64_t s_scan[NW + 2];
+  __shared__ int64_t s_scan[NW + 4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, col = lane & 3;
   // Everything but lse was written before the attention kernel ran, which waited for it and only then let
   // this one start; lse is waited for below.
@@ -817,7 +843,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
   while (rg.x < rg.x1) {
     const int u = rg.u, b = u / a.kv.h_kv, g = u % a.kv.h_kv;
     const int n_tiles = kv4_tiles<false>(a, u);
-    const int seg0 = rg.off, seg1 = seg0 + (int)min((int64_t)(n_tiles - rg.off), rg.x1 - rg.x);
+    const int seg0 = rg.off, seg1 = kv4_range_end(rg, n_tiles);
     const int L = min(max(a.kv.seq_lens[b], 0), a.kv.max_seq_len);
     ld.unit(b, g, L, L, nullptr);
     int next = seg0 + warp;
@@ -900,9 +926,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
       issue();
     }
     __syncthreads();
-    rg.x += seg1 - seg0;
-    rg.u = u + 1;
-    rg.off = 0;
+    kv4_range_next(rg, n_tiles);
   }
 }
 

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
   const uint32_t bars = smem_u32(s_red + 4 * NP);
   const uint32_t b_raw = bars, b_free = bars + 8 * C::kStages, b_k = b_free + 8 * C::kStages, b_s = b_k + 8, b_v = b_s + 8, b_p = b_v + 16,
                  b_pv = b_p + 8, b_l = b_pv + 8, b_lfree = b_l + 8, b_drain = b_lfree + 8;
-  __shared__ int64_t s_scan[kKv4TcWarps + 2];
+  __shared__ int64_t s_scan[kKv4TcWarps + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -328,11 +328,11 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
     s.b = rg.u / (a.kv.h_kv * a.n_chunk), s.g = (rg.u / a.n_chunk) % a.kv.h_kv, s.r0 = (rg.u % a.n_chunk) * 2 * CW;
     s.rows = min(2 * CW, a.R - s.r0);
     s.n_tiles = kv4_tiles<false, kKv4TcTile>(a, rg.u);
-    s.t0 = rg.off, s.t1 = rg.off + (int)min((int64_t)(s.n_tiles - rg.off), rg.x1 - rg.x);
+    s.t0 = rg.off, s.t1 = kv4_range_end<kKv4TcTile>(rg, s.n_tiles);
     s.L = min(max(a.kv.seq_lens[s.b], 0), a.kv.max_seq_len);
     return s;
   };
-  auto advance = [&](const Seg &s) { rg.x += s.t1 - s.t0, rg.u += 1, rg.off = 0; };
+  auto advance = [&](const Seg &s) { kv4_range_next<kKv4TcTile>(rg, s.n_tiles); };
   uint32_t n = 0;  // tiles so far
   if (!mine) rg.x = rg.x1 = 0;
 
@@ -602,10 +602,9 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
       wait(b_l, seg);
       tc_fence_after();
       const int d = 32 * w + 4 * (lane & 7) + 2 * (lane >> 4) + ((lane >> 3) & 1);
-      const int64_t ua = rg.x - rg.off;
-      const int blk0 = (int)(ua / rg.per), blk1 = (int)((ua + s.n_tiles - 1) / rg.per);
-      const bool whole = blk0 == blk1;
-      const int64_t slot = (int64_t)blockIdx.x * 2 + (rg.x == rg.per * blockIdx.x ? 0 : 1);
+      const Kv4Parts parts(rg, rg.x, kKv4Lead<kKv4TcTile>, s.n_tiles);
+      const bool whole = parts.more == 0;
+      const int64_t slot = parts.slot((int)blockIdx.x - parts.first);
       auto column = [&](int q) { return q / CW * H + q % CW; };  // of the pass's row q
       auto row_of = [&](int q) {
         const int rr = s.r0 + q;
@@ -647,16 +646,14 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
         // The last block of the unit to arrive joins the partial results.
         named_sync(2, 128);
         if (tw == 0) {
-          s_last = kv4_arrive(a.counters + blk0) == (unsigned)(blk1 - blk0);
-          if (s_last) a.counters[blk0] = 0;
+          s_last = kv4_arrive(a.counters + parts.first) == (unsigned)parts.more;
+          if (s_last) a.counters[parts.first] = 0;
         }
         named_sync(2, 128);
-        if (s_last) {
-          const int64_t slot0 = (int64_t)blk0 * 2 + (ua == rg.per * blk0 ? 0 : 1);
+        if (s_last)
           kv4_join<128, 128>(
-              a, blk1 - blk0 + 1, s.rows, tw, s_jm, s_jf, s_jl, [&](int k) { return (k ? (int64_t)(blk0 + k) * 2 : slot0) * NP; }, row_of,
+              a, parts.more + 1, s.rows, tw, s_jm, s_jf, s_jl, [&](int k) { return parts.slot(k) * NP; }, row_of,
               [] { named_sync(2, 128); });
-        }
         named_sync(2, 128);
       }
       advance(s);
@@ -701,7 +698,7 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
   float *s_sl = reinterpret_cast<float *>(sm + C::kMisc), *s_lse = s_sl + NP;
   const uint32_t bars = smem_u32(s_lse + NP);
   const uint32_t b_raw = bars, b_free = bars + 8 * kKv4CritTcStages, b_k = b_free + 8 * kKv4CritTcStages, b_s = b_k + 8, b_drain = b_s + 16;
-  __shared__ int64_t s_scan[kKv4CritTcWarps + 2];
+  __shared__ int64_t s_scan[kKv4CritTcWarps + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -728,10 +725,10 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
   };
   uint32_t n = 0;
   if (!mine) rg.x = rg.x1 = 0;
-  auto seg_end = [&](int n_tiles) { return rg.off + (int)min((int64_t)(n_tiles - rg.off), rg.x1 - rg.x); };
   if (warp == 5) {
     for (; rg.x < rg.x1;) {
-      const int b = rg.u / a.kv.h_kv, g = rg.u % a.kv.h_kv, t1 = seg_end(kv4_tiles<false, kKv4TcTile>(a, rg.u));
+      const int b = rg.u / a.kv.h_kv, g = rg.u % a.kv.h_kv, n_tiles = kv4_tiles<false, kKv4TcTile>(a, rg.u);
+      const int t1 = kv4_range_end<kKv4TcTile>(rg, n_tiles);
       const int L = min(max(a.kv.seq_lens[b], 0), a.kv.max_seq_len);
       const char *head = static_cast<const char *>(a.kv.pool) + (uint32_t)g * a.kv.page_size * 72;
       const int32_t *table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
@@ -744,14 +741,19 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
         kv4_raw_load<false>(a, head, now, t0, L - t0, sbase + st * C::kStage, lane);
         cp_async_arrive(b_raw + 8 * st);
       }
-      rg.x += t1 - rg.off, rg.u += 1, rg.off = 0;
+      kv4_range_next<kKv4TcTile>(rg, n_tiles);
     }
     cp_async_commit();
     cp_async_wait<0>();
   } else if (warp == 4) {
     const uint32_t id_qk = idesc_f16_f32(128, NP, 0), tmu = __shfl_sync(0xffffffffu, tm, 0);
     const uint64_t qd = smem_desc(sbase + C::kQ, 16, 1024);
-    const int64_t total = rg.x1 - rg.x;
+    uint32_t total = 0;
+    while (rg.x < rg.x1) {
+      const int n_tiles = kv4_tiles<false, kKv4TcTile>(a, rg.u);
+      total += kv4_range_end<kKv4TcTile>(rg, n_tiles) - rg.off;
+      kv4_range_next<kKv4TcTile>(rg, n_tiles);
+    }
     for (; n < total; ++n) {
       wait(b_k, n);
       tc_fence_after();
@@ -784,7 +786,8 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
       if (lane == 0) mbar_arrive(b_k), mbar_arrive(b_free + 8 * st);
     };
     for (; rg.x < rg.x1;) {
-      const int b = rg.u / a.kv.h_kv, g = rg.u % a.kv.h_kv, t1 = seg_end(kv4_tiles<false, kKv4TcTile>(a, rg.u));
+      const int b = rg.u / a.kv.h_kv, g = rg.u % a.kv.h_kv, n_tiles = kv4_tiles<false, kKv4TcTile>(a, rg.u);
+      const int t1 = kv4_range_end<kKv4TcTile>(rg, n_tiles);
       const int L = min(max(a.kv.seq_lens[b], 0), a.kv.max_seq_len);
       kv4_tc_stage_q<NP, QS, NP, NP>(a, b, g, 0, min(NP, a.R), sm + C::kQ, s_sl);
       fence_proxy_async_smem();
@@ -846,7 +849,7 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
         tc_fence_before();
       }
       named_sync(1, 128);
-      rg.x += t1 - rg.off, rg.u += 1, rg.off = 0;
+      kv4_range_next<kKv4TcTile>(rg, n_tiles);
     }
   }
   pdl_wait();
