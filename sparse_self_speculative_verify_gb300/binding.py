@@ -718,6 +718,8 @@ def ssd_kv4_append(kv: KV4Cache, k_new: torch.Tensor, v_new: torch.Tensor, count
     dt = _typed(k_new, "k_new", kv.device)
     _shaped(v_new, "v_new", k_new.dtype, kv.device, k_new.shape)
     _shaped(counts, "counts", torch.int32, kv.device, (kv.batch,))
+    if kv.batch == 0:
+        return
     with _scope(kv.device, stream):
         _check(_lib().ssd_kv4_append(kv.ref(), _ptr(k_new), _ptr(v_new), dt, k_new.shape[1], _ptr(counts),
                                      float(kv.k_scale), float(kv.v_scale), _raw_stream(kv.device)))
@@ -738,8 +740,9 @@ def ssd_kv4_read(kv: KV4Cache, first: torch.Tensor, n: int, counts: Optional[tor
             v = torch.empty(shape, dtype=k.dtype, device=dev)
         dt = _typed(k, "k", dev, shape)
         _shaped(v, "v", k.dtype, dev, shape)
-        _check(_lib().ssd_kv4_read(kv.ref(), _ptr(first), _ptr(counts), int(n), float(kv.k_scale), float(kv.v_scale), dt,
-                                   _ptr(k), _ptr(v), _raw_stream(dev)))
+        if kv.batch:  # (a tensor without elements has no address)
+            _check(_lib().ssd_kv4_read(kv.ref(), _ptr(first), _ptr(counts), int(n), float(kv.k_scale), float(kv.v_scale),
+                                       dt, _ptr(k), _ptr(v), _raw_stream(dev)))
     return k, v
 
 
@@ -765,6 +768,8 @@ def ssd_kv4_verify_attn(kv: KV4Cache, q: torch.Tensor, n_cand: int, scale: float
         _shaped(lse, "lse", torch.float32, dev, (B, nc, h_q))
         if scores is not None:
             _shaped(scores, "scores", torch.float32, dev, (B, kv.h_kv, scores.shape[-1] if scores.dim() else 0))
+        if B == 0:
+            return {"out": out, "lse": lse, "scores": scores}
         L = _lib()
         need = L.ssd_kv4_verify_workspace_bytes(kv.ref(), h_q, n_cand)
         wsp, avail = _stream_ws(dev, "kv4", need, workspace)
@@ -798,6 +803,8 @@ def ssd_kv4_draft_attn(kv: KV4Cache, q: torch.Tensor, idx: torch.Tensor, cnt: to
             lse = torch.empty((B, h_q), dtype=torch.float32, device=dev)
         ot = _typed(out, "out", dev, (B, h_q, d))
         _shaped(lse, "lse", torch.float32, dev, (B, h_q))
+        if B == 0:
+            return {"out": out, "lse": lse}
         L = _lib()
         need = L.ssd_kv4_draft_workspace_bytes(kv.ref(), h_q, k_max)
         wsp, avail = _stream_ws(dev, "kv4", need, workspace)
@@ -863,6 +870,8 @@ def ssd_kv_reserve(kv, pages: PagePool, counts: torch.Tensor, *, workspace: Opti
     copied.  All or nothing: with too few free pages the status reports FAULT_NOPAGE and nothing changes."""
     refs = _pages_of(kv, pages)
     _rows(counts, "counts", kv.device, kv.batch)
+    if kv.batch == 0:
+        return
     with _scope(kv.device, stream):
         L = _lib()
         wsp, avail = _stream_ws(kv.device, "pages", L.ssd_kv_reserve_workspace_bytes(kv.ref()), workspace)
@@ -874,6 +883,8 @@ def ssd_kv_release(kv, pages: PagePool, keep: torch.Tensor, stream=None) -> None
     length becomes min(length, keep[b])."""
     refs = _pages_of(kv, pages)
     _rows(keep, "keep", kv.device, kv.batch)
+    if kv.batch == 0:
+        return
     with _scope(kv.device, stream):
         _check(_lib().ssd_kv_release(kv.ref(), refs, _ptr(keep), _raw_stream(kv.device)))
 

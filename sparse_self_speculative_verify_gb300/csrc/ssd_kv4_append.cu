@@ -32,8 +32,8 @@ __device__ __forceinline__ void load32(const void *p, bool wide, uint4 &x, uint4
                  : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
                  : "l"(p));
   } else {
-    x = __ldg(static_cast<const uint4 *>(p));
-    y = __ldg(static_cast<const uint4 *>(p) + 1);
+    x = static_cast<const uint4 *>(p)[0];
+    y = static_cast<const uint4 *>(p)[1];
   }
 }
 __device__ __forceinline__ void store32(void *p, bool wide, const uint4 &x, const uint4 &y) {
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kKv4Threads, sizeof(T) == 2 ? 5 : 4) kv4_appen
   const int32_t *table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
   bool ok = true;
   for (int j = (L >> a.kv.log2_ps) + tid; j <= (L + n - 1) >> a.kv.log2_ps; j += kKv4Threads) {
-    const int32_t p = __ldg(table + j);
+    const int32_t p = table[j];
     ok &= p >= 0 && (int64_t)p < a.kv.num_pages;
   }
   if (!__syncthreads_and(ok)) {
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kKv4Threads, sizeof(T) == 2 ? 5 : 4) kv4_appen
     const unsigned jt = e / per_token, in = e - jt * per_token;
     const int g = in >> log2_gpr, c = in & ((1 << log2_gpr) - 1);
     const int t = L + j0 + (int)jt, slot = t & (a.kv.page_size - 1);
-    const int32_t p = __ldg(table + (t >> a.kv.log2_ps));
+    const int32_t p = table[t >> a.kv.log2_ps];
     char *blk = a.pool + ((int64_t)p * 2 * a.kv.h_kv + g) * block_bytes;
     char *to = blk + slot * cb + c * 8, *ts = blk + a.kv.page_size * cb + slot * sb + c;
     uint2 w;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4RowsArgs a) {
       if (e < total && (int)jt < live) {
         const int g = in >> log2_gpr, c = in & ((1 << log2_gpr) - 1);
         const int t = f0 + j0 + (int)jt, slot = t & (a.kv.page_size - 1);
-        const int32_t p = __ldg(table + (t >> a.kv.log2_ps));
+        const int32_t p = table[t >> a.kv.log2_ps];
         if (p < 0 || (int64_t)p >= a.kv.num_pages) {
           atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
         } else {

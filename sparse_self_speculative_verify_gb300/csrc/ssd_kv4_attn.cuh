@@ -227,7 +227,7 @@ struct Kv4Loader {
   // nothing uses them.
   __device__ __forceinline__ int32_t peek(int tile, int lane) const {
     const int at = tile * kKv4Tile + (lane << log2_cs);
-    return lane < (kKv4Tile >> log2_cs) && at < n ? __ldg(table + (at >> a.kv.log2_ps)) : 0;
+    return lane < (kKv4Tile >> log2_cs) && at < n ? table[at >> a.kv.log2_ps] : 0;
   }
   // The codes of G consecutive tokens of a page are G * kCb consecutive bytes.
   template <int G, bool K_ONLY>
@@ -281,7 +281,7 @@ struct Kv4Loader {
   // List tiles: each lane resolves one entry, then pieces of the rows go out.  An entry that is not there reads
   // as zeros.
   __device__ __forceinline__ int32_t peek_list(int tile, int lane) const {
-    return tile * kKv4Tile + lane < n ? __ldg(list + tile * kKv4Tile + lane) : -1;
+    return tile * kKv4Tile + lane < n ? list[tile * kKv4Tile + lane] : -1;
   }
   __device__ __forceinline__ void load_list(int tile, int32_t token, uint32_t dst, int lane) const {
     const char *row = nullptr, *scales = head;  // the entry's codes and scales in the head's K block
@@ -289,7 +289,7 @@ struct Kv4Loader {
       if (token < 0 || token >= L) {
         atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
       } else {
-        const int32_t p = __ldg(table + (token >> a.kv.log2_ps));
+        const int32_t p = table[token >> a.kv.log2_ps];
         if (in_pool(p)) {
           const int slot = token & (a.kv.page_size - 1);
           row = head + (uint64_t)(uint32_t)p * page_bytes + slot * S::kCb;
@@ -394,7 +394,7 @@ struct Kv4Queries {
         const int64_t off = (((int64_t)b * a.n_c + i) * a.h_q + h) * D + lane * V;
 #pragma unroll
         for (int k = 0; k < V; ++k)
-          xs[n][k] = QS == 2 ? __ldg(static_cast<const float *>(a.q) + off + k)
+          xs[n][k] = QS == 2 ? static_cast<const float *>(a.q)[off + k]
                              : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q)[off + k]);
       }
     }
@@ -527,14 +527,14 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
   __shared__ float s_join[3 * ROWS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, col = lane & 3;
   pdl_wait();
-  Kv4Range rg;
-  if (!kv4_range<LIST, NW>(a, rg, s_scan)) return;
   if (blockIdx.x == 0) {  // lengths out of range are clamped; say so once
     for (int b = tid; b < a.kv.batch; b += NW * 32) effective_len(a.kv, b, LIST ? 0 : a.n_c, a.status);
     if (LIST)
       for (int u = tid; u < a.n_units; u += NW * 32)
         if (a.cnt[u] < 0 || a.cnt[u] > a.k_max) atomicOr(a.status, (unsigned)SSD_FAULT_KMAX);
   }
+  Kv4Range rg;
+  if (!kv4_range<LIST, NW>(a, rg, s_scan)) return;
   const char *my_tiles = ring + warp * NST * S::kStage;
   const uint32_t my_ring = smem_u32(my_tiles);
   Kv4Loader<D> ld(a);

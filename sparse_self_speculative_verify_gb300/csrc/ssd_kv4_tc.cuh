@@ -153,7 +153,7 @@ __device__ __forceinline__ int kv4_raw_piece(int t, int c) { return (t >> 1) * 1
 // Page `lane` of the tile of tokens [t0, t0 + nv) (0 where it has none).
 __device__ __forceinline__ int32_t kv4_raw_peek(const Kv4AttnArgs &a, const int32_t *table, int t0, int nv, int lane) {
   const int log2_cs = min(a.kv.log2_ps, 7), at = lane << log2_cs;
-  return lane < (kKv4TcTile >> log2_cs) && at < nv ? __ldg(table + ((t0 + at) >> a.kv.log2_ps)) : 0;
+  return lane < (kKv4TcTile >> log2_cs) && at < nv ? table[(t0 + at) >> a.kv.log2_ps] : 0;
 }
 // That raw tile of head `head` (its K block of page 0).
 template <bool WITH_V>
@@ -243,10 +243,10 @@ __device__ __forceinline__ void kv4_tc_stage_q(const Kv4AttnArgs &a, int b, int 
         const int rr = r0 + row;
         const int64_t off = (((int64_t)b * a.n_c + rr / a.G) * a.h_q + g * a.G + rr % a.G) * 128 + lane * 4;
         if (QS == 2) {
-          const float4 v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + off));
+          const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + off);
           x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
         } else {
-          const uint2 v = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + off));
+          const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + off);
           x[k][0] = bf16_lo(v.x), x[k][1] = bf16_hi(v.x), x[k][2] = bf16_lo(v.y), x[k][3] = bf16_hi(v.y);
         }
       }

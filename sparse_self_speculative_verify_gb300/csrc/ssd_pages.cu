@@ -374,13 +374,13 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactArgs
     if (t < 0 || t >= L) {
       atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
     } else {
-      const int32_t p = __ldg(a.from.page_table + (int64_t)s * a.from.max_pages + (t >> a.from.log2_ps));
+      const int32_t p = a.from.page_table[(int64_t)s * a.from.max_pages + (t >> a.from.log2_ps)];
       if (p < 0 || (int64_t)p >= a.from.num_pages)
         atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
       else
         f = ((int64_t)p * 2 * h + g) * fb;
     }
-    const int32_t p = __ldg(a.to.page_table + (int64_t)d * a.to.max_pages + (j >> a.to.log2_ps));
+    const int32_t p = a.to.page_table[(int64_t)d * a.to.max_pages + (j >> a.to.log2_ps)];
     if (p < 0 || (int64_t)p >= a.to.num_pages || (a.to_refs && a.to_refs[p] != 1))
       atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
     else
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactArgs
       for (int k = 0; k < U; ++k) {
         const int e = e0 + k * kCompactThreads, c = e & ((1 << sh) - 1), which = (e >> sh) & 1, j = e >> (sh + 1);
         v[k] = V{};
-        if (e < total && s_from[j] >= 0) v[k] = __ldg(reinterpret_cast<const V *>(from + s_from[j] + (which ? fv : 0) + at_from + s_slots[j] * width) + c);
+        if (e < total && s_from[j] >= 0) v[k] = reinterpret_cast<const V *>(from + s_from[j] + (which ? fv : 0) + at_from + s_slots[j] * width)[c];
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {

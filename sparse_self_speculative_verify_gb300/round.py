@@ -6,13 +6,17 @@ SparseSpec ("Accelerating Large-Scale Reasoning Model Inference: Self-Speculativ
 Sparse Attention") §4.1: the sparse pattern is refreshed by every verify and stays fixed for the k
 drafts that follow it (the refresh stride equals k); §2.3 / §3.2: a round is k drafts plus one
 verify of the k+1 positions.
+
+The cache may be a 4-bit one (``KV4Cache``): the same round runs on ``ssd_kv4_verify_attn`` and
+``ssd_kv4_draft_attn``.  Its rows are read where they are (no row pack: four 72-byte rows fill what one
+packed bf16 row does), and ``verify_select`` is a verify followed by a select.
 """
 
 from __future__ import annotations
 
 import math
 from contextlib import nullcontext as _nullcontext
-from typing import Optional
+from typing import Optional, Union
 
 import torch
 
@@ -20,9 +24,12 @@ from . import binding as B
 
 
 class SpecRound:
-    def __init__(self, kv: B.KVCache, h_q: int, n_cand: int, k_max: int, scale: Optional[float] = None,
+    def __init__(self, kv: Union[B.KVCache, B.KV4Cache], h_q: int, n_cand: int, k_max: int, scale: Optional[float] = None,
                  workspace: Optional[B.Workspace] = None, pack_rows: bool = True, pack_in_select: bool = False):
         self.kv = kv
+        self._nvfp4 = isinstance(kv, B.KV4Cache)
+        if self._nvfp4 and pack_in_select:
+            raise ValueError("a 4-bit cache has no row pack")
         self.h_q = h_q
         self.n_cand = n_cand
         self.k_max = k_max
@@ -43,7 +50,7 @@ class SpecRound:
         # (the criticality pass's copy lengthens the verify call by more than it saves the draft).
         self.pack_in_select = pack_in_select
         self.pack = None
-        if pack_rows:
+        if pack_rows and not self._nvfp4:
             n = B.ssd_draft_pack_bytes(kv, k_max)
             self.pack = torch.empty(n + 256, dtype=torch.uint8, device=dev)
             off = (-self.pack.data_ptr()) % 256
@@ -51,12 +58,16 @@ class SpecRound:
         self._packed = False
 
     def verify(self, q_verify: torch.Tensor, stream=None):
-        return B.ssd_verify_attn(self.kv, q_verify, self.n_cand, self.scale, out=self.out_v, lse=self.lse_v,
-                                 scores=self.scores, workspace=self.ws, stream=stream)
+        call = B.ssd_kv4_verify_attn if self._nvfp4 else B.ssd_verify_attn
+        return call(self.kv, q_verify, self.n_cand, self.scale, out=self.out_v, lse=self.lse_v, scores=self.scores,
+                    workspace=self.ws, stream=stream)
 
     def verify_select(self, q_verify: torch.Tensor, k_per_req: torch.Tensor, stream=None):
         """verify + select in one call: the selection runs inside the criticality pass, which also
         stores the selected rows in the row pack (pack_in_select), so every draft reads it."""
+        if self._nvfp4:
+            r = self.verify(q_verify, stream)
+            return dict(r, **dict(zip(("idx", "cnt"), self.select(k_per_req, stream))))
         pack = self.pack if self.pack_in_select else None
         r = B.ssd_verify_select(self.kv, q_verify, self.n_cand, self.scale, k_per_req, self.k_max, out=self.out_v,
                                 lse=self.lse_v, scores=self.scores, idx=self.idx, cnt=self.cnt, pack=pack,
@@ -89,8 +100,9 @@ class SpecRound:
         cnt = self.cnt.view(self.kv.batch, self.kv.h_kv)
         o = out if out is not None else self.out_d
         if self.pack is None:
-            return B.ssd_draft_attn(self.kv, q_draft, idx, cnt, self.scale, out=o, lse=self.lse_d, workspace=self.ws,
-                                    stream=stream)
+            call = B.ssd_kv4_draft_attn if self._nvfp4 else B.ssd_draft_attn
+            return call(self.kv, q_draft, idx, cnt, self.scale, out=o, lse=self.lse_d, workspace=self.ws,
+                        stream=stream)
         if not self._packed:
             mode = B.PACK_WRITE
         else:
@@ -119,13 +131,14 @@ class SpecRound:
             self._o_cnt = torch.empty((Bsz * hkv,), dtype=torch.int32, device=dev)
             self._o_out = torch.empty((Bsz, self.h_q, d), dtype=torch.float32, device=dev)
             self._o_lse_d = torch.empty((Bsz, self.h_q), dtype=torch.float32, device=dev)
-        B.ssd_verify_attn(kv, q_draft.view(Bsz, 1, self.h_q, d), 1, self.scale, out=self._o_dense, lse=self._o_lse,
-                          scores=self._o_scores, workspace=self.ws, stream=stream)
+        verify, draft = (B.ssd_kv4_verify_attn, B.ssd_kv4_draft_attn) if self._nvfp4 else (B.ssd_verify_attn, B.ssd_draft_attn)
+        verify(kv, q_draft.view(Bsz, 1, self.h_q, d), 1, self.scale, out=self._o_dense, lse=self._o_lse,
+               scores=self._o_scores, workspace=self.ws, stream=stream)
         B.ssd_select_topk(self._o_scores, kv.seq_lens, k_per_req, self.k_max, hkv, max_len=kv.max_seq_len,
                           idx=self._o_idx, cnt=self._o_cnt, stream=stream)
         o = out if out is not None else self._o_out
-        B.ssd_draft_attn(kv, q_draft, self._o_idx.view(Bsz, hkv, self.k_max), self._o_cnt.view(Bsz, hkv), self.scale,
-                         out=o, lse=self._o_lse_d, workspace=self.ws, stream=stream)
+        draft(kv, q_draft, self._o_idx.view(Bsz, hkv, self.k_max), self._o_cnt.view(Bsz, hkv), self.scale,
+              out=o, lse=self._o_lse_d, workspace=self.ws, stream=stream)
         return {"out": o, "lse": self._o_lse_d, "dense": self._o_dense.view(Bsz, self.h_q, d),
                 "scores": self._o_scores, "idx": self._o_idx, "cnt": self._o_cnt}
 

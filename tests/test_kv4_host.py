@@ -146,3 +146,34 @@ def test_binding_refuses_what_is_not_a_cuda_tensor():
     with pytest.raises(TypeError):
         F.ssd_kv4_read(object(), None, 3)
     assert F.KV4Cache.pool_shape(4, 1, 16, 128) == (4, 2, 1, 16, 72)
+
+
+def test_round_over_a_4_bit_cache(monkeypatch):
+    """SpecRound on a KV4Cache makes the 4-bit calls, with no row pack."""
+    class _KV4(F.KV4Cache):
+        device = torch.device("cpu")
+        batch, h_kv, d = 2, 2, 64
+
+        def __init__(self):
+            self.max_seq_len, self.seq_lens = 128, torch.tensor([100, 128], dtype=torch.int32)
+
+    calls = []
+    for name in ("ssd_verify_attn", "ssd_verify_select", "ssd_draft_attn", "ssd_draft_attn_packed", "ssd_select_topk",
+                 "ssd_kv4_verify_attn", "ssd_kv4_draft_attn"):
+        out = (0, 1) if name == "ssd_select_topk" else {"out": 2}
+        monkeypatch.setattr(binding, name, lambda *a, _n=name, _o=out, **k: calls.append(_n) or _o)
+    r = F.SpecRound(_KV4(), h_q=4, n_cand=3, k_max=8)
+    assert r.pack is None
+    q, qd, ks = torch.zeros((2, 3, 4, 64)), torch.zeros((2, 2, 4, 64)), torch.full((2,), 8, dtype=torch.int32)
+    want = ["ssd_kv4_verify_attn", "ssd_select_topk", "ssd_kv4_draft_attn", "ssd_kv4_draft_attn"]
+    r.run(q, qd, ks)
+    assert calls == want
+    calls.clear()
+    r.run(q, qd, ks, fused_select=True)
+    assert calls == want
+    assert r.verify_select(q, ks) == {"out": 2, "idx": 0, "cnt": 1}
+    calls.clear()
+    r.draft_oracle_topk(qd[0], ks)
+    assert calls == want[:3]
+    with pytest.raises(ValueError):
+        F.SpecRound(_KV4(), h_q=4, n_cand=3, k_max=8, pack_in_select=True)
