@@ -181,6 +181,7 @@ class KVCache:
             self.pool.shape[0], self.pool.shape[3], self.pool.shape[2], self.pool.shape[4],
             self.page_table.data_ptr(), self.page_table.shape[1], self.seq_lens.data_ptr(),
             self.seq_lens.shape[0], int(self.max_seq_len))
+        self._geometry = (self.pool.get_device(), self.batch, self.h_kv, self.d)
 
     @property
     def h_kv(self) -> int:
@@ -628,6 +629,9 @@ class KV4Cache:
             self.pool.data_ptr(), SSD_DTYPE_NVFP4, self.pool.shape[0], self.pool.shape[3], self.pool.shape[2], self.d,
             self.page_table.data_ptr(), self.page_table.shape[1], self.seq_lens.data_ptr(), self.seq_lens.shape[0],
             int(self.max_seq_len))
+        self.k_scale, self.v_scale = float(self.k_scale), float(self.v_scale)
+        self._geometry = (self.pool.get_device(), self.batch, self.h_kv, self.d)
+        self._need = {}  # workspace bytes of the calls' shapes
 
     @staticmethod
     def pool_shape(num_pages: int, h_kv: int, page_size: int, d: int):
@@ -654,38 +658,39 @@ class KV4Cache:
 
 
 _TYPES = {torch.float32: SSD_DTYPE_F32, torch.bfloat16: SSD_DTYPE_BF16}
-
-
 _HERE = contextlib.nullcontext()
+# The current stream's handle without a Stream object (1 us of a call that takes 10).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _scope(device, stream):
-    """The caches' device and the call's stream current, for allocations as for launches."""
+def _scope(device: int, stream):
+    """The cache's device and the call's stream current, for allocations as for launches."""
     if stream is None:
-        return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-    return torch.cuda.stream(stream)  # switches to the stream's device as well
+        return _HERE if torch.cuda.current_device() == device else torch.cuda.device(device)
+    if stream.device_index != device:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, expected cuda:{device}")
+    return torch.cuda.stream(stream)
 
 
-def _raw_stream(device) -> int:
-    return torch.cuda.current_stream(device.index).cuda_stream
-
-
-def _typed(t: torch.Tensor, name: str, device, shape=None) -> int:
-    _need(t, name, None, device)
-    if t.dtype not in _TYPES:
-        raise TypeError(f"{name} must be bf16 or fp32, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return _TYPES[t.dtype]
-
-
-def _shaped(t: Optional[torch.Tensor], name: str, dtype, device, shape):
-    if t is None:
-        return None
-    _need(t, name, dtype, device)
+def _shaped(t, name: str, dtype, device: int, shape) -> int:
+    """Address of a contiguous tensor of that type, device and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous()):
+        _need(t, name, dtype, torch.device("cuda", device))  # says what is wrong
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    return t.data_ptr()
+
+
+def _maybe(t, name: str, dtype, device: int, shape) -> Optional[int]:
+    return None if t is None else _shaped(t, name, dtype, device, shape)
+
+
+def _typed(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be bf16 or fp32, got {t.dtype}")
+    return _TYPES[t.dtype]
 
 
 def _is_kv4(kv):
@@ -693,18 +698,26 @@ def _is_kv4(kv):
         raise TypeError(f"kv must be a KV4Cache, got {type(kv).__name__}")
 
 
-def _stream_ws(device, name: str, nbytes: int, workspace: Optional[Workspace]):
+_STREAM_WS = {}  # (device, stream, name): buffer, aligned address, bytes from there
+
+
+def _stream_ws(device: int, name: str, nbytes: int, workspace: Optional[Workspace]):
     """Workspace of a call on the current stream: the caller's, or one kept for (device, stream), so that
     calls on different streams never share one; a call under stream capture without a workspace takes a
-    buffer of its graph's own memory, whose counters a node of the graph clears.  A caller's workspace is sized before a capture that uses
-    it and must outlive the graph."""
+    buffer of its graph's own memory, whose counters a node of the graph clears.  A caller's workspace is
+    sized before a capture that uses it and must outlive the graph."""
     if workspace is not None:
-        return _ws(device, name, nbytes, workspace)
+        return _ws(torch.device("cuda", device), name, nbytes, workspace)
     if torch.cuda.is_current_stream_capturing():
-        buf = torch.empty(int(nbytes) + 256, dtype=torch.uint8, device=device)
+        buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
         buf[:COUNTER_BYTES + 256].zero_()
-        return ctypes.c_void_p(Workspace.aligned(buf)), int(nbytes)
-    return _ws(device, (name, _raw_stream(device)), nbytes, None)
+        return Workspace.aligned(buf), nbytes
+    key = (device, _raw_stream(device), name)
+    kept = _STREAM_WS.get(key)
+    if kept is None or kept[2] < nbytes:
+        buf = torch.zeros(nbytes + 256, dtype=torch.uint8, device=device)
+        kept = _STREAM_WS[key] = (buf, Workspace.aligned(buf), nbytes)
+    return kept[1], kept[2]
 
 
 def ssd_kv4_append(kv: KV4Cache, k_new: torch.Tensor, v_new: torch.Tensor, counts: Optional[torch.Tensor] = None,
@@ -712,17 +725,18 @@ def ssd_kv4_append(kv: KV4Cache, k_new: torch.Tensor, v_new: torch.Tensor, count
     """Quantises rows k_new / v_new [B, n_new, h_kv, d] (bf16 or fp32) into positions seq_lens[b] + j of every
     request, j < counts[b] (int32 [B]; None: all n_new); kv.pool is modified in place, kv.seq_lens is not."""
     _is_kv4(kv)
-    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4 or k_new.shape[0] != kv.batch or \
-            k_new.shape[2] != kv.h_kv or k_new.shape[3] != kv.d:
+    dev, B, h, d = kv._geometry
+    dt = _typed(k_new, "k_new")
+    n = k_new.shape[1] if k_new.dim() == 4 else -1
+    if n < 0 or k_new.shape != (B, n, h, d):
         raise ValueError("k_new and v_new must both be [batch, n_new, h_kv, d]")
-    dt = _typed(k_new, "k_new", kv.device)
-    _shaped(v_new, "v_new", k_new.dtype, kv.device, k_new.shape)
-    _shaped(counts, "counts", torch.int32, kv.device, (kv.batch,))
-    if kv.batch == 0:
+    pk = _shaped(k_new, "k_new", k_new.dtype, dev, (B, n, h, d))
+    pv = _shaped(v_new, "v_new", k_new.dtype, dev, (B, n, h, d))
+    pc = _maybe(counts, "counts", torch.int32, dev, (B,))
+    if B == 0:  # (a tensor without elements has no address)
         return
-    with _scope(kv.device, stream):
-        _check(_lib().ssd_kv4_append(kv.ref(), _ptr(k_new), _ptr(v_new), dt, k_new.shape[1], _ptr(counts),
-                                     float(kv.k_scale), float(kv.v_scale), _raw_stream(kv.device)))
+    with _scope(dev, stream):
+        _check(_lib().ssd_kv4_append(kv.ref(), pk, pv, dt, n, pc, kv.k_scale, kv.v_scale, _raw_stream(dev)))
 
 
 def ssd_kv4_read(kv: KV4Cache, first: torch.Tensor, n: int, counts: Optional[torch.Tensor] = None, *, k=None, v=None,
@@ -730,19 +744,20 @@ def ssd_kv4_read(kv: KV4Cache, first: torch.Tensor, n: int, counts: Optional[tor
     """The values of the tokens first[b] + j, j < counts[b] (None: n), as k, v [B, n, h_kv, d] of `dtype` (bf16 or
     fp32; both exact); rows from counts[b] on are zeros."""
     _is_kv4(kv)
-    dev, shape = kv.device, (kv.batch, int(n), kv.h_kv, kv.d)
-    _shaped(first, "first", torch.int32, dev, (kv.batch,))
-    _shaped(counts, "counts", torch.int32, dev, (kv.batch,))
+    dev, B, h, d = kv._geometry
+    shape = (B, int(n), h, d)
+    pf = _shaped(first, "first", torch.int32, dev, (B,))
+    pc = _maybe(counts, "counts", torch.int32, dev, (B,))
     with _scope(dev, stream):
         if k is None:
             k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=dev)
         if v is None:
             v = torch.empty(shape, dtype=k.dtype, device=dev)
-        dt = _typed(k, "k", dev, shape)
-        _shaped(v, "v", k.dtype, dev, shape)
-        if kv.batch:  # (a tensor without elements has no address)
-            _check(_lib().ssd_kv4_read(kv.ref(), _ptr(first), _ptr(counts), int(n), float(kv.k_scale), float(kv.v_scale),
-                                       dt, _ptr(k), _ptr(v), _raw_stream(dev)))
+        dt = _typed(k, "k")
+        pk = _shaped(k, "k", k.dtype, dev, shape)
+        pv = _shaped(v, "v", k.dtype, dev, shape)
+        if B:
+            _check(_lib().ssd_kv4_read(kv.ref(), pf, pc, int(n), kv.k_scale, kv.v_scale, dt, pk, pv, _raw_stream(dev)))
     return k, v
 
 
@@ -752,30 +767,33 @@ def ssd_kv4_verify_attn(kv: KV4Cache, q: torch.Tensor, n_cand: int, scale: float
     """Verify attention over a 4-bit cache, with the tokens' criticality on request (n_cand = 1: plain
     decoding).  q [B, n_cand, h_q, d] bf16 or fp32; out fp32 or bf16 (`out_dtype` where it is not given)."""
     _is_kv4(kv)
-    dev = kv.device
-    qt = _typed(q, "q", dev)
-    if q.dim() != 4 or q.shape[0] != kv.batch or q.shape[1] != n_cand or q.shape[3] != kv.d:
+    dev, B, h, d = kv._geometry
+    qt = _typed(q, "q")
+    h_q = q.shape[2] if q.dim() == 4 else -1
+    shape = (B, n_cand, h_q, d)
+    if q.shape != shape:
         raise ValueError("q must be [batch, n_cand, h_q, d]")
-    B, nc, h_q, d = q.shape
+    pq = _shaped(q, "q", q.dtype, dev, shape)
     with _scope(dev, stream):
         if out is None:
-            out = torch.empty((B, nc, h_q, d), dtype=out_dtype, device=dev)
+            out = torch.empty(shape, dtype=out_dtype, device=dev)
         if lse is None and want_lse:
-            lse = torch.empty((B, nc, h_q), dtype=torch.float32, device=dev)
+            lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
         if scores is None and want_scores:
-            scores = torch.zeros((B, kv.h_kv, max(kv.max_seq_len, 1)), dtype=torch.float32, device=dev)
-        ot = _typed(out, "out", dev, (B, nc, h_q, d))
-        _shaped(lse, "lse", torch.float32, dev, (B, nc, h_q))
-        if scores is not None:
-            _shaped(scores, "scores", torch.float32, dev, (B, kv.h_kv, scores.shape[-1] if scores.dim() else 0))
-        if B == 0:
-            return {"out": out, "lse": lse, "scores": scores}
-        L = _lib()
-        need = L.ssd_kv4_verify_workspace_bytes(kv.ref(), h_q, n_cand)
-        wsp, avail = _stream_ws(dev, "kv4", need, workspace)
-        _check(L.ssd_kv4_verify_attn(kv.ref(), _ptr(q), qt, h_q, n_cand, float(scale), float(kv.k_scale),
-                                     float(kv.v_scale), _ptr(out), ot, _ptr(lse), _ptr(scores),
-                                     scores.shape[-1] if scores is not None else 0, wsp, avail, _raw_stream(dev)))
+            scores = torch.zeros((B, h, max(kv.max_seq_len, 1)), dtype=torch.float32, device=dev)
+        ot = _typed(out, "out")
+        po = _shaped(out, "out", out.dtype, dev, shape)
+        pl = _maybe(lse, "lse", torch.float32, dev, shape[:3])
+        stride = 0 if scores is None else scores.shape[-1] if scores.dim() else 0
+        ps = _maybe(scores, "scores", torch.float32, dev, (B, h, stride))
+        if B:
+            L = _lib()
+            need = kv._need.get((h_q, n_cand))
+            if need is None:
+                need = kv._need[h_q, n_cand] = L.ssd_kv4_verify_workspace_bytes(kv.ref(), h_q, n_cand)
+            ws, avail = _stream_ws(dev, "kv4", need, workspace)
+            _check(L.ssd_kv4_verify_attn(kv.ref(), pq, qt, h_q, n_cand, float(scale), kv.k_scale, kv.v_scale, po, ot, pl, ps,
+                                         stride, ws, avail, _raw_stream(dev)))
     return {"out": out, "lse": lse, "scores": scores}
 
 
@@ -785,32 +803,33 @@ def ssd_kv4_draft_attn(kv: KV4Cache, q: torch.Tensor, idx: torch.Tensor, cnt: to
     """Single-query attention over the selected tokens of a 4-bit cache.  q [B, h_q, d] bf16 or fp32;
     idx [B, h_kv, k_max] and cnt [B, h_kv] int32; out fp32 or bf16 (`out_dtype` where it is not given)."""
     _is_kv4(kv)
-    dev = kv.device
-    qt = _typed(q, "q", dev)
-    if q.dim() != 3 or q.shape[0] != kv.batch or q.shape[2] != kv.d:
+    dev, B, h, d = kv._geometry
+    qt = _typed(q, "q")
+    h_q = q.shape[1] if q.dim() == 3 else -1
+    if q.shape != (B, h_q, d):
         raise ValueError("q must be [batch, h_q, d]")
+    pq = _shaped(q, "q", q.dtype, dev, (B, h_q, d))
     if not isinstance(idx, torch.Tensor) or idx.dim() != 3:
         raise ValueError("idx must be [batch, h_kv, k_max]")
-    B, h_q, d = q.shape
     k_max = idx.shape[2]
-    _shaped(idx, "idx", torch.int32, dev, (B, kv.h_kv, k_max))
-    _need(cnt, "cnt", torch.int32, dev)
-    _shaped(cnt, "cnt", torch.int32, dev, (B, kv.h_kv))
+    pi = _shaped(idx, "idx", torch.int32, dev, (B, h, k_max))
+    pc = _shaped(cnt, "cnt", torch.int32, dev, (B, h))
     with _scope(dev, stream):
         if out is None:
             out = torch.empty((B, h_q, d), dtype=out_dtype, device=dev)
         if lse is None and want_lse:
             lse = torch.empty((B, h_q), dtype=torch.float32, device=dev)
-        ot = _typed(out, "out", dev, (B, h_q, d))
-        _shaped(lse, "lse", torch.float32, dev, (B, h_q))
-        if B == 0:
-            return {"out": out, "lse": lse}
-        L = _lib()
-        need = L.ssd_kv4_draft_workspace_bytes(kv.ref(), h_q, k_max)
-        wsp, avail = _stream_ws(dev, "kv4", need, workspace)
-        _check(L.ssd_kv4_draft_attn(kv.ref(), _ptr(q), qt, h_q, _ptr(idx), k_max, _ptr(cnt), float(scale),
-                                    float(kv.k_scale), float(kv.v_scale), _ptr(out), ot, _ptr(lse), wsp, avail,
-                                    _raw_stream(dev)))
+        ot = _typed(out, "out")
+        po = _shaped(out, "out", out.dtype, dev, (B, h_q, d))
+        pl = _maybe(lse, "lse", torch.float32, dev, (B, h_q))
+        if B:
+            L = _lib()
+            need = kv._need.get((h_q, -1, k_max))
+            if need is None:
+                need = kv._need[h_q, -1, k_max] = L.ssd_kv4_draft_workspace_bytes(kv.ref(), h_q, k_max)
+            ws, avail = _stream_ws(dev, "kv4", need, workspace)
+            _check(L.ssd_kv4_draft_attn(kv.ref(), pq, qt, h_q, pi, k_max, pc, float(scale), kv.k_scale, kv.v_scale, po, ot, pl,
+                                        ws, avail, _raw_stream(dev)))
     return {"out": out, "lse": lse}
 
 
@@ -839,29 +858,34 @@ class PagePool:
         return cls(refs.scatter_add_(0, held, torch.ones_like(held, dtype=torch.int32)))
 
 
-def _pages_of(kv, pages: PagePool):
+def _pages_of(kv, pages: PagePool) -> int:
     if not isinstance(kv, (KVCache, KV4Cache)):
         raise TypeError(f"kv must be a KVCache or a KV4Cache, got {type(kv).__name__}")
     if not isinstance(pages, PagePool):
         raise TypeError(f"pages must be a PagePool, got {type(pages).__name__}")
-    return _ptr(_shaped(pages.refs, "pages.refs", torch.int32, kv.device, (kv.pool.shape[0],)))
+    return _shaped(pages.refs, "pages.refs", torch.int32, kv._geometry[0], (kv.pool.shape[0],))
 
 
-def _rows(t: torch.Tensor, name: str, device, n: Optional[int] = None):
-    _need(t, name, torch.int32, device)
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be [{'n' if n is None else n}]")
-    return t
+def _count(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be [n]")
+    return t.shape[0]
 
 
 def ssd_kv_fork(kv, pages: PagePool, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """Row dst[i] (empty before) shares the pages of row src[i] and takes its length; src, dst int32 [n].
     kv.page_table, kv.seq_lens and pages.refs are modified in place; no K / V moves."""
     refs = _pages_of(kv, pages)
-    _rows(src, "src", kv.device)
-    _rows(dst, "dst", kv.device, src.shape[0])
-    with _scope(kv.device, stream):
-        _check(_lib().ssd_kv_fork(kv.ref(), refs, _ptr(src), _ptr(dst), src.shape[0], _raw_stream(kv.device)))
+    dev = kv._geometry[0]
+    n = _count(src, "src")
+    ps = _shaped(src, "src", torch.int32, dev, (n,))
+    pd = _shaped(dst, "dst", torch.int32, dev, (n,))
+    if n == 0:
+        return
+    with _scope(dev, stream):
+        _check(_lib().ssd_kv_fork(kv.ref(), refs, ps, pd, n, _raw_stream(dev)))
 
 
 def ssd_kv_reserve(kv, pages: PagePool, counts: torch.Tensor, *, workspace: Optional[Workspace] = None,
@@ -869,24 +893,26 @@ def ssd_kv_reserve(kv, pages: PagePool, counts: torch.Tensor, *, workspace: Opti
     """Pages of its own for the next counts[b] tokens of every request (int32 [B]); what a request shares there is
     copied.  All or nothing: with too few free pages the status reports FAULT_NOPAGE and nothing changes."""
     refs = _pages_of(kv, pages)
-    _rows(counts, "counts", kv.device, kv.batch)
-    if kv.batch == 0:
+    dev, B = kv._geometry[:2]
+    pc = _shaped(counts, "counts", torch.int32, dev, (B,))
+    if B == 0:
         return
-    with _scope(kv.device, stream):
+    with _scope(dev, stream):
         L = _lib()
-        wsp, avail = _stream_ws(kv.device, "pages", L.ssd_kv_reserve_workspace_bytes(kv.ref()), workspace)
-        _check(L.ssd_kv_reserve(kv.ref(), refs, _ptr(counts), wsp, avail, _raw_stream(kv.device)))
+        ws, avail = _stream_ws(dev, "pages", L.ssd_kv_reserve_workspace_bytes(kv.ref()), workspace)
+        _check(L.ssd_kv_reserve(kv.ref(), refs, pc, ws, avail, _raw_stream(dev)))
 
 
 def ssd_kv_release(kv, pages: PagePool, keep: torch.Tensor, stream=None) -> None:
     """Row b gives back the pages behind its first keep[b] tokens (int32 [B]; 0: all, negative: none) and its
     length becomes min(length, keep[b])."""
     refs = _pages_of(kv, pages)
-    _rows(keep, "keep", kv.device, kv.batch)
-    if kv.batch == 0:
+    dev, B = kv._geometry[:2]
+    pk = _shaped(keep, "keep", torch.int32, dev, (B,))
+    if B == 0:
         return
-    with _scope(kv.device, stream):
-        _check(_lib().ssd_kv_release(kv.ref(), refs, _ptr(keep), _raw_stream(kv.device)))
+    with _scope(dev, stream):
+        _check(_lib().ssd_kv_release(kv.ref(), refs, pk, _raw_stream(dev)))
 
 
 def ssd_kv_compact(kv, to, src: torch.Tensor, dst: torch.Tensor, idx: torch.Tensor, cnt: torch.Tensor,
@@ -894,22 +920,23 @@ def ssd_kv_compact(kv, to, src: torch.Tensor, dst: torch.Tensor, idx: torch.Tens
     """The listed tokens idx [n, h_kv, k_max] (cnt [n, h_kv] of them, the same for every head) of row src[i] of `kv`
     go to positions 0 .. of row dst[i] of `to`, whose length becomes the count.  dst's pages are reserved
     beforehand; with `pages` (the PagePool of `to`) shared ones are left alone and reported."""
-    dev = kv.device
     if not isinstance(kv, (KVCache, KV4Cache)) or type(to) is not type(kv):
         raise TypeError("kv and to must both be a KVCache or both a KV4Cache")
+    dev, _, h, _ = kv._geometry
     refs = None if pages is None else _pages_of(to, pages)
-    if to.device != dev:
-        raise ValueError(f"to is on {to.device}, expected {dev}")
+    if to._geometry[0] != dev:
+        raise ValueError(f"to is on {to.device}, expected {kv.device}")
     if isinstance(kv, KV4Cache) and (kv.k_scale, kv.v_scale) != (to.k_scale, to.v_scale):
         raise ValueError("the two caches differ in k_scale or v_scale")
-    _rows(src, "src", dev)
-    n = src.shape[0]
-    _rows(dst, "dst", dev, n)
+    n = _count(src, "src")
+    ps = _shaped(src, "src", torch.int32, dev, (n,))
+    pd = _shaped(dst, "dst", torch.int32, dev, (n,))
     if not isinstance(idx, torch.Tensor) or idx.dim() != 3:
         raise ValueError("idx must be [n, h_kv, k_max]")
-    _need(cnt, "cnt", torch.int32, dev)
-    _shaped(idx, "idx", torch.int32, dev, (n, kv.h_kv, idx.shape[2]))
-    _shaped(cnt, "cnt", torch.int32, dev, (n, kv.h_kv))
+    k_max = idx.shape[2]
+    pi = _shaped(idx, "idx", torch.int32, dev, (n, h, k_max))
+    pc = _shaped(cnt, "cnt", torch.int32, dev, (n, h))
+    if n == 0:
+        return
     with _scope(dev, stream):
-        _check(_lib().ssd_kv_compact(kv.ref(), to.ref(), refs, _ptr(src), _ptr(dst), n, _ptr(idx), idx.shape[2], _ptr(cnt),
-                                     _raw_stream(dev)))
+        _check(_lib().ssd_kv_compact(kv.ref(), to.ref(), refs, ps, pd, n, pi, k_max, pc, _raw_stream(dev)))
