@@ -450,6 +450,36 @@ __device__ __forceinline__ void kv4_join(const Kv4AttnArgs &a, int parts, int ro
                                          PartRow part, OutRow row_of, Sync sync) {
   const int lane = tid & 31, warp = tid >> 5;
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
+  if (parts <= 8) {  // every thread loads all it needs at once
+    for (int e = tid; e < rows * (D / 4); e += NT) {
+      const int q = e / (D / 4), piece = e % (D / 4);
+      float4 y[8];
+      float2 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        y[j] = make_float4(0.f, 0.f, 0.f, 0.f), v[j] = make_float2(-1e30f, 0.f);
+        if (j < parts) {
+          const int64_t at = part(j) + q;
+          v[j] = __ldcg(ml + at);
+          y[j] = __ldcg(reinterpret_cast<const float4 *>(a.part_o) + at * (D / 4) + piece);
+        }
+      }
+      float M = v[0].x, Z = 0.f;
+#pragma unroll
+      for (int j = 1; j < 8; ++j) M = fmaxf(M, v[j].x);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = fast_exp2(v[j].x - M);
+        Z = fmaf(v[j].y, f, Z);
+        acc.x = fmaf(y[j].x, f, acc.x), acc.y = fmaf(y[j].y, f, acc.y), acc.z = fmaf(y[j].z, f, acc.z), acc.w = fmaf(y[j].w, f, acc.w);
+      }
+      const float f = Z == 0.f ? 0.f : a.v_scale / Z;
+      kv4_write4(a, row_of(q) * D + piece * 4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+      if (piece == 0 && a.lse) a.lse[row_of(q)] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
+    }
+    return;
+  }
   constexpr int U = 4;  // rows of a warp at once
   for (int q0 = warp; q0 < rows; q0 += U * (NT / 32)) {
     float2 v[U];
@@ -758,7 +788,8 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
         for (int k = 0; k < 2; ++k) {
           const int q = 8 * nt + 2 * col + k;
           float M = -1e30f;
-          for (int w = 0; w < nw; ++w) M = fmaxf(M, s_m[w * ROWS + q]);
+#pragma unroll
+          for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * ROWS + q]);
           const float f = fast_exp2(m[nt][k] - M);
           float4 *dst = reinterpret_cast<float4 *>(acc) + (warp * ROWS + q) * PIECES;
 #pragma unroll
@@ -778,10 +809,14 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
     for (int e = tid; e < rows * PIECES; e += NW * 32) {
       const int q = e / PIECES, piece = e % PIECES, rr = piece / (MT / 2);
       float M = -1e30f, Z = 0.f;
-      for (int w = 0; w < nw; ++w) M = fmaxf(M, s_m[w * ROWS + q]);
-      for (int w = 0; w < nw; ++w) Z += s_l[w * ROWS + q] * fast_exp2(s_m[w * ROWS + q] - M);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * ROWS + q]);  // (a warp without a tile: -1e30 and 0)
+#pragma unroll
+      for (int w = 0; w < NW; ++w) Z += s_l[w * ROWS + q] * fast_exp2(s_m[w * ROWS + q] - M);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < nw; ++w) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        if (w >= nw) break;
         const float4 y = reinterpret_cast<const float4 *>(acc)[(w * ROWS + q) * PIECES + (piece ^ (rr >> 1) ^ ((q >> 1) & 3))];
         v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
       }
