@@ -239,59 +239,57 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4RowsArgs a) {
     n = 0;
   }
   const int j0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n - j0), live = min(nt, n - j0);
-  const int log2_gpr = a.d == 128 ? 3 : 2;
-  const unsigned per_token = (unsigned)a.kv.h_kv << log2_gpr, total = nt * per_token;
+  const int log2_ppr = a.d == 128 ? 2 : 1;
+  const unsigned per_token = (unsigned)a.kv.h_kv << log2_ppr, total = nt * per_token;
   const int32_t *table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
   const int cb = kv4_code_bytes(a.d), sb = kv4_scale_bytes(a.d);
   const int64_t block_bytes = (int64_t)a.kv.page_size * (cb + sb), v_off = a.kv.h_kv * block_bytes;
   const int64_t dst0 = ((int64_t)b * a.n + j0) * a.kv.h_kv * a.d;
   T *ko = static_cast<T *>(a.k_out) + dst0, *vo = static_cast<T *>(a.v_out) + dst0;
   const bool wide = ((reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.v_out)) & 31) == 0;
-  constexpr int U = 2;  // groups in flight per thread
-  for (unsigned e0 = tid; e0 < total; e0 += U * kKv4Threads) {
-    uint2 w[U][2];
-    uint32_t sc[U][2];
+  // Two groups of 16 elements per thread and step (with one, the narrow loads filled the load/store queue).
+#pragma unroll 1
+  for (unsigned e = tid; e < total; e += kKv4Threads) {
+    const unsigned jt = e / per_token, in = e - jt * per_token;
+    uint4 w[2] = {};
+    uint32_t sc[2] = {};
+    if ((int)jt < live) {
+      const int g = in >> log2_ppr, c = in & ((1 << log2_ppr) - 1);
+      const int t = f0 + j0 + (int)jt, slot = t & (a.kv.page_size - 1);
+      const int32_t p = table[t >> a.kv.log2_ps];
+      if (p < 0 || (int64_t)p >= a.kv.num_pages) {
+        atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
+      } else {
+        const char *blk = a.pool + ((int64_t)p * 2 * a.kv.h_kv + g) * block_bytes;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned e = e0 + u * kKv4Threads, jt = e / per_token, in = e - jt * per_token;
-      w[u][0] = w[u][1] = make_uint2(0, 0), sc[u][0] = sc[u][1] = 0;
-      if (e < total && (int)jt < live) {
-        const int g = in >> log2_gpr, c = in & ((1 << log2_gpr) - 1);
-        const int t = f0 + j0 + (int)jt, slot = t & (a.kv.page_size - 1);
-        const int32_t p = table[t >> a.kv.log2_ps];
-        if (p < 0 || (int64_t)p >= a.kv.num_pages) {
-          atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
-        } else {
-          const char *blk = a.pool + ((int64_t)p * 2 * a.kv.h_kv + g) * block_bytes;
-#pragma unroll
-          for (int which = 0; which < 2; ++which) {
-            w[u][which] = *reinterpret_cast<const uint2 *>(blk + which * v_off + slot * cb + c * 8);
-            sc[u][which] = (unsigned char)blk[which * v_off + a.kv.page_size * cb + slot * sb + c];
-          }
+        for (int which = 0; which < 2; ++which) {
+          w[which] = *reinterpret_cast<const uint4 *>(blk + which * v_off + slot * cb + c * 16);
+          sc[which] = *reinterpret_cast<const uint16_t *>(blk + which * v_off + a.kv.page_size * cb + slot * sb + c * 2);
         }
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned e = e0 + u * kKv4Threads;
-      if (e >= total) break;
+    for (int which = 0; which < 2; ++which) {
+      const uint32_t s2 = e4m3x2_to_f16x2(sc[which]);
+      const float2 s = __half22float2(*reinterpret_cast<const __half2 *>(&s2));
+      const float mul = which ? a.v_mul : a.k_mul;
+      const uint32_t words[4] = {w[which].x, w[which].y, w[which].z, w[which].w};
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(sc[u][which]) & 0xffffu))) *
-                        (which ? a.v_mul : a.k_mul);
+      for (int y = 0; y < 2; ++y) {
+        const float f = (y ? s.y : s.x) * mul;
         float x[16];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t h[4];
-          e2m1_to_f16x2(k ? w[u][which].y : w[u][which].x, h);
+          e2m1_to_f16x2(words[2 * y + k], h);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-            x[8 * k + 2 * i] = v.x * s;
-            x[8 * k + 2 * i + 1] = v.y * s;
+            x[8 * k + 2 * i] = v.x * f;
+            x[8 * k + 2 * i + 1] = v.y * f;
           }
         }
-        store_group((which ? vo : ko) + (int64_t)e * 16, x, wide);
+        store_group((which ? vo : ko) + (int64_t)e * 32 + y * 16, x, wide);
       }
     }
   }

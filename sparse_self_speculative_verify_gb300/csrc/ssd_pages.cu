@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(char *pool, const
 
 // ---- compact --------------------------------------------------------------------------------
 constexpr int kCompactThreads = 256;
-constexpr int kCompactTokens = 128;  // list entries per block
+constexpr int kCompactTokens = kCompactThreads;  // list entries per block at most
 
 struct CompactArgs {
   KVView from, to;
@@ -353,60 +353,60 @@ struct CompactArgs {
   int32_t *to_lens;
   const int32_t *to_refs;
   const int32_t *src, *dst, *idx, *cnt;
-  int n, k_max;
+  int n, k_max, tokens;  // tokens: list entries per block
   bool same;  // one cache
   RowShape rs;
   unsigned *status;
 };
 
-// Block (x, g, i): list entries [x * kCompactTokens, ...) of head g of pair i.  Addresses first, one entry
-// per thread, then 16-byte pieces of the rows.
+// Block (x, g, i): list entries [x * a.tokens, ...) of head g of pair i.  Addresses first, one entry per thread,
+// then 16-byte pieces of the rows.  What a block needs before its first row is loaded in two steps (all that hangs on
+// i alone, then lengths and page ids): as a chain of seven loads it cost more than the rows, 72 us for 839 k rows.
 __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactArgs a) {
-  const int i = blockIdx.z, g = blockIdx.y, j0 = blockIdx.x * kCompactTokens, tid = threadIdx.x;
+  const int i = blockIdx.z, g = blockIdx.y, j0 = blockIdx.x * a.tokens, tid = threadIdx.x, j = j0 + tid;
   const int h = a.from.h_kv;
   __shared__ int64_t s_from[kCompactTokens], s_to[kCompactTokens];  // K block of the entry, or -1
   __shared__ int s_slots[kCompactTokens];
   pdl_trigger();
   pdl_wait();
-  const int s = a.src[i], d = a.dst[i];
+  const bool entry = tid < a.tokens && j < a.k_max;
+  const int t = entry ? a.idx[((int64_t)i * h + g) * a.k_max + j] : -1;
+  const int s = a.src[i], d = a.dst[i], count = a.cnt[(int64_t)i * h];
+  bool same_count = count >= 0 && count <= a.k_max;
+  for (int k = tid; k < h; k += kCompactThreads) same_count &= a.cnt[(int64_t)i * h + k] == count;
   bool ok = s >= 0 && s < a.from.batch && d >= 0 && d < a.to.batch;
-  for (int j = tid; j < a.n && ok; j += kCompactThreads) ok = !(j < i && a.dst[j] == d) && !(a.same && a.src[j] == d);
+  for (int k = tid; k < a.n && ok; k += kCompactThreads) ok = !(k < i && a.dst[k] == d) && !(a.same && a.src[k] == d);
   if (!__syncthreads_and(ok)) {
     if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
     return;
   }
-  const int count = a.cnt[(int64_t)i * h];
-  for (int j = tid; j < h; j += kCompactThreads) ok &= a.cnt[(int64_t)i * h + j] == count;
-  ok &= count >= 0 && count <= a.k_max;
-  if (!__syncthreads_and(ok)) {
+  if (!__syncthreads_and(same_count)) {
     if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_KMAX);
     return;
   }
+  const int nj = min(a.tokens, count - j0);
+  const bool mine = tid < nj && count <= a.to.max_seq_len, in_table = mine && t >= 0 && t < a.from.max_seq_len;
   const int L = a.from.seq_lens[s];
+  const int32_t pf = in_table ? a.from.page_table[(int64_t)s * a.from.max_pages + (t >> a.from.log2_ps)] : -1;
+  const int32_t pt = mine ? a.to.page_table[(int64_t)d * a.to.max_pages + (j >> a.to.log2_ps)] : -1;
   if (L < 0 || L > a.from.max_seq_len || count > a.to.max_seq_len) {
     if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_SEQLEN);
     return;
   }
   if (tid == 0 && j0 == 0 && g == 0) a.to_lens[d] = count;
-  const int nj = min(kCompactTokens, count - j0);
   const int64_t fb = (int64_t)a.from.page_size * (a.rs.wide + a.rs.thin), tb = (int64_t)a.to.page_size * (a.rs.wide + a.rs.thin);
-  if (tid < nj) {
-    const int j = j0 + tid, t = a.idx[((int64_t)i * h + g) * a.k_max + j];
+  if (mine) {
     int64_t f = -1, to = -1;
-    if (t < 0 || t >= L) {
+    if (t < 0 || t >= L)
       atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
-    } else {
-      const int32_t p = a.from.page_table[(int64_t)s * a.from.max_pages + (t >> a.from.log2_ps)];
-      if (p < 0 || (int64_t)p >= a.from.num_pages)
-        atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
-      else
-        f = ((int64_t)p * 2 * h + g) * fb;
-    }
-    const int32_t p = a.to.page_table[(int64_t)d * a.to.max_pages + (j >> a.to.log2_ps)];
-    if (p < 0 || (int64_t)p >= a.to.num_pages || (a.to_refs && a.to_refs[p] != 1))
+    else if (pf < 0 || (int64_t)pf >= a.from.num_pages)
       atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
     else
-      to = ((int64_t)p * 2 * h + g) * tb;
+      f = ((int64_t)pf * 2 * h + g) * fb;
+    if (pt < 0 || (int64_t)pt >= a.to.num_pages || (a.to_refs && a.to_refs[pt] != 1))
+      atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
+    else
+      to = ((int64_t)pt * 2 * h + g) * tb;
     s_from[tid] = f, s_to[tid] = to;
     s_slots[tid] = t & (a.from.page_size - 1);
   }
@@ -541,6 +541,9 @@ extern "C" int ssd_kv_compact(const ssd_paged_kv *kv, const ssd_paged_kv *to, co
   a.src = src, a.dst = dst, a.idx = idx, a.cnt = cnt, a.n = n, a.k_max = k_max;
   a.same = kv->page_table == to->page_table;
   a.rs = row_shape(kv);
-  return launch(kv_compact_kernel, dim3(cdiv(k_max > 0 ? k_max : 1, kCompactTokens), kv->h_kv, n), dim3(kCompactThreads), 0,
+  // Half as many entries per block while that leaves SMs without work.
+  const int k = k_max > 0 ? k_max : 1;
+  a.tokens = (int64_t)cdiv(k, kCompactTokens) * kv->h_kv * n < (int64_t)sm_count() * 8 ? kCompactTokens / 2 : kCompactTokens;
+  return launch(kv_compact_kernel, dim3(cdiv(k, a.tokens), kv->h_kv, n), dim3(kCompactThreads), 0,
                 reinterpret_cast<cudaStream_t>(stream), "kv_compact_kernel", a);
 }
