@@ -106,27 +106,27 @@ __device__ __forceinline__ int kv4_tiles(const Kv4AttnArgs &a, int u) {
 
 // Dealing out the units' tiles to blocks.  All units stand in one line, each with a lead before its own tiles:
 // about what starting, merging and writing a unit costs, in tiles.  Blocks take equal contiguous stretches of the
-// line.  A boundary inside a lead, or at most `snap` tiles from a unit's start or end, moves there: a unit cut in
+// line.  A boundary inside a lead, or at most kKv4Snap tiles from a unit's start or end, moves there: a unit cut in
 // two costs a join as well.  (Without leads, a block whose stretch held many short units ran twice as long as the
 // others: 128 requests of 1 to 2048 tokens, 8 heads of 128, one query row a head: 143 us against 85 with them; the
 // same with 5 candidates: 292 against 148.)
 template <int TILE>
 constexpr int kKv4Lead = TILE == kKv4Tile ? 16 : 6;  // 4 us of a block's time
 template <int TILE>
-__device__ __forceinline__ int64_t kv4_snap(int64_t per) {
-  return TILE == kKv4Tile ? min(max(per / 4, (int64_t)4), (int64_t)20) : 0;  // tcgen05's tiles are 128 tokens
-}
+constexpr int kKv4Snap = TILE == kKv4Tile ? 4 : 0;  // (20: decode 48.8 us against 47.5)
 struct Kv4Range {
-  int64_t x, x1, per, snap;  // place of the unit u in the line, the block's end, a stretch's length
+  int64_t x, x1, per;  // place of the unit u in the line, the block's end, a stretch's length
   int u, off;                // next unit, and its first tile of this block
 };
 // Blocks that hold parts of the unit of n tiles at place x: `first` and `more` blocks after it.  The unit's start
 // is stored in the first one's second slot, other parts in their block's first one.
+template <int TILE>
 struct Kv4Parts {
   int first, more;
-  __device__ __forceinline__ Kv4Parts(const Kv4Range &r, int64_t x, int lead, int n) {
-    first = (int)((x + lead + r.snap) / r.per);
-    more = max(0, (int)((x + lead + n - r.snap + r.per - 1) / r.per) - 1 - first);
+  __device__ __forceinline__ Kv4Parts(const Kv4Range &r, int64_t x, int n) {
+    constexpr int lead = kKv4Lead<TILE>;
+    first = (int)((x + lead + kKv4Snap<TILE>) / r.per);
+    more = max(0, (int)((x + lead + n - kKv4Snap<TILE> + r.per - 1) / r.per) - 1 - first);
   }
   __device__ __forceinline__ int64_t slot(int k) const { return k ? (int64_t)(first + k) * 2 : (int64_t)first * 2 + 1; }
 };
@@ -156,7 +156,7 @@ __device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int
   }
   int64_t per = (total + gridDim.x - 1) / gridDim.x;
   if (per < MIN) per = MIN;  // MIN = NW: a tile for every warp before another block is used
-  r.per = per, r.snap = kv4_snap<TILE>(per);
+  r.per = per;
   const int64_t excl = base + inc - sum;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -170,7 +170,7 @@ __device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int
         if (y < e + n) break;
         e += n;
       }
-      const bool down = y - e <= LEAD + r.snap, up = !down && e + n - y <= r.snap;
+      const bool down = y - e <= LEAD + kKv4Snap<TILE>, up = !down && e + n - y <= kKv4Snap<TILE>;
       s_scan[NW + 2 * k] = down ? e : up ? e + n : y;
       if (k == 0) s_scan[NW + 1] = (int64_t)(u + up) << 32 | (uint32_t)(down || up ? 0 : (int)(y - e) - LEAD);
     }
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
         }
     }
     __syncthreads();
-    const Kv4Parts parts(rg, place, kKv4Lead<kKv4Tile>, n_tiles);
+    const Kv4Parts<kKv4Tile> parts(rg, place, n_tiles);
     const bool whole = parts.more == 0;
     const int64_t slot = parts.slot((int)blockIdx.x - parts.first);
     auto row_of = [&](int q) {

@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
       wait(b_l, seg);
       tc_fence_after();
       const int d = 32 * w + 4 * (lane & 7) + 2 * (lane >> 4) + ((lane >> 3) & 1);
-      const Kv4Parts parts(rg, rg.x, kKv4Lead<kKv4TcTile>, s.n_tiles);
+      const Kv4Parts<kKv4TcTile> parts(rg, rg.x, s.n_tiles);
       const bool whole = parts.more == 0;
       const int64_t slot = parts.slot((int)blockIdx.x - parts.first);
       auto column = [&](int q) { return q / CW * H + q % CW; };  // of the pass's row q
