@@ -1,7 +1,8 @@
 """GB300 (sm_103a) attention hot path of sparse self-speculative decoding.
 
 Verify attention with fused criticality, Top-K selection, sparse draft attention, the unified
-verify/draft launch and the block-granular variant, as CUDA kernels behind the C ABI in
+verify/draft launch and the block-granular variant, the same verify and draft over a 4-bit cache, and
+the calls that share, reserve, release and compact a cache's pages, as CUDA kernels behind the C ABI in
 ``include/ssd.h``.  ``binding`` is the thin Python layer over that ABI; ``round`` strings the calls
 of one speculative round together; ``workloads`` draws the seeded synthetic inputs.
 """

@@ -154,7 +154,8 @@ __device__ __forceinline__ bool quantise(const Raw<T> &raw, float mul, uint2 &co
 // at all, so every block first looks at all the page ids its request needs.
 //
 // Bound: 2.56 bytes per bf16 element against about 8 instructions; at the first version's 13 (an element's NaN
-// looked at on its own, 64-bit index divisions) issue bound it, 62 us for 168 MB of input.
+// looked at on its own, 64-bit index divisions) issue bound it, 62 us for 168 MB of input; 47 us now, at 74 % of
+// the issue rate of the cycles with work and 0.68 of the measured HBM rate.
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads, sizeof(T) == 2 ? 5 : 4) kv4_append_kernel(Kv4RowsArgs a) {
   const int b = blockIdx.y, tid = threadIdx.x;
@@ -227,6 +228,7 @@ __device__ __forceinline__ void store_group(__nv_bfloat16 *p, const float (&x)[1
 
 // The reverse: rows first[b] + j, j < counts[b], as T; rows from counts[b] on are zeros.  The values are
 // exact in both types (6 significant bits times a power of two).
+// Bound by HBM (0.66 of its measured rate: 215 MB in 48 us).
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4RowsArgs a) {
   const int b = blockIdx.y, tid = threadIdx.x;

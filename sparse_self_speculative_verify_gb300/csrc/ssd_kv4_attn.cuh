@@ -20,9 +20,12 @@
 // fragment column stands for is free for K as long as Q is laid out alike, and for V it only permutes the
 // output rows, so a lane reads consecutive bytes of both.  P^T is S^T's fragment transposed (movmatrix).
 //
-// What bounds it: instructions, about 600 per tile of a head at d = 128 and up to 8 rows, 256 of them the
-// conversions (HBM delivers a tile in 195 clocks an SM).  With more rows the O accumulators leave room for
-// few warps, and the kernel of ssd_kv4_tc.cuh takes over at d = 128.
+// What bounds it: its steady loop takes 185 clocks a tile and SM, what HBM takes to deliver one (195), at about
+// 600 instructions, 256 of them the conversions; the rest is the start (5 us), merges and joins where
+// blocks change units (4 us each), and blocks ending apart.  8 heads of d = 128, 4 rows each: 32 requests of
+// 2048 to 8192 tokens 48 us (59 % of the measured HBM rate), 128 such requests 154 us (73 %), 8 of 65536 tokens
+// 114 us (78 %).  With more rows the O accumulators leave room for few warps, and the kernel of ssd_kv4_tc.cuh
+// takes over at d = 128.
 #pragma once
 
 #include "ssd_kv4.cuh"

@@ -11,6 +11,11 @@
 // and head at 20 rows and 800 for the K half alone of the criticality; converting 144 bytes to 512 takes
 // about 350 whatever the rows.
 //
+// What bounds it: instructions.  A tile takes about 1000 per warp's 32 tokens (V's conversion 260, K's 200, the
+// softmax and its probabilities 160, loads 75), at two thirds of the issue rate; the MMAs fill 40 % of their pipe.
+// 8 heads, 20 rows: 32 requests of 2048 to 8192 tokens 80 us (36 % of the measured HBM rate; mma.sync took 120),
+// 8 requests of 131072 tokens 335 us (53 %).
+//
 // Roles of a block (two blocks share an SM, each filling the other's gaps):
 //   warps 0-7  two groups of four (a group covers the 128 lanes), each with half of every step:
 //              K: a thread converts 64 d of a token's row into its TMEM lane;
@@ -687,7 +692,8 @@ struct Kv4CritCfg {
 // the first pass would cost 2 R bytes per token each way, more than K's 72 for R > 18, and a rounding to
 // f16.)
 //
-// CR: columns that hold rows (the MMA takes NP).  Four blocks share an SM.
+// CR: columns that hold rows (the MMA takes NP).  Four blocks share an SM (two, and one S^T: attention and
+// criticality of 32 requests of 2048 to 8192 tokens, 8 heads, 20 rows, took 134 us instead of 128).
 template <int NP, int CR, int QS, int BPS>
 __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(Kv4AttnArgs a) {
   using C = Kv4CritCfg<NP, QS>;
