@@ -7,8 +7,9 @@ namespace ssd {
 template <int NP, int CW, int QS, int PS>
 static int launch_tc(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
   constexpr auto kernel = kv4_tc_kernel<NP, CW, QS, PS>;
-  constexpr int smem = Kv4TcCfg<NP, QS>::kSmem;
+  constexpr int smem = Kv4TcCfg<NP, QS, PS>::kSmem;
   int rc = ensure_smem<kernel>(smem);
+  static_assert(smem * 2 <= 225 * 1024, "the blocks of an SM fit");
   if (rc) return rc;
   return launch(kernel, dim3(grid), dim3(kKv4TcWarps * 32), smem, st, "kv4_tc_kernel", a);
 }
@@ -35,10 +36,9 @@ static int launch_crit_types(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
   return a.q_f32 ? launch_crit<NP, CR, 2>(a, grid, st) : launch_crit<NP, CR, 1>(a, grid, st);
 }
 
-// rows: of a pass (at most 32).
+// rows: of a pass (more than 8, at most 32).
 int kv4_tc_attn(const Kv4AttnArgs &a, int rows, int grid, cudaStream_t st) {
-  return rows <= 8    ? launch_types<16, 4>(a, grid, st)
-         : rows <= 16 ? launch_types<16, 8>(a, grid, st)
+  return rows <= 16   ? launch_types<16, 8>(a, grid, st)
          : rows <= 24 ? launch_types<32, 12>(a, grid, st)
                       : launch_types<32, 16>(a, grid, st);
 }

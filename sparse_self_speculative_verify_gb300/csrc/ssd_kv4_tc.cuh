@@ -36,9 +36,15 @@ namespace ssd {
 constexpr int kKv4TcTile = 128;
 constexpr int kKv4TcWarps = 10;
 
-template <int NP, int QS>
+// For fp32 outputs O^T leaves tensor memory every so many tiles, to be added up in shared memory: the tensor cores add
+// with truncation, and over a block's whole part of a context that grew to 3.0e-6 of the output (relative 2-norm; a
+// plain fp32 computation is off by 1.2e-6).  Every 8 tiles 2.0e-6, 4 tiles 1.0e-6, 2 tiles 0.6e-6; the round 116.5 us
+// without, 119, 119.7, 121.
+constexpr int kKv4TcFlush = 4;
+
+template <int NP, int QS, int PS>
 struct Kv4TcCfg {
-  static constexpr int kStages = QS == 1 ? 4 : 3;  // raw tiles: two blocks' shared memory fits an SM
+  static constexpr int kStages = PS == 1 ? 4 : 3;  // raw tiles: two blocks' shared memory fits an SM
   // raw stage: K codes, V codes (64 bytes a token, 16-byte pieces permuted), K scales, V scales
   static constexpr int kCodes = kKv4TcTile * 64, kScales = kKv4TcTile * 8;
   static constexpr int kVCodes = kCodes, kKScales = 2 * kCodes, kVScales = 2 * kCodes + kScales;
@@ -47,7 +53,8 @@ struct Kv4TcCfg {
   static constexpr int kQ = kP + kKv4TcTile * 128;
   static constexpr int kQBytes = NP * 256;          // one part of Q: two panels of 64 d
   static constexpr int kSv = kQ + QS * kQBytes;     // V scales as f16 [2][8 groups][128 tokens]
-  static constexpr int kMisc = kSv + 2 * 8 * kKv4TcTile * 2;
+  static constexpr int kO = kSv + 2 * 8 * kKv4TcTile * 2;  // O^T so far [NP][128]
+  static constexpr int kMisc = kO + (PS == 2 ? NP * 128 * 4 : 0);
   // per row: factor, reference, change of it, final reference, join's three; per warp and row: two
   static constexpr int kSmem = kMisc + (7 * NP + 8 * NP) * 4 + 32 * 8 + 64 + 1024;
   static constexpr int kTmem = 256;
@@ -107,13 +114,12 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, float *v) {
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t *r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
-// N = 4, 8, 12 or 16 columns.
+// N = 8, 12 or 16 columns.
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, float *v) {
   if (N == 16) tmem_ld16(taddr, v);
   if (N == 8 || N == 12) tmem_ld8(taddr, v);
   if (N == 12) tmem_ld4(taddr + 8, v + 8);
-  if (N == 4) tmem_ld4(taddr, v);
 }
 template <int N>
 __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float *v) {
@@ -121,7 +127,6 @@ __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float *v) {
   if (N == 16) tmem_st16(taddr, r);
   if (N == 8 || N == 12) tmem_st8(taddr, r);
   if (N == 12) tmem_st4(taddr + 8, r + 8);
-  if (N == 4) tmem_st4(taddr, r);
 }
 // 16 lanes x 16 columns: register 2 j + e of lane 4 r + c is row r + 8 e, column 4 j + c.
 __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t *r) {
@@ -284,7 +289,7 @@ __device__ __forceinline__ void kv4_tc_stage_q(const Kv4AttnArgs &a, int b, int 
 // softmax of padding is not worth its instructions.
 template <int NP, int CW, int QS, int PS>
 __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs a) {
-  using C = Kv4TcCfg<NP, QS>;
+  using C = Kv4TcCfg<NP, QS, PS>;
   constexpr int H = NP / 2;
   using namespace sm100;
   extern __shared__ __align__(16) char smem_raw[];
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
         wait(b_p, n);
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t vt = tmu + C::kColV + (n & 1) * 64, acc = t > s.t0 ? 1u : 0u;
+          const uint32_t vt = tmu + C::kColV + (n & 1) * 64, acc = (PS == 2 ? (t - s.t0) % kKv4TcFlush != 0 : t > s.t0) ? 1u : 0u;
           // The parts of P are panels' columns [0, NP) and [NP, 2 NP).
 #pragma unroll
           for (int q = 0; q < PS; ++q)
@@ -533,6 +538,16 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
         for (int q = 0; q < CW; ++q) top = fmaxf(top, x[q]);
         const bool moved = group_any(bar, 128, top > kKv4Slack);  // (and the next V scales are staged)
         if (n > 0) wait(b_pv, n - 1);  // P, O and the other V^T are free
+        const bool flush = PS == 2 && t > s.t0 && (t - s.t0) % kKv4TcFlush == 0;
+        float *so = reinterpret_cast<float *>(sm + C::kO) + c0 * 128 + tw;  // this lane's [CW]
+        if (flush) {
+          tc_fence_after();
+          float o[CW];
+          tmem_ld_n<CW>(tm + lanes + C::kColO + c0, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < CW; ++k) so[k * 128] = t == s.t0 + kKv4TcFlush ? o[k] : so[k * 128] + o[k];
+        }
         if (moved) {
           // The references move up to the tile's largest logits; O and the sums follow.
 #pragma unroll
@@ -551,7 +566,11 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
           named_sync(bar, 128);
 #pragma unroll
           for (int q = 0; q < CW; ++q) x[q] -= s_f[c0 + q], l[q] *= fast_exp2(-s_f[c0 + q]);
-          if (t > s.t0) {
+          if (PS == 2 && t - s.t0 >= kKv4TcFlush) {
+#pragma unroll
+            for (int k = 0; k < CW; ++k) so[k * 128] *= fast_exp2(-s_f[c0 + k]);
+          }
+          if (t > s.t0 && !flush) {
             tc_fence_after();
             float o[CW];
             tmem_ld_n<CW>(tm + lanes + C::kColO + c0, o);
@@ -627,6 +646,11 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
         float o[CW];
         tmem_ld_n<CW>(tm + lanes + C::kColO + h * H, o);
         tmem_ld_wait();
+        if (PS == 2 && s.t1 - s.t0 > kKv4TcFlush) {
+          const float *so = reinterpret_cast<const float *>(sm + C::kO) + h * H * 128 + tw;
+#pragma unroll
+          for (int k = 0; k < CW; ++k) o[k] += so[k * 128];
+        }
 #pragma unroll
         for (int k = 0; k < CW; ++k) {
           const int q = h * CW + k;
