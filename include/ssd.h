@@ -408,6 +408,8 @@ int ssd_kv4_read(const ssd_paged_kv *kv, const int32_t *first, const int32_t *co
  *        carried in f16 (2^-12 relative) for a bf16 out and in 22 bits for an fp32 out or q.
  *   scores  as in ssd_verify_attn, or NULL.
  *   workspace  device, >= the matching query's bytes, 256-byte aligned.
+ * At most 64 query rows per KV head (h_q / h_kv * n_cand; 16 in a draft), 65535 (request, KV head) pairs and 2^24
+ * tokens (max_seq_len, k_max).
  */
 size_t ssd_kv4_verify_workspace_bytes(const ssd_paged_kv *kv, int h_q, int n_cand);
 int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_dtype, int h_q, int n_cand, float scale,

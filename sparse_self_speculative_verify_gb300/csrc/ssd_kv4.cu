@@ -42,6 +42,7 @@ static Kv4Layout kv4_layout(const ssd_paged_kv *kv, int h_q, int n_rows, int max
   return y;
 }
 
+constexpr int kMaxList = 1 << 24;  // as max_seq_len: positions, and tiles past their end, stay in 32 bits
 static bool kv4_shape_ok(const ssd_paged_kv *kv, int h_q, int n) {
   return kv && kv->h_kv > 0 && h_q > 0 && h_q % kv->h_kv == 0 && n > 0 && kv->batch >= 0 && kv->max_seq_len >= 0 &&
          (kv->d == 64 || kv->d == 128) && (int64_t)(h_q / kv->h_kv) * n <= kMaxRows;
@@ -151,7 +152,7 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
 }
 
 extern "C" size_t ssd_kv4_draft_workspace_bytes(const ssd_paged_kv *kv, int h_q, int k_max) {
-  return kv4_shape_ok(kv, h_q, 1) && k_max >= 0 ? kv4_layout(kv, h_q, 1, k_max).total : 0;
+  return kv4_shape_ok(kv, h_q, 1) && k_max >= 0 && k_max <= kMaxList ? kv4_layout(kv, h_q, 1, k_max).total : 0;
 }
 
 extern "C" int ssd_kv4_draft_attn(const ssd_paged_kv *kv, const void *q, int q_dtype, int h_q, const int32_t *idx, int k_max,
@@ -162,6 +163,7 @@ extern "C" int ssd_kv4_draft_attn(const ssd_paged_kv *kv, const void *q, int q_d
   Kv4AttnArgs a{};
   Kv4Layout lay;
   if (k_max < 0) return fail(SSD_ERR_INVALID_ARG, "%s: k_max < 0", who);
+  if (k_max > kMaxList) return fail(SSD_ERR_UNSUPPORTED, "%s: k_max above 2^24", who);
   int rc = kv4_prepare(c, k_max, &a, &lay, who);
   if (rc) return rc;
   if (!cnt || (!idx && k_max > 0)) return fail(SSD_ERR_INVALID_ARG, "%s: idx and cnt must be non-NULL", who);

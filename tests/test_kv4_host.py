@@ -89,6 +89,17 @@ def test_attention_arguments(lib):
     assert _verify(lib, empty) == OK and _draft(lib, empty) == OK  # nothing to do, nothing launched
 
 
+def test_attention_limits(lib):
+    """What the kernels' 32-bit positions, rows and grids do not hold is refused before a launch."""
+    far = dict(max_pages=1 << 27, max_seq_len=(1 << 24) + 1)
+    for call in (_verify, _draft):
+        assert call(lib, ctypes.byref(_kv(**far))) == U and b"2^24" in lib.ssd_last_error()
+        assert call(lib, ctypes.byref(_kv(batch=8192))) == U
+    assert _draft(lib, ctypes.byref(_kv()), k=(1 << 24) + 1) == U
+    assert _verify(lib, ctypes.byref(_kv()), n=17) == U  # 68 rows
+    assert _draft(lib, ctypes.byref(_kv(h_kv=1)), h_q=17) == U
+
+
 def test_workspace_queries(lib):
     kv = _kv()
     a = lib.ssd_kv4_verify_workspace_bytes(ctypes.byref(kv), 32, 5)
