@@ -10,7 +10,7 @@ namespace ssd {
 
 int kv4_dense_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
 int kv4_dense_d128(const Kv4AttnArgs &a, int grid, cudaStream_t st);
-int kv4_tc_attn(const Kv4AttnArgs &a, int rows, int grid, cudaStream_t st);
+int kv4_tc_attn(Kv4AttnArgs a, int rows, int grid, cudaStream_t st);
 int kv4_tc_crit(const Kv4AttnArgs &a, int grid, cudaStream_t st);
 int kv4_list_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);
 int kv4_list_d128(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st);

@@ -59,6 +59,7 @@ struct Kv4AttnArgs {
   int64_t scores_stride;
   const float *lse_in;    // criticality pass
   int n_units;            // batch * h_kv * n_chunk
+  int join_blocks;        // tcgen05: blocks whose parts kv4_join_kernel joins, or 0: the last block of a unit does
   unsigned *status;
 };
 
@@ -133,6 +134,11 @@ struct Kv4Parts {
   }
   __device__ __forceinline__ int64_t slot(int k) const { return k ? (int64_t)(first + k) * 2 : (int64_t)first * 2 + 1; }
 };
+// Length of a block's stretch of the line.  least: a tile for every warp before another block is used.
+__device__ __forceinline__ int64_t kv4_per(int64_t total, int blocks, int least) {
+  const int64_t per = (total + blocks - 1) / blocks;
+  return per < least ? least : per;
+}
 // Returns false when the block has no tile.
 template <bool LIST, int NW, int TILE = kKv4Tile, int MIN = NW>
 __device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int64_t *s_scan /* [NW + 4] */) {
@@ -157,9 +163,7 @@ __device__ __forceinline__ bool kv4_range(const Kv4AttnArgs &a, Kv4Range &r, int
     if (w < warp) base += v;
     total += v;
   }
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < MIN) per = MIN;  // MIN = NW: a tile for every warp before another block is used
-  r.per = per;
+  const int64_t per = r.per = kv4_per(total, gridDim.x, MIN);
   const int64_t excl = base + inc - sum;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {

@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
       }
       tc_fence_before();
       arrive(b_lfree);
-      if (!whole) {
+      if (!whole && !a.join_blocks) {
         // The last block of the unit to arrive joins the partial results.
         named_sync(2, 128);
         if (tw == 0) {
@@ -692,6 +692,71 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
   __syncthreads();
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tm, C::kTmem);
+}
+
+// Joins the units' parts where a unit has many: a warp per row of a unit, 16 parts' loads on their way at once.  The
+// last block's 128 threads took 12 us for 17 parts of 20 rows and would take 19 for the 38 of a single long request.
+constexpr int kKv4JoinRows = 4;          // per block
+constexpr int kKv4JoinMost = 64;         // units
+template <int NP>
+__global__ void __launch_bounds__(kKv4JoinRows * 32) kv4_join_kernel(Kv4AttnArgs a) {
+  constexpr int LEAD = kKv4Lead<kKv4TcTile>;
+  const int lane = threadIdx.x & 31, u = blockIdx.y, q = blockIdx.x * kKv4JoinRows + (threadIdx.x >> 5);
+  pdl_wait();
+  // The unit's place in the line, as kv4_range has it.
+  int64_t at = 0, total = 0;
+#pragma unroll
+  for (int k = 0; k < kKv4JoinMost; k += 32) {
+    const int64_t own = k + lane < a.n_units ? kv4_tiles<false, kKv4TcTile>(a, k + lane) + LEAD : 0;
+    int64_t inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const int64_t before = __shfl_sync(0xffffffffu, total + inc - own, u & 31);
+    if (u >> 5 == k >> 5) at = before;
+    total += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  Kv4Range r;
+  r.per = kv4_per(total, a.join_blocks, 1);
+  const Kv4Parts<kKv4TcTile> parts(r, at, kv4_tiles<false, kKv4TcTile>(a, u));
+  const int r0 = u % a.n_chunk * 32;
+  if (parts.more == 0 || q >= min(32, a.R - r0)) return;
+  const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
+  const float4 *po = reinterpret_cast<const float4 *>(a.part_o);
+  float M = -1e30f, Z = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int U = 16;
+  for (int k0 = 0; k0 <= parts.more; k0 += U) {
+    float2 v[U];
+    float4 y[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      v[k] = make_float2(-1e30f, 0.f), y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k <= parts.more) {
+        const int64_t row = parts.slot(k0 + k) * NP + q;
+        v[k] = __ldcg(ml + row), y[k] = __ldcg(po + row * 32 + lane);
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < U; ++k) top = fmaxf(top, v[k].x);
+    const float f0 = fast_exp2(M - top);
+    Z *= f0, acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+    M = top;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const float f = fast_exp2(v[k].x - M);
+      Z = fmaf(v[k].y, f, Z);
+      acc.x = fmaf(y[k].x, f, acc.x), acc.y = fmaf(y[k].y, f, acc.y), acc.z = fmaf(y[k].z, f, acc.z), acc.w = fmaf(y[k].w, f, acc.w);
+    }
+  }
+  const int rr = r0 + q, unit = u / a.n_chunk, b = unit / a.kv.h_kv, g = unit % a.kv.h_kv;
+  const int64_t row = ((int64_t)b * a.n_c + rr / a.G) * a.h_q + g * a.G + rr % a.G;
+  const float f = Z == 0.f ? 0.f : a.v_scale / Z;
+  kv4_write4(a, row * 128 + lane * 4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+  if (lane == 0 && a.lse) a.lse[row] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
 }
 
 // ---- criticality ------------------------------------------------------------------------------
