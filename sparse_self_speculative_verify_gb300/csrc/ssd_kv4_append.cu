@@ -99,23 +99,37 @@ struct Raw<__nv_bfloat16> {
   }
 };
 
-// Eight values over the group's scale s (r = 1 / s, rounded) as codes.  fp32 inputs take the IEEE division.
-// bf16 inputs (8 significant bits) take x r, off by less than 2^-22 relative, rounded to a multiple of 2^-10
-// by adding and taking away 1.5 * 2^13: x / s is either one of e2m1's ties (multiples of 1/4, with s's 4 bits
-// at most 7 significant bits, so the rounding restores it exactly) or at least 2^-8 relative, so 2^-10,
-// away from every tie, and the code is that of the exact quotient.  (Above 8 the spacing is wider, but
-// everything there is 6.)
+// A group's scale byte, e4m3(m mul / 6) of its largest magnitude m, and eight values x mul over the scale s as codes.
+// fp32 inputs take IEEE divisions.  For bf16 inputs (8 significant bits) the quotients are approximated and
+// rounded to fewer bits first:
+//   m mul / 6, off by less than 2^-22 relative, to 12 significant bits: it is either one of e4m3's ties (at most
+//   5 significant bits, so the rounding restores it exactly) or at least 2^-8 relative away from every tie;
+//   x mul r with r = 1 / s, off by less than 2^-21, to a multiple of 2^-10 by adding and taking away 1.5 * 2^13:
+//   it is either one of e2m1's ties (multiples of 1/4) or at least 2^-8 relative, so 2^-10, away from every
+//   tie.  (Above 8 the spacing is wider, but everything there is 6.)
+// The bytes are those of the exact quotients either way.
 template <typename T>
-__device__ __forceinline__ uint32_t codes_of(const float *x, float s, float r);
+__device__ __forceinline__ uint32_t scale_of(float m, float mul);
 template <>
-__device__ __forceinline__ uint32_t codes_of<float>(const float *x, float s, float r) {
+__device__ __forceinline__ uint32_t scale_of<float>(float m, float mul) {
+  return f32_to_e4m3(__fdiv_rn(m * mul, 6.f));
+}
+template <>
+__device__ __forceinline__ uint32_t scale_of<__nv_bfloat16>(float m, float mul) {
+  return f32_to_e4m3(__uint_as_float((__float_as_uint(m * mul * (1.f / 6.f)) + 0x400u) & 0xfffff800u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t codes_of(const float *x, float mul, float s);
+template <>
+__device__ __forceinline__ uint32_t codes_of<float>(const float *x, float mul, float s) {
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i] * mul, s);
   return f32_to_e2m1(y);
 }
 template <>
-__device__ __forceinline__ uint32_t codes_of<__nv_bfloat16>(const float *x, float s, float r) {
+__device__ __forceinline__ uint32_t codes_of<__nv_bfloat16>(const float *x, float mul, float s) {
+  const float r = __fdividef(mul, s);
   constexpr float C = 12288.f;
   float y[8];
 #pragma unroll
@@ -138,14 +152,9 @@ __device__ __forceinline__ bool quantise(const Raw<T> &raw, float mul, uint2 &co
       amax = fmaxf(amax, fabsf(x[i]));
     }
   }
-  sc = f32_to_e4m3(__fdiv_rn(amax * mul, 6.f));
+  sc = scale_of<T>(amax, mul);
   const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(sc) & 0xffffu)));
-  const float r = __frcp_rn(s);
-  if (mul != 1.f) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] *= mul;
-  }
-  codes = s > 0.f ? make_uint2(codes_of<T>(x, s, r), codes_of<T>(x + 8, s, r)) : make_uint2(0, 0);
+  codes = s > 0.f ? make_uint2(codes_of<T>(x, mul, s), codes_of<T>(x + 8, mul, s)) : make_uint2(0, 0);
   return bad;
 }
 
@@ -154,8 +163,8 @@ __device__ __forceinline__ bool quantise(const Raw<T> &raw, float mul, uint2 &co
 // at all, so every block first looks at all the page ids its request needs.
 //
 // Bound: 2.56 bytes per bf16 element against about 8 instructions; at the first version's 13 (an element's NaN
-// looked at on its own, 64-bit index divisions) issue bound it, 62 us for 168 MB of input; 47 us now, at 74 % of
-// the issue rate of the cycles with work and 0.68 of the measured HBM rate.
+// looked at on its own, 64-bit index divisions) issue bound it, 62 us for 168 MB of input; 45 us now, 0.7 of the
+// measured HBM rate, at 60 % of the issue rate.
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads, sizeof(T) == 2 ? 5 : 4) kv4_append_kernel(Kv4RowsArgs a) {
   const int b = blockIdx.y, tid = threadIdx.x;
@@ -228,7 +237,8 @@ __device__ __forceinline__ void store_group(__nv_bfloat16 *p, const float (&x)[1
 
 // The reverse: rows first[b] + j, j < counts[b], as T; rows from counts[b] on are zeros.  The values are
 // exact in both types (6 significant bits times a power of two).
-// Bound by HBM (0.66 of its measured rate: 215 MB in 48 us).
+// Bound by HBM: 8 requests of up to 8192 rows of 8 heads of 128, 53 MB read and 268 MB written (rows behind the counts
+// included) in 49 us, 0.97 of its measured rate.
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4RowsArgs a) {
   const int b = blockIdx.y, tid = threadIdx.x;
@@ -297,12 +307,12 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4RowsArgs a) {
   }
 }
 
-// Tokens per block: enough groups for the threads, more (up to eight steps each) while the grid still covers the
-// SMs eight times.
+// Tokens per block: enough groups for the threads, more (up to four steps each) while the grid still covers the
+// SMs eight times.  (8 prompts of up to 8192 tokens, 1 / 2 / 4 / 8 / 16 steps: 104 / 96 / 95 / 97 / 109 us with the read.)
 static int tokens_per_block(const ssd_paged_kv *kv, int n) {
   const int64_t per_token = (int64_t)kv->h_kv * (kv->d / kKv4Group);
   int64_t steps = per_token * n * kv->batch / ((int64_t)sm_count() * 8 * kKv4Threads);
-  steps = steps < 1 ? 1 : (steps > 8 ? 8 : steps);
+  steps = steps < 1 ? 1 : (steps > 4 ? 4 : steps);
   int64_t t = steps * kKv4Threads / per_token;
   const int64_t least = cdiv64(n, 65535 * 16);  // grid.x stays far below its limit
   t = t < least ? least : t;

@@ -131,6 +131,37 @@ def test_append_of_nan_and_infinities(dtype):
     assert ssd_status() == 0
 
 
+@pytest.mark.parametrize("mul", [1.0, 2.0 ** -20, 2.0 ** 32])
+def test_every_bf16_as_the_largest_of_a_group(mul):
+    """Scales of all 32640 finite magnitudes, and codes of multiples and neighbours of e2m1's ties under them."""
+    _gpu.lib()
+    d, page, h = 128, 64, 1
+    top = np.arange(0, 0x7f80, dtype=np.uint16).view(np.int16)
+    rng = np.random.default_rng(3)
+    frac = rng.choice([0.25 / 6, 0.75 / 6, 1.25 / 6, 1.75 / 6, 2.5 / 6, 3.5 / 6, 5.0 / 6], (len(top), 16)) * rng.choice([1.0, -1.0], (len(top), 16))
+    m = torch.from_numpy(top.copy()).view(torch.bfloat16)
+    x = (m.double()[:, None] * torch.from_numpy(frac)).to(torch.bfloat16)
+    near = torch.from_numpy(rng.integers(-1, 2, x.shape).astype(np.int16))
+    x = torch.where(x.abs() > 1e-30, (x.view(torch.int16) + near).view(torch.bfloat16), x)
+    x = torch.where(x.abs() > m[:, None], m[:, None], x)
+    x[:, 5] = m
+    n = len(top) // 8
+    rows = x.view(1, n, h, d)
+    kv, pool, table = _cache([0], h, d, page, room=n, seed=34, k_scale=mul, v_scale=mul)
+    ssd_kv4_append(kv, rows.to(DEV), rows.flip(1).contiguous().to(DEV))
+    k, v = ssd_kv4_read(kv, kv.seq_lens, n, dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert ssd_status() == 0
+    c, s = _kv4.quantise(rows.double().numpy(), mul)
+    want = _kv4.values(c, s, mul)
+    np.testing.assert_array_equal(k.double().cpu().numpy(), want)
+    np.testing.assert_array_equal(v.double().cpu().numpy(), want[:, ::-1])
+    got = kv.pool.cpu().numpy()[table[0, 0], 0, 0].reshape(-1)  # bytes of the first page's K rows
+    want = np.zeros((page, d // 2), np.uint8)
+    want[:] = c[0, :page, 0, 0::2] | (c[0, :page, 0, 1::2] << 4)
+    np.testing.assert_array_equal(got[:page * d // 2], want.reshape(-1))
+
+
 def test_append_and_read_out_of_range():
     _gpu.lib()
     h, d, page = 2, 128, 16
