@@ -182,6 +182,7 @@ class KVCache:
             self.page_table.data_ptr(), self.page_table.shape[1], self.seq_lens.data_ptr(),
             self.seq_lens.shape[0], int(self.max_seq_len))
         self._geometry = (self.pool.get_device(), self.batch, self.h_kv, self.d)
+        self._ref = ctypes.byref(self._struct)
 
     @property
     def h_kv(self) -> int:
@@ -200,7 +201,7 @@ class KVCache:
         return self.pool.device
 
     def ref(self):
-        return ctypes.byref(self._struct)
+        return self._ref
 
     @classmethod
     def from_workload(cls, w) -> "KVCache":
@@ -631,6 +632,7 @@ class KV4Cache:
             int(self.max_seq_len))
         self.k_scale, self.v_scale = float(self.k_scale), float(self.v_scale)
         self._geometry = (self.pool.get_device(), self.batch, self.h_kv, self.d)
+        self._ref = ctypes.byref(self._struct)
         self._need = {}  # workspace bytes of the calls' shapes
 
     @staticmethod
@@ -654,19 +656,23 @@ class KV4Cache:
         return self.pool.device
 
     def ref(self):
-        return ctypes.byref(self._struct)
+        return self._ref
 
 
 _TYPES = {torch.float32: SSD_DTYPE_F32, torch.bfloat16: SSD_DTYPE_BF16}
 _HERE = contextlib.nullcontext()
-# The current stream's handle without a Stream object (1 us of a call that takes 10).
+_Tensor = torch.Tensor
+# What torch.cuda.current_stream, current_device and is_current_stream_capturing ask, without their objects and
+# initialisation checks (a cache's tensors are on the device already): 1.5 us of a call that took 11.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _scope(device: int, stream):
     """The cache's device and the call's stream current, for allocations as for launches."""
     if stream is None:
-        return _HERE if torch.cuda.current_device() == device else torch.cuda.device(device)
+        return _HERE if _current_device() == device else torch.cuda.device(device)
     if stream.device_index != device:
         raise ValueError(f"stream is on cuda:{stream.device_index}, expected cuda:{device}")
     return torch.cuda.stream(stream)
@@ -674,11 +680,10 @@ def _scope(device: int, stream):
 
 def _shaped(t, name: str, dtype, device: int, shape) -> int:
     """Address of a contiguous tensor of that type, device and shape."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous()):
-        _need(t, name, dtype, torch.device("cuda", device))  # says what is wrong
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr()
+    _need(t, name, dtype, torch.device("cuda", device))  # says what is wrong
+    raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _maybe(t, name: str, dtype, device: int, shape) -> Optional[int]:
@@ -686,11 +691,10 @@ def _maybe(t, name: str, dtype, device: int, shape) -> Optional[int]:
 
 
 def _typed(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _TYPES:
-        raise TypeError(f"{name} must be bf16 or fp32, got {t.dtype}")
-    return _TYPES[t.dtype]
+    code = _TYPES.get(t.dtype) if isinstance(t, _Tensor) else None
+    if code is None:
+        raise TypeError(f"{name} must be a bf16 or fp32 torch.Tensor, got {t.dtype if isinstance(t, _Tensor) else type(t).__name__}")
+    return code
 
 
 def _is_kv4(kv):
@@ -708,7 +712,7 @@ def _stream_ws(device: int, name: str, nbytes: int, workspace: Optional[Workspac
     sized before a capture that uses it and must outlive the graph."""
     if workspace is not None:
         return _ws(torch.device("cuda", device), name, nbytes, workspace)
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing():
         buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
         buf[:COUNTER_BYTES + 256].zero_()
         return Workspace.aligned(buf), nbytes
@@ -863,7 +867,7 @@ def _pages_of(kv, pages: PagePool) -> int:
         raise TypeError(f"kv must be a KVCache or a KV4Cache, got {type(kv).__name__}")
     if not isinstance(pages, PagePool):
         raise TypeError(f"pages must be a PagePool, got {type(pages).__name__}")
-    return _shaped(pages.refs, "pages.refs", torch.int32, kv._geometry[0], (kv.pool.shape[0],))
+    return _shaped(pages.refs, "pages.refs", torch.int32, kv._geometry[0], (kv._struct.num_pages,))
 
 
 def _count(t: torch.Tensor, name: str) -> int:
