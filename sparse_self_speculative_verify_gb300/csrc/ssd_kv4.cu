@@ -102,9 +102,11 @@ static int kv4_grid(int64_t units, int max_tokens, int tile, int blocks_per_sm) 
   return (int)(bound < dev ? bound : dev);
 }
 
-static int kv4_blocks_per_sm(int nt) {
-  return nt == 1 ? Kv4Tune<1>::kBlocks : nt == 2 ? Kv4Tune<2>::kBlocks : nt == 3 ? Kv4Tune<3>::kBlocks : Kv4Tune<4>::kBlocks;
+template <int D>
+static int kv4_blocks_of(int nt) {
+  return nt == 1 ? Kv4Tune<D, 1>::kBlocks : nt == 2 ? Kv4Tune<D, 2>::kBlocks : nt == 3 ? Kv4Tune<D, 3>::kBlocks : Kv4Tune<D, 4>::kBlocks;
 }
+static int kv4_blocks_per_sm(int d, int nt) { return d == 128 ? kv4_blocks_of<128>(nt) : kv4_blocks_of<64>(nt); }
 
 }  // namespace ssd
 
@@ -135,11 +137,11 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
   // fill half the rows of tcgen05's M = 128.
   const int nt = kv4_nt(a.R);
   if (kv->d == 128 && a.R <= 8)
-    rc = kv4_dense_d128(a, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(nt)), st);
+    rc = kv4_dense_d128(a, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(kv->d, nt)), st);
   else if (kv->d == 128)
     rc = kv4_tc_attn(a, a.R > 32 ? 32 : a.R, kv4_grid(a.n_units, kv->max_seq_len, kKv4TcTile, 2), st);
   else
-    rc = kv4_dense_d64(a, nt, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(nt)), st);
+    rc = kv4_dense_d64(a, nt, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(kv->d, nt)), st);
   if (rc || !scores) return rc;
   a.lse_in = a.lse;
   a.scores = scores;
@@ -172,6 +174,6 @@ extern "C" int ssd_kv4_draft_attn(const ssd_paged_kv *kv, const void *q, int q_d
   if (!(a.status = device_status())) return SSD_ERR_CUDA;
   a.idx = idx, a.cnt = cnt, a.k_max = k_max;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int nt = kv4_nt(a.R), grid = kv4_grid(a.n_units, k_max, kKv4Tile * 4, kv4_blocks_per_sm(nt));
+  const int nt = kv4_nt(a.R), grid = kv4_grid(a.n_units, k_max, kKv4Tile * 4, kv4_blocks_per_sm(kv->d, nt));
   return kv->d == 128 ? kv4_list_d128(a, nt, grid, st) : kv4_list_d64(a, nt, grid, st);
 }

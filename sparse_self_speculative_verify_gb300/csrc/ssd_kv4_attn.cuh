@@ -979,19 +979,22 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
 
 namespace ssd {
 
-// Warps and blocks per SM, and ring depth, by the rows of a pass: registers bound the warps (the O
-// accumulators take 32 NT a lane at d = 128), and the ring also holds the warps' O at a segment's end.
-template <int NT>
+// Warps and blocks per SM, and ring depth, by the rows of a pass: registers bound the warps (the O accumulators take
+// 32 NT a lane at d = 128, 16 NT at d = 64), and the ring also holds the warps' O at a segment's end.  d = 64, 32
+// requests of 2048 to 8192 tokens, 8 heads: 16 rows 44 us with two blocks of 8 warps, 52 with one; 20 rows 65 with 8
+// warps, 62 with 12, 60 with two blocks of 8, which spill and take 16.5 us instead of 15 for a short request; 32
+// rows 76 with 8 warps, 84 with 12, 106 with two blocks of 8; 4 rows 34.4 with two blocks, 36.5 with three.
+template <int D, int NT>
 struct Kv4Tune {
-  static constexpr int kWarps = 8;
-  static constexpr int kBlocks = NT == 1 ? 2 : 1;
+  static constexpr int kWarps = D == 64 && NT == 3 ? 12 : 8;
+  static constexpr int kBlocks = NT == 1 || (D == 64 && NT == 2) ? 2 : 1;
   static constexpr int kStages = NT == 1 ? 2 : NT == 2 ? 3 : 4;
 };
 constexpr int kKv4CritWarps = 8, kKv4CritBlocks = 2, kKv4CritStages = 4;
 
 template <int D, int NT, int QS, int PS, bool LIST>
 int kv4_launch_attn(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
-  constexpr int NST = Kv4Tune<NT>::kStages, BPS = Kv4Tune<NT>::kBlocks, NW = Kv4Tune<NT>::kWarps;
+  constexpr int NST = Kv4Tune<D, NT>::kStages, BPS = Kv4Tune<D, NT>::kBlocks, NW = Kv4Tune<D, NT>::kWarps;
   static_assert(kv4_ahead(NT) || NST * Kv4Smem<D>::kStage >= NT * 8 * D * 4, "the ring holds the warps' O");
   constexpr int smem = kv4_smem_bytes<D, NT, QS, NW, NST>();
   constexpr auto kernel = kv4_attn_kernel<D, NT, QS, PS, NW, NST, BPS, LIST>;
