@@ -29,7 +29,7 @@ static int64_t kv4_grid_bound(int64_t units, int max_tokens, int tile) {
 }
 
 struct Kv4Layout {
-  size_t o, ml, lse, total;
+  size_t o, ml, fin, total;
 };
 static Kv4Layout kv4_layout(const ssd_paged_kv *kv, int h_q, int n_rows, int max_tokens) {
   const int R = h_q / kv->h_kv * n_rows, rows = kv4_np(R);
@@ -37,8 +37,8 @@ static Kv4Layout kv4_layout(const ssd_paged_kv *kv, int h_q, int n_rows, int max
   Kv4Layout y{};
   y.o = kCounterBytes;
   y.ml = y.o + align256(slots * rows * kv->d * sizeof(float));
-  y.lse = y.ml + align256(slots * rows * 2 * sizeof(float));
-  y.total = y.lse + align256((size_t)kv->batch * n_rows * h_q * sizeof(float));
+  y.fin = y.ml + align256(slots * rows * 2 * sizeof(float));
+  y.total = y.fin + align256((size_t)kv->batch * n_rows * h_q * sizeof(float2));
   return y;
 }
 
@@ -129,7 +129,7 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
     return fail(SSD_ERR_INVALID_ARG, "%s: scores_stride %lld < max_seq_len %d", who, (long long)scores_stride, kv->max_seq_len);
   if (kv->batch == 0) return SSD_OK;
   if (!(a.status = device_status())) return SSD_ERR_CUDA;
-  if (scores && !a.lse) a.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + lay.lse);
+  if (scores) a.fin = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + lay.fin);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // d = 128 runs on tcgen05 from 9 rows on.  32 requests of 2048 to 8192 tokens, 8 heads: 4 rows 48 us on mma.sync
   // against 62, 8 rows 49 against 63, 12 rows 70.5 against 68.5 (fp32 outputs: 78 against 70), 16 rows 72
@@ -143,7 +143,6 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
   else
     rc = kv4_dense_d64(a, nt, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(kv->d, nt)), st);
   if (rc || !scores) return rc;
-  a.lse_in = a.lse;
   a.scores = scores;
   a.scores_stride = scores_stride;
   a.n_chunk = 1;

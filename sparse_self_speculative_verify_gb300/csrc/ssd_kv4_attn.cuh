@@ -57,7 +57,7 @@ struct Kv4AttnArgs {
   unsigned *counters;
   float *scores;
   int64_t scores_stride;
-  const float *lse_in;    // criticality pass
+  float2 *fin;            // per query row: its reference and 1 / sum, for the criticality pass; or NULL
   int n_units;            // batch * h_kv * n_chunk
   int join_blocks;        // tcgen05: blocks whose parts kv4_join_kernel joins, or 0: the last block of a unit does
   unsigned *status;
@@ -441,6 +441,13 @@ __device__ __forceinline__ void kv4_write4(const Kv4AttnArgs &a, int64_t elem, c
     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + elem) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
+// A row's log-sum-exp from its reference M and the sum Z of exp2(x - M).  The criticality pass takes M and 1 / Z
+// themselves: exp2(x - M) / Z is off by 1e-7, exp(x - lse) by lse's own rounding, up to 1e-6.
+__device__ __forceinline__ void kv4_row_done(const Kv4AttnArgs &a, int64_t row, float M, float Z) {
+  if (a.lse) a.lse[row] = Z == 0.f ? -INFINITY : (M + log2f(Z)) * kLn2;
+  if (a.fin) a.fin[row] = Z == 0.f ? make_float2(INFINITY, 0.f) : make_float2(M, 1.f / Z);
+}
+
 // Counts a block in, after a barrier of the threads that wrote its part: releases those writes, and lets the last
 // block's threads (after a barrier) see the others'.
 __device__ __forceinline__ unsigned kv4_arrive(unsigned *counter) {
@@ -450,10 +457,10 @@ __device__ __forceinline__ unsigned kv4_arrive(unsigned *counter) {
 }
 
 // Joins the `parts` partial results of a unit's pass, in the blocks' order: part k lies in rows row_of_part(k) .. of
-// part_o / part_ml.  NT threads (whole warps), `sync` their barrier; s_M, s_F, s_L: `rows` floats each.  Several loads
+// part_o / part_ml.  NT threads (whole warps), `sync` their barrier; s_M, s_F, s_Z: `rows` floats each.  Several loads
 // are kept on their way: a part's load behind the last one's took 0.7 us each.
 template <int D, int NT, typename PartRow, typename OutRow, typename Sync>
-__device__ __forceinline__ void kv4_join(const Kv4AttnArgs &a, int parts, int rows, int tid, float *s_M, float *s_F, float *s_L,
+__device__ __forceinline__ void kv4_join(const Kv4AttnArgs &a, int parts, int rows, int tid, float *s_M, float *s_F, float *s_Z,
                                          PartRow part, OutRow row_of, Sync sync) {
   const int lane = tid & 31, warp = tid >> 5;
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
@@ -483,7 +490,7 @@ __device__ __forceinline__ void kv4_join(const Kv4AttnArgs &a, int parts, int ro
       }
       const float f = Z == 0.f ? 0.f : a.v_scale / Z;
       kv4_write4(a, row_of(q) * D + piece * 4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
-      if (piece == 0 && a.lse) a.lse[row_of(q)] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
+      if (piece == 0) kv4_row_done(a, row_of(q), M, Z);
     }
     return;
   }
@@ -511,7 +518,7 @@ __device__ __forceinline__ void kv4_join(const Kv4AttnArgs &a, int parts, int ro
       if (lane == 0) {
         s_M[q] = M;
         s_F[q] = Z == 0.f ? 0.f : a.v_scale / Z;
-        s_L[q] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
+        s_Z[q] = Z;
       }
     }
   }
@@ -540,7 +547,7 @@ __device__ __forceinline__ void kv4_join(const Kv4AttnArgs &a, int parts, int ro
     }
     const float f = s_F[q];
     kv4_write4(a, row_of(q) * D + piece * 4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
-    if (piece == 0 && a.lse) a.lse[row_of(q)] = s_L[q];
+    if (piece == 0) kv4_row_done(a, row_of(q), M, s_Z[q]);
   }
 }
 
@@ -831,7 +838,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
         const int64_t row = row_of(q);
         const float f = Z == 0.f ? 0.f : a.v_scale / Z;
         kv4_write4(a, row * D + piece * 4, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-        if (piece == 0 && a.lse) a.lse[row] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
+        if (piece == 0) kv4_row_done(a, row, M, Z);
       } else {
         __stcg(reinterpret_cast<float4 *>(a.part_o + (slot * ROWS + q) * D) + piece, v);
         if (piece == 0) __stcg(reinterpret_cast<float2 *>(a.part_ml) + slot * ROWS + q, make_float2(M, Z));
@@ -867,11 +874,11 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
   char *ring = smem;
   char *qf = ring + NW * NST * S::kCritStage;
   float *s_sl = reinterpret_cast<float *>(qf + 2 * ROWS * D * 2 * QS);  // two chunks of rows at most
-  float *s_lse = s_sl + 2 * ROWS;
+  float *s_ref = s_sl + 2 * ROWS, *s_inv = s_ref + 2 * ROWS;
   __shared__ int64_t s_scan[NW + 4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, col = lane & 3;
-  // Everything but lse was written before the attention kernel ran, which waited for it and only then let
-  // this one start; lse is waited for below.
+  // Everything but a.fin was written before the attention kernel ran, which waited for it and only then let
+  // this one start; a.fin is waited for below.
   Kv4Range rg;
   if (!kv4_range<false, NW>(a, rg, s_scan)) {
     pdl_wait();
@@ -909,12 +916,9 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
     }
     pdl_wait();
     for (int q = tid; q < n_chunk * ROWS; q += NW * 32) {
-      float v = INFINITY;  // rows that see nothing, and the padding: exp(x - inf) = 0
-      if (q < a.R) {
-        v = a.lse_in[((int64_t)b * a.n_c + q / a.G) * a.h_q + g * a.G + q % a.G];
-        v = v == -INFINITY ? INFINITY : v * kLog2e;
-      }
-      s_lse[q] = v;
+      float2 v = make_float2(INFINITY, 0.f);  // the padding, as rows that see nothing: exp2(x - inf) = 0
+      if (q < a.R) v = a.fin[((int64_t)b * a.n_c + q / a.G) * a.h_q + g * a.G + q % a.G];
+      s_ref[q] = v.x, s_inv[q] = v.y;
     }
     __syncthreads();
     for (int tile = seg0 + warp; tile < seg1; tile += NW) {
@@ -927,7 +931,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
       for (int ch = 0; ch < n_chunk; ++ch) {
         float c[2][NT][4];
         kv4_qk<D, NT, QS>(c, kt, kt + S::kCritScales, qf + ch * ROWS * D * 2 * QS, lane);
-        const float *fac = s_sl + ch * ROWS + 2 * col, *off = s_lse + ch * ROWS + 2 * col;
+        const float *fac = s_sl + ch * ROWS + 2 * col, *off = s_ref + ch * ROWS + 2 * col, *inv = s_inv + ch * ROWS + 2 * col;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float2 f = *reinterpret_cast<const float2 *>(fac + 8 * nt), z = *reinterpret_cast<const float2 *>(off + 8 * nt);
@@ -948,11 +952,13 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
             }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          const float2 f = *reinterpret_cast<const float2 *>(inv + 8 * nt);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sum[2 * h + (k >> 1)] += fast_exp2(c[h][nt][k]);
+            for (int k = 0; k < 4; ++k) sum[2 * h + (k >> 1)] = fmaf(fast_exp2(c[h][nt][k]), k & 1 ? f.y : f.x, sum[2 * h + (k >> 1)]);
+        }
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -1013,7 +1019,7 @@ int kv4_attn_types(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
 template <int D, int NT, int QS>
 int kv4_launch_crit(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
   constexpr int NW = kKv4CritWarps, NST = kKv4CritStages, BPS = kKv4CritBlocks;
-  constexpr int smem = NW * NST * Kv4Smem<D>::kCritStage + 2 * NT * 8 * D * 2 * QS + 4 * NT * 8 * 4;
+  constexpr int smem = NW * NST * Kv4Smem<D>::kCritStage + 2 * NT * 8 * D * 2 * QS + 6 * NT * 8 * 4;
   constexpr auto kernel = kv4_crit_kernel<D, NT, QS, NW, NST, BPS>;
   int rc = ensure_smem<kernel>(smem);
   if (rc) return rc;

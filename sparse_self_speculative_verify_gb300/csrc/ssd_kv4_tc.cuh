@@ -666,8 +666,8 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
         const float Z = sum_of(column(tw)), M = s_mfin[column(tw)];
         if (!whole)
           __stcg(reinterpret_cast<float2 *>(a.part_ml) + slot * NP + tw, make_float2(M, Z));
-        else if (a.lse)
-          a.lse[row_of(tw)] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
+        else
+          kv4_row_done(a, row_of(tw), M, Z);
       }
       tc_fence_before();
       arrive(b_lfree);
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(kKv4JoinRows * 32) kv4_join_kernel(Kv4AttnArgs
   const int64_t row = ((int64_t)b * a.n_c + rr / a.G) * a.h_q + g * a.G + rr % a.G;
   const float f = Z == 0.f ? 0.f : a.v_scale / Z;
   kv4_write4(a, row * 128 + lane * 4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
-  if (lane == 0 && a.lse) a.lse[row] = Z == 0.f ? -INFINITY : (M + __log2f(Z)) * kLn2;
+  if (lane == 0) kv4_row_done(a, row, M, Z);
 }
 
 // ---- criticality ------------------------------------------------------------------------------
@@ -770,7 +770,7 @@ struct Kv4CritCfg {
   static constexpr int kQ = (kKv4CritTcStages * kStage + 1023) / 1024 * 1024;
   static constexpr int kQBytes = NP * 256;
   static constexpr int kMisc = kQ + QS * kQBytes;
-  static constexpr int kSmem = kMisc + 2 * NP * 4 + 16 * 8 + 64 + 1024;
+  static constexpr int kSmem = kMisc + 3 * NP * 4 + 16 * 8 + 64 + 1024;
   // tensor memory: K, S^T of two tiles (of one, where the rows are many)
   static constexpr int kBufs = NP <= 32 ? 2 : 1;
   static constexpr int kTmem = 128, kColS = 64;
@@ -790,8 +790,8 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
   extern __shared__ __align__(16) char smem_raw[];
   char *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(sm);
-  float *s_sl = reinterpret_cast<float *>(sm + C::kMisc), *s_lse = s_sl + NP;
-  const uint32_t bars = smem_u32(s_lse + NP);
+  float *s_sl = reinterpret_cast<float *>(sm + C::kMisc), *s_ref = s_sl + NP, *s_inv = s_ref + NP;
+  const uint32_t bars = smem_u32(s_inv + NP);
   const uint32_t b_raw = bars, b_free = bars + 8 * kKv4CritTcStages, b_k = b_free + 8 * kKv4CritTcStages, b_s = b_k + 8, b_drain = b_s + 16;
   __shared__ int64_t s_scan[kKv4CritTcWarps + 4];
   __shared__ uint32_t s_tmem;
@@ -811,8 +811,8 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = s_tmem;
-  // Everything but lse was written before the attention kernel ran, which waited for it and only then let
-  // this one start; lse is waited for below.
+  // Everything but a.fin was written before the attention kernel ran, which waited for it and only then let
+  // this one start; a.fin is waited for below.
   Kv4Range rg;
   const bool mine = kv4_range<false, kKv4CritTcWarps, kKv4TcTile, 1>(a, rg, s_scan);
   auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -890,12 +890,9 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
       convert(n);
       pdl_wait();
       for (int q = tw; q < NP; q += 128) {
-        float v = INFINITY;  // rows that see nothing, and the padding: exp(x - inf) = 0
-        if (q < a.R) {
-          v = __ldcg(a.lse_in + ((int64_t)b * a.n_c + q / a.G) * a.h_q + g * a.G + q % a.G);
-          v = v == -INFINITY ? INFINITY : v * kLog2e;
-        }
-        s_lse[q] = v;
+        float2 v = make_float2(INFINITY, 0.f);  // the padding, as rows that see nothing: exp2(x - inf) = 0
+        if (q < a.R) v = __ldcg(a.fin + ((int64_t)b * a.n_c + q / a.G) * a.h_q + g * a.G + q % a.G);
+        s_ref[q] = v.x, s_inv[q] = v.y;
       }
       named_sync(1, 128);
       for (int t = rg.off; t < t1; ++t, ++n) {
@@ -928,7 +925,7 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
           }
 #pragma unroll
           for (int q = 0; q < W; q += 4) {
-            const float4 sl = *reinterpret_cast<const float4 *>(s_sl + c + q), ls = *reinterpret_cast<const float4 *>(s_lse + c + q);
+            const float4 sl = *reinterpret_cast<const float4 *>(s_sl + c + q), ls = *reinterpret_cast<const float4 *>(s_ref + c + q);
             v[q] = fmaf(v[q], sl.x, -ls.x), v[q + 1] = fmaf(v[q + 1], sl.y, -ls.y);
             v[q + 2] = fmaf(v[q + 2], sl.z, -ls.z), v[q + 3] = fmaf(v[q + 3], sl.w, -ls.w);
           }
@@ -938,7 +935,11 @@ __global__ void __launch_bounds__(kKv4CritTcWarps * 32, BPS) kv4_crit_tc_kernel(
               if (c + q < first) v[q] = -INFINITY;
           }
 #pragma unroll
-          for (int q = 0; q < W; ++q) sum[q & 3] += fast_exp2(v[q]);
+          for (int q = 0; q < W; q += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(s_inv + c + q);
+            sum[0] = fmaf(fast_exp2(v[q]), f.x, sum[0]), sum[1] = fmaf(fast_exp2(v[q + 1]), f.y, sum[1]);
+            sum[2] = fmaf(fast_exp2(v[q + 2]), f.z, sum[2]), sum[3] = fmaf(fast_exp2(v[q + 3]), f.w, sum[3]);
+          }
         }
         if (tok < L) a.scores[(int64_t)rg.u * a.scores_stride + tok] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tc_fence_before();
