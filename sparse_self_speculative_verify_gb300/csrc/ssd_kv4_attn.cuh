@@ -120,7 +120,7 @@ template <int TILE>
 constexpr int kKv4Snap = TILE == kKv4Tile ? 4 : 0;  // (20: decode 48.8 us against 47.5)
 struct Kv4Range {
   int64_t x, x1, per;  // place of the unit u in the line, the block's end, a stretch's length
-  int u, off;                // next unit, and its first tile of this block
+  int u, off;          // next unit, and its first tile of this block
 };
 // Blocks that hold parts of the unit of n tiles at place x: `first` and `more` blocks after it.  The unit's start
 // is stored in the first one's second slot, other parts in their block's first one.
