@@ -135,28 +135,29 @@ struct ReserveArgs {
   unsigned *status;
 };
 
-// Inclusive sum of v over the block's threads in order; s_warp: 33 ints.  total: the block's.
-__device__ __forceinline__ int block_scan(int v, int *s_warp, int &total) {
+// Inclusive sum of v over the block's threads in order; s_warp: 32 values.  total: the block's.  64 bits: the pages that
+// a table's rows ask for may be more than 2^31.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_t &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+  int64_t inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    int w = s_warp[lane];
+    int64_t w = s_warp[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += y;
     }
     s_warp[lane] = w;
   }
   __syncthreads();
-  const int base = warp ? s_warp[warp - 1] : 0;
+  const int64_t base = warp ? s_warp[warp - 1] : 0;
   total = s_warp[31];
   __syncthreads();
   return base + inc;
@@ -169,7 +170,7 @@ __device__ __forceinline__ int block_scan(int v, int *s_warp, int &total) {
 // LPR lanes share a request: bound by the latency of a dozen dependent loads, so a thread per request
 // (all requests at once) where they need a page or two, a warp for long prompts.
 template <int LPR>
-__device__ __forceinline__ void reserve_rows(const ReserveArgs &a, int *s_warp) {
+__device__ __forceinline__ void reserve_rows(const ReserveArgs &a, int64_t *s_warp) {
   const int tid = threadIdx.x, gl = tid % LPR, grp = tid / LPR;
   constexpr int kGroups = kResThreads / LPR;
   const KVView &kv = a.kv;
@@ -228,16 +229,20 @@ __device__ __forceinline__ void reserve_rows(const ReserveArgs &a, int *s_warp) 
   }
   __syncthreads();
   // Sums over the requests, in their order.
-  int total = 0;
+  int64_t total = 0;
   for (int b0 = 0; b0 < kv.batch; b0 += kResThreads) {
     const int b = b0 + tid, v = b < kv.batch ? a.row[b].z : 0;
-    int part;
-    const int inc = block_scan(v, s_warp, part);
-    if (b < kv.batch) a.row[b].w = total + inc - v;
+    int64_t part;
+    const int64_t inc = block_scan(v, s_warp, part);
+    if (b < kv.batch) a.row[b].w = (int)(total + inc - v);  // read only where the total is at most num_pages
     total += part;
   }
+  if (total > kv.num_pages) {  // whatever the counts say
+    if (tid == 0) atomicOr(a.status, (unsigned)SSD_FAULT_NOPAGE);
+    return;
+  }
   // The first `total` free pages, 16 counts a thread and step.
-  int found = 0;
+  int64_t found = 0;
   const bool vec = (reinterpret_cast<uintptr_t>(a.refs) & 15) == 0;
   for (int64_t p0 = 0; p0 < kv.num_pages && found < total; p0 += kResThreads * 16) {
     const int64_t p = p0 + tid * 16;
@@ -253,8 +258,8 @@ __device__ __forceinline__ void reserve_rows(const ReserveArgs &a, int *s_warp) 
         if (p + k < kv.num_pages && a.refs[p + k] == 0) free |= 1u << k;
     }
     const int mine = __popc(free);
-    int part;
-    int at = found + block_scan(mine, s_warp, part) - mine;
+    int64_t part;
+    int64_t at = found + block_scan(mine, s_warp, part) - mine;
     for (; free && at < total; free &= free - 1) a.fresh[at++] = (int32_t)(p + __ffs(free) - 1);
     found += part;
   }
@@ -289,7 +294,7 @@ __device__ __forceinline__ void reserve_rows(const ReserveArgs &a, int *s_warp) 
 }
 
 __global__ void __launch_bounds__(kResThreads) kv_reserve_kernel(ReserveArgs a) {
-  __shared__ int s_warp[33];
+  __shared__ int64_t s_warp[32];
   pdl_wait();
   bool many = false;
   for (int b = threadIdx.x; b < a.kv.batch; b += kResThreads) {

@@ -1,0 +1,42 @@
+"""The page calls at the ends of their ranges on the GPU: sums, positions and byte offsets past 32 bits."""
+
+import pytest
+import torch
+
+from sparse_self_speculative_verify_gb300 import KVCache, PagePool, binding, ssd_kv_reserve, ssd_status
+from tests import _gpu
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def test_reserve_of_2_to_the_31_pages_in_one_call():
+    """1024 rows that each ask for 2^21 pages: far more than the pool has, so nothing changes."""
+    _gpu.lib()
+    rows, cap, page = 1024, 1 << 21, 8
+    pool = torch.ones((64, 2, 1, page, 64), dtype=torch.bfloat16, device=DEV)
+    table = torch.full((rows, cap), -1, dtype=torch.int32, device=DEV)
+    table[3, 0] = 5
+    lens = torch.zeros(rows, dtype=torch.int32, device=DEV)
+    lens[3] = 2
+    kv = KVCache(pool, table, lens, cap * page)
+    pages = PagePool(torch.zeros(64, dtype=torch.int32, device=DEV))
+    pages.refs[5] = 1
+    counts = torch.full((rows,), cap * page, dtype=torch.int32, device=DEV)
+    counts[3] -= 2
+    ssd_kv_reserve(kv, pages, counts)
+    torch.cuda.synchronize()
+    assert ssd_status() == binding.FAULT_NOPAGE
+    assert table[3, 0].item() == 5 and (table.sum(1, dtype=torch.int64) == -cap).sum().item() == rows - 1
+    assert table[3].sum(dtype=torch.int64).item() == 5 - (cap - 1)
+    assert pages.refs.tolist() == [int(p == 5) for p in range(64)]
+    assert lens.tolist() == [2 * (b == 3) for b in range(rows)]
+    # The same rows, asking for what there is.
+    counts.fill_(0)
+    counts[3], counts[1023] = page, page
+    ssd_kv_reserve(kv, pages, counts)
+    torch.cuda.synchronize()
+    assert ssd_status() == 0
+    assert table[3, :3].tolist() == [5, 0, -1] and table[1023, :2].tolist() == [1, -1]
+    del table, kv
+    torch.cuda.empty_cache()
