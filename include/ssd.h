@@ -449,8 +449,8 @@ int ssd_kv4_draft_attn(const ssd_paged_kv *kv, const void *q, int q_dtype, int h
  *   name pages outside the pool or not held are cleared and raise SSD_FAULT_PAGE.
  * ssd_kv_compact: for n pairs, the listed tokens of row src[i] of kv go to positions 0 .. of row dst[i] of
  *   the cache `to` (same dtype, h_kv and d; the page size may differ; it may be kv itself), whose length
- *   becomes the count.  idx: device int32 [n][h_kv][k_max], cnt: device int32 [n][h_kv], the same for every head
- *   of a pair.  Token order is the list's.  dst's pages must be reserved beforehand; slots behind the last
+ *   becomes the count.  idx: device int32 [n][h_kv][k_max] (k_max at most 2^24), cnt: device int32 [n][h_kv],
+ *   the same for every head of a pair.  Token order is the list's.  dst's pages must be reserved beforehand; slots behind the last
  *   token stay as they are.  to_refs: page_refs of `to`, or NULL; with it, rows go only into pages held once.
  *   A pair is skipped when a row is out of range, when its dst is an earlier pair's or, within one cache,
  *   any pair's src (SSD_FAULT_INDEX), when its counts differ or lie outside [0, k_max] (SSD_FAULT_KMAX), or

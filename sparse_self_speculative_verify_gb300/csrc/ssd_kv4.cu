@@ -42,7 +42,6 @@ static Kv4Layout kv4_layout(const ssd_paged_kv *kv, int h_q, int n_rows, int max
   return y;
 }
 
-constexpr int kMaxList = 1 << 24;  // as max_seq_len: positions, and tiles past their end, stay in 32 bits
 static bool kv4_shape_ok(const ssd_paged_kv *kv, int h_q, int n) {
   return kv && kv->h_kv > 0 && h_q > 0 && h_q % kv->h_kv == 0 && n > 0 && kv->batch >= 0 && kv->max_seq_len >= 0 &&
          (kv->d == 64 || kv->d == 128) && (int64_t)(h_q / kv->h_kv) * n <= kMaxRows;

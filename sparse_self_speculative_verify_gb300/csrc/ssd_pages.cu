@@ -540,6 +540,7 @@ extern "C" int ssd_kv_compact(const ssd_paged_kv *kv, const ssd_paged_kv *to, co
   if (kv->dtype != to->dtype || kv->h_kv != to->h_kv || kv->d != to->d)
     return fail(SSD_ERR_INVALID_ARG, "%s: the two caches differ in dtype, h_kv or d", who);
   if (n < 0 || k_max < 0) return fail(SSD_ERR_INVALID_ARG, "%s: n and k_max must be >= 0", who);
+  if (k_max > kMaxList) return fail(SSD_ERR_UNSUPPORTED, "%s: k_max above 2^24", who);
   if (n > 65535 || kv->h_kv > 65535) return fail(SSD_ERR_UNSUPPORTED, "%s: n or h_kv above 65535", who);
   if (n == 0) return SSD_OK;
   if (!src || !dst || !cnt || (!idx && k_max > 0)) return fail(SSD_ERR_INVALID_ARG, "%s: src, dst, idx and cnt must be non-NULL", who);
