@@ -371,7 +371,8 @@ int ssd_combine(const float *o_parts, const float *lse_parts, int n_rows, int n_
  * 4-bit paged KV cache (NVFP4).  An ssd_paged_kv with dtype SSD_DTYPE_NVFP4; its pool is bytes:
  *   pool  device, [num_pages][2][h_kv] blocks of page_size * (d / 2 + d / 16) bytes, index 0 = K,
  *         1 = V, 16-byte aligned.  A block holds its tokens' codes (d / 2 bytes each, element 2i in the
- *         low nibble of byte i), then their scales (d / 16 bytes each).  page_size is at least 8.
+ *         low nibble of byte i), then their scales (d / 16 bytes each).  page_size is at least 8,
+ *         and a page takes less than 2 GB.
  * Elements 16 j .. 16 j + 15 of a row share scale j.  A code is e2m1 (bit 3: sign; magnitudes 0, 0.5, 1,
  * 1.5, 2, 3, 4, 6), a scale e4m3; the element stands for code * scale * k_scale (V: v_scale).  k_scale and
  * v_scale are host constants of a cache, powers of two between 2^-32 and 2^32, and go to every call.

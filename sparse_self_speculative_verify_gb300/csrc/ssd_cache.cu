@@ -20,6 +20,8 @@ int validate_cache(const ssd_paged_kv *kv, KVView *v, const char *who, unsigned 
   if (rc) return rc;
   if (kv->page_size < kKv4MinPage)
     return fail(SSD_ERR_UNSUPPORTED, "%s: page_size %d of a 4-bit cache is below %d", who, kv->page_size, kKv4MinPage);
+  if ((int64_t)kv->page_size * kv->h_kv * kv4_row_bytes(kv->d) >= (int64_t)1 << 30)  // offsets inside a page: 32 bits
+    return fail(SSD_ERR_UNSUPPORTED, "%s: a page of 2 GB or more", who);
   return SSD_OK;
 }
 

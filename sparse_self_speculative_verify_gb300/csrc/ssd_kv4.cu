@@ -74,8 +74,6 @@ static int kv4_prepare(const Kv4Call &c, int max_tokens, Kv4AttnArgs *a, Kv4Layo
   if (R > kMaxRows) return fail(SSD_ERR_UNSUPPORTED, "%s: %lld query rows per KV head (at most %d)", who, (long long)R, kMaxRows);
   if (!isfinite(c.scale)) return fail(SSD_ERR_INVALID_ARG, "%s: scale is not finite", who);
   if ((rc = kv4_scales_ok(c.k_scale, c.v_scale, who))) return rc;
-  if ((int64_t)c.kv->page_size * c.kv->h_kv * kv4_row_bytes(c.kv->d) >= (int64_t)1 << 30)
-    return fail(SSD_ERR_UNSUPPORTED, "%s: a page of 2 GB or more", who);
   if ((int64_t)c.kv->batch * c.kv->h_kv > 65535) return fail(SSD_ERR_UNSUPPORTED, "%s: batch*h_kv above 65535", who);
   *lay = kv4_layout(c.kv, c.h_q, c.n_rows, max_tokens);
   if (!c.workspace || c.workspace_bytes < lay->total)

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(char *pool, const
   const char *src = pool + ((int64_t)c.x * 2 * h_kv + part) * block_bytes;
   char *dst = pool + ((int64_t)c.y * 2 * h_kv + part) * block_bytes;
   constexpr int U = 4;  // pieces in flight per thread
-  const int n = c.z * rs.wide / 16;
+  const int n = c.z * (rs.wide / 16);  // (up to 2^24 tokens of 512 bytes)
 #pragma unroll 1
   for (int e0 = lane; e0 < n; e0 += 32 * U) {
     uint4 v[U];
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(char *pool, const
     for (int k = 0; k < U; ++k)
       if (e0 + 32 * k < n) reinterpret_cast<uint4 *>(dst)[e0 + 32 * k] = v[k];
   }
-  const int thin0 = page_size * rs.wide;
+  const int64_t thin0 = (int64_t)page_size * rs.wide;
   for (int e = lane; e < c.z * rs.thin / 4; e += 32)
     reinterpret_cast<uint32_t *>(dst + thin0)[e] = reinterpret_cast<const uint32_t *>(src + thin0)[e];
 }
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactArgs
   // Pieces of 16 bytes, four loads on their way per thread; then a 4-bit cache's scales in words.
   const char *from = static_cast<const char *>(a.from.pool);
   const int64_t fv = h * fb, tv = h * tb;
-  auto copy = [&](auto *tag, int width, int at_from, int at_to) {
+  auto copy = [&](auto *tag, int width, int64_t at_from, int64_t at_to) {
     using V = typename std::remove_pointer<decltype(tag)>::type;
     const int sh = 31 - __clz(width / (int)sizeof(V));  // log2 of the pieces of a row (widths are powers of two)
     const int total = nj << (sh + 1);
@@ -434,18 +434,18 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactArgs
       for (int k = 0; k < U; ++k) {
         const int e = e0 + k * kCompactThreads, c = e & ((1 << sh) - 1), which = (e >> sh) & 1, j = e >> (sh + 1);
         v[k] = V{};
-        if (e < total && s_from[j] >= 0) v[k] = reinterpret_cast<const V *>(from + s_from[j] + (which ? fv : 0) + at_from + s_slots[j] * width)[c];
+        if (e < total && s_from[j] >= 0) v[k] = reinterpret_cast<const V *>(from + s_from[j] + (which ? fv : 0) + at_from + (int64_t)s_slots[j] * width)[c];
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int e = e0 + k * kCompactThreads, c = e & ((1 << sh) - 1), which = (e >> sh) & 1, j = e >> (sh + 1);
         if (e < total && s_to[j] >= 0)
-          reinterpret_cast<V *>(a.to_pool + s_to[j] + (which ? tv : 0) + at_to + ((j0 + j) & (a.to.page_size - 1)) * width)[c] = v[k];
+          reinterpret_cast<V *>(a.to_pool + s_to[j] + (which ? tv : 0) + at_to + (int64_t)((j0 + j) & (a.to.page_size - 1)) * width)[c] = v[k];
       }
     }
   };
   copy(static_cast<uint4 *>(nullptr), a.rs.wide, 0, 0);
-  if (a.rs.thin) copy(static_cast<uint32_t *>(nullptr), a.rs.thin, a.from.page_size * a.rs.wide, a.to.page_size * a.rs.wide);
+  if (a.rs.thin) copy(static_cast<uint32_t *>(nullptr), a.rs.thin, (int64_t)a.from.page_size * a.rs.wide, (int64_t)a.to.page_size * a.rs.wide);
 }
 
 static int page_checks(const ssd_paged_kv *kv, KVView *v, const int32_t *refs, const char *who) {

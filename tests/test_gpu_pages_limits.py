@@ -3,7 +3,8 @@
 import pytest
 import torch
 
-from sparse_self_speculative_verify_gb300 import KVCache, PagePool, binding, ssd_kv_reserve, ssd_status
+from sparse_self_speculative_verify_gb300 import (KVCache, PagePool, binding, ssd_kv_compact, ssd_kv_fork, ssd_kv_reserve,
+                                                 ssd_status)
 from tests import _gpu
 
 pytestmark = pytest.mark.gpu
@@ -39,4 +40,36 @@ def test_reserve_of_2_to_the_31_pages_in_one_call():
     assert ssd_status() == 0
     assert table[3, :3].tolist() == [5, 0, -1] and table[1023, :2].tolist() == [1, -1]
     del table, kv
+    torch.cuda.empty_cache()
+
+
+def test_pages_whose_rows_lie_past_2_gb():
+    """One page per request, as of a cache that is not paged: fp32 rows of 512 bytes, 2^22 and more of them."""
+    _gpu.lib()
+    page, d, L = 1 << 23, 128, (1 << 22) + 5
+    pool = torch.empty((3, 2, 1, page, d), dtype=torch.float32, device=DEV)
+    pool[2, :, 0, :L] = torch.arange(L, dtype=torch.float32, device=DEV)[:, None]
+    pool[2, 1, 0, :L] += 0.5
+    pool[0].zero_()
+    table = torch.tensor([[2], [-1], [1]], dtype=torch.int32, device=DEV)
+    kv = KVCache(pool, table, torch.tensor([L, 0, 0], dtype=torch.int32, device=DEV), page)
+    pages = PagePool.from_table(table, 3)
+    row = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    # Compaction out of slots behind 2 GB, and one of its rows to such a slot.
+    n = L - 3
+    idx = torch.arange(n, dtype=torch.int32, device=DEV).flip(0)[None, None].contiguous()  # the last tokens first
+    ssd_kv_compact(kv, kv, row(0), row(2), idx, torch.full((1, 1), n, dtype=torch.int32, device=DEV), pages=pages)
+    torch.cuda.synchronize()
+    assert ssd_status() == 0 and kv.seq_lens.tolist() == [L, 0, n]
+    for w in range(2):
+        assert torch.equal(pool[1, w, 0, :n], pool[2, w, 0, :n].flip(0)), w
+    # A branch: its page is replaced by a free one, with all of the live tokens.
+    ssd_kv_fork(kv, pages, row(0), row(1))
+    ssd_kv_reserve(kv, pages, row(2, 2, 0))
+    torch.cuda.synchronize()
+    assert ssd_status() == 0
+    assert table.tolist() == [[2], [0], [1]] and pages.refs.tolist() == [1, 1, 1]
+    for w in range(2):
+        assert torch.equal(pool[0, w, 0, :L], pool[2, w, 0, :L]), w
+    del pool, kv
     torch.cuda.empty_cache()

@@ -23,3 +23,23 @@ def test_compact_refuses_lists_whose_positions_pass_32_bits(lib):
         assert lib.ssd_kv_compact(kv, kv, None, 64, 64, 1, 64, k_max, 64, None) == U
         assert b"2^24" in lib.ssd_last_error()
     assert lib.ssd_kv_compact(kv, kv, None, 64, 64, 0, 64, 1 << 24, 64, None) == OK  # no pairs: nothing is launched
+
+
+def test_pages_of_2_gb_are_refused_by_every_call_on_a_4_bit_cache(lib):
+    """Offsets inside a page are 32 bits in all of them."""
+    big = ctypes.byref(_kv(page_size=1 << 24, max_seq_len=1 << 24))
+    ok = ctypes.byref(_kv())
+    calls = {
+        "append": lambda: lib.ssd_kv4_append(big, 4096, 4096, 1, 3, None, 1.0, 1.0, None),
+        "read": lambda: lib.ssd_kv4_read(big, 64, None, 3, 1.0, 1.0, 1, 4096, 4096, None),
+        "verify": lambda: lib.ssd_kv4_verify_attn(big, 4096, 1, 32, 5, 0.1, 1.0, 1.0, 8192, 0, None, None, 0, 1 << 20, 1 << 40, None),
+        "draft": lambda: lib.ssd_kv4_draft_attn(big, 4096, 1, 32, 64, 8, 64, 0.1, 1.0, 1.0, 8192, 0, None, 1 << 20, 1 << 40, None),
+        "fork": lambda: lib.ssd_kv_fork(big, 64, 64, 64, 1, None),
+        "reserve": lambda: lib.ssd_kv_reserve(big, 64, 64, 1 << 20, 1 << 30, None),
+        "release": lambda: lib.ssd_kv_release(big, 64, 64, None),
+        "compact from": lambda: lib.ssd_kv_compact(big, ok, None, 64, 64, 1, 64, 4, 64, None),
+        "compact to": lambda: lib.ssd_kv_compact(ok, big, None, 64, 64, 1, 64, 4, 64, None),
+    }
+    for name, call in calls.items():
+        assert call() == U, name
+        assert b"2 GB" in lib.ssd_last_error(), name
