@@ -855,9 +855,11 @@ class PagePool:
 
     @classmethod
     def from_table(cls, page_table: torch.Tensor, num_pages: int) -> "PagePool":
-        """The counts of the pages a page table holds (entries >= 0)."""
+        """The counts of the pages a page table holds (entries >= 0, all of them below num_pages)."""
         held = page_table.reshape(-1)
         held = held[held >= 0].to(torch.int64)
+        if held.numel() and int(held.max()) >= num_pages:
+            raise ValueError(f"page_table names page {int(held.max())} of a pool of {num_pages} pages")
         refs = torch.zeros((num_pages,), dtype=torch.int32, device=page_table.device)
         return cls(refs.scatter_add_(0, held, torch.ones_like(held, dtype=torch.int32)))
 

@@ -3,8 +3,9 @@
 import ctypes
 
 import pytest
+import torch
 
-from sparse_self_speculative_verify_gb300 import binding
+from sparse_self_speculative_verify_gb300 import PagePool, binding
 from sparse_self_speculative_verify_gb300 import build as libbuild
 from tests.test_kv4_host import _kv
 
@@ -43,3 +44,13 @@ def test_pages_of_2_gb_are_refused_by_every_call_on_a_4_bit_cache(lib):
     for name, call in calls.items():
         assert call() == U, name
         assert b"2 GB" in lib.ssd_last_error(), name
+
+
+def test_page_counts_of_a_table_with_ids_outside_the_pool():
+    """Refused before the counts are scattered: on a GPU an id past their end fails a device assertion."""
+    table = torch.tensor([[3, -1], [0, 7]], dtype=torch.int32)
+    for num_pages in (7, 1):
+        with pytest.raises(ValueError, match="page 7 of a pool"):
+            PagePool.from_table(table, num_pages)
+    with pytest.raises(ValueError, match="CUDA"):  # the table is fine; counts live on the GPU
+        PagePool.from_table(table, 8)
