@@ -1,0 +1,166 @@
+"""The 4-bit attention on stretches as long as a user's: hundreds of rows share the pages of one request of 32768
+tokens, so that every block walks 200 tiles of 128 tokens, or every warp 100 of 32, of a unit.  Against 64 bits on the
+GPU, from the values that the pool's bytes stand for, every row of the batch.
+
+Limits, as relative 2-norms over all outputs of a head (`fp32 outputs`; F = 64 products in a row, 4 tiles x 16 on tcgen05
+and 16 x 4 on mma.sync, between two times that O is added up to nearest):
+ * the tensor cores add with truncation: a step loses less than 2^-23 of the sum so far, which grows from nothing over
+   F = 64 steps: 2^-23 * 64 / 2 = 2^-18 at most, where V is positive; the sums of the periods (64 at most, to nearest)
+   and of the blocks' parts 2^-25 * 8, with errors of either sign;
+ * a logit x: d / 16 <= 8 truncating steps (16 for fp32 queries, whose second half is 2^-11 of the first), which take up to
+   2^-23 * 4 relative off |q k| <= 20: as all logits shrink alike, outputs move by 2^-21 times the spread of x under the
+   softmax (under 4): 2^-19; exp2 and the subtraction 2^-21, either sign;
+ * P in 22 bits: 2^-23.
+In all under 6e-6 (2^-18 + 2^-19 + ...).  lse: 2^-21 * 20 and its own half steps at 16 to 32 (2^-20): 2^-16.  Scores:
+the same shrinking logits, weighted by p, 2^-18, as a norm.  bf16 outputs: their half step 2^-9 (rms 2^-9 / sqrt 3) and
+P's 2^-12: under 2^-8.
+
+Where logits grow ("grow"), all products of a logit have one sign and add up to 60.  A step then truncates 16 products and
+the sum so far, each by less than 2^-25 of that sum: 17 * 2^-25 < 2^-20.9, or 2^-21 with the products' spread.  Over d / 16
+= 8 steps the sum grows evenly: 8 / 2 of them.  The second half of an fp32 query adds 8 steps at its full height: 12 in
+all.  The softmax is sharp (its neighbours' logits lose alike, but not equally), so outputs, lse and scores may be off by
+all of it: 60 * 2^-21 * 4, and * 12 for fp32 queries, on top of the above."""
+
+import functools
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from sparse_self_speculative_verify_gb300 import KV4Cache, ssd_kv4_draft_attn, ssd_kv4_verify_attn, ssd_status
+from tests import _gpu, _kv4
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+L, PAGE = 32768, 16
+F32_OUT, F32_LSE, F32_SCORES, BF16_OUT = 6e-6, 2.0 ** -16, 2.0 ** -18, 2.0 ** -8
+
+
+def _bytes(codes, scales):
+    """Codes [h, n, d] and scales [h, n, d / 16] as pages' blocks [n / PAGE, h, PAGE * 9 d / 16]."""
+    h, n, d = codes.shape
+    packed = (codes[..., 0::2] | (codes[..., 1::2] << 4)).reshape(h, n // PAGE, PAGE * d // 2)
+    return np.concatenate([packed, scales.reshape(h, n // PAGE, PAGE * d // 16)], -1).transpose(1, 0, 2)
+
+
+@functools.lru_cache(maxsize=4)
+def _tokens(kind, h, d, n=L):
+    """(pool, K, V in 64 bits [h, n, d]) on the GPU."""
+    rng = np.random.default_rng(41)
+    k, v = rng.standard_normal((2, h, n, d))
+    if kind == "positive":
+        v = np.abs(v)
+    if kind == "grow":  # logits that rise all along, with falls in between; q holds the signs
+        t = np.arange(n)
+        ramp = 2.0 * t / n - 1 - 0.15 * (t // 700 % 3 == 1)
+        k = 4.0 * ramp[:, None] * _signs(d) + 0.05 * k
+    ck, cv = _kv4.quantise(k), _kv4.quantise(v)
+    pool = np.stack([_bytes(*ck), _bytes(*cv)], 1)
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(DEV)  # noqa: E731
+    return dev(pool).view(KV4Cache.pool_shape(n // PAGE, h, PAGE, d)), dev(_kv4.values(*ck)), dev(_kv4.values(*cv))
+
+
+def _signs(d):
+    return np.sign(np.random.default_rng(5).standard_normal(d))
+
+
+def _cache(pool, B, n=L):
+    table = torch.arange(n // PAGE, dtype=torch.int32, device=DEV).expand(B, -1).contiguous()
+    return KV4Cache(pool, table, torch.full((B,), n, dtype=torch.int32, device=DEV), n)
+
+
+def _queries(kind, shape, dtype):
+    g = torch.Generator(device=DEV).manual_seed(6)
+    if kind == "grow":
+        s = torch.from_numpy(_signs(shape[-1])).to(DEV, torch.float32)
+        return (s * (0.7 + 0.3 * torch.rand(shape[:-1] + (1,), generator=g, device=DEV))).to(dtype)
+    return (1.5 * torch.randn(shape, generator=g, device=DEV)).to(dtype)
+
+
+def _attend(q, K, V, limit, scale):
+    """Rows q [r, d] that see the first limit[r] tokens: out, lse, probabilities [n, r]; 64 bits."""
+    x = scale * (K @ q.double().T)
+    x.masked_fill_(torch.arange(len(K), device=DEV)[:, None] >= limit[None], -math.inf)
+    lse = torch.logsumexp(x, 0)
+    P = x.sub_(lse).exp_()
+    return P.T @ V, lse, P
+
+
+def _off(got, want):
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+def _types(types):
+    return (torch.bfloat16 if t == "bf16" else torch.float32 for t in types.split("-"))
+
+
+FORMS = [  # h_kv, G, d, n_cand
+    (2, 4, 128, 1), (2, 8, 128, 1), (2, 4, 128, 3), (2, 4, 128, 4), (2, 4, 128, 5), (2, 8, 128, 4), (1, 16, 128, 3),
+    (1, 16, 128, 4),
+    (2, 4, 64, 1), (2, 3, 64, 3), (2, 4, 64, 4), (2, 4, 64, 5), (2, 8, 64, 4), (1, 16, 64, 3),
+]
+
+
+@pytest.mark.parametrize("types", ["bf16-f32", "f32-f32", "bf16-bf16"])
+@pytest.mark.parametrize("kind", ["spread", "positive", "grow"])
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: f"h{f[0]}G{f[1]}d{f[2]}n{f[3]}")
+def test_verify_over_long_stretches(form, kind, types):
+    _gpu.lib()
+    h, G, d, nc = form
+    B = 330 // h
+    qt, ot = _types(types)
+    pool, K, V = _tokens(kind, h, d)
+    kv = _cache(pool, B)
+    q = _queries(kind, (B, nc, G * h, d), qt)
+    scale = 60.0 / (4 * d) if kind == "grow" else 1 / math.sqrt(d)
+    r = ssd_kv4_verify_attn(kv, q, nc, scale, out_dtype=ot)
+    again = ssd_kv4_verify_attn(kv, q, nc, scale, out_dtype=ot)
+    torch.cuda.synchronize()
+    assert ssd_status() == 0
+    for name in ("out", "lse", "scores"):
+        assert torch.equal(r[name], again[name]), name
+    more = 60 * 2.0 ** -21 * (12 if qt == torch.float32 else 4) if kind == "grow" else 0.0
+    for g in range(h):
+        heads = slice(g * G, (g + 1) * G)
+        rows = q[:, :, heads].reshape(-1, d)
+        limit = (L - nc + 1 + torch.arange(nc, device=DEV)).repeat_interleave(G).repeat(B)
+        out, lse, P = _attend(rows, K[g], V[g], limit, scale)
+        scores = P.view(L, B, nc * G).sum(2).T
+        del P
+        off = _off(r["out"][:, :, heads].reshape(-1, d), out)
+        assert off <= more + (F32_OUT if ot == torch.float32 else BF16_OUT), f"out off by {off:.2e}"
+        off = (r["lse"][:, :, heads].reshape(-1).double() - lse).abs().max().item()
+        assert off <= more + F32_LSE, f"lse off by {off:.2e}"
+        off = _off(r["scores"][:, g], scores)
+        assert off <= more + F32_SCORES, f"scores off by {off:.2e}"
+
+
+@pytest.mark.parametrize("types", ["bf16-f32", "f32-f32", "bf16-bf16"])
+@pytest.mark.parametrize("kind", ["spread", "positive", "grow"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [4, 9, 16])
+def test_draft_over_long_lists(G, d, kind, types):
+    """Lists in any order: all the tokens but some, shuffled except where the logits grow."""
+    _gpu.lib()
+    h, B = 2, 165
+    qt, ot = _types(types)
+    pool, K, V = _tokens(kind, h, d)
+    kv = _cache(pool, B)
+    q = _queries(kind, (B, G * h, d), qt)
+    scale = 60.0 / (4 * d) if kind == "grow" else 1 / math.sqrt(d)
+    g = torch.Generator().manual_seed(7)
+    perm = (torch.arange(L) if kind == "grow" else torch.randperm(L, generator=g))[:L - 37].to(DEV)
+    idx = perm.to(torch.int32).expand(B, h, -1).contiguous()
+    cnt = torch.full((B, h), len(perm), dtype=torch.int32, device=DEV)
+    r = ssd_kv4_draft_attn(kv, q, idx, cnt, scale, out_dtype=ot)
+    torch.cuda.synchronize()
+    assert ssd_status() == 0
+    more = 60 * 2.0 ** -21 * (12 if qt == torch.float32 else 4) if kind == "grow" else 0.0
+    for g in range(h):
+        heads = slice(g * G, (g + 1) * G)
+        out, lse, _ = _attend(q[:, heads].reshape(-1, d), K[g][perm], V[g][perm], torch.full((B * G,), L, device=DEV), scale)
+        off = _off(r["out"][:, heads].reshape(-1, d), out)
+        assert off <= more + (F32_OUT if ot == torch.float32 else BF16_OUT), f"out off by {off:.2e}"
+        off = (r["lse"][:, heads].reshape(-1).double() - lse).abs().max().item()
+        assert off <= more + F32_LSE, f"lse off by {off:.2e}"
