@@ -406,7 +406,8 @@ int ssd_kv4_read(const ssd_paged_kv *kv, const int32_t *first, const int32_t *co
  * (a candidate that sees no token, an empty list: out = 0, lse = -inf), except:
  *   q    device of q_dtype, 16-byte aligned; out device of out_dtype, 16-byte aligned (each
  *        SSD_DTYPE_BF16 or SSD_DTYPE_F32).  Products and sums are held in fp32; probabilities are
- *        carried in f16 (2^-12 relative) for a bf16 out and in 22 bits for an fp32 out or q.
+ *        carried in f16 for a bf16 out (to 2^-12 relative, or 2^-31 of the row's largest where that is more) and in
+ *        two f16 for an fp32 out or q (22 bits, or 2^-35 of the largest).
  *   scores  as in ssd_verify_attn, or NULL.
  *   workspace  device, >= the matching query's bytes, 256-byte aligned.
  * At most 64 query rows per KV head (h_q / h_kv * n_cand; 16 in a draft), 65535 (request, KV head) pairs and 2^24

@@ -35,11 +35,17 @@ namespace ssd {
 constexpr int kKv4Tile = 32;         // tokens per warp tile
 constexpr int kKv4MaxBlocks = 1024;  // bound of the grid (sizes the workspace)
 constexpr int kKv4MaxNT = 4;         // query rows are taken 8 NT <= 32 at a time
-// A row's reference m is the largest logit (log2) seen when it last moved, less kKv4Lift; it moves again when a
-// logit exceeds it by kKv4Slack.  exp2(x - m) then reaches 2^14 and f16 (11 bits down to 2^-14, 2^-25 absolute
-// below) keeps probabilities down to 2^-31 of the largest.
-constexpr float kKv4Lift = 6.f;
-constexpr float kKv4Slack = 14.f;
+// A row's reference m is the largest logit (log2) seen when it last moved, less the lift; it moves again when a logit
+// exceeds it by the slack.  exp2(x - m), at least 2^lift where the largest is, goes to the tensor cores in f16, which
+// holds 11 bits down to 2^-14 and steps of 2^-24 below.
+//   bf16 outputs (one f16): 2^-12 relative down to 2^-20 of the largest, 2^-31 of it absolute below.
+//   fp32 outputs (two f16): 22 bits down to 2^-13 of the largest, 2^-35 of it absolute below: n tokens that far down may
+//     take n 2^-35 off a row's weight; fp32 sums of n / 128 terms take as much.  (With a lift of 6, 131072 tokens of
+//     2^-31 each were lost altogether: 5.6e-5 of the outputs.)  The slack stays below f16's 2^16.  Each reference that
+//     moves costs a pass over O: lifts of 6, 9, 10, 11, 13 took 99.5, 101.5, 101.5, 103.5, 124 us for 32 requests of
+//     2048 to 8192 tokens, 8 heads, d = 64, 32 rows, and 99.5, 99.5, 99.5, 100.5, 107 for d = 128, 20 rows (L2 flushed).
+constexpr float kv4_lift(int ps) { return ps == 2 ? 10.f : 6.f; }
+constexpr float kv4_slack(int ps) { return ps == 2 ? 15.75f : 14.f; }
 
 struct Kv4AttnArgs {
   KVView kv;
@@ -92,7 +98,7 @@ constexpr bool kv4_own_o(int nt, int ps) { return kv4_ahead(nt) || ps == 2; }
 // memory: mma.sync adds with truncation, one-sided.  Parts of 65536 tokens, relative 2-norm off the 64-bit result
 // (normal V | positive V): 2.0e-5 | 4.4e-5 without, 1.3e-6 | 1.5e-6 every 16 tiles, 0.8e-6 | 0.7e-6 every 8; a plain
 // fp32 computation 1.0e-6 | 0.2e-6.  32 requests of 2048 to 8192 tokens, 8 heads, d = 128 with 4 rows, d = 64 with 20 and
-// 32: 58.5, 81, 99.5 us without, 59.5, 81, 101.5 every 8.
+// 32 (L2 flushed): 58.5, 81, 99.5 us without, 60.5, 81, 99.5 every 16, 59.5, 81, 101.5 every 8.
 constexpr int kKv4Flush = 16;
 
 template <int D, int NT, int QS, int PS, int NW, int NST>
@@ -559,8 +565,8 @@ __device__ __forceinline__ void kv4_join(const Kv4AttnArgs &a, int parts, int ro
   }
 }
 
-// PS = 2 carries a probability as the sum of two f16 (22 bits) for fp32 outputs; PS = 1 rounds it to f16
-// (2^-12 relative) for bf16 outputs, whose own rounding is 2^-9.
+// PS = 2 carries a probability as the sum of two f16 for fp32 outputs; PS = 1 rounds it to f16 for bf16 outputs, whose
+// own rounding is 2^-9.
 template <int D, int NT, int QS, int PS, int NW, int NST, int BPS, bool LIST>
 __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
   using S = Kv4Smem<D>;
@@ -568,6 +574,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
   constexpr int ROWS = NT * 8;
   constexpr int PIECES = D / 4;  // 16-byte pieces of a row of O
   constexpr bool AHEAD = kv4_ahead(NT), OWN_O = kv4_own_o(NT, PS);
+  constexpr float kLift = kv4_lift(PS), kSlack = kv4_slack(PS);
   extern __shared__ __align__(128) char smem[];
   char *ring = smem;
   char *qf = ring + NW * NST * S::kStage + (OWN_O ? NW * ROWS * D * 4 : 0);
@@ -700,7 +707,7 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 4; ++k) top = fmaxf(top, x[h][nt][k]);
-      if (__any_sync(0xffffffffu, top > kKv4Slack)) {
+      if (__any_sync(0xffffffffu, top > kSlack)) {
         // The references move to the tile's largest logits; O and the sums follow.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -714,9 +721,9 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
                 if (!edge || visible(h, nt, j)) mx = fmaxf(mx, c[h][nt][j] * sl[nt][k]);
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-            mx = fmaxf(mx, m[nt][k] + kKv4Lift);
-            const float f = fast_exp2(m[nt][k] + kKv4Lift - mx);
-            m[nt][k] = mx - kKv4Lift;
+            mx = fmaxf(mx, m[nt][k] + kLift);
+            const float f = fast_exp2(m[nt][k] + kLift - mx);
+            m[nt][k] = mx - kLift;
             l[nt][k] *= f;
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i][nt][k] *= f, o[i][nt][k + 2] *= f;

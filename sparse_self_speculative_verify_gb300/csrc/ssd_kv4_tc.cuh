@@ -291,6 +291,7 @@ template <int NP, int CW, int QS, int PS>
 __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs a) {
   using C = Kv4TcCfg<NP, QS, PS>;
   constexpr int H = NP / 2;
+  constexpr float kLift = kv4_lift(PS), kSlack = kv4_slack(PS);
   using namespace sm100;
   extern __shared__ __align__(16) char smem_raw[];
   char *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
           named_sync(bar, 128);
           if (tw < CW) {
             const int q = c0 + tw;
-            s_ms[q] = fmaxf(fmaxf(fmaxf(s_red[q], s_red[NP + q]), fmaxf(s_red[2 * NP + q], s_red[3 * NP + q])), -1e30f) - kKv4Lift;
+            s_ms[q] = fmaxf(fmaxf(fmaxf(s_red[q], s_red[NP + q]), fmaxf(s_red[2 * NP + q], s_red[3 * NP + q])), -1e30f) - kLift;
           }
           named_sync(bar, 128);
         }
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
         }
 #pragma unroll
         for (int q = 0; q < CW; ++q) top = fmaxf(top, x[q]);
-        const bool moved = group_any(bar, 128, top > kKv4Slack);  // (and the next V scales are staged)
+        const bool moved = group_any(bar, 128, top > kSlack);  // (and the next V scales are staged)
         if (n > 0) wait(b_pv, n - 1);  // P, O and the other V^T are free
         const bool flush = PS == 2 && t > s.t0 && (t - s.t0) % kKv4TcFlush == 0;
         float *so = reinterpret_cast<float *>(sm + C::kO) + c0 * 128 + tw;  // this lane's [CW]
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(kKv4TcWarps * 32, 2) kv4_tc_kernel(Kv4AttnArgs
           if (tw < CW) {
             const int q = c0 + tw;
             const float up =
-                fmaxf(fmaxf(fmaxf(s_red[q], s_red[NP + q]), fmaxf(s_red[2 * NP + q], s_red[3 * NP + q])) - kKv4Lift, 0.f);
+                fmaxf(fmaxf(fmaxf(s_red[q], s_red[NP + q]), fmaxf(s_red[2 * NP + q], s_red[3 * NP + q])) - kLift, 0.f);
             s_f[q] = up;
             s_ms[q] += up;
           }

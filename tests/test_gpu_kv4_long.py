@@ -10,7 +10,7 @@ and 16 x 4 on mma.sync, between two times that O is added up to nearest):
  * a logit x: d / 16 <= 8 truncating steps (16 for fp32 queries, whose second half is 2^-11 of the first), which take up to
    2^-23 * 4 relative off |q k| <= 20: as all logits shrink alike, outputs move by 2^-21 times the spread of x under the
    softmax (under 4): 2^-19; exp2 and the subtraction 2^-21, either sign;
- * P in 22 bits: 2^-23.
+ * P in 22 bits, or 2^-35 of the largest: 2^-23, and 32768 * 2^-35 = 2^-20 at most.
 In all under 6e-6 (2^-18 + 2^-19 + ...).  lse: 2^-21 * 20 and its own half steps at 16 to 32 (2^-20): 2^-16.  Scores:
 the same shrinking logits, weighted by p, 2^-18, as a norm.  bf16 outputs: their half step 2^-9 (rms 2^-9 / sqrt 3) and
 P's 2^-12: under 2^-8.
@@ -164,3 +164,43 @@ def test_draft_over_long_lists(G, d, kind, types):
         assert off <= more + (F32_OUT if ot == torch.float32 else BF16_OUT), f"out off by {off:.2e}"
         off = (r["lse"][:, heads].reshape(-1).double() - lse).abs().max().item()
         assert off <= more + F32_LSE, f"lse off by {off:.2e}"
+
+
+def _sink(d, n, below):
+    """One token `below` powers of two above n - 1 others of equal weight, and of the opposite value: the cache of 330
+    such requests, the query and scale that make it so, and the output."""
+    k, v = np.zeros((1, n, d)), np.ones((1, n, d))
+    k[0, 0], v[0, 0] = 4.0 * _signs(d), -1.0
+    ck, cv = _kv4.quantise(k), _kv4.quantise(v)
+    pool = torch.from_numpy(np.ascontiguousarray(np.stack([_bytes(*ck), _bytes(*cv)], 1))).to(DEV)
+    K, V = _kv4.values(ck[0][:, :2], ck[1][:, :2]), _kv4.values(cv[0][:, :2], cv[1][:, :2])
+    scale = below * math.log(2) / (K[0, 0] @ _signs(d))
+    w = (n - 1) * 2.0 ** -below
+    return _cache(pool.view(KV4Cache.pool_shape(n // PAGE, 1, PAGE, d)), 330, n), scale, (V[0, 0, 0] + w * V[0, 1, 0]) / (1 + w)
+
+
+@pytest.mark.parametrize("below", [31, 32.4])
+@pytest.mark.parametrize("q_type", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("form", [(4, 128, 1), (4, 128, 5), (16, 128, 2), (4, 64, 1), (4, 64, 4), (4, 64, 5), (8, 64, 4), (4, 128, 0),
+                                  (16, 128, 0), (4, 64, 0), (16, 64, 0)], ids=lambda f: f"G{f[0]}d{f[1]}n{f[2]}")
+def test_a_flat_tail_far_below_one_token(form, q_type, below):
+    """131071 tokens, each 2^-31 and less of the first one's weight: together 6.1e-5 (and 2.3e-5) of it, so without them
+    the outputs are off by twice that, 1.2e-4 (4.6e-5).  What fp32 may lose: O is added up at most 256 times to nearest,
+    half a step of the first token's part each, 256 * 2^-24 = 2^-16; P holds steps of 2^-34 of the largest, half of one a
+    token, 2^17 * 2^-35 = 2^-18, twice (O and its sign against the first token's): 2^-17; the sum of the one thread that has
+    the first token loses its tail, 1 / 64 of 6.1e-5, and the logits' rounding is 32 * 2^-24 of the tail: under 2^-19.
+    n_cand 0: a draft over all the tokens."""
+    _gpu.lib()
+    G, d, nc = form
+    n = 131072
+    kv, scale, want = _sink(d, n, below)
+    q = torch.from_numpy(_signs(d)).to(DEV, q_type).expand(330, max(nc, 1), G, d).contiguous()
+    if nc:
+        r = ssd_kv4_verify_attn(kv, q, nc, scale, want_scores=False)
+    else:
+        idx = torch.arange(n, dtype=torch.int32, device=DEV).expand(330, 1, n).contiguous()
+        r = ssd_kv4_draft_attn(kv, q[:, 0].contiguous(), idx, torch.full((330, 1), n, dtype=torch.int32, device=DEV), scale)
+    torch.cuda.synchronize()
+    assert ssd_status() == 0
+    off = ((r["out"].double() - want).abs().max() / abs(want)).item()
+    assert off <= 2.0 ** -16 + 2.0 ** -17 + 2.0 ** -19, f"out off by {off:.2e}"
