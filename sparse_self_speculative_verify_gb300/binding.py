@@ -663,10 +663,11 @@ _TYPES = {torch.float32: SSD_DTYPE_F32, torch.bfloat16: SSD_DTYPE_BF16}
 _HERE = contextlib.nullcontext()
 _Tensor = torch.Tensor
 # What torch.cuda.current_stream, current_device and is_current_stream_capturing ask, without their objects and
-# initialisation checks (a cache's tensors are on the device already): 1.5 us of a call that took 11.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-_capturing = torch._C._cuda_isCurrentStreamCapturing
+# initialisation checks (a cache's tensors are on the device already): 1.5 us of a call that took 11.  A torch without
+# these private names gets the public calls.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 
 
 def _scope(device: int, stream):

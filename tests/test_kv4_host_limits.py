@@ -1,6 +1,9 @@
 """What the 4-bit and the page calls refuse at the ends of their ranges, on the host (no kernel is launched)."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -9,6 +12,7 @@ from sparse_self_speculative_verify_gb300 import PagePool, binding
 from sparse_self_speculative_verify_gb300 import build as libbuild
 from tests.test_kv4_host import _kv
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 E, U, W, OK = binding.SSD_ERR_INVALID_ARG, binding.SSD_ERR_UNSUPPORTED, binding.SSD_ERR_WORKSPACE, binding.SSD_OK
 
 
@@ -54,3 +58,16 @@ def test_page_counts_of_a_table_with_ids_outside_the_pool():
             PagePool.from_table(table, num_pages)
     with pytest.raises(ValueError, match="CUDA"):  # the table is fine; counts live on the GPU
         PagePool.from_table(table, 8)
+
+
+def test_import_without_torchs_private_names():
+    """The host parts import on a torch that lacks them (one built without CUDA, or of another version)."""
+    code = ("import torch\n"
+            "for name in ('_cuda_getCurrentRawStream', '_cuda_getDevice', '_cuda_isCurrentStreamCapturing'):\n"
+            "    if hasattr(torch._C, name): delattr(torch._C, name)\n"
+            "from sparse_self_speculative_verify_gb300 import binding\n"
+            "assert binding._current_device is torch.cuda.current_device\n"
+            "assert binding._capturing is torch.cuda.is_current_stream_capturing\n"
+            "assert callable(binding._raw_stream)\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0, r.stderr
