@@ -704,13 +704,16 @@ def _is_kv4(kv):
 
 
 _STREAM_WS = {}  # (device, stream, name): buffer, aligned address, bytes from there
+# Held from a call's look up of its workspace until its last launch: ctypes lets other threads run meanwhile, and two
+# threads on one stream share a workspace, so their calls' launches must not fall between each other's.
+_WS_LOCK = threading.RLock()
 
 
 def _stream_ws(device: int, name: str, nbytes: int, workspace: Optional[Workspace]):
     """Workspace of a call on the current stream: the caller's, or one kept for (device, stream), so that
     calls on different streams never share one; a call under stream capture without a workspace takes a
     buffer of its graph's own memory, whose counters a node of the graph clears.  A caller's workspace is
-    sized before a capture that uses it and must outlive the graph."""
+    sized before a capture that uses it and must outlive the graph.  Under _WS_LOCK."""
     if workspace is not None:
         return _ws(torch.device("cuda", device), name, nbytes, workspace)
     if _capturing():
@@ -796,9 +799,10 @@ def ssd_kv4_verify_attn(kv: KV4Cache, q: torch.Tensor, n_cand: int, scale: float
             need = kv._need.get((h_q, n_cand))
             if need is None:
                 need = kv._need[h_q, n_cand] = L.ssd_kv4_verify_workspace_bytes(kv.ref(), h_q, n_cand)
-            ws, avail = _stream_ws(dev, "kv4", need, workspace)
-            _check(L.ssd_kv4_verify_attn(kv.ref(), pq, qt, h_q, n_cand, float(scale), kv.k_scale, kv.v_scale, po, ot, pl, ps,
-                                         stride, ws, avail, _raw_stream(dev)))
+            with _WS_LOCK:
+                ws, avail = _stream_ws(dev, "kv4", need, workspace)
+                _check(L.ssd_kv4_verify_attn(kv.ref(), pq, qt, h_q, n_cand, float(scale), kv.k_scale, kv.v_scale, po, ot, pl,
+                                             ps, stride, ws, avail, _raw_stream(dev)))
     return {"out": out, "lse": lse, "scores": scores}
 
 
@@ -832,9 +836,10 @@ def ssd_kv4_draft_attn(kv: KV4Cache, q: torch.Tensor, idx: torch.Tensor, cnt: to
             need = kv._need.get((h_q, -1, k_max))
             if need is None:
                 need = kv._need[h_q, -1, k_max] = L.ssd_kv4_draft_workspace_bytes(kv.ref(), h_q, k_max)
-            ws, avail = _stream_ws(dev, "kv4", need, workspace)
-            _check(L.ssd_kv4_draft_attn(kv.ref(), pq, qt, h_q, pi, k_max, pc, float(scale), kv.k_scale, kv.v_scale, po, ot, pl,
-                                        ws, avail, _raw_stream(dev)))
+            with _WS_LOCK:
+                ws, avail = _stream_ws(dev, "kv4", need, workspace)
+                _check(L.ssd_kv4_draft_attn(kv.ref(), pq, qt, h_q, pi, k_max, pc, float(scale), kv.k_scale, kv.v_scale, po, ot,
+                                            pl, ws, avail, _raw_stream(dev)))
     return {"out": out, "lse": lse}
 
 
@@ -906,8 +911,10 @@ def ssd_kv_reserve(kv, pages: PagePool, counts: torch.Tensor, *, workspace: Opti
         return
     with _scope(dev, stream):
         L = _lib()
-        ws, avail = _stream_ws(dev, "pages", L.ssd_kv_reserve_workspace_bytes(kv.ref()), workspace)
-        _check(L.ssd_kv_reserve(kv.ref(), refs, pc, ws, avail, _raw_stream(dev)))
+        need = L.ssd_kv_reserve_workspace_bytes(kv.ref())
+        with _WS_LOCK:
+            ws, avail = _stream_ws(dev, "pages", need, workspace)
+            _check(L.ssd_kv_reserve(kv.ref(), refs, pc, ws, avail, _raw_stream(dev)))
 
 
 def ssd_kv_release(kv, pages: PagePool, keep: torch.Tensor, stream=None) -> None:

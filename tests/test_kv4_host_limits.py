@@ -4,11 +4,13 @@ import ctypes
 import os
 import subprocess
 import sys
+import threading
+import time
 
 import pytest
 import torch
 
-from sparse_self_speculative_verify_gb300 import PagePool, binding
+from sparse_self_speculative_verify_gb300 import KV4Cache, PagePool, binding
 from sparse_self_speculative_verify_gb300 import build as libbuild
 from tests.test_kv4_host import _kv
 
@@ -71,3 +73,53 @@ def test_import_without_torchs_private_names():
             "assert callable(binding._raw_stream)\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
     assert r.returncode == 0, r.stderr
+
+
+class _Cache(KV4Cache):
+    """Enough of a cache for the calls' host side, on the CPU."""
+
+    def __init__(self):
+        self.max_seq_len, self.k_scale, self.v_scale, self._need = 64, 1.0, 1.0, {}
+        self._geometry, self._struct = (-1, 2, 1, 64), _kv(batch=2, h_kv=1, d=64)
+        self._ref = ctypes.byref(self._struct)
+
+
+class _Pages(PagePool):
+    def __init__(self):
+        self.refs = torch.zeros(10, dtype=torch.int32)
+
+
+def test_threads_on_one_stream_take_turns_with_its_workspace(monkeypatch):
+    """A call's launches hand their results on through the workspace, and ctypes lets other threads run meanwhile."""
+    inside, most = [], []
+
+    def native(*args):
+        inside.append(1)
+        most.append(len(inside))
+        time.sleep(0.02)
+        inside.pop()
+        return OK
+
+    class Lib:
+        ssd_kv4_verify_attn = ssd_kv4_draft_attn = ssd_kv_reserve = staticmethod(native)
+        ssd_kv4_verify_workspace_bytes = ssd_kv4_draft_workspace_bytes = ssd_kv_reserve_workspace_bytes = staticmethod(lambda *a: 1024)
+
+    monkeypatch.setattr(binding, "_lib", Lib)
+    monkeypatch.setattr(binding, "_current_device", lambda: -1)
+    monkeypatch.setattr(binding, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(binding, "_capturing", lambda: False)
+    monkeypatch.setattr(binding, "_STREAM_WS", {(-1, 0, name): (None, 256, 1 << 20) for name in ("kv4", "pages")})
+    kv, pages = _Cache(), _Pages()
+    q, out = torch.zeros((2, 1, 4, 64)), torch.zeros((2, 1, 4, 64))
+    idx, cnt = torch.zeros((2, 1, 3), dtype=torch.int32), torch.zeros((2, 1), dtype=torch.int32)
+    calls = [
+        lambda: binding.ssd_kv4_verify_attn(kv, q, 1, 0.1, out=out, want_lse=False, want_scores=False),
+        lambda: binding.ssd_kv4_draft_attn(kv, q[:, 0].contiguous(), idx, cnt, 0.1, out=out[:, 0].contiguous(), want_lse=False),
+        lambda: binding.ssd_kv_reserve(kv, pages, torch.zeros(2, dtype=torch.int32)),
+    ]
+    threads = [threading.Thread(target=c) for c in calls for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(most) == 9 and max(most) == 1
