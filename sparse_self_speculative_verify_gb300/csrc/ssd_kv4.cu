@@ -99,11 +99,11 @@ static int kv4_grid(int64_t units, int max_tokens, int tile, int blocks_per_sm) 
   return (int)(bound < dev ? bound : dev);
 }
 
-template <int D>
-static int kv4_blocks_of(int nt) {
-  return nt == 1 ? Kv4Tune<D, 1>::kBlocks : nt == 2 ? Kv4Tune<D, 2>::kBlocks : nt == 3 ? Kv4Tune<D, 3>::kBlocks : Kv4Tune<D, 4>::kBlocks;
+// Blocks per SM of kv4_attn_kernel: at d = 128 it takes up to 16 rows (drafts), at d = 64 up to 32.
+static int kv4_blocks_per_sm(int d, int nt) {
+  if (d == 128) return nt == 1 ? Kv4Tune<128, 1>::kBlocks : Kv4Tune<128, 2>::kBlocks;
+  return nt == 1 ? Kv4Tune<64, 1>::kBlocks : nt == 2 ? Kv4Tune<64, 2>::kBlocks : nt == 3 ? Kv4Tune<64, 3>::kBlocks : Kv4Tune<64, 4>::kBlocks;
 }
-static int kv4_blocks_per_sm(int d, int nt) { return d == 128 ? kv4_blocks_of<128>(nt) : kv4_blocks_of<64>(nt); }
 
 }  // namespace ssd
 

@@ -913,8 +913,10 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
 // Criticality: a second pass over K alone recomputes the logits and sums exp(x - lse) over the rows.
 // (Keeping them from the first pass would cost 2 R bytes per token each way, more than K's 72 for R > 18,
 // and a rounding to f16.)
-template <int D, int NT, int QS, int NW, int NST, int BPS>
+// d = 64 (at d = 128 kv4_crit_tc_kernel takes all calls).
+template <int NT, int QS, int NW, int NST, int BPS>
 __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {
+  constexpr int D = 64;
   using S = Kv4Smem<D>;
   constexpr int ROWS = NT * 8;
   extern __shared__ __align__(128) char smem[];
@@ -1064,11 +1066,11 @@ int kv4_attn_types(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
   return kv4_launch_attn<D, NT, 1, 1, LIST>(a, grid, st);
 }
 
-template <int D, int NT, int QS>
+template <int NT, int QS>
 int kv4_launch_crit(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
   constexpr int NW = kKv4CritWarps, NST = kKv4CritStages, BPS = kKv4CritBlocks;
-  constexpr int smem = NW * NST * Kv4Smem<D>::kCritStage + 2 * NT * 8 * D * 2 * QS + 6 * NT * 8 * 4;
-  constexpr auto kernel = kv4_crit_kernel<D, NT, QS, NW, NST, BPS>;
+  constexpr int smem = NW * NST * Kv4Smem<64>::kCritStage + 2 * NT * 8 * 64 * 2 * QS + 6 * NT * 8 * 4;
+  constexpr auto kernel = kv4_crit_kernel<NT, QS, NW, NST, BPS>;
   int rc = ensure_smem<kernel>(smem);
   if (rc) return rc;
   return launch(kernel, dim3(grid), dim3(NW * 32), smem, st, "kv4_crit_kernel", a);

@@ -7,10 +7,10 @@ int kv4_list_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st) {
 }
 int kv4_crit_d64(const Kv4AttnArgs &a, int nt, int grid, cudaStream_t st) {
   switch (nt) {
-    case 1: return a.q_f32 ? kv4_launch_crit<64, 1, 2>(a, grid, st) : kv4_launch_crit<64, 1, 1>(a, grid, st);
-    case 2: return a.q_f32 ? kv4_launch_crit<64, 2, 2>(a, grid, st) : kv4_launch_crit<64, 2, 1>(a, grid, st);
-    case 3: return a.q_f32 ? kv4_launch_crit<64, 3, 2>(a, grid, st) : kv4_launch_crit<64, 3, 1>(a, grid, st);
-    default: return a.q_f32 ? kv4_launch_crit<64, 4, 2>(a, grid, st) : kv4_launch_crit<64, 4, 1>(a, grid, st);
+    case 1: return a.q_f32 ? kv4_launch_crit<1, 2>(a, grid, st) : kv4_launch_crit<1, 1>(a, grid, st);
+    case 2: return a.q_f32 ? kv4_launch_crit<2, 2>(a, grid, st) : kv4_launch_crit<2, 1>(a, grid, st);
+    case 3: return a.q_f32 ? kv4_launch_crit<3, 2>(a, grid, st) : kv4_launch_crit<3, 1>(a, grid, st);
+    default: return a.q_f32 ? kv4_launch_crit<4, 2>(a, grid, st) : kv4_launch_crit<4, 1>(a, grid, st);
   }
 }
 }  // namespace ssd
