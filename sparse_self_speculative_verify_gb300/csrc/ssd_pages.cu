@@ -359,7 +359,7 @@ struct CompactArgs {
   const int32_t *to_refs;
   const int32_t *src, *dst, *idx, *cnt;
   int n, k_max, tokens;  // tokens: list entries per block
-  bool same;  // one cache
+  bool same;  // one cache, or two with the same lengths: a row read must not be one that is written
   RowShape rs;
   unsigned *status;
 };
@@ -549,7 +549,7 @@ extern "C" int ssd_kv_compact(const ssd_paged_kv *kv, const ssd_paged_kv *to, co
   a.to_lens = const_cast<int32_t *>(to->seq_lens);
   a.to_refs = to_refs;
   a.src = src, a.dst = dst, a.idx = idx, a.cnt = cnt, a.n = n, a.k_max = k_max;
-  a.same = kv->page_table == to->page_table;
+  a.same = kv->page_table == to->page_table || kv->seq_lens == to->seq_lens;
   a.rs = row_shape(kv);
   // Half as many entries per block while that leaves SMs without work.
   const int k = k_max > 0 ? k_max : 1;

@@ -73,3 +73,27 @@ def test_pages_whose_rows_lie_past_2_gb():
         assert torch.equal(pool[0, w, 0, :L], pool[2, w, 0, :L]), w
     del pool, kv
     torch.cuda.empty_cache()
+
+
+def test_compact_between_two_caches_with_the_same_lengths():
+    """Row 0 of one cache into row 0 of the other would write the length that its own blocks still read."""
+    _gpu.lib()
+    page, d, n, k = 16, 64, 4096, 3000
+    g = torch.Generator(device=DEV).manual_seed(1)
+    lens = torch.tensor([n, 0], dtype=torch.int32, device=DEV)
+    pools = [torch.randn((n // page + 4, 2, 2, page, d), generator=g, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    tables = [torch.arange(n // page, dtype=torch.int32, device=DEV).expand(2, -1).contiguous() for _ in range(2)]
+    kv, to = (KVCache(p, t, lens, n) for p, t in zip(pools, tables))
+    before = pools[1].clone()
+    idx = torch.arange(n - k, n, dtype=torch.int32, device=DEV).expand(1, 2, k).contiguous()
+    cnt = torch.full((1, 2), k, dtype=torch.int32, device=DEV)
+    row = lambda x: torch.tensor([x], dtype=torch.int32, device=DEV)  # noqa: E731
+    ssd_kv_compact(kv, to, row(0), row(0), idx, cnt)
+    torch.cuda.synchronize()
+    assert ssd_status() == binding.FAULT_INDEX
+    assert lens.tolist() == [n, 0] and torch.equal(pools[1], before)
+    ssd_kv_compact(kv, to, row(0), row(1), idx, cnt)  # another row's length
+    torch.cuda.synchronize()
+    assert ssd_status() == 0 and lens.tolist() == [n, k]
+    flat = lambda p: p[tables[0][0].long()].transpose(0, 2).transpose(0, 1).reshape(2, 2, n, d)  # noqa: E731
+    assert torch.equal(flat(pools[1])[:, :, :k], flat(pools[0])[:, :, n - k:])
