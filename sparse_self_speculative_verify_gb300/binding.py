@@ -711,12 +711,17 @@ _WS_LOCK = threading.RLock()
 
 def _stream_ws(device: int, name: str, nbytes: int, workspace: Optional[Workspace]):
     """Workspace of a call on the current stream: the caller's, or one kept for (device, stream), so that
-    calls on different streams never share one; a call under stream capture without a workspace takes a
-    buffer of its graph's own memory, whose counters a node of the graph clears.  A caller's workspace is
-    sized before a capture that uses it and must outlive the graph.  Under _WS_LOCK."""
+    calls on different streams never share one; a call under stream capture without a workspace, or with one that an
+    earlier call has not made large enough, takes a buffer of its graph's own memory, whose counters a node of the
+    graph clears.  A caller's workspace that graphs were captured with must outlive them, and
+    they run one after the other.  Under _WS_LOCK."""
+    capturing = _capturing()
     if workspace is not None:
-        return _ws(torch.device("cuda", device), name, nbytes, workspace)
-    if _capturing():
+        at = torch.device("cuda", device)
+        buf = workspace._bufs.get((str(at), name))
+        if not capturing or (buf is not None and buf.numel() >= nbytes):
+            return _ws(at, name, nbytes, workspace)
+    if capturing:
         buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
         buf[:COUNTER_BYTES + 256].zero_()
         return Workspace.aligned(buf), nbytes
