@@ -218,6 +218,7 @@ class Workspace:
 
     def __init__(self):
         self._bufs = {}
+        self._captured = []  # buffers that graphs captured from the 4-bit and page calls hold: kept when others replace them
 
     def get(self, device, name: str, nbytes: int) -> torch.Tensor:
         key = (str(device), name)
@@ -720,6 +721,8 @@ def _stream_ws(device: int, name: str, nbytes: int, workspace: Optional[Workspac
         at = torch.device("cuda", device)
         buf = workspace._bufs.get((str(at), name))
         if not capturing or (buf is not None and buf.numel() >= nbytes):
+            if capturing and not any(b is buf for b in workspace._captured):
+                workspace._captured.append(buf)
             return _ws(at, name, nbytes, workspace)
     if capturing:
         buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)

@@ -1,4 +1,4 @@
-"""Workspaces of the 4-bit calls under stream capture."""
+"""Workspaces of the 4-bit calls under stream capture: not sized before, and grown after."""
 
 import pytest
 import torch
@@ -53,6 +53,32 @@ def test_capture_with_a_workspace_that_no_call_has_sized():
         graph.replay()
         assert _equal(out, want)
     assert ssd_status() == 0
+
+
+def test_workspace_that_grows_after_a_capture():
+    """A larger call replaces the workspace's buffer; the graph that holds the smaller one keeps it."""
+    _gpu.lib()
+    kv = _cache(_tokens("spread", H, D)[0], 1)
+    small, large = (_rows((1, nc, G * H, D), torch.bfloat16, 62, 1.5).to(DEV) for nc in (1, 16))
+    ws, out, big = Workspace(), _out(small, kv), _out(large, kv)
+    want = [t.clone() for t in _call(kv, small, ws, out)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _call(kv, small, ws, out)
+    held = ws._bufs[(DEV, "kv4")]
+    lo, hi, size = held.data_ptr(), held.data_ptr() + held.numel(), held.numel()
+    del held
+    _call(kv, large, ws, big)
+    torch.cuda.synchronize()
+    assert ws._bufs[(DEV, "kv4")].data_ptr() != lo
+    others = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(4)]  # whoever asks for memory next
+    assert not any(lo <= t.data_ptr() < hi for t in others)
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        assert _equal(out, want)
+    assert all((t == 7).all() for t in others) and ssd_status() == 0
 
 
 def test_round_captured_without_a_run_before():
