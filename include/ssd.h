@@ -454,6 +454,8 @@ int ssd_kv4_draft_attn(const ssd_paged_kv *kv, const void *q, int q_dtype, int h
  *   becomes the count.  idx: device int32 [n][h_kv][k_max] (k_max at most 2^24), cnt: device int32 [n][h_kv],
  *   the same for every head of a pair.  Token order is the list's.  dst's pages must be reserved beforehand; slots behind the last
  *   token stay as they are.  to_refs: page_refs of `to`, or NULL; with it, rows go only into pages held once.
+ *   Without it nothing checks that: the caller answers for dst's pages being held by dst alone, of the same cache
+ *   too (a branch that still shares its parent's pages would be written into the parent).
  *   A pair is skipped when a row is out of range, when its dst is an earlier pair's or, within one cache
  *   (or two with one page_table or one seq_lens), any pair's src (SSD_FAULT_INDEX), when its counts differ or lie outside [0, k_max] (SSD_FAULT_KMAX), or
  *   when src's length or the count does not fit (SSD_FAULT_SEQLEN).  An entry outside [0, length of src)

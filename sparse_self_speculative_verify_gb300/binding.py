@@ -941,7 +941,8 @@ def ssd_kv_compact(kv, to, src: torch.Tensor, dst: torch.Tensor, idx: torch.Tens
                    pages: Optional[PagePool] = None, stream=None) -> None:
     """The listed tokens idx [n, h_kv, k_max] (cnt [n, h_kv] of them, the same for every head) of row src[i] of `kv`
     go to positions 0 .. of row dst[i] of `to`, whose length becomes the count.  dst's pages are reserved
-    beforehand; with `pages` (the PagePool of `to`) shared ones are left alone and reported."""
+    beforehand; with `pages` (the PagePool of `to`) shared ones are left alone and reported, without it the caller
+    answers for their being held by dst alone."""
     if not isinstance(kv, (KVCache, KV4Cache)) or type(to) is not type(kv):
         raise TypeError("kv and to must both be a KVCache or both a KV4Cache")
     dev, _, h, _ = kv._geometry

@@ -130,8 +130,8 @@ extern "C" int ssd_kv4_verify_attn(const ssd_paged_kv *kv, const void *q, int q_
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // d = 128 runs on tcgen05 from 9 rows on.  32 requests of 2048 to 8192 tokens, 8 heads: 4 rows 48 us on mma.sync
   // against 62, 8 rows 49 against 63, 12 rows 70.5 against 68.5 (fp32 outputs: 78 against 70), 16 rows 72
-  // against 70.  (Two such requests alone, 4 rows: 11.8 against 13.6; 16 rows: 16 against 22.)  At d = 64 V^T would
-  // fill half the rows of tcgen05's M = 128.
+  // against 70.  (Two such requests alone, 4 rows: 11.8 against 13.6; 16 rows: 16 against 22.)  d = 64 has no tcgen05
+  // form: V^T would fill half of M = 128, and M = 64 (which kind::f16 has too) has not been built.
   const int nt = kv4_nt(a.R);
   if (kv->d == 128 && a.R <= 8)
     rc = kv4_dense_d128(a, kv4_grid(a.n_units, kv->max_seq_len, kKv4Tile * 4, kv4_blocks_per_sm(kv->d, nt)), st);

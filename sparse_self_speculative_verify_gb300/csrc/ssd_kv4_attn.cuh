@@ -6,8 +6,8 @@
 //   out_r = sum_t exp(x_rt) v_t / sum_t exp(x_rt) over the tokens row r sees, lse_r = log sum_t exp(x_rt),
 //   crit_t = sum_r exp(x_rt - lse_r)   (SparseSpec §4.1: criticality summed over the group's heads and
 //   the verify positions).
-// One pass over K and V keeps a running reference m_r (a past maximum), the sum of exp2(x - m) and
-// the weighted sum of V, all in fp32.
+// One pass over K and V keeps a running reference m_r (a past maximum, in log2 units), the sum l_r of exp2(x - m) and
+// the weighted sum of V, all in fp32; the criticality takes exp2(x - m_r) / l_r.
 //
 // Bound: 9 bits per (K, V) element pair stored, 144 bytes per token of a head at d = 128, so HBM bounds
 // small R; the f16 tensor-core rate of mma.sync (1024 multiply-adds per clock and SM) bounds R > 20.
@@ -22,7 +22,7 @@
 //
 // What bounds it: its steady loop takes 185 clocks a tile and SM, what HBM takes to deliver one (195), at about
 // 600 instructions, 256 of them the conversions; the rest is the start (5 us), merges and joins where
-// blocks change units (4 us each), and blocks ending apart.  8 heads of d = 128, 4 rows each: 32 requests of
+// blocks change units (4 us each), and blocks ending apart.  8 heads of d = 128, 4 rows each, bf16 outputs: 32 requests of
 // 2048 to 8192 tokens 48 us (59 % of the measured HBM rate), 128 such requests 154 us (73 %), 8 of 65536 tokens
 // 114 us (78 %).  With more rows the O accumulators leave room for few warps, and the kernel of ssd_kv4_tc.cuh
 // takes over at d = 128.
@@ -910,9 +910,9 @@ __global__ void __launch_bounds__(NW * 32, BPS) kv4_attn_kernel(Kv4AttnArgs a) {
   }
 }
 
-// Criticality: a second pass over K alone recomputes the logits and sums exp(x - lse) over the rows.
-// (Keeping them from the first pass would cost 2 R bytes per token each way, more than K's 72 for R > 18,
-// and a rounding to f16.)
+// Criticality: a second pass over K alone recomputes the logits and sums exp2(x - m) / l over the rows, from each row's
+// reference and 1 / sum.  (Keeping them from the first pass would cost 2 R bytes per token each way, more than K's 36
+// for R > 9, and a rounding to f16.)
 // d = 64 (at d = 128 kv4_crit_tc_kernel takes all calls).
 template <int NT, int QS, int NW, int NST, int BPS>
 __global__ void __launch_bounds__(NW * 32, BPS) kv4_crit_kernel(Kv4AttnArgs a) {

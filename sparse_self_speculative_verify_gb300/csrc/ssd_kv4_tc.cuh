@@ -13,8 +13,8 @@
 //
 // What bounds it: instructions.  A tile takes about 1000 per warp's 32 tokens (V's conversion 260, K's 200, the
 // softmax and its probabilities 160, loads 75), at two thirds of the issue rate; the MMAs fill 40 % of their pipe.
-// 8 heads, 20 rows: 32 requests of 2048 to 8192 tokens 80 us (36 % of the measured HBM rate; mma.sync took 120),
-// 8 requests of 131072 tokens 335 us (53 %).
+// 8 heads, 20 rows: 32 requests of 2048 to 8192 tokens 81 us with bf16 outputs (35 % of the measured HBM rate; mma.sync
+// took 120), 92 with fp32 ones, 8 requests of 131072 tokens 335 us (53 %) and 387.
 //
 // Roles of a block (two blocks share an SM, each filling the other's gaps):
 //   warps 0-7  two groups of four (a group covers the 128 lanes), each with half of every step:
@@ -25,7 +25,7 @@
 //              to shared memory as the B operand, N-major with 128-byte rows; each half has its own references
 //              (warps 4-7 also write the output at a segment's end)
 //   warp 8     issues the MMAs
-//   warp 9     loads the raw tiles (cp.async, three stages)
+//   warp 9     loads the raw tiles (cp.async, four stages for bf16 outputs, three for fp32)
 #pragma once
 
 #include "ssd_kv4_attn.cuh"
@@ -778,9 +778,9 @@ struct Kv4CritCfg {
   static_assert(kColS + kBufs * NP <= kTmem, "tensor memory");
 };
 
-// A second pass over K alone recomputes the logits of all rows and sums exp(x - lse) per token.  (Keeping them from
-// the first pass would cost 2 R bytes per token each way, more than K's 72 for R > 18, and a rounding to
-// f16.)
+// A second pass over K alone recomputes the logits of all rows and sums exp2(x - m) / l per token, from each row's
+// reference m and 1 / l.  (Keeping them from the first pass would cost 2 R bytes per token each way, more than K's 72
+// for R > 18, and a rounding to f16.)
 //
 // CR: columns that hold rows (the MMA takes NP).  Four blocks share an SM (two, and one S^T: attention and
 // criticality of 32 requests of 2048 to 8192 tokens, 8 heads, 20 rows, took 134 us instead of 128).
