@@ -106,9 +106,20 @@ FORMS = [  # h_kv, G, d, n_cand
 @pytest.mark.parametrize("kind", ["spread", "positive", "grow"])
 @pytest.mark.parametrize("form", FORMS, ids=lambda f: f"h{f[0]}G{f[1]}d{f[2]}n{f[3]}")
 def test_verify_over_long_stretches(form, kind, types):
+    _verify(form, kind, types, 330 // form[0])
+
+
+@pytest.mark.parametrize("types", ["bf16-f32", "bf16-bf16"])
+@pytest.mark.parametrize("B", [1, 3, 20])
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: f"h{f[0]}G{f[1]}d{f[2]}n{f[3]}")
+def test_verify_of_few_long_requests(form, B, types):
+    """Units of a hundred parts down to eight, joined by the last block to arrive or, on tcgen05, by a launch of their own."""
+    _verify(form, "spread", types, B)
+
+
+def _verify(form, kind, types, B):
     _gpu.lib()
     h, G, d, nc = form
-    B = 330 // h
     qt, ot = _types(types)
     pool, K, V = _tokens(kind, h, d)
     kv = _cache(pool, B)
