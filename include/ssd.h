@@ -472,6 +472,84 @@ int ssd_kv_release(const ssd_paged_kv *kv, int32_t *page_refs, const int32_t *ke
 int ssd_kv_compact(const ssd_paged_kv *kv, const ssd_paged_kv *to, const int32_t *to_refs, const int32_t *src,
                    const int32_t *dst, int n, const int32_t *idx, int k_max, const int32_t *cnt, ssd_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Attention of a request's last tokens, by position and by tree (speculation with trees of drafted tokens:
+ * SpecSA "branch handling"; the chain of ssd_verify_attn is the tree in which every node hangs on the one before).
+ * Request b's queries are its last counts[b] tokens (device int32 [batch], each in [0, n]; NULL: n for everyone):
+ * query i < counts[b] sits at position p = seq_lens[b] - counts[b] + i, its K and V among the cache's rows.
+ *   ssd_tree_attn    the queries are the nodes of a tree.  parents: device int32 [batch][n], the node that node i
+ *                    hangs on, before it (parents[b][i] < i), or -1.  Node i sees every token before the tree, its
+ *                    ancestors and itself.  A parent outside [-1, i) ends the node's ancestors and raises
+ *                    SSD_FAULT_INDEX.  n at most 512, n * h_q / h_kv at most 8192.
+ *   ssd_window_attn  query i sees the tokens t <= p with t < sink or t > p - window (window >= 1, sink >= 0, each at
+ *                    most 2^30): the last `window` ones and the request's first `sink`.  Pages that hold no token
+ *                    of these are not read; their entries of the page table may be free.
+ *   q     device [batch][n][h_q][d] of kv->dtype, 16-byte aligned; h_q / h_kv at most 128.
+ *   scale softmax scale, positive and finite.
+ *   out   device [batch][n][h_q][d] of kv->dtype, 16-byte aligned; lse device float [batch][n][h_q] or NULL.
+ *         Products and sums are held in fp32; over a bf16 cache probabilities are rounded to bf16 (2^-9 of each) before
+ *         they meet V.  Rows i >= counts[b], and queries whose position would be negative, get out = 0, lse = -inf.
+ *   workspace  device, >= the matching query's bytes, 256-byte aligned.
+ * A length outside [counts[b], max_seq_len] and a count outside [0, n] raise SSD_FAULT_SEQLEN and are clamped.  K and V
+ * of tokens that no query of the call sees may hold anything; V of a token that some queries see and others do not has
+ * to be finite (an infinity or NaN there can reach the latter).
+ */
+size_t ssd_tree_workspace_bytes(const ssd_paged_kv *kv, int h_q, int n);
+int ssd_tree_attn(const ssd_paged_kv *kv, const void *q, int h_q, int n, const int32_t *parents, const int32_t *counts,
+                  float scale, void *out, float *lse, void *workspace, size_t workspace_bytes, ssd_stream_t stream);
+size_t ssd_window_workspace_bytes(const ssd_paged_kv *kv, int h_q, int n, int window, int sink);
+int ssd_window_attn(const ssd_paged_kv *kv, const void *q, int h_q, int n, const int32_t *counts, int window, int sink,
+                    float scale, void *out, float *lse, void *workspace, size_t workspace_bytes, ssd_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Log probabilities of given tokens under rows of logits, with each row's log-sum-exp, entropy and top alternatives:
+ * what acceptance of drafted tokens, and the next tree's growth, go by.
+ *   logits   device [n_rows] rows of `vocab` elements of dtype (SSD_DTYPE_BF16 or SSD_DTYPE_F32), row_stride elements
+ *            apart (any stride and alignment of its element).
+ *   tokens   device int32 [n_tokens].  rows: device int32 [n_tokens], the row that each is looked up in; NULL: n_tokens
+ *            is a multiple of n_rows and belongs to the rows in order.  A token outside [0, vocab) or a row
+ *            outside [0, n_rows) raises SSD_FAULT_INDEX and gets NaN; a row of -1 (the token of a tree's root, which has
+ *            no row) gets 0 without a fault.
+ *   logprob  device float [n_tokens] (may be NULL when n_tokens is 0): ln softmax(row)[token].
+ *   lse, entropy  device float [n_rows] (lse is required, entropy may be NULL): ln sum exp x; -sum p ln p.
+ *   top_ids, top_logprobs  device int32 / float [n_rows][top_k]: the top_k largest logits of each row, descending, equal
+ *            ones in the order of their index.  0 <= top_k <= min(vocab, 64).
+ * Sums are held in fp32 relative to the row's maximum.  -inf is a token that cannot occur; a row of nothing else has
+ * lse = -inf, entropy 0 and log probabilities -inf.  A row with NaN or +inf has lse, entropy and log probabilities NaN;
+ * NaN is never among the top, and where a row has fewer than top_k others the rest of top_ids is -1.
+ */
+int ssd_token_logprobs(const void *logits, int dtype, int64_t row_stride, int n_rows, int vocab, const int32_t *tokens,
+                       const int32_t *rows, int n_tokens, float *logprob, float *lse, float *entropy, int32_t *top_ids,
+                       float *top_logprobs, int top_k, ssd_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * What stays of a drafted tree (SparseSpec §2.3 and SpecSA "branch handling": accepted tokens' K / V stay, the others
+ * are dropped).  Node 0 is the token that the last step gave and always stays; a node c > 0 stays when its parent does and
+ *   logprob == NULL:  tokens[c] == target[parent of c], the model's own (greedy or sampled) token after the parent;
+ *   else:             logprob[c] > min(ln epsilon, ln delta - entropy[parent of c])   (in fp32),
+ * with logprob[c] that of node c's token under its parent's row and entropy[p] that of node p's own row.
+ *   parents, tokens, target  device int32 [batch][n], n at most 512 (tokens is not read when logprob is given);
+ *   logprob, entropy  device float [batch][n], both or neither; epsilon, delta > 0.
+ *   counts   device int32 [batch]: nodes of each tree, in [0, n] (SSD_FAULT_SEQLEN otherwise, clamped); NULL: n.
+ * Of the nodes that stay at a depth below max_path the deepest is taken, the lowest of equally deep ones:
+ *   path     device int32 [batch][max_path]: the nodes from node 0 to it, ascending, -1 behind them;
+ *   cnt      device int32 [batch]: how many;  next  device int32 [batch]: its target, the step's new token;
+ *   advance  device int32 [batch]: cnt - counts, for ssd_kv_advance once every layer's rows are committed.
+ * A tree of 0 nodes gives cnt 0, next -1.  A parent outside [-1, i) (for node 0: other than -1) raises SSD_FAULT_INDEX; such
+ * a node c > 0 does not stay, nor does one with parent -1.
+ */
+int ssd_tree_accept(const int32_t *parents, const int32_t *tokens, const int32_t *target, const float *logprob,
+                    const float *entropy, double epsilon, double delta, const int32_t *counts, int batch, int n,
+                    int max_path, int32_t *path, int32_t *cnt, int32_t *next, int32_t *advance, ssd_stream_t stream);
+/* Moves the rows of the path's nodes together: node path[b][j]'s K and V (position seq_lens[b] - counts[b] + path[b][j])
+ * go to position seq_lens[b] - counts[b] + j, j < cnt[b], in place; seq_lens stays (layers may share it: advance it
+ * afterwards).  The tree's pages are held by the request alone (ssd_kv_reserve).  path: device int32 [batch][max_path],
+ * max_path at most 512.  A request is left as it was when its entries do not ascend within [0, counts[b]) (SSD_FAULT_INDEX),
+ * its count lies outside [0, min(max_path, counts[b])] (SSD_FAULT_KMAX), its length outside [counts[b], max_seq_len] or its
+ * tree's size outside [0, n] (SSD_FAULT_SEQLEN), or a page of the rows outside the pool (SSD_FAULT_PAGE). */
+int ssd_tree_commit(const ssd_paged_kv *kv, int n, const int32_t *counts, const int32_t *path, int max_path,
+                    const int32_t *cnt, ssd_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

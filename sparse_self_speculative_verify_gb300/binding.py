@@ -35,7 +35,9 @@ EXPORTED = ["ssd_last_error", "ssd_version", "ssd_status", "ssd_verify_workspace
             "ssd_combine",
             "ssd_kv4_append", "ssd_kv4_read", "ssd_kv4_verify_workspace_bytes", "ssd_kv4_verify_attn",
             "ssd_kv4_draft_workspace_bytes", "ssd_kv4_draft_attn",
-            "ssd_kv_fork", "ssd_kv_reserve_workspace_bytes", "ssd_kv_reserve", "ssd_kv_release", "ssd_kv_compact"]
+            "ssd_kv_fork", "ssd_kv_reserve_workspace_bytes", "ssd_kv_reserve", "ssd_kv_release", "ssd_kv_compact",
+            "ssd_tree_workspace_bytes", "ssd_tree_attn", "ssd_window_workspace_bytes", "ssd_window_attn",
+            "ssd_token_logprobs", "ssd_tree_accept", "ssd_tree_commit"]
 
 
 class LibraryNotBuilt(RuntimeError):
@@ -75,6 +77,7 @@ def load(path: Optional[str] = None, as_default: bool = False):
             raise LibraryNotBuilt(f"{p} does not exist; build it with sparse_self_speculative_verify_gb300.build.build()")
         L = ctypes.CDLL(p)
         P, I, I64, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+        D = ctypes.c_double
         KV = ctypes.POINTER(PagedKVStruct)
         sig = {
             "ssd_last_error": ([], ctypes.c_char_p),
@@ -111,6 +114,13 @@ def load(path: Optional[str] = None, as_default: bool = False):
             "ssd_kv_reserve": ([KV, P, P, P, S, P], I),
             "ssd_kv_release": ([KV, P, P, P], I),
             "ssd_kv_compact": ([KV, KV, P, P, P, I, P, I, P, P], I),
+            "ssd_tree_workspace_bytes": ([KV, I, I], S),
+            "ssd_tree_attn": ([KV, P, I, I, P, P, F, P, P, P, S, P], I),
+            "ssd_window_workspace_bytes": ([KV, I, I, I, I], S),
+            "ssd_window_attn": ([KV, P, I, I, P, I, I, F, P, P, P, S, P], I),
+            "ssd_token_logprobs": ([P, I, I64, I, I, P, P, I, P, P, P, P, P, I, P], I),
+            "ssd_tree_accept": ([P, P, P, P, P, D, D, P, I, I, I, P, P, P, P, P], I),
+            "ssd_tree_commit": ([KV, I, P, P, I, P, P], I),
             "ssd_kv4_draft_attn": ([KV, P, I, I, P, I, P, F, F, F, P, I, P, P, S, P], I),
         }
         for name, (args, res) in sig.items():
@@ -183,6 +193,7 @@ class KVCache:
             self.seq_lens.shape[0], int(self.max_seq_len))
         self._geometry = (self.pool.get_device(), self.batch, self.h_kv, self.d)
         self._ref = ctypes.byref(self._struct)
+        self._need = {}  # workspace bytes of the tree and window calls' shapes
 
     @property
     def h_kv(self) -> int:
@@ -963,3 +974,170 @@ def ssd_kv_compact(kv, to, src: torch.Tensor, dst: torch.Tensor, idx: torch.Tens
         return
     with _scope(dev, stream):
         _check(_lib().ssd_kv_compact(kv.ref(), to.ref(), refs, ps, pd, n, pi, k_max, pc, _raw_stream(dev)))
+
+
+# ------------------------------------------------------------------------------------------------
+# A step that drafts a tree of tokens: attention of a request's last tokens, scores, acceptance, commit.
+# ------------------------------------------------------------------------------------------------
+
+
+def _span_attn(kv, q, parents, counts, window, sink, scale, out, lse, want_lse, workspace, stream) -> dict:
+    if not isinstance(kv, KVCache):
+        raise TypeError(f"kv must be a KVCache, got {type(kv).__name__}")
+    dev, B, h, d = kv._geometry
+    if not isinstance(q, _Tensor) or q.dim() != 4:
+        raise ValueError("q must be a torch.Tensor [batch, n, h_q, d]")
+    n, h_q = q.shape[1], q.shape[2]
+    shape = (B, n, h_q, d)
+    dtype = kv.pool.dtype
+    pq = _shaped(q, "q", dtype, dev, shape)
+    pp = None if window is not None else _shaped(parents, "parents", torch.int32, dev, (B, n))
+    pc = _maybe(counts, "counts", torch.int32, dev, (B,))
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
+        po = _shaped(out, "out", dtype, dev, shape)
+        pl = _maybe(lse, "lse", torch.float32, dev, shape[:3])
+        if B:
+            L = _lib()
+            key = (h_q, n, window, sink)
+            need = kv._need.get(key)
+            if need is None:
+                need = kv._need[key] = L.ssd_tree_workspace_bytes(kv.ref(), h_q, n) if window is None else \
+                    L.ssd_window_workspace_bytes(kv.ref(), h_q, n, window, sink)
+            with _WS_LOCK:
+                ws, avail = _stream_ws(dev, "span", need, workspace)
+                st = _raw_stream(dev)
+                _check(L.ssd_tree_attn(kv.ref(), pq, h_q, n, pp, pc, scale, po, pl, ws, avail, st) if window is None else
+                       L.ssd_window_attn(kv.ref(), pq, h_q, n, pc, window, sink, scale, po, pl, ws, avail, st))
+    return {"out": out, "lse": lse}
+
+
+def ssd_tree_attn(kv: KVCache, q: torch.Tensor, parents: torch.Tensor, scale: float, *, counts: Optional[torch.Tensor] = None,
+                  out=None, lse=None, want_lse: bool = True, workspace: Optional[Workspace] = None, stream=None) -> dict:
+    """Attention of a drafted tree over the paged cache: the nodes are the last counts[b] (int32 [B]; None: n) tokens of
+    request b, and node i sees all tokens before the tree, its ancestors and itself.  q [B, n, h_q, d] and out have the
+    cache's type; parents int32 [B, n], the earlier node that a node hangs on or -1.  Rows behind counts[b]: out 0,
+    lse -inf."""
+    return _span_attn(kv, q, parents, counts, None, 0, float(scale), out, lse, want_lse, workspace, stream)
+
+
+def ssd_window_attn(kv: KVCache, q: torch.Tensor, window: int, sink: int, scale: float, *, counts: Optional[torch.Tensor] = None,
+                    out=None, lse=None, want_lse: bool = True, workspace: Optional[Workspace] = None, stream=None) -> dict:
+    """Attention of each request's last counts[b] (int32 [B]; None: n) tokens, a decoding step's one or a prompt's many, with
+    a sliding window: position p sees the tokens t <= p with t > p - window or t < sink.  q [B, n, h_q, d] and out have the
+    cache's type.  Rows behind counts[b]: out 0, lse -inf."""
+    return _span_attn(kv, q, None, counts, int(window), int(sink), float(scale), out, lse, want_lse, workspace, stream)
+
+
+def ssd_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, rows: Optional[torch.Tensor] = None, top_k: int = 0,
+                       logprob=None, lse=None, entropy=None, top_ids=None, top_logprobs=None, stream=None) -> dict:
+    """Log probabilities of given tokens under rows of logits [N, V] (bf16 or fp32; rows may be strided), with every row's
+    log-sum-exp and entropy and, for top_k > 0, its top_k largest logits' ids and log probabilities (descending, equal ones
+    by index).  tokens int32: [N] or [N, m], each row's own, or with rows (int32 [M]) [M], token i looked up in row
+    rows[i] (-1: a tree's root, which gets 0)."""
+    dt = _typed(logits, "logits")
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA tensor [rows, vocab] with its last dimension dense")
+    N, V = logits.shape
+    dev = logits.get_device()
+    M = 0
+    pt = pr = None
+    if tokens is not None:
+        if not isinstance(tokens, _Tensor):
+            raise TypeError("tokens must be a torch.Tensor")
+        pt = _shaped(tokens, "tokens", torch.int32, dev, tokens.shape)
+        M = tokens.numel()
+        if rows is not None:
+            pr = _shaped(rows, "rows", torch.int32, dev, tokens.shape)
+        elif tokens.dim() not in (1, 2) or tokens.shape[0] != N:
+            raise ValueError("tokens must be [rows] or [rows, m]; give rows= for tokens of chosen rows")
+    elif rows is not None or logprob is not None:
+        raise ValueError("rows and logprob go with tokens")
+    if top_k < 0 or top_k > V:
+        raise ValueError(f"top_k {top_k} outside [0, {V}]")
+    with _scope(dev, stream):
+        f32, i32 = torch.float32, torch.int32
+        if logprob is None and tokens is not None:
+            logprob = torch.empty(tokens.shape, dtype=f32, device=dev)
+        if lse is None:
+            lse = torch.empty((N,), dtype=f32, device=dev)
+        if entropy is None:
+            entropy = torch.empty((N,), dtype=f32, device=dev)
+        if top_k and top_ids is None:
+            top_ids = torch.empty((N, top_k), dtype=i32, device=dev)
+        if top_k and top_logprobs is None:
+            top_logprobs = torch.empty((N, top_k), dtype=f32, device=dev)
+        pg = None if tokens is None else _shaped(logprob, "logprob", f32, dev, tokens.shape)
+        pl = _shaped(lse, "lse", f32, dev, (N,))
+        pe = _shaped(entropy, "entropy", f32, dev, (N,))
+        pi = _maybe(top_ids, "top_ids", i32, dev, (N, top_k))
+        pv = _maybe(top_logprobs, "top_logprobs", f32, dev, (N, top_k))
+        if N or M:
+            _check(_lib().ssd_token_logprobs(logits.data_ptr(), dt, logits.stride(0), N, V, pt, pr, M, pg, pl, pe, pi, pv, top_k,
+                                             _raw_stream(dev)))
+    return {"logprob": logprob, "lse": lse, "entropy": entropy, "top_ids": top_ids, "top_logprobs": top_logprobs}
+
+
+def ssd_tree_accept(parents: torch.Tensor, tokens: Optional[torch.Tensor], target: torch.Tensor, *, counts: Optional[torch.Tensor] = None,
+                    max_path: Optional[int] = None, logprob: Optional[torch.Tensor] = None,
+                    entropy: Optional[torch.Tensor] = None, epsilon: float = 0.0, delta: float = 0.0, path=None, cnt=None,
+                    next=None, advance=None, stream=None) -> dict:
+    """The path of a drafted tree that stays.  parents, tokens, target int32 [B, n]: node 0 is the last step's token and
+    stays; node c stays when its parent does and tokens[c] equals target[parent], or, with logprob and entropy (float
+    [B, n]; tokens may then be None), when logprob[c] > min(ln epsilon, ln delta - entropy[parent]).  The deepest such node
+    below max_path (None: n) gives path int32 [B, max_path] (-1 behind it), cnt, next = its target, and advance =
+    cnt - counts for ``ssd_kv_advance``."""
+    if not isinstance(parents, _Tensor) or parents.dim() != 2 or not parents.is_cuda:
+        raise ValueError("parents must be a CUDA tensor [batch, n]")
+    B, n = parents.shape
+    dev = parents.get_device()
+    i32, f32 = torch.int32, torch.float32
+    pp = _shaped(parents, "parents", i32, dev, (B, n))
+    if tokens is None and logprob is None:
+        raise ValueError("tokens or logprob must be given")
+    pt = _maybe(tokens, "tokens", i32, dev, (B, n))
+    pg = _shaped(target, "target", i32, dev, (B, n))
+    pc = _maybe(counts, "counts", i32, dev, (B,))
+    if (logprob is None) != (entropy is None):
+        raise ValueError("logprob and entropy go together")
+    pl = _maybe(logprob, "logprob", f32, dev, (B, n))
+    pe = _maybe(entropy, "entropy", f32, dev, (B, n))
+    m = n if max_path is None else int(max_path)
+    if m < 1:
+        raise ValueError(f"max_path {m} < 1")
+    with _scope(dev, stream):
+        if path is None:
+            path = torch.empty((B, m), dtype=i32, device=dev)
+        if cnt is None:
+            cnt = torch.empty((B,), dtype=i32, device=dev)
+        if next is None:
+            next = torch.empty((B,), dtype=i32, device=dev)
+        if advance is None:
+            advance = torch.empty((B,), dtype=i32, device=dev)
+        ph = _shaped(path, "path", i32, dev, (B, m))
+        pk, pn, pa = _shaped(cnt, "cnt", i32, dev, (B,)), _shaped(next, "next", i32, dev, (B,)), _shaped(advance, "advance", i32, dev, (B,))
+        if B:
+            _check(_lib().ssd_tree_accept(pp, pt, pg, pl, pe, float(epsilon), float(delta), pc, B, n, m, ph, pk, pn, pa, _raw_stream(dev)))
+    return {"path": path, "cnt": cnt, "next": next, "advance": advance}
+
+
+def ssd_tree_commit(kv: KVCache, path: torch.Tensor, cnt: torch.Tensor, n: int, *, counts: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Moves the K and V rows of the nodes path[b, :cnt[b]] (int32 [B, max_path], ascending; int32 [B]) of each request's tree,
+    its last counts[b] (int32 [B]; None: n) tokens, to the tree's first positions.  kv.pool is modified in place,
+    kv.seq_lens is not: ``ssd_kv_advance`` it once every layer is done.  The tree's pages are the request's own."""
+    if not isinstance(kv, KVCache):
+        raise TypeError(f"kv must be a KVCache, got {type(kv).__name__}")
+    dev, B = kv._geometry[:2]
+    if not isinstance(path, _Tensor) or path.dim() != 2:
+        raise ValueError("path must be a torch.Tensor [batch, max_path]")
+    m = path.shape[1]
+    pp = _shaped(path, "path", torch.int32, dev, (B, m))
+    pk = _shaped(cnt, "cnt", torch.int32, dev, (B,))
+    pc = _maybe(counts, "counts", torch.int32, dev, (B,))
+    if B == 0:
+        return
+    with _scope(dev, stream):
+        _check(_lib().ssd_tree_commit(kv.ref(), int(n), pc, pp, m, pk, _raw_stream(dev)))
