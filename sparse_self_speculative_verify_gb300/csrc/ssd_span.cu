@@ -25,7 +25,9 @@ static int span_args(const char *who, const ssd_paged_kv *kv, int h_q, int n, in
   return SSD_OK;
 }
 
-static size_t span_workspace(const ssd_paged_kv *kv, const SpanArgs &a) { return span_simt_workspace(kv, a); }
+static size_t span_workspace(const ssd_paged_kv *kv, const SpanArgs &a) {
+  return span_tc_takes(kv) ? span_tc_workspace(kv, a) : span_simt_workspace(kv, a);
+}
 
 static int span_attn(const char *who, const ssd_paged_kv *kv, const void *q, int h_q, int n, const int32_t *parents,
                      const int32_t *counts, int window, int sink, bool tree, float scale, void *out, float *lse,
@@ -46,7 +48,8 @@ static int span_attn(const char *who, const ssd_paged_kv *kv, const void *q, int
   a.counts = counts;
   a.scale_log2 = scale * kLog2e;
   if (!(a.status = device_status())) return SSD_ERR_CUDA;
-  return span_simt(kv, a, workspace, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return span_tc_takes(kv) ? span_tc(kv, a, workspace, st) : span_simt(kv, a, workspace, st);
 }
 
 }  // namespace ssd

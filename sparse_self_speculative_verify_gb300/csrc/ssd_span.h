@@ -10,4 +10,9 @@ namespace ssd {
 size_t span_simt_workspace(const ssd_paged_kv *kv, const SpanArgs &a);
 int span_simt(const ssd_paged_kv *kv, const SpanArgs &a, void *workspace, cudaStream_t st);
 
+// Tensor cores: the others.
+bool span_tc_takes(const ssd_paged_kv *kv);
+size_t span_tc_workspace(const ssd_paged_kv *kv, const SpanArgs &a);
+int span_tc(const ssd_paged_kv *kv, const SpanArgs &a, void *workspace, cudaStream_t st);
+
 }  // namespace ssd
