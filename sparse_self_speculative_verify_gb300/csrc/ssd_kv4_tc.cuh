@@ -148,13 +148,6 @@ __device__ __forceinline__ bool group_any(int id, int count, bool v) {
   return r != 0;
 }
 
-// True in one lane of the warp, which is converged here.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{ .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p; }\n" : "=r"(r)::"memory");
-  return r != 0;
-}
-
 // Byte of 16-byte piece c (of 4) of token t in a raw tile's codes: rows of 64 bytes, two to a line, the pieces
 // of four consecutive lines permuted differently.  A thread per token reading one piece each, and ldmatrix
 // reading one piece of eight tokens, both touch every bank once.

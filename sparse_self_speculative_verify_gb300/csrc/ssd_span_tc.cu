@@ -13,8 +13,9 @@
 // Work.  A unit is one (request, KV head); its rows are split into n_groups groups of one block's rows.  n_groups blocks
 // form a team, one group each, that walks the same tokens side by side, so that K and V come from memory once and from L2
 // for the others.  The units' tiles lie end to end and are cut into equal shares, one per team; a cut close to a unit's
-// border moves there.  A unit that several teams share leaves partial results, joined by span_join_kernel.  Where there
-// are many units with few tiles each (prompts with a window), blocks take whole (unit, group) items instead.
+// border moves there.  A unit that several teams share leaves partial results, joined by span_join_kernel.  Where the groups
+// see different tokens and there are many of them (prompts with a window), a team is one block, and the groups lie end to
+// end too.
 #include "ssd_sm100.cuh"
 #include "ssd_span.h"
 #include "ssd_tma.h"
@@ -23,7 +24,7 @@ namespace ssd {
 using namespace sm100;
 
 constexpr int kSpanTile = 128;          // tokens of a tile, rows of a stream
-constexpr int kSpanThreads = 11 * 32;
+constexpr int kSpanThreads = 12 * 32;  // (warp 11 completes the warpgroup whose registers the softmax takes)
 constexpr int kSpanProducer = 8, kSpanMma = 9;
 constexpr int kSpanMaxBatch = 1024;     // requests of a launch (their sizes lie in shared memory)
 constexpr int kSpanOverhead = 1;        // what starting and ending a unit costs, in tiles
@@ -32,12 +33,23 @@ constexpr int kSpanMinShare = 4;        // least share of a team
 constexpr float kSpanLazy = 8.f;        // a row's reference moves when a score exceeds it by this (log2)
 
 struct SpanPlan {
-  int n_groups, nodes;   // row groups of a unit, queries of a group
-  int teams;             // 0: items
-  int64_t items;
+  int n_groups;          // row groups of a unit
+  int row_nodes;         // queries of a stream's tile
+  int nodes;             // of a group
+  int teams, width;      // teams of blocks: n_groups (a group each) or 1 (a block takes whole groups in turn)
   int32_t *cut_unit;     // [teams]: the unit that team t's share begins inside of, or -1
-  float *o, *lse;        // [teams][2][n_groups][rows of a block][D], ... (log2)
+  float *o, *lse;        // [teams][2][width][D / 4][rows of a block][4], [teams][2][width][rows] (log2)
 };
+
+struct SpanSeg {
+  int b, g, rg;       // request, KV head, row group
+  int k0, k1;         // tiles of the unit
+  int part;           // -1: the whole unit; else the slot of its results
+  int c;              // the request's queries
+  SpanTiles st;
+};
+constexpr int kSpanRing = 8;  // segments handed from the producer to the other warps
+// (It is at most kStages tiles ahead of the products, they at most one ahead of the softmax, and every segment has a tile.)
 
 template <int D, bool WIDE>
 struct SpanCfg {
@@ -46,48 +58,87 @@ struct SpanCfg {
   static constexpr int kGroup = 1024 * kPanels;  // bytes of 8 tokens: panel after panel of 8 x 128 bytes
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes, kMisc = kV + kStages * kTileBytes;
-  static constexpr int kBars = 4 * kStages + 16;
-  // barriers, the requests' prefix, length, queries and tiles, the streams' maxima and sums
-  static constexpr int kSmem = kMisc + kBars * 8 + (kSpanMaxBatch + 1) * 8 + 3 * kSpanMaxBatch * 4 + 4 * 128 * 4 + 1024;
+  static constexpr int kBars = 4 * kStages + 16 + kSpanRing;
+  // barriers, the requests' prefix, size, length and queries, the streams' maxima and sums
+  static constexpr int kSmem = kMisc + kBars * 8 + (2 * kSpanMaxBatch + 1) * 8 + 2 * kSpanMaxBatch * 4 + 1024 * 4 + kSpanRing * (int)sizeof(SpanSeg) + 1024;
   static constexpr int kRows = WIDE ? 256 : 128;
   static constexpr int kColO = 256;  // tensor memory: S (P) of the streams, O of the streams
 };
 
-struct SpanSeg {
-  int b, g, rg;       // request, KV head, row group
-  int k0, k1;         // tiles of the unit
-  int part;           // -1: the whole unit; else the slot of its results
-  SpanTiles st;
-  int L, c;
-};
+// x / y, x >= 0, y > 0: in 32 bits where they fit.
+__device__ __forceinline__ int64_t span_div(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
 
-// The segments of a block, in order; every role walks them by itself.
+// The segments of a block, in order.
 struct SpanWalk {
   const SpanArgs &a;
   const SpanPlan &pl;
-  const int64_t *pre;
-  const int *len, *cnt, *tiles;
-  int64_t pos, end, start, item;
-  int b, team;
+  const int64_t *pre, *size;  // prefix of the requests' costs; cost of a request's unit (of all its groups, where width is 1)
+  const int *len, *cnt;
+  int64_t pos, end, u0, u1;   // of the share; the unit at pos
+  int b, g, rg, team;
+  bool inside;                // the share begins inside a unit
 
-  __device__ SpanWalk(const SpanArgs &a_, const SpanPlan &p_, const int64_t *pre_, const int *len_, const int *cnt_, const int *tiles_)
-      : a(a_), pl(p_), pre(pre_), len(len_), cnt(cnt_), tiles(tiles_), b(0) {
-    item = blockIdx.x;
-    team = pl.teams ? blockIdx.x / pl.n_groups : 0;
-    if (pl.teams) {
-      start = pos = cut(team);
+  __device__ SpanWalk(const SpanArgs &a_, const SpanPlan &p_, const int64_t *pre_, const int64_t *size_, const int *len_, const int *cnt_)
+      : a(a_), pl(p_), pre(pre_), size(size_), len(len_), cnt(cnt_) {
+    team = blockIdx.x / pl.width;
+    rg = blockIdx.x % pl.width;
+    if (pl.width > 1 || pl.n_groups == 1) {  // both ends at once, by even and odd lanes
+      const int64_t x = cut(team + (threadIdx.x & 1));
+      pos = __shfl_sync(0xffffffffu, x, 0);
+      end = __shfl_sync(0xffffffffu, x, 1);
+    } else {
+      pos = cut(team);
       end = cut(team + 1);
-      if (pos < end) b = find(pos);
+    }
+    inside = false;
+    if (pos < end) {
+      locate(pos);
+      inside = pos > u0;
     }
   }
-  // The request that position x < pre[batch] lies in.
-  __device__ int find(int64_t x) {
+  __device__ SpanTiles tiles_of(int at, int group) const {
+    return span_tiles<kSpanTile>(a, len[at], cnt[at], group * pl.nodes, group * pl.nodes + pl.nodes - 1);
+  }
+  // What group `group` of a request costs, in tiles.
+  __device__ int cost(int at, int group) const {
+    const int n = tiles_of(at, group).n_tiles;
+    return n ? n + kSpanOverhead : 0;
+  }
+  // Sets the unit that position x < pre[batch] lies in (by a converged warp where a unit has groups of its own).
+  __device__ void locate(int64_t x) {
     int lo = 0, hi = a.kv.batch;  // pre[lo] <= x < pre[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (pre[mid] <= x) lo = mid; else hi = mid;
     }
-    return lo;
+    b = lo;
+    const int64_t sz = size[lo], rem = x - pre[lo];
+    g = (int)span_div(rem, sz);
+    u0 = pre[lo] + g * sz;
+    u1 = u0 + sz;
+    if (pl.width > 1 || pl.n_groups == 1) return;
+    const int lane = threadIdx.x & 31;
+    int64_t at = u0;
+    for (int r0 = 0;; r0 += 32) {  // 32 groups at a time
+      const int mine = r0 + lane < pl.n_groups ? cost(b, r0 + lane) : 0;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, at + incl > x);
+      if (past || r0 + 32 >= pl.n_groups) {
+        const int w = past ? __ffs(past) - 1 : 31;
+        rg = r0 + w;
+        u1 = at + __shfl_sync(0xffffffffu, incl, w);
+        u0 = u1 - __shfl_sync(0xffffffffu, mine, w);
+        return;
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
   }
   // Where team t's share begins.
   __device__ int64_t cut(int t) {
@@ -95,66 +146,79 @@ struct SpanWalk {
     const int64_t n = min((int64_t)pl.teams, max((int64_t)1, total / kSpanMinShare));
     if (t >= n) return total;
     if (total == 0) return 0;
-    const int64_t x = total * t / n;
-    const int lo = find(x);
-    const unsigned size = tiles[lo] + kSpanOverhead, off = (unsigned)(x - pre[lo]) % size;
-    if (off < kSpanSnap) return x - off;
-    return size - off < kSpanSnap ? x - off + size : x;
+    const int64_t per = span_div(total, n), x = per * t + (uint32_t)(total - per * n) * (uint32_t)t / (uint32_t)n;
+    const int keep = rg;
+    locate(x);
+    if (pl.width > 1) rg = keep;
+    return x - u0 < kSpanSnap ? u0 : u1 - x < kSpanSnap ? u1 : x;
   }
-  // The unit that the share begins inside of, or -1.
-  __device__ int begins_inside() {
-    if (start >= pre[a.kv.batch]) return -1;
-    const int at = find(start);
-    const unsigned size = tiles[at] + kSpanOverhead, off = (unsigned)(start - pre[at]);
-    return off % size ? at * a.kv.h_kv + (int)(off / size) : -1;
-  }
-  __device__ void fill(SpanSeg &s) {
-    s.L = len[s.b];
-    s.c = cnt[s.b];
-    s.st = span_tiles<kSpanTile>(a, s.L, s.c, s.rg * pl.nodes, s.rg * pl.nodes + pl.nodes - 1);
-  }
+  // The unit's number; where the share begins inside one.
+  __device__ int unit() const { return pl.width > 1 ? b * a.kv.h_kv + g : (b * a.kv.h_kv + g) * pl.n_groups + rg; }
   __device__ bool next(SpanSeg &s) {
-    if (!pl.teams) {
-      if (item >= pl.items) return false;
-      const int64_t bg = item / pl.n_groups;
-      s.rg = pl.n_groups - 1 - (int)(item - bg * pl.n_groups);  // the last queries see most
-      s.b = (int)(bg / a.kv.h_kv);
-      s.g = (int)(bg - (int64_t)s.b * a.kv.h_kv);
-      item += gridDim.x;
-      fill(s);
-      s.k0 = 0;
-      s.k1 = s.st.n_tiles;
-      s.part = -1;
-      return true;
-    }
     if (pos >= end) return false;
-    while (pre[b + 1] <= pos) ++b;
-    const unsigned size = tiles[b] + kSpanOverhead, rem = (unsigned)(pos - pre[b]);
+    if (pos >= u1) {  // the next unit that costs something
+      do {
+        if (pl.width > 1 || ++rg >= pl.n_groups) {
+          if (pl.width == 1) rg = 0;
+          if (++g >= a.kv.h_kv) {
+            g = 0;
+            do ++b; while (pre[b + 1] <= pos);
+          }
+        }
+        u0 = u1;
+        u1 = u0 + (pl.width > 1 ? size[b] : cost(b, rg));
+      } while (u1 == u0);
+    }
     s.b = b;
-    s.g = (int)(rem / size);
-    s.rg = blockIdx.x % pl.n_groups;
-    const int64_t u0 = pre[b] + (int64_t)s.g * size, u1 = u0 + size, stop = min(u1, end);
-    fill(s);
+    s.g = g;
+    s.rg = rg;
+    s.c = cnt[b];
+    s.st = tiles_of(b, rg);
+    const int64_t stop = min(u1, end);
     s.k0 = min(max(0, (int)(pos - u0) - kSpanOverhead), s.st.n_tiles);
     s.k1 = stop == u1 ? s.st.n_tiles : min(max(0, (int)(stop - u0) - kSpanOverhead), s.st.n_tiles);
-    s.part = pos == u0 && stop == u1 ? -1 : (team * 2 + (pos == u0)) * pl.n_groups + s.rg;
+    s.part = pos == u0 && stop == u1 ? -1 : (team * 2 + (pos == u0)) * pl.width + (pl.width > 1 ? rg : 0);
     pos = stop;
     return true;
   }
 };
 
-// D columns of 32 of a lane of O, times f, to dst.
-template <int D, typename T>
-__device__ __forceinline__ void span_store32(T *dst, const float *v) {
-  if constexpr (sizeof(T) == 4) {
+// Two floats in a 64-bit register, and operations on both.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 16 columns of this thread's lane of tensor memory (one of the 32-bit registers each).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+      "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// 16 columns of this thread's lane of tensor memory.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-      *reinterpret_cast<uint4 *>(dst + i) = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4], v[i + 5]),
-                                                       pack_bf16(v[i + 6], v[i + 7]));
-  }
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 template <int D, bool WIDE>
@@ -172,10 +236,12 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   const uint32_t bars = sbase + C::kMisc;
   const uint32_t k_full = bars, k_empty = k_full + 8 * NS, v_full = k_empty + 8 * NS, v_empty = v_full + 8 * NS;
   const uint32_t q_full = v_empty + 8 * NS, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 16,
-                 drained = o_done + 16;
+                 drained = o_done + 16, group = drained + 16, seg_full = group + 8;
   int64_t *pre = reinterpret_cast<int64_t *>(sm + C::kMisc + C::kBars * 8);
-  int *s_len = reinterpret_cast<int *>(pre + kSpanMaxBatch + 1), *s_cnt = s_len + kSpanMaxBatch, *s_tiles = s_cnt + kSpanMaxBatch;
-  float *s_m = reinterpret_cast<float *>(s_tiles + kSpanMaxBatch), *s_l = s_m + 256;  // [stream][row]
+  int64_t *s_size = pre + kSpanMaxBatch + 1;
+  int *s_len = reinterpret_cast<int *>(s_size + kSpanMaxBatch), *s_cnt = s_len + kSpanMaxBatch;
+  float *s_m = reinterpret_cast<float *>(s_cnt + kSpanMaxBatch);  // [segment % 2][maxima, sums][stream][row]
+  SpanSeg *ring = reinterpret_cast<SpanSeg *>(s_m + 1024);
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int64_t s_scan[kSpanThreads / 32];
@@ -184,12 +250,14 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     s_abort = 0;
     for (int i = 0; i < NS; ++i) {
       mbar_init(k_full + 8 * i, 1), mbar_init(v_full + 8 * i, 1);
-      mbar_init(k_empty + 8 * i, WIDE ? 2 : 1), mbar_init(v_empty + 8 * i, WIDE ? 2 : 1);
+      mbar_init(k_empty + 8 * i, 1), mbar_init(v_empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, 1), mbar_init(q_empty + 8 * i, 1);
+      mbar_init(q_full + 8 * i, 1), mbar_init(q_empty + 8 * i, WIDE ? 1 : 8);
       mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4), mbar_init(o_done + 8 * i, 1), mbar_init(drained + 8 * i, 1);
     }
+    mbar_init(group, 8);
+    for (int i = 0; i < kSpanRing; ++i) mbar_init(seg_full + 8 * i, 1);
     mbar_init_fence();
   }
   if (warp == kSpanMma) {
@@ -202,24 +270,31 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   }
   pdl_wait();
 
-  // Sizes of the requests, and the prefix of their units' costs.
+  // Sizes of the requests; the costs of their units; the prefix of the requests' costs.
+  for (int b = tid; b < B; b += kSpanThreads) {
+    span_sizes(a, b, blockIdx.x == 0, s_len[b], s_cnt[b]);
+    s_size[b] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  for (int64_t e = tid; e < (int64_t)B * pl.n_groups; e += kSpanThreads) {
+    const int b = (int)(e / pl.n_groups), group = (int)(e - (int64_t)b * pl.n_groups);
+    const int n = span_tiles<kSpanTile>(a, s_len[b], s_cnt[b], group * pl.nodes, group * pl.nodes + pl.nodes - 1).n_tiles;
+    if (n == 0) continue;
+    if (pl.width > 1)  // a team walks the most tiles of its groups
+      atomicMax(reinterpret_cast<unsigned long long *>(s_size + b), (unsigned long long)(n + kSpanOverhead));
+    else
+      atomicAdd(reinterpret_cast<unsigned long long *>(s_size + b), (unsigned long long)(n + kSpanOverhead));
+  }
+  __syncthreads();
   {
     constexpr int CH = cdiv(kSpanMaxBatch, kSpanThreads);
     int64_t mine[CH], sum = 0;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int b = tid * CH + k;
-      mine[k] = 0;
-      if (b < B) {
-        int L, c;
-        span_sizes(a, b, blockIdx.x == 0, L, c);
-        int most = 0;
-        if (pl.teams)
-          for (int rg = 0; rg < pl.n_groups; ++rg)
-            most = max(most, span_tiles<kSpanTile>(a, L, c, rg * pl.nodes, rg * pl.nodes + pl.nodes - 1).n_tiles);
-        s_len[b] = L, s_cnt[b] = c, s_tiles[b] = most;
-        mine[k] = most ? (int64_t)h_kv * (most + kSpanOverhead) : 0;
-      }
+      mine[k] = b < B ? h_kv * s_size[b] : 0;
       sum += mine[k];
     }
     int64_t incl = sum;
@@ -229,9 +304,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       if (lane >= o) incl += t;
     }
     if (lane == 31) s_scan[warp] = incl;
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
     int64_t off = incl - sum;
     for (int w = 0; w < warp; ++w) off += s_scan[w];
 #pragma unroll
@@ -246,11 +319,11 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   const uint32_t tm = s_tmem;
   volatile int *abort = &s_abort;
 
-  // Rows that see nothing.
-  for (int b = blockIdx.x; b < B; b += gridDim.x) {
+  // Rows that see nothing; a request's are shared by every B-th block.
+  for (int b = blockIdx.x % B; b < B; b += gridDim.x) {
     const int c = s_cnt[b], below = min(max(0, c - s_len[b]), c);  // queries [0, below) and [c, n)
-    const int rows = below + a.n - c;
-    for (int64_t e = tid; e < (int64_t)rows * a.h_q * (D / 8); e += kSpanThreads) {
+    const int rows = below + a.n - c, sharers = max(1, cdiv((int)gridDim.x - b, B));
+    for (int64_t e = (blockIdx.x / B) * kSpanThreads + tid; e < (int64_t)rows * a.h_q * (D / 8); e += sharers * kSpanThreads) {
       const int64_t r = e / (D / 8);
       const int i0 = (int)(r / a.h_q), i = i0 < below ? i0 : c + i0 - below;
       const int64_t at = ((int64_t)b * a.n + i) * a.h_q + r % a.h_q;
@@ -259,182 +332,257 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     }
   }
 
-  SpanWalk walk(a, pl, pre, s_len, s_cnt, s_tiles);
-  SpanSeg seg;
-  const int row_nodes = kSpanTile / a.G;  // queries of a stream's tile
+  const int row_nodes = pl.row_nodes;
+  // Segment j of the block, once the producer has published it; nullptr behind the last one (and where a wait ran out).
+  auto segment = [&](int j) -> const SpanSeg * {
+    const bool ok = mbar_wait(seg_full + 8 * (j % kSpanRing), (j / kSpanRing) & 1, abort);
+    const SpanSeg *x = ring + j % kSpanRing;
+    return __all_sync(0xffffffffu, ok) && x->b >= 0 ? x : nullptr;
+  };
+  // Whether stream 1 of a WIDE block has rows in a segment.
+  auto second = [&](const SpanSeg &x) { return x.rg * pl.nodes + row_nodes < x.c; };
 
+  // Registers: 256 x 208 + 128 x 88 are the launch's 384 x 168.
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == kSpanProducer) {
     // ---------------------------------------------------------------- loads
-    if (pl.teams && blockIdx.x % pl.n_groups == 0) {
-      const int u = walk.begins_inside();
-      if (lane == 0) pl.cut_unit[walk.team] = u;
-    }
+    SpanWalk walk(a, pl, pre, s_size, s_len, s_cnt);
+    if (blockIdx.x % pl.width == 0 && lane == 0) pl.cut_unit[walk.team] = walk.inside ? walk.unit() : -1;
     const int box_rows = min(ps, kSpanTile), boxes = kSpanTile / box_rows;
-    const uint64_t pol = pl.teams && pl.n_groups == 1 ? policy_evict_first() : policy_evict_normal();
+    const uint64_t pol = a.parents && pl.n_groups == 1 ? policy_evict_first() : policy_evict_normal();
     const int oob = (int)((int64_t)a.kv.num_pages * 2 * h_kv * ps / 8);
-    uint32_t f = 0;  // tiles so far
-    int j = 0;       // segments so far
-    auto next_seg = [&](SpanSeg &s) {  // the next one with tiles
-      for (;;) {
-        if (!walk.next(s)) return false;
-        if (s.k0 < s.k1) return true;
-      }
-    };
-    // The group of 8 rows that lane's box of tile k starts at (K), or where nothing of it is seen `oob`.
+    uint32_t q_uses[2] = {0, 0};
+    int j = 0;  // segments so far
+    bool ok = true;
+    // Page of lane's box of tile k, INT32_MIN where nothing of it is seen.
     auto page_of = [&](const SpanSeg &s, int k) -> int32_t {
       const int t = s.st.tile(k) * kSpanTile + lane * box_rows;
       const bool seen = lane < boxes && t < s.st.hi && (t < s.st.sink || t + box_rows > s.st.lo);
       return seen ? a.kv.page_table[(int64_t)s.b * a.kv.max_pages + (t >> a.kv.log2_ps)] : INT32_MIN;
     };
-    bool more = next_seg(seg);
-    int k = seg.k0;
-    int32_t pid = more ? page_of(seg, k) : 0;
-    bool ok = true;
-    while (more && ok) {
-      if (k == seg.k0) {
-        const int i0 = seg.rg * pl.nodes;
+    auto load_q = [&](const SpanSeg &s) {
 #pragma unroll
-        for (int s = 0; s < (WIDE ? 2 : 1); ++s) {
-          const int buf = WIDE ? s : j & 1, use = WIDE ? j : j >> 1;
-          ok &= mbar_wait(q_empty + 8 * buf, (use & 1) ^ 1, abort);
-          if (__all_sync(0xffffffffu, ok) && lane == 0) {
-            mbar_arrive_expect_tx(q_full + 8 * buf, row_nodes * a.G * D * 2);
-            for (int p = 0; p < C::kPanels; ++p)
-              tma_load_4d(sbase + C::kQ + buf * C::kTileBytes + p * (kSpanTile * 128), &qmap, p * 64, seg.g * a.G, i0 + s * row_nodes, seg.b,
-                          q_full + 8 * buf);
-          }
-          __syncwarp();
+      for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+        const int buf = WIDE ? w : j & 1;
+        if (WIDE && w && !second(s)) continue;
+        ok = __all_sync(0xffffffffu, ok & mbar_wait(q_empty + 8 * buf, (q_uses[buf] & 1) ^ 1, abort));
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(q_full + 8 * buf, row_nodes * a.G * D * 2);
+          for (int p = 0; p < C::kPanels; ++p)
+            tma_load_4d(sbase + C::kQ + buf * C::kTileBytes + p * (kSpanTile * 128), &qmap, p * 64, s.g * a.G, s.rg * pl.nodes + w * row_nodes,
+                        s.b, q_full + 8 * buf);
         }
-        ++j;
+        __syncwarp();
+        ++q_uses[buf];
       }
-      // What follows, its page ids on their way.
-      SpanSeg ns = seg;
-      int nk = k + 1;
-      bool nmore = true;
-      if (nk == seg.k1) {
-        nmore = next_seg(ns);
-        nk = ns.k0;
-      }
-      const int32_t npid = nmore ? page_of(ns, nk) : 0;
-      const int t = seg.st.tile(k) * kSpanTile + lane * box_rows;
+      ++j;
+    };
+    // K (w = 0) or V of the block's tile f, tile k of segment s.
+    auto load_tile = [&](const SpanSeg &s, int k, int32_t pid, uint32_t f, int w) {
+      const uint32_t slot = f % NS, full = (w ? v_full : k_full) + 8 * slot;
+      ok = __all_sync(0xffffffffu, ok & mbar_wait((w ? v_empty : k_empty) + 8 * slot, ((f / NS) & 1) ^ 1, abort));
+      if (!ok) return;
+      const int t = s.st.tile(k) * kSpanTile + lane * box_rows;
       const bool page_ok = pid >= 0 && (int64_t)pid < a.kv.num_pages;
-      if (pid != INT32_MIN && !page_ok) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
-      const int row8 = page_ok ? (int)((((int64_t)pid * 2 * h_kv + seg.g) * ps + (t & (ps - 1))) >> 3) : oob;
-      const int slot = f % NS;
-      const uint32_t use = f / NS;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const uint32_t full = (w ? v_full : k_full) + 8 * slot;
-        ok &= mbar_wait((w ? v_empty : k_empty) + 8 * slot, (use & 1) ^ 1, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
-          __syncwarp();
-          if (lane < boxes)
-            tma_load_4d(sbase + (w ? C::kV : C::kK) + slot * C::kTileBytes + (lane * box_rows >> 3) * C::kGroup, &kvmap, 0, 0, 0,
-                        page_ok ? row8 + (w ? h_kv * ps >> 3 : 0) : oob, full, pol);
-          __syncwarp();
-        }
+      if (w == 0 && pid != INT32_MIN && !page_ok) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
+      const int row8 = page_ok ? (int)((((int64_t)pid * 2 * h_kv + (w ? h_kv : 0) + s.g) * ps + (t & (ps - 1))) >> 3) : oob;
+      if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
+      __syncwarp();
+      if (lane < boxes)
+        tma_load_4d(sbase + (w ? C::kV : C::kK) + slot * C::kTileBytes + (lane * box_rows >> 3) * C::kGroup, &kvmap, 0, 0, 0, row8, full, pol);
+      __syncwarp();
+    };
+    // Publishes the next segment that has tiles.
+    int published = 0;
+    auto next_segment = [&]() -> const SpanSeg * {
+      SpanSeg x;
+      bool more;
+      while ((more = walk.next(x)) && x.k0 >= x.k1) {  // (a group that sees less than its team walks)
+        for (int r = lane; x.part >= 0 && r < C::kRows; r += 32) pl.lse[(int64_t)x.part * C::kRows + r] = -INFINITY;
       }
+      SpanSeg *to = ring + published % kSpanRing;
+      if (!more) x.b = -1;
+      if (lane == 0) {
+        *to = x;
+        mbar_arrive(seg_full + 8 * (published % kSpanRing));
+      }
+      __syncwarp();
+      ++published;
+      return more ? to : nullptr;
+    };
+    // K runs one tile ahead of V.  At a segment's end its last V goes first: the next queries may have to wait for their buffer.
+    uint32_t f = 0;
+    const SpanSeg *seg = next_segment();
+    int k = 0;
+    int32_t pid = 0;
+    if (seg) {
+      k = seg->k0;
+      pid = page_of(*seg, k);
+      load_q(*seg);
+      load_tile(*seg, k, pid, 0, 0);
+    }
+    while (seg && ok) {
+      const SpanSeg *ns = seg;
+      int nk = k + 1;
+      const bool turn = nk == seg->k1;
+      if (turn) {
+        load_tile(*seg, k, pid, f, 1);
+        ns = next_segment();
+        nk = ns ? ns->k0 : 0;
+      }
+      const int32_t npid = ns ? page_of(*ns, nk) : 0;
+      if (turn && ns) load_q(*ns);
+      if (ns) load_tile(*ns, nk, npid, f + 1, 0);
+      if (!turn) load_tile(*seg, k, pid, f, 1);
       ++f;
       seg = ns;
       k = nk;
       pid = npid;
-      more = nmore;
     }
     pdl_trigger();
     if (!ok && lane == 0) {  // every copy in flight lands before the block's memory is released
       volatile int never = 0;
-      for (uint32_t i = f > (uint32_t)NS ? f - NS : 0; i < f; ++i) {
+      for (uint32_t i = f > (uint32_t)NS ? f - NS : 0; i <= f; ++i) {
         mbar_wait(k_full + 8 * (i % NS), (i / NS) & 1, &never, 200000000ll);
         mbar_wait(v_full + 8 * (i % NS), (i / NS) & 1, &never, 200000000ll);
       }
     }
     __syncwarp();
-  } else if (warp >= kSpanMma) {
+  } else if (warp == kSpanMma || warp == kSpanMma + 1) {
     // ---------------------------------------------------------------- products
-    const int s = warp - kSpanMma;
+    // WIDE: warp 9 issues for both streams in turn, O += P V of a tile and at once S of the next, so that one stream's
+    // softmax always has the other's products beside it (issued by two warps they fell into step, and the tensor cores idled
+    // during both softmaxes).  Else a warp per stream, which waits for its own tiles only.
+    const int mine = warp - kSpanMma;
     const uint32_t id_qk = idesc_bf16_f32(128, 128, 0, 0), id_pv = idesc_bf16_f32(128, D, 0, 1);
-    const uint32_t col_s = tm + s * 128, col_o = tm + C::kColO + s * 128;
-    uint32_t f = 0, n = 0;  // tiles of the block, of this stream
-    int j = 0;
-    while (walk.next(seg)) {
-      if (seg.k0 >= seg.k1) continue;
-      const int buf = WIDE ? s : j & 1, use = WIDE ? j : j >> 1;
-      mbar_wait(q_full + 8 * buf, use & 1, abort);
-      const uint64_t qd = smem_desc(sbase + C::kQ + buf * C::kTileBytes, 16, 1024);
-      bool first = true;
-      for (int k = seg.k0; k < seg.k1; ++k, ++f) {
-        if (!WIDE && (f & 1) != (uint32_t)s) continue;
-        const int slot = f % NS;
-        const uint32_t ph = (f / NS) & 1;
-        mbar_wait(k_full + 8 * slot, ph, abort);
-        tc_fence_after();
-        if (lane == 0 && !*abort) {
-          const uint64_t kd = smem_desc(sbase + C::kK + slot * C::kTileBytes, 16, C::kGroup);
+    // One elected lane of a converged warp issues, so that the operands stay warp-uniform: from a lane chosen by its number an
+    // instruction took 95 clocks.
+    const uint64_t qd = smem_desc(sbase + C::kQ, 16, 1024), kd = smem_desc(sbase + C::kK, 16, C::kGroup), vd = smem_desc(sbase + C::kV, 1024, C::kGroup);
+    const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
+    auto issue_qk = [&](int s, int buf, int slot, bool free_k, bool free_q) {
+      const uint64_t q = qd + (uint64_t)(buf * C::kTileBytes >> 4), k = kd + (uint64_t)(slot * C::kTileBytes >> 4);
+      if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16_ss(col_s, qd + (uint64_t)(((kk >> 2) * (kSpanTile * 128) + (kk & 3) * 32) >> 4),
-                        kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0);
-          mma_commit(s_full + 8 * s);
-          mma_commit(k_empty + 8 * slot);
-          if (WIDE && k == seg.k1 - 1) mma_commit(q_empty + 8 * s);
-        }
-        __syncwarp();
-        mbar_wait(v_full + 8 * slot, ph, abort);
-        // Rows of V that nobody sees may hold anything, and 0 times it has to be 0.
-        const int t0 = seg.st.tile(k) * kSpanTile, t1 = t0 + kSpanTile;
-        if (t1 > seg.st.hi || !(t1 <= seg.st.sink || t0 >= seg.st.lo || seg.st.sink >= seg.st.lo)) {
-          constexpr int CPR = D / 8;  // 16-byte pieces of a row
-          for (int r = lane / CPR; r < kSpanTile; r += 32 / CPR) {
-            const int c = lane % CPR;
-            if (!seg.st.seen(t0 + r))
-              *reinterpret_cast<uint4 *>(sm + C::kV + slot * C::kTileBytes + (r >> 3) * C::kGroup + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        mbar_wait(p_full + 8 * s, n & 1, abort);
-        tc_fence_after();
-        if (lane == 0 && !*abort) {
-          const uint64_t vd = smem_desc(sbase + C::kV + slot * C::kTileBytes, 1024, C::kGroup);
-#pragma unroll
-          for (int kk = 0; kk < kSpanTile / 16; ++kk)
-            mma_bf16_ts(col_o, col_s + kk * 8, vd + (uint64_t)((kk * 2 * C::kGroup) >> 4), id_pv, !first || kk > 0);
-          mma_commit(o_done + 8 * s);
-          mma_commit(v_empty + 8 * slot);
-        }
-        __syncwarp();
-        first = false;
-        ++n;
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16_ss(tmu + s * 128, q + (uint64_t)(((kk >> 2) * (kSpanTile * 128) + (kk & 3) * 32) >> 4),
+                      k + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0 ? 1u : 0u);
+        mma_commit(s_full + 8 * s);
+        if (free_k) mma_commit(k_empty + 8 * slot);
+        if (free_q) mma_commit(q_empty + 8 * buf);
       }
-      ++j;
+      __syncwarp();
+    };
+    auto issue_pv = [&](int s, int slot, bool first, bool free_v) {
+      const uint64_t v = vd + (uint64_t)(slot * C::kTileBytes >> 4);
+      const uint32_t acc = first ? 0u : 1u;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kSpanTile / 16; ++kk)
+          mma_bf16_ts(tmu + C::kColO + s * 128, tmu + s * 128 + kk * 8, v + (uint64_t)((kk * 2 * C::kGroup) >> 4), id_pv, kk > 0 ? 1u : acc);
+        mma_commit(o_done + 8 * s);
+        if (free_v) mma_commit(v_empty + 8 * slot);
+      }
+      __syncwarp();
+    };
+    // Rows of V that nobody sees may hold anything, and 0 times it has to be 0: those behind `hi` and those from `sink` to `lo`.
+    auto clear_unseen = [&](int hi, int sink, int lo, int t0, int slot) {
+      if (t0 + kSpanTile <= hi && (t0 + kSpanTile <= sink || t0 >= lo || sink >= lo)) return;
+      constexpr int CPR = D / 8;  // 16-byte pieces of a row
+      char *v = sm + C::kV + slot * C::kTileBytes + ((lane % CPR) >> 3) * 1024 + (lane % CPR & 7) * 16;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int r0 = max(0, (w ? sink : hi) - t0), r1 = w ? min(kSpanTile, min(lo, hi) - t0) : kSpanTile;
+#pragma unroll 4
+        for (int r = r0 + lane / CPR; r < r1; r += 32 / CPR) *reinterpret_cast<uint4 *>(v + (r >> 3) * C::kGroup + (r & 7) * 128) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    uint32_t f = 0;  // tiles of the block
+    if (WIDE && mine == 0) {
+      uint32_t n[2] = {0, 0}, q_uses[2] = {0, 0};
+      const SpanSeg *sp;
+      for (int j = 0; (sp = segment(j)); ++j) {
+        const SpanSeg seg = *sp;
+        const int streams = second(seg) ? 2 : 1;
+        mbar_wait(k_full + 8 * (f % NS), (f / NS) & 1, abort);
+        for (int s = 0; s < streams; ++s) {
+          mbar_wait(q_full + 8 * s, q_uses[s]++ & 1, abort);
+          tc_fence_after();
+          issue_qk(s, s, f % NS, s == streams - 1, seg.k1 - seg.k0 == 1);
+        }
+        for (int k = seg.k0; k < seg.k1; ++k, ++f) {
+          const int slot = f % NS, nslot = (f + 1) % NS;
+          mbar_wait(v_full + 8 * slot, (f / NS) & 1, abort);
+          clear_unseen(seg.st.hi, seg.st.sink, seg.st.lo, seg.st.tile(k) * kSpanTile, slot);
+          for (int s = 0; s < streams; ++s) {
+            mbar_wait(p_full + 8 * s, n[s]++ & 1, abort);
+            tc_fence_after();
+            issue_pv(s, slot, k == seg.k0, s == streams - 1);
+            if (k + 1 < seg.k1) {
+              if (s == 0) {
+                mbar_wait(k_full + 8 * nslot, ((f + 1) / NS) & 1, abort);
+                tc_fence_after();
+              }
+              issue_qk(s, s, nslot, s == streams - 1, k + 2 == seg.k1);
+            }
+          }
+        }
+      }
     }
-    if (lane == 0) {
-      mma_commit(drained + 8 * s);
-      volatile int never = 0;
-      mbar_wait(drained + 8 * s, 0, &never);
+    if (!WIDE) {
+      const int s = mine;
+      uint32_t n = 0;
+      const SpanSeg *sp;
+      for (int j = 0; (sp = segment(j)); ++j) {
+        const SpanSeg seg = *sp;
+        mbar_wait(q_full + 8 * (j & 1), (j >> 1) & 1, abort);
+        bool first = true;
+        for (int k = seg.k0; k < seg.k1; ++k, ++f) {
+          if ((f & 1) != (uint32_t)s) continue;
+          const int slot = f % NS;
+          mbar_wait(k_full + 8 * slot, (f / NS) & 1, abort);
+          tc_fence_after();
+          issue_qk(s, j & 1, slot, true, false);
+          mbar_wait(v_full + 8 * slot, (f / NS) & 1, abort);
+          clear_unseen(seg.st.hi, seg.st.sink, seg.st.lo, seg.st.tile(k) * kSpanTile, slot);
+          mbar_wait(p_full + 8 * s, n++ & 1, abort);
+          tc_fence_after();
+          issue_pv(s, slot, first, true);
+          first = false;
+        }
+      }
     }
+    if (elect_one()) mma_commit(drained + 8 * mine);
     __syncwarp();
+    volatile int never = 0;
+    mbar_wait(drained + 8 * mine, 0, &never);
+    __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------------------------------------------------------- softmax, O
     const int s = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t col_s = tm + s * 128 + lanes, col_o = tm + C::kColO + s * 128 + lanes;
     const int node = row / a.G;  // of the stream's tile
-    uint32_t f = 0, n = 0;
-    int j = 0;
-    while (walk.next(seg)) {
+    uint32_t f = 0, n = 0, syncs = 0;
+    // Arrive and wait of both streams' warps.
+    auto sync_streams = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(group);
+      mbar_wait(group, syncs++ & 1, abort);
+    };
+    const SpanSeg *sp;
+    for (int j = 0; (sp = segment(j)); ++j) {
+      const SpanSeg &seg = *sp;
+      if (WIDE && s && !second(seg)) continue;
       const int i = seg.rg * pl.nodes + (WIDE ? s * row_nodes : 0) + node;
       const bool valid = node < row_nodes && i < seg.c && seg.st.base + i >= 0;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       const int64_t at = ((int64_t)seg.b * a.n + i) * a.h_q + seg.g * a.G + (row - node * a.G);
       const int64_t prow = (int64_t)seg.part * C::kRows + (WIDE ? s * 128 : 0) + row;
-      if (seg.k0 >= seg.k1) {
-        if (seg.part >= 0 && valid && (WIDE || s == 0)) pl.lse[prow] = -INFINITY;
-        continue;
-      }
       const int32_t *parents = a.parents ? a.parents + (int64_t)seg.b * a.n : nullptr;
       // Tokens [0, all_to) and, behind lo_all, up to it are seen by every row of the group.
       const int i_first = max(seg.rg * pl.nodes, -seg.st.base), i_last = min(seg.rg * pl.nodes + pl.nodes, seg.c) - 1;
@@ -462,7 +610,11 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) mx[q] = x[q];
 #pragma unroll
-          for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
+          for (int e = 4; e < 124; e += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx[q] = fmaxf(fmaxf(mx[q], x[e + q]), x[e + 4 + q]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], x[124 + q]);
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
           const bool need = valid && top > mref + kSpanLazy;
           if (__any_sync(0xffffffffu, need)) {
@@ -484,20 +636,25 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
             if (need) mref = top;
           }
           const float ref = mref == -INFINITY ? 0.f : mref;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sl2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int e = 0; e < 128; ++e) {
-            x[e] = fast_exp2(fmaf(x[e], a.scale_log2, -ref));
-            sum[e & 3] += x[e];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float y0, y1;
+              unpack2(fma2(pack2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), sl2, ref2), y0, y1);
+              y0 = fast_exp2(y0);
+              y1 = fast_exp2(y1);
+              sum[e & 1] = add2(sum[e & 1], pack2(y0, y1));
+              p[e] = pack_bf16(y0, y1);
+            }
+            tmem_st16(col_s + 16 * q, p);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float p[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) p[e] = __uint_as_float(pack_bf16(x[64 * q + 2 * e], x[64 * q + 2 * e + 1]));
-            tmem_st32(col_s + 32 * q, p);
-          }
+          float l0, l1;
+          unpack2(add2(sum[0], sum[1]), l0, l1);
+          l += l0 + l1;
           tmem_st_wait();
         }
         have = true;
@@ -511,74 +668,88 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
         mbar_wait(o_done + 8 * s, (n - 1) & 1, abort);
         tc_fence_after();
       }
-      float scale = 1.f, lse2;
-      if constexpr (!WIDE) {
-        s_m[s * 128 + row] = have ? mref : -INFINITY;
-        s_l[s * 128 + row] = have ? l : 0.f;
-        named_sync(1, 256);
-        const float m0 = s_m[row], m1 = s_m[128 + row], m = fmaxf(m0, m1), ref = m == -INFINITY ? 0.f : m;
-        const float f0 = fast_exp2(m0 - ref), f1 = fast_exp2(m1 - ref);
-        l = s_l[row] * f0 + s_l[128 + row] * f1;
-        scale = s ? f1 : f0;
-        mref = m;
-      }
-      lse2 = mref + log2f(l);
-      scale *= 1.f / l;
       const bool part = seg.part >= 0;
+      // Columns [c0, c0 + 16) of the row: to the output, or to the part's slot as [4 columns][row].
+      auto put = [&](const float *o, int c0) {
+        if (!valid) return;
+        if (part) {
+          float4 *to = reinterpret_cast<float4 *>(pl.o) + ((int64_t)seg.part * (D / 4) + c0 / 4) * C::kRows + (WIDE ? s * 128 : 0) + row;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[e * C::kRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else {
+          uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + c0);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            to[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]), pack_bf16(o[8 * e + 4], o[8 * e + 5]),
+                               pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+        }
+      };
       if constexpr (WIDE) {
+        const float f = 1.f / l;
         if (warp_valid) {
-#pragma unroll 1
+#pragma unroll 2
           for (int q = 0; q < D / 32; ++q) {
             float o[32];
             tmem_ld32(col_o + 32 * q, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= scale;
-            if (valid && part) span_store32<D>(pl.o + prow * D + 32 * q, o);
-            if (valid && !part) span_store32<D>(static_cast<__nv_bfloat16 *>(a.out) + at * D + 32 * q, o);
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            put(o, 32 * q);
+            put(o + 16, 32 * q + 16);
           }
         }
       } else {
-        // Stream 1's share goes through the segment's Q buffer, whose products are done, half of the columns at a time.
-        float *box = reinterpret_cast<float *>(sm + C::kQ + (j & 1) * C::kTileBytes);
-#pragma unroll 1
-        for (int hcol = 0; hcol < D; hcol += D / 2) {
-          if (s == 1 && warp_valid) {
-#pragma unroll 1
-            for (int q = 0; q < D / 64; ++q) {
-              float o[32];
-              tmem_ld32(col_o + hcol + 32 * q, o);
-              tmem_ld_wait();
+        // Each stream ends half of the columns (or, with more than 64 rows, a quarter at a time) and passes its share of the
+        // other's on through the segment's Q buffer, whose products are done.
+        const bool many = row_nodes * a.G > 64;
+        const int stride = many ? 128 : 64, step = many ? D / 4 : D / 2;  // rows and columns of a box
+        float *boxes = reinterpret_cast<float *>(sm + C::kQ + (j & 1) * C::kTileBytes), *mine = boxes + s * stride * step, *theirs = boxes + (1 - s) * stride * step;
+        float *my_m = s_m + (j & 1) * 512;  // [stream][row], and the sums behind them
+        my_m[s * 128 + row] = have ? mref : -INFINITY;
+        my_m[256 + s * 128 + row] = have ? l : 0.f;
+        sync_streams();  // (the other stream's products with Q are done too)
+        const float m_two = my_m[(1 - s) * 128 + row], m = fmaxf(my_m[s * 128 + row], m_two), ref = m == -INFINITY ? 0.f : m;
+        float f0 = have ? fast_exp2(mref - ref) : 0.f, f1 = fast_exp2(m_two - ref);
+        l = (have ? l : 0.f) * f0 + my_m[256 + (1 - s) * 128 + row] * f1;
+        mref = m;
+        f0 /= l, f1 /= l;
+        for (int c0 = 0; c0 < D / 2; c0 += step) {
+          if (warp_valid)
+            for (int e0 = 0; e0 < step; e0 += 16) {
+              float o[16];
+              if (have) {
+                tmem_ld16(col_o + (1 - s) * (D / 2) + c0 + e0, o);
+                tmem_ld_wait();
+              }
 #pragma unroll
-              for (int e = 0; e < 32; ++e) box[(32 * q + e) * 128 + row] = have ? o[e] * scale : 0.f;
+              for (int e = 0; e < 16; ++e) mine[(e0 + e) * stride + row] = have ? o[e] : 0.f;
             }
-            fence_proxy_async_smem();  // before the next queries' copies
-          }
-          named_sync(1, 256);
-          if (s == 0 && warp_valid) {
-#pragma unroll 1
-            for (int q = 0; q < D / 64; ++q) {
-              float o[32];
-              tmem_ld32(col_o + hcol + 32 * q, o);
-              tmem_ld_wait();
+          fence_proxy_async_smem();  // before the next queries' copies
+          sync_streams();
+          if (warp_valid)
+            for (int e0 = 0; e0 < step; e0 += 16) {
+              float o[16];
+              if (have) {
+                tmem_ld16(col_o + s * (D / 2) + c0 + e0, o);
+                tmem_ld_wait();
+              }
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = (have ? o[e] * scale : 0.f) + box[(32 * q + e) * 128 + row];
-              if (valid && part) span_store32<D>(pl.o + prow * D + hcol + 32 * q, o);
-              if (valid && !part) span_store32<D>(static_cast<__nv_bfloat16 *>(a.out) + at * D + hcol + 32 * q, o);
+              for (int e = 0; e < 16; ++e) o[e] = (have ? o[e] * f0 : 0.f) + theirs[(e0 + e) * stride + row] * f1;
+              put(o, s * (D / 2) + c0 + e0);
             }
-          }
-          named_sync(1, 256);
+          if (c0 + step < D / 2) sync_streams();
         }
-        if (tid == 0) mbar_arrive(q_empty + 8 * (j & 1));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty + 8 * (j & 1));
       }
       if (valid && (WIDE || s == 0)) {
+        const float lse2 = mref + log2f(l);
         if (part)
           pl.lse[prow] = lse2;
         else if (a.lse)
           a.lse[at] = lse2 * kLn2;
       }
       tc_fence_before();
-      ++j;
     }
   }
   tc_fence_before();
@@ -588,12 +759,13 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   if (warp == kSpanMma) tmem_dealloc(tm, 512);
 }
 
-// Joins the parts of the units that teams share.  Blocks (team, group, eight rows): the one of the first team that begins inside
+// Joins the parts of the units that teams share.  Blocks (team, group, 32 rows; a warp per D / 8 columns): the one of the first team that begins inside
 // a unit has that unit; its parts are the team before's slot 1 and slot 0 of every team that begins inside it.
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(256) span_join_kernel(SpanArgs a, SpanPlan pl) {
   using C = SpanCfg<D, WIDE>;
-  const int lane = threadIdx.x & 31, team = blockIdx.x, rg = blockIdx.y, r = blockIdx.z * 8 + (threadIdx.x >> 5);
+  constexpr int COLS = D / 8;  // of a warp
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = blockIdx.x, r = blockIdx.z * 32 + lane;
   pdl_wait();
   pdl_trigger();
   const int unit = pl.cut_unit[team];
@@ -605,46 +777,39 @@ __global__ void __launch_bounds__(256) span_join_kernel(SpanArgs a, SpanPlan pl)
     parts += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
     if (m != 0xffffffffu) break;
   }
-  const int b = unit / a.kv.h_kv, g = unit % a.kv.h_kv;
+  const int rg = pl.width > 1 ? blockIdx.y : unit % pl.n_groups, bg = pl.width > 1 ? unit : unit / pl.n_groups;
+  const int b = bg / a.kv.h_kv, g = bg % a.kv.h_kv;
   int L, c;
   span_sizes(a, b, false, L, c);
-  const int row_nodes = kSpanTile / a.G, s = r >> 7, node = (r & 127) / a.G;
+  const int row_nodes = pl.row_nodes, s = r >> 7, node = (r & 127) / a.G;
   const int i = rg * pl.nodes + s * row_nodes + node;
-  if (node >= row_nodes || i >= c || i >= (rg + 1) * pl.nodes || L - c + i < 0) return;
+  if (node >= row_nodes || i >= c || L - c + i < 0) return;
   const int64_t at = ((int64_t)b * a.n + i) * a.h_q + g * a.G + ((r & 127) - node * a.G);
-  auto row_of = [&](int k) { return ((int64_t)(k ? (team + k - 1) * 2 : (team - 1) * 2 + 1) * pl.n_groups + rg) * C::kRows + r; };
-  float m = -INFINITY;
-  for (int k = lane; k < parts; k += 32) m = fmaxf(m, pl.lse[row_of(k)]);
-  m = warp_max(m);
-  const float ref = m == -INFINITY ? 0.f : m;
-  constexpr int PER = D / 32;
-  float o[PER] = {}, z = 0.f;
-  for (int k0 = 0; k0 < parts; k0 += 32) {
-    const float w = k0 + lane < parts ? fast_exp2(pl.lse[row_of(k0 + lane)] - ref) : 0.f;
-    z += w;
-    const int n = min(32, parts - k0);
+  auto slot = [&](int k) { return (int64_t)(k ? (team + k - 1) * 2 : (team - 1) * 2 + 1) * pl.width + blockIdx.y; };
+  float m = -INFINITY, z = 0.f, o[COLS] = {};
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      if (wk == 0.f) continue;  // a part without tiles left no O
-      const float *src = pl.o + row_of(k0 + k) * D + lane * PER;
-      if constexpr (PER == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(src);
-        o[0] = fmaf(wk, v.x, o[0]), o[1] = fmaf(wk, v.y, o[1]), o[2] = fmaf(wk, v.z, o[2]), o[3] = fmaf(wk, v.w, o[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2 *>(src);
-        o[0] = fmaf(wk, v.x, o[0]), o[1] = fmaf(wk, v.y, o[1]);
-      }
+  for (int k = 0; k < parts; ++k) m = fmaxf(m, pl.lse[slot(k) * C::kRows + r]);
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 2
+  for (int k = 0; k < parts; ++k) {
+    const float w = fast_exp2(pl.lse[slot(k) * C::kRows + r] - ref);
+    const float4 *src = reinterpret_cast<const float4 *>(pl.o) + (slot(k) * (D / 4) + warp * (COLS / 4)) * C::kRows + r;
+    z += w;
+#pragma unroll
+    for (int e = 0; e < COLS / 4; ++e) {
+      const float4 v = src[e * C::kRows];
+      if (w == 0.f) continue;  // a part that this row sees nothing of left no O
+      o[4 * e] = fmaf(w, v.x, o[4 * e]), o[4 * e + 1] = fmaf(w, v.y, o[4 * e + 1]);
+      o[4 * e + 2] = fmaf(w, v.z, o[4 * e + 2]), o[4 * e + 3] = fmaf(w, v.w, o[4 * e + 3]);
     }
   }
-  z = warp_sum(z);
   const float f = 1.f / z;
-  uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + lane * PER);
-  if constexpr (PER == 4)
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
-  else
-    *dst = pack_bf16(o[0] * f, o[1] * f);
-  if (a.lse && lane == 0) a.lse[at] = (m + log2f(z)) * kLn2;
+  uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + warp * COLS);
+#pragma unroll
+  for (int e = 0; e < COLS / 8; ++e)
+    dst[e] = make_uint4(pack_bf16(o[8 * e] * f, o[8 * e + 1] * f), pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f),
+                        pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f), pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f));
+  if (a.lse && warp == 0) a.lse[at] = (m + log2f(z)) * kLn2;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -659,25 +824,24 @@ static bool span_wide(const SpanArgs &a) { return a.n > kSpanTile / a.G; }
 
 static SpanPlan span_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
   SpanPlan p = {};
-  p.nodes = (span_wide(a) ? 2 : 1) * (kSpanTile / a.G);
-  p.n_groups = cdiv(a.n, p.nodes);
-  const int sms = sm_count(), batch = kv->batch < kSpanMaxBatch ? kv->batch : kSpanMaxBatch;
-  p.items = (int64_t)batch * kv->h_kv * p.n_groups;
-  // Shares while the units would not fill the SMs about twice, and for trees, whose units are long; teams have to fit.
-  const bool shares = p.n_groups <= sms && (a.parents || a.window == kSpanAll || p.n_groups == 1 || p.items < 2 * sms);
-  p.teams = shares ? sms / p.n_groups : 0;
+  const int streams = span_wide(a) ? 2 : 1, sms = sm_count(), batch = kv->batch < kSpanMaxBatch ? kv->batch : kSpanMaxBatch;
+  p.n_groups = cdiv(a.n, streams * (kSpanTile / a.G));
+  p.row_nodes = cdiv(a.n, streams * p.n_groups);  // even groups
+  p.nodes = streams * p.row_nodes;
+  // Teams where the groups of a unit see the same long stretch of tokens, or too few units would be left to share out.
+  const bool together = a.window >= 8192 || (int64_t)batch * kv->h_kv * p.n_groups < 2 * sms;
+  p.width = together && p.n_groups <= 32 ? p.n_groups : 1;
+  p.teams = sms / p.width;
   return p;
 }
 
 static size_t span_carve(const ssd_paged_kv *kv, SpanPlan &p, bool wide, void *ws) {
   Carver c(ws);
   c.take<char>(kCounterBytes);
-  if (p.teams) {
-    const size_t rows = (size_t)p.teams * 2 * p.n_groups * (wide ? 256 : 128);
-    p.cut_unit = c.take<int32_t>(p.teams);
-    p.o = c.take<float>(rows * kv->d);
-    p.lse = c.take<float>(rows);
-  }
+  const size_t rows = (size_t)p.teams * 2 * p.width * (wide ? 256 : 128);
+  p.cut_unit = c.take<int32_t>(p.teams);
+  p.o = c.take<float>(rows * kv->d);
+  p.lse = c.take<float>(rows);
   return c.off;
 }
 
@@ -693,16 +857,16 @@ static int span_tc_launch(const CUtensorMap &kvmap, const CUtensorMap &qmap, con
   static_assert(smem <= 227 * 1024, "a block's shared memory");
   int rc = ensure_smem<kernel>(smem);
   if (rc) return rc;
-  const int64_t items = (int64_t)a.kv.batch * a.kv.h_kv * p.n_groups;
-  const int grid = p.teams ? p.teams * p.n_groups : (int)(items < sm_count() ? items : sm_count());
-  if ((rc = launch(kernel, dim3(grid), dim3(kSpanThreads), smem, st, "span_tc_kernel", kvmap, qmap, a, p)) || p.teams < 2) return rc;
-  const int rows = WIDE ? 256 : a.n * a.G;
-  return launch(span_join_kernel<D, WIDE>, dim3(p.teams, p.n_groups, cdiv(rows, 8)), dim3(256), 0, st, "span_join_kernel", a, p);
+  if ((rc = launch(kernel, dim3(p.teams * p.width), dim3(kSpanThreads), smem, st, "span_tc_kernel", kvmap, qmap, a, p)) || p.teams < 2) return rc;
+  const int rows = (WIDE ? 128 : 0) + p.row_nodes * a.G;  // (stream 1's behind 128 of stream 0's)
+  return launch(span_join_kernel<D, WIDE>, dim3(p.teams, p.width, cdiv(rows, 32)), dim3(256), 0, st, "span_join_kernel", a, p);
 }
 
 int span_tc(const ssd_paged_kv *kv, const SpanArgs &args, void *workspace, cudaStream_t st) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  if ((int64_t)kSpanMaxBatch * kv->h_kv * cdiv(args.n, kSpanTile / args.G) >= (int64_t)1 << 31)
+    return fail(SSD_ERR_UNSUPPORTED, "span attention: %d queries of %d heads", args.n, args.h_q);
   const bool wide = span_wide(args);
   const int d = kv->d, panels = d / 64, box_rows = kv->page_size < kSpanTile ? kv->page_size : kSpanTile;
   SpanPlan p = span_plan(kv, args);
@@ -728,11 +892,10 @@ int span_tc(const ssd_paged_kv *kv, const SpanArgs &args, void *workspace, cudaS
     if (a.lse) a.lse += rows;
     if (a.parents) a.parents += (int64_t)b0 * a.n;
     if (a.counts) a.counts += b0;
-    p.items = (int64_t)a.kv.batch * kv->h_kv * p.n_groups;
     // Queries [B][n][h_q][d]: a box holds a panel of the group's heads of a stream's queries; queries past n read as zeros.
     const cuuint64_t qdims[4] = {(cuuint64_t)d, (cuuint64_t)a.h_q, (cuuint64_t)a.n, (cuuint64_t)a.kv.batch};
     const cuuint64_t qstrides[3] = {(cuuint64_t)d * 2, (cuuint64_t)a.h_q * d * 2, (cuuint64_t)a.n * a.h_q * d * 2};
-    const cuuint32_t qbox[4] = {64, (cuuint32_t)a.G, (cuuint32_t)(kSpanTile / a.G), 1};
+    const cuuint32_t qbox[4] = {64, (cuuint32_t)a.G, (cuuint32_t)p.row_nodes, 1};
     r = enc(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(a.q), qdims, qstrides, qbox, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled (queries) failed (%d)", (int)r);
