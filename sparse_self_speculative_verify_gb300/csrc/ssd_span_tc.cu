@@ -29,6 +29,7 @@ constexpr int kSpanProducer = 8, kSpanMma = 9;
 constexpr int kSpanMaxBatch = 1024;     // requests of a launch (their sizes lie in shared memory)
 constexpr int kSpanOverhead = 1;        // what starting and ending a unit costs, in tiles
 constexpr int kSpanSnap = 3;            // a cut this close to a unit's border moves there
+constexpr int kSpanWhole = 6;           // units of so many tiles are not cut
 constexpr int kSpanMinShare = 4;        // least share of a team
 constexpr float kSpanLazy = 8.f;        // a row's reference moves when a score exceeds it by this (log2)
 
@@ -37,6 +38,7 @@ struct SpanPlan {
   int row_nodes;         // queries of a stream's tile
   int nodes;             // of a group
   int teams, width;      // teams of blocks: n_groups (a group each) or 1 (a block takes whole groups in turn)
+  int split;             // whether units are cut; else shares end at their borders and nothing is left to join
   int32_t *cut_unit;     // [teams]: the unit that team t's share begins inside of, or -1
   float *o, *lse;        // [teams][2][width][D / 4][rows of a block][4], [teams][2][width][rows] (log2)
 };
@@ -58,45 +60,40 @@ struct SpanCfg {
   static constexpr int kGroup = 1024 * kPanels;  // bytes of 8 tokens: panel after panel of 8 x 128 bytes
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes, kMisc = kV + kStages * kTileBytes;
-  static constexpr int kBars = 4 * kStages + 16 + kSpanRing;
+  static constexpr int kBars = 4 * kStages + 18 + kSpanRing;
   // barriers, the requests' prefix, size, length and queries, the streams' maxima and sums
-  static constexpr int kSmem = kMisc + kBars * 8 + (2 * kSpanMaxBatch + 1) * 8 + 2 * kSpanMaxBatch * 4 + 1024 * 4 + kSpanRing * (int)sizeof(SpanSeg) + 1024;
+  static constexpr int kSmem = kMisc + kBars * 8 + (4 * kSpanMaxBatch + 2) * 4 + 1024 * 4 + kSpanRing * (int)sizeof(SpanSeg) + 1024;
   static constexpr int kRows = WIDE ? 256 : 128;
   static constexpr int kColO = 256;  // tensor memory: S (P) of the streams, O of the streams
 };
 
-// x / y, x >= 0, y > 0: in 32 bits where they fit.
-__device__ __forceinline__ int64_t span_div(int64_t x, int64_t y) {
-  return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
-}
-
-// The segments of a block, in order.
+// The segments of a block, in order.  (Costs of a launch fit 31 bits: span_tc cuts the batch so.)
 struct SpanWalk {
   const SpanArgs &a;
   const SpanPlan &pl;
-  const int64_t *pre, *size;  // prefix of the requests' costs; cost of a request's unit (of all its groups, where width is 1)
+  const int *pre, *size;      // prefix of the requests' costs; cost of a request's unit (of all its groups, where width is 1)
   const int *len, *cnt;
-  int64_t pos, end, u0, u1;   // of the share; the unit at pos
+  int pos, end, u0, u1;       // of the share; the unit at pos
   int b, g, rg, team;
   bool inside;                // the share begins inside a unit
 
-  __device__ SpanWalk(const SpanArgs &a_, const SpanPlan &p_, const int64_t *pre_, const int64_t *size_, const int *len_, const int *cnt_)
-      : a(a_), pl(p_), pre(pre_), size(size_), len(len_), cnt(cnt_) {
+  __device__ SpanWalk(const SpanArgs &a_, const SpanPlan &p_, const int *pre_, const int *size_, const int *len_, const int *cnt_)
+      : a(a_), pl(p_), pre(pre_), size(size_), len(len_), cnt(cnt_), u0(0), u1(0), b(0), g(0) {
     team = blockIdx.x / pl.width;
     rg = blockIdx.x % pl.width;
     if (pl.width > 1 || pl.n_groups == 1) {  // both ends at once, by even and odd lanes
-      const int64_t x = cut(team + (threadIdx.x & 1));
+      const int x = cut(team + (threadIdx.x & 1));
       pos = __shfl_sync(0xffffffffu, x, 0);
       end = __shfl_sync(0xffffffffu, x, 1);
+      u0 = __shfl_sync(0xffffffffu, u0, 0);
+      u1 = __shfl_sync(0xffffffffu, u1, 0);
+      b = __shfl_sync(0xffffffffu, b, 0);
+      g = __shfl_sync(0xffffffffu, g, 0);
     } else {
-      pos = cut(team);
       end = cut(team + 1);
+      pos = cut(team);
     }
-    inside = false;
-    if (pos < end) {
-      locate(pos);
-      inside = pos > u0;
-    }
+    inside = pos > u0 && pos < u1;
   }
   __device__ SpanTiles tiles_of(int at, int group) const {
     return span_tiles<kSpanTile>(a, len[at], cnt[at], group * pl.nodes, group * pl.nodes + pl.nodes - 1);
@@ -107,20 +104,20 @@ struct SpanWalk {
     return n ? n + kSpanOverhead : 0;
   }
   // Sets the unit that position x < pre[batch] lies in (by a converged warp where a unit has groups of its own).
-  __device__ void locate(int64_t x) {
+  __device__ void locate(int x) {
     int lo = 0, hi = a.kv.batch;  // pre[lo] <= x < pre[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (pre[mid] <= x) lo = mid; else hi = mid;
     }
     b = lo;
-    const int64_t sz = size[lo], rem = x - pre[lo];
-    g = (int)span_div(rem, sz);
+    const unsigned sz = size[lo], rem = x - pre[lo];
+    g = rem / sz;
     u0 = pre[lo] + g * sz;
     u1 = u0 + sz;
     if (pl.width > 1 || pl.n_groups == 1) return;
     const int lane = threadIdx.x & 31;
-    int64_t at = u0;
+    int at = u0;
     for (int r0 = 0;; r0 += 32) {  // 32 groups at a time
       const int mine = r0 + lane < pl.n_groups ? cost(b, r0 + lane) : 0;
       int incl = mine;
@@ -140,19 +137,15 @@ struct SpanWalk {
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  // Where team t's share begins.
-  __device__ int64_t cut(int t) {
-    const int64_t total = pre[a.kv.batch];
-    const int64_t n = min((int64_t)pl.teams, max((int64_t)1, total / kSpanMinShare));
-    if (t >= n) return total;
-    if (total == 0) return 0;
-    const int64_t per = span_div(total, n), x = per * t + (uint32_t)(total - per * n) * (uint32_t)t / (uint32_t)n;
-    const int keep = rg;
+  // Where team t's share begins; sets the unit there, or the one that ends there.
+  __device__ int cut(int t) {
+    const unsigned total = pre[a.kv.batch], n = min((unsigned)pl.teams, max(1u, total / kSpanMinShare));
+    if (t >= (int)n || total == 0) return total;
+    const unsigned per = total / n, x = per * t + (total - per * n) * t / n;
     locate(x);
-    if (pl.width > 1) rg = keep;
-    return x - u0 < kSpanSnap ? u0 : u1 - x < kSpanSnap ? u1 : x;
+    if (!pl.split) return 2 * ((int)x - u0) < u1 - u0 ? u0 : u1;
+    return (int)x - u0 < kSpanSnap ? u0 : u1 - (int)x < kSpanSnap ? u1 : (int)x;
   }
-  // The unit's number; where the share begins inside one.
   __device__ int unit() const { return pl.width > 1 ? b * a.kv.h_kv + g : (b * a.kv.h_kv + g) * pl.n_groups + rg; }
   __device__ bool next(SpanSeg &s) {
     if (pos >= end) return false;
@@ -174,9 +167,9 @@ struct SpanWalk {
     s.rg = rg;
     s.c = cnt[b];
     s.st = tiles_of(b, rg);
-    const int64_t stop = min(u1, end);
-    s.k0 = min(max(0, (int)(pos - u0) - kSpanOverhead), s.st.n_tiles);
-    s.k1 = stop == u1 ? s.st.n_tiles : min(max(0, (int)(stop - u0) - kSpanOverhead), s.st.n_tiles);
+    const int stop = min(u1, end);
+    s.k0 = min(max(0, pos - u0 - kSpanOverhead), s.st.n_tiles);
+    s.k1 = stop == u1 ? s.st.n_tiles : min(max(0, stop - u0 - kSpanOverhead), s.st.n_tiles);
     s.part = pos == u0 && stop == u1 ? -1 : (team * 2 + (pos == u0)) * pl.width + (pl.width > 1 ? rg : 0);
     pos = stop;
     return true;
@@ -221,6 +214,42 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+template <int V>
+struct SpanInt {
+  static constexpr int value = V;
+};
+
+// Joins a row's parts, team `first`'s slot 1 and slot 0 of the parts - 1 teams behind it: weights 2^(lse - max) over their sum.
+// COLS columns from c0 on of row r of the slots' member y, to row `at` of the output.
+template <int D, int ROWS, int COLS>
+__device__ __forceinline__ void span_join_row(const SpanArgs &a, const SpanPlan &pl, int first, int parts, int y, int r, int c0, int64_t at) {
+  auto slot = [&](int k) { return (int64_t)(k ? (first + k) * 2 : first * 2 + 1) * pl.width + y; };
+  float m = -INFINITY, z = 0.f, o[COLS] = {};
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) m = fmaxf(m, __ldcg(pl.lse + slot(k) * ROWS + r));
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 2
+  for (int k = 0; k < parts; ++k) {
+    const float w = fast_exp2(__ldcg(pl.lse + slot(k) * ROWS + r) - ref);
+    const float4 *src = reinterpret_cast<const float4 *>(pl.o) + (slot(k) * (D / 4) + c0 / 4) * ROWS + r;
+    z += w;
+#pragma unroll
+    for (int e = 0; e < COLS / 4; ++e) {
+      const float4 v = __ldcg(src + e * ROWS);
+      if (w == 0.f) continue;  // a part that this row sees nothing of left no O
+      o[4 * e] = fmaf(w, v.x, o[4 * e]), o[4 * e + 1] = fmaf(w, v.y, o[4 * e + 1]);
+      o[4 * e + 2] = fmaf(w, v.z, o[4 * e + 2]), o[4 * e + 3] = fmaf(w, v.w, o[4 * e + 3]);
+    }
+  }
+  const float f = 1.f / z;
+  uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + c0);
+#pragma unroll
+  for (int e = 0; e < COLS / 8; ++e)
+    dst[e] = make_uint4(pack_bf16(o[8 * e] * f, o[8 * e + 1] * f), pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f),
+                        pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f), pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f));
+  if (a.lse && c0 == 0) a.lse[at] = (m + log2f(z)) * kLn2;
+}
+
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kSpanThreads, 1)
     span_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap, SpanArgs a, SpanPlan pl) {
@@ -232,19 +261,18 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = a.kv.batch, h_kv = a.kv.h_kv, ps = a.kv.page_size;
 
-  // K and V slots' full / empty, Q buffers' full / empty, the streams' S full, P full, O done, drain
+  // K and V slots' full / empty, Q buffers' full / empty, the streams' S full, P's halves full, O done, drain
   const uint32_t bars = sbase + C::kMisc;
   const uint32_t k_full = bars, k_empty = k_full + 8 * NS, v_full = k_empty + 8 * NS, v_empty = v_full + 8 * NS;
-  const uint32_t q_full = v_empty + 8 * NS, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 16,
+  const uint32_t q_full = v_empty + 8 * NS, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 32,
                  drained = o_done + 16, group = drained + 16, seg_full = group + 8;
-  int64_t *pre = reinterpret_cast<int64_t *>(sm + C::kMisc + C::kBars * 8);
-  int64_t *s_size = pre + kSpanMaxBatch + 1;
-  int *s_len = reinterpret_cast<int *>(s_size + kSpanMaxBatch), *s_cnt = s_len + kSpanMaxBatch;
+  int *pre = reinterpret_cast<int *>(sm + C::kMisc + C::kBars * 8);
+  int *s_size = pre + kSpanMaxBatch + 2, *s_len = s_size + kSpanMaxBatch, *s_cnt = s_len + kSpanMaxBatch;
   float *s_m = reinterpret_cast<float *>(s_cnt + kSpanMaxBatch);  // [segment % 2][maxima, sums][stream][row]
   SpanSeg *ring = reinterpret_cast<SpanSeg *>(s_m + 1024);
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ int64_t s_scan[kSpanThreads / 32];
+  __shared__ int s_scan[kSpanThreads / 32];
 
   if (tid == 0) {
     s_abort = 0;
@@ -254,7 +282,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1), mbar_init(q_empty + 8 * i, WIDE ? 1 : 8);
-      mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4), mbar_init(o_done + 8 * i, 1), mbar_init(drained + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4), mbar_init(p_full + 16 + 8 * i, 4), mbar_init(o_done + 8 * i, 1), mbar_init(drained + 8 * i, 1);
     }
     mbar_init(group, 8);
     for (int i = 0; i < kSpanRing; ++i) mbar_init(seg_full + 8 * i, 1);
@@ -272,40 +300,45 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
 
   // Sizes of the requests; the costs of their units; the prefix of the requests' costs.
   for (int b = tid; b < B; b += kSpanThreads) {
-    span_sizes(a, b, blockIdx.x == 0, s_len[b], s_cnt[b]);
-    s_size[b] = 0;
+    int L, c;
+    span_sizes(a, b, blockIdx.x == 0, L, c);
+    s_len[b] = L, s_cnt[b] = c;
+    const int n = pl.n_groups == 1 ? span_tiles<kSpanTile>(a, L, c, 0, pl.nodes - 1).n_tiles : 0;
+    s_size[b] = n ? n + kSpanOverhead : 0;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  for (int64_t e = tid; e < (int64_t)B * pl.n_groups; e += kSpanThreads) {
-    const int b = (int)(e / pl.n_groups), group = (int)(e - (int64_t)b * pl.n_groups);
-    const int n = span_tiles<kSpanTile>(a, s_len[b], s_cnt[b], group * pl.nodes, group * pl.nodes + pl.nodes - 1).n_tiles;
-    if (n == 0) continue;
-    if (pl.width > 1)  // a team walks the most tiles of its groups
-      atomicMax(reinterpret_cast<unsigned long long *>(s_size + b), (unsigned long long)(n + kSpanOverhead));
-    else
-      atomicAdd(reinterpret_cast<unsigned long long *>(s_size + b), (unsigned long long)(n + kSpanOverhead));
+  if (pl.n_groups > 1) {
+    for (unsigned e = tid; e < (unsigned)B * pl.n_groups; e += kSpanThreads) {
+      const int b = (int)(e / pl.n_groups), group = (int)(e - (unsigned)b * pl.n_groups);
+      const int n = span_tiles<kSpanTile>(a, s_len[b], s_cnt[b], group * pl.nodes, group * pl.nodes + pl.nodes - 1).n_tiles;
+      if (n == 0) continue;
+      if (pl.width > 1)  // a team walks the most tiles of its groups
+        atomicMax(s_size + b, n + kSpanOverhead);
+      else
+        atomicAdd(s_size + b, n + kSpanOverhead);
+    }
+    __syncthreads();
   }
-  __syncthreads();
   {
     constexpr int CH = cdiv(kSpanMaxBatch, kSpanThreads);
-    int64_t mine[CH], sum = 0;
+    int mine[CH], sum = 0;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int b = tid * CH + k;
       mine[k] = b < B ? h_kv * s_size[b] : 0;
       sum += mine[k];
     }
-    int64_t incl = sum;
+    int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += t;
     }
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    int64_t off = incl - sum;
+    int off = incl - sum;
     for (int w = 0; w < warp; ++w) off += s_scan[w];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -318,19 +351,6 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   }
   const uint32_t tm = s_tmem;
   volatile int *abort = &s_abort;
-
-  // Rows that see nothing; a request's are shared by every B-th block.
-  for (int b = blockIdx.x % B; b < B; b += gridDim.x) {
-    const int c = s_cnt[b], below = min(max(0, c - s_len[b]), c);  // queries [0, below) and [c, n)
-    const int rows = below + a.n - c, sharers = max(1, cdiv((int)gridDim.x - b, B));
-    for (int64_t e = (blockIdx.x / B) * kSpanThreads + tid; e < (int64_t)rows * a.h_q * (D / 8); e += sharers * kSpanThreads) {
-      const int64_t r = e / (D / 8);
-      const int i0 = (int)(r / a.h_q), i = i0 < below ? i0 : c + i0 - below;
-      const int64_t at = ((int64_t)b * a.n + i) * a.h_q + r % a.h_q;
-      reinterpret_cast<uint4 *>(a.out)[at * (D / 8) + e % (D / 8)] = make_uint4(0, 0, 0, 0);
-      if (a.lse && e % (D / 8) == 0) a.lse[at] = -INFINITY;
-    }
-  }
 
   const int row_nodes = pl.row_nodes;
   // Segment j of the block, once the producer has published it; nullptr behind the last one (and where a wait ran out).
@@ -473,17 +493,25 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int s, int slot, bool first, bool free_v) {
+    // O += P V of stream s's tile n, a half of the tokens as soon as its half of P is there.
+    auto issue_pv = [&](int s, uint32_t n, int slot, bool first, bool free_v) {
       const uint64_t v = vd + (uint64_t)(slot * C::kTileBytes >> 4);
       const uint32_t acc = first ? 0u : 1u;
-      if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kSpanTile / 16; ++kk)
-          mma_bf16_ts(tmu + C::kColO + s * 128, tmu + s * 128 + kk * 8, v + (uint64_t)((kk * 2 * C::kGroup) >> 4), id_pv, kk > 0 ? 1u : acc);
-        mma_commit(o_done + 8 * s);
-        if (free_v) mma_commit(v_empty + 8 * slot);
+      for (int h = 0; h < 2; ++h) {
+        mbar_wait(p_full + 16 * h + 8 * s, n & 1, abort);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+            mma_bf16_ts(tmu + C::kColO + s * 128, tmu + s * 128 + kk * 8, v + (uint64_t)((kk * 2 * C::kGroup) >> 4), id_pv, kk > 0 ? 1u : acc);
+          if (h) {
+            mma_commit(o_done + 8 * s);
+            if (free_v) mma_commit(v_empty + 8 * slot);
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
     };
     // Rows of V that nobody sees may hold anything, and 0 times it has to be 0: those behind `hi` and those from `sink` to `lo`.
     auto clear_unseen = [&](int hi, int sink, int lo, int t0, int slot) {
@@ -517,9 +545,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
           mbar_wait(v_full + 8 * slot, (f / NS) & 1, abort);
           clear_unseen(seg.st.hi, seg.st.sink, seg.st.lo, seg.st.tile(k) * kSpanTile, slot);
           for (int s = 0; s < streams; ++s) {
-            mbar_wait(p_full + 8 * s, n[s]++ & 1, abort);
-            tc_fence_after();
-            issue_pv(s, slot, k == seg.k0, s == streams - 1);
+            issue_pv(s, n[s]++, slot, k == seg.k0, s == streams - 1);
             if (k + 1 < seg.k1) {
               if (s == 0) {
                 mbar_wait(k_full + 8 * nslot, ((f + 1) / NS) & 1, abort);
@@ -547,9 +573,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
           issue_qk(s, j & 1, slot, true, false);
           mbar_wait(v_full + 8 * slot, (f / NS) & 1, abort);
           clear_unseen(seg.st.hi, seg.st.sink, seg.st.lo, seg.st.tile(k) * kSpanTile, slot);
-          mbar_wait(p_full + 8 * s, n++ & 1, abort);
-          tc_fence_after();
-          issue_pv(s, slot, first, true);
+          issue_pv(s, n++, slot, first, true);
           first = false;
         }
       }
@@ -563,6 +587,18 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------------------------------------------------------- softmax, O
+    // Rows that see nothing; a request's are shared by every B-th block.
+    for (int b = blockIdx.x % B; b < B; b += gridDim.x) {
+      const int c = s_cnt[b], below = min(max(0, c - s_len[b]), c);  // queries [0, below) and [c, n)
+      const int rows = below + a.n - c, sharers = max(1, cdiv((int)gridDim.x - b, B));
+      for (int64_t e = (blockIdx.x / B) * 256 + tid; e < (int64_t)rows * a.h_q * (D / 8); e += sharers * 256) {
+        const int64_t r = e / (D / 8);
+        const int i0 = (int)(r / a.h_q), i = i0 < below ? i0 : c + i0 - below;
+        const int64_t at = ((int64_t)b * a.n + i) * a.h_q + r % a.h_q;
+        reinterpret_cast<uint4 *>(a.out)[at * (D / 8) + e % (D / 8)] = make_uint4(0, 0, 0, 0);
+        if (a.lse && e % (D / 8) == 0) a.lse[at] = -INFINITY;
+      }
+    }
     const int s = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t col_s = tm + s * 128 + lanes, col_o = tm + C::kColO + s * 128 + lanes;
@@ -651,16 +687,24 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
               p[e] = pack_bf16(y0, y1);
             }
             tmem_st16(col_s + 16 * q, p);
+            if (q == 1) {
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(p_full + 8 * s);
+            }
           }
           float l0, l1;
           unpack2(add2(sum[0], sum[1]), l0, l1);
           l += l0 + l1;
           tmem_st_wait();
+          tc_fence_before();
+        } else if (lane == 0) {
+          mbar_arrive(p_full + 8 * s);
         }
         have = true;
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * s);
+        if (lane == 0) mbar_arrive(p_full + 16 + 8 * s);
         ++n;
       }
       // The segment's end.
@@ -699,46 +743,55 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
           }
         }
       } else {
-        // Each stream ends half of the columns (or, with more than 64 rows, a quarter at a time) and passes its share of the
-        // other's on through the segment's Q buffer, whose products are done.
-        const bool many = row_nodes * a.G > 64;
-        const int stride = many ? 128 : 64, step = many ? D / 4 : D / 2;  // rows and columns of a box
-        float *boxes = reinterpret_cast<float *>(sm + C::kQ + (j & 1) * C::kTileBytes), *mine = boxes + s * stride * step, *theirs = boxes + (1 - s) * stride * step;
+        // Each stream ends half of the columns and passes its share of the others on through the segment's Q buffer, whose
+        // products are done by then: in one step, or with more than 64 rows in two.
+        float *boxes = reinterpret_cast<float *>(sm + C::kQ + (j & 1) * C::kTileBytes);
         float *my_m = s_m + (j & 1) * 512;  // [stream][row], and the sums behind them
         my_m[s * 128 + row] = have ? mref : -INFINITY;
         my_m[256 + s * 128 + row] = have ? l : 0.f;
-        sync_streams();  // (the other stream's products with Q are done too)
+        sync_streams();
         const float m_two = my_m[(1 - s) * 128 + row], m = fmaxf(my_m[s * 128 + row], m_two), ref = m == -INFINITY ? 0.f : m;
         float f0 = have ? fast_exp2(mref - ref) : 0.f, f1 = fast_exp2(m_two - ref);
         l = (have ? l : 0.f) * f0 + my_m[256 + (1 - s) * 128 + row] * f1;
         mref = m;
-        f0 /= l, f1 /= l;
-        for (int c0 = 0; c0 < D / 2; c0 += step) {
-          if (warp_valid)
-            for (int e0 = 0; e0 < step; e0 += 16) {
-              float o[16];
+        const float f = 1.f / l;
+        f0 *= f, f1 *= f;
+        auto end = [&](auto rows_of_box, auto steps) {
+          constexpr int RB = decltype(rows_of_box)::value, STEPS = decltype(steps)::value, W = D / 2 / STEPS;
+          float *mine = boxes + s * RB * W, *theirs = boxes + (1 - s) * RB * W;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D / 2; c0 += W) {
+            if (warp_valid) {
+              float o[W];
               if (have) {
-                tmem_ld16(col_o + (1 - s) * (D / 2) + c0 + e0, o);
+#pragma unroll
+                for (int e = 0; e < W; e += 16) tmem_ld16(col_o + (1 - s) * (D / 2) + c0 + e, o + e);
                 tmem_ld_wait();
               }
 #pragma unroll
-              for (int e = 0; e < 16; ++e) mine[(e0 + e) * stride + row] = have ? o[e] : 0.f;
+              for (int e = 0; e < W; ++e) mine[e * RB + row] = have ? o[e] : 0.f;
             }
-          fence_proxy_async_smem();  // before the next queries' copies
-          sync_streams();
-          if (warp_valid)
-            for (int e0 = 0; e0 < step; e0 += 16) {
-              float o[16];
-              if (have) {
-                tmem_ld16(col_o + s * (D / 2) + c0 + e0, o);
-                tmem_ld_wait();
-              }
+            fence_proxy_async_smem();  // before the next queries' copies
+            sync_streams();
+            if (warp_valid)
+#pragma unroll 1
+              for (int e0 = 0; e0 < W; e0 += 16) {
+                float o[16];
+                if (have) {
+                  tmem_ld16(col_o + s * (D / 2) + c0 + e0, o);
+                  tmem_ld_wait();
+                }
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = (have ? o[e] * f0 : 0.f) + theirs[(e0 + e) * stride + row] * f1;
-              put(o, s * (D / 2) + c0 + e0);
-            }
-          if (c0 + step < D / 2) sync_streams();
-        }
+                for (int e = 0; e < 16; ++e) o[e] = (have ? o[e] * f0 : 0.f) + theirs[(e0 + e) * RB + row] * f1;
+                put(o, s * (D / 2) + c0 + e0);
+              }
+            if (STEPS > 1) sync_streams();
+          }
+        };
+        if (row_nodes * a.G <= 64)
+          end(SpanInt<64>{}, SpanInt<1>{});
+        else
+          end(SpanInt<128>{}, SpanInt<2>{});
         __syncwarp();
         if (lane == 0) mbar_arrive(q_empty + 8 * (j & 1));
       }
@@ -785,31 +838,7 @@ __global__ void __launch_bounds__(256) span_join_kernel(SpanArgs a, SpanPlan pl)
   const int i = rg * pl.nodes + s * row_nodes + node;
   if (node >= row_nodes || i >= c || L - c + i < 0) return;
   const int64_t at = ((int64_t)b * a.n + i) * a.h_q + g * a.G + ((r & 127) - node * a.G);
-  auto slot = [&](int k) { return (int64_t)(k ? (team + k - 1) * 2 : (team - 1) * 2 + 1) * pl.width + blockIdx.y; };
-  float m = -INFINITY, z = 0.f, o[COLS] = {};
-#pragma unroll 4
-  for (int k = 0; k < parts; ++k) m = fmaxf(m, pl.lse[slot(k) * C::kRows + r]);
-  const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 2
-  for (int k = 0; k < parts; ++k) {
-    const float w = fast_exp2(pl.lse[slot(k) * C::kRows + r] - ref);
-    const float4 *src = reinterpret_cast<const float4 *>(pl.o) + (slot(k) * (D / 4) + warp * (COLS / 4)) * C::kRows + r;
-    z += w;
-#pragma unroll
-    for (int e = 0; e < COLS / 4; ++e) {
-      const float4 v = src[e * C::kRows];
-      if (w == 0.f) continue;  // a part that this row sees nothing of left no O
-      o[4 * e] = fmaf(w, v.x, o[4 * e]), o[4 * e + 1] = fmaf(w, v.y, o[4 * e + 1]);
-      o[4 * e + 2] = fmaf(w, v.z, o[4 * e + 2]), o[4 * e + 3] = fmaf(w, v.w, o[4 * e + 3]);
-    }
-  }
-  const float f = 1.f / z;
-  uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + warp * COLS);
-#pragma unroll
-  for (int e = 0; e < COLS / 8; ++e)
-    dst[e] = make_uint4(pack_bf16(o[8 * e] * f, o[8 * e + 1] * f), pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f),
-                        pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f), pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f));
-  if (a.lse && warp == 0) a.lse[at] = (m + log2f(z)) * kLn2;
+  span_join_row<D, C::kRows, COLS>(a, pl, team - 1, parts, blockIdx.y, r, warp * COLS, at);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -822,6 +851,12 @@ bool span_tc_takes(const ssd_paged_kv *kv) {
 
 static bool span_wide(const SpanArgs &a) { return a.n > kSpanTile / a.G; }
 
+// Tiles of a unit's group, at most.
+static int64_t span_most_tiles(const ssd_paged_kv *kv, const SpanArgs &a, const SpanPlan &p) {
+  const int64_t all = cdiv(kv->max_seq_len, kSpanTile), most = cdiv64(a.sink, kSpanTile) + ((int64_t)a.window + p.nodes) / kSpanTile + 2;
+  return all < most ? all : most;
+}
+
 static SpanPlan span_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
   SpanPlan p = {};
   const int streams = span_wide(a) ? 2 : 1, sms = sm_count(), batch = kv->batch < kSpanMaxBatch ? kv->batch : kSpanMaxBatch;
@@ -832,6 +867,9 @@ static SpanPlan span_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
   const bool together = a.window >= 8192 || (int64_t)batch * kv->h_kv * p.n_groups < 2 * sms;
   p.width = together && p.n_groups <= 32 ? p.n_groups : 1;
   p.teams = sms / p.width;
+  // A unit's tiles, at most; short ones stay whole, which saves the join's launch (17 requests of up to 33 queries with a window
+  // of 301: 20.1 us cut, 17.1 whole).
+  p.split = span_most_tiles(kv, a, p) > kSpanWhole;
   return p;
 }
 
@@ -857,7 +895,7 @@ static int span_tc_launch(const CUtensorMap &kvmap, const CUtensorMap &qmap, con
   static_assert(smem <= 227 * 1024, "a block's shared memory");
   int rc = ensure_smem<kernel>(smem);
   if (rc) return rc;
-  if ((rc = launch(kernel, dim3(p.teams * p.width), dim3(kSpanThreads), smem, st, "span_tc_kernel", kvmap, qmap, a, p)) || p.teams < 2) return rc;
+  if ((rc = launch(kernel, dim3(p.teams * p.width), dim3(kSpanThreads), smem, st, "span_tc_kernel", kvmap, qmap, a, p)) || !p.split || p.teams < 2) return rc;
   const int rows = (WIDE ? 128 : 0) + p.row_nodes * a.G;  // (stream 1's behind 128 of stream 0's)
   return launch(span_join_kernel<D, WIDE>, dim3(p.teams, p.width, cdiv(rows, 32)), dim3(256), 0, st, "span_join_kernel", a, p);
 }
@@ -865,8 +903,6 @@ static int span_tc_launch(const CUtensorMap &kvmap, const CUtensorMap &qmap, con
 int span_tc(const ssd_paged_kv *kv, const SpanArgs &args, void *workspace, cudaStream_t st) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  if ((int64_t)kSpanMaxBatch * kv->h_kv * cdiv(args.n, kSpanTile / args.G) >= (int64_t)1 << 31)
-    return fail(SSD_ERR_UNSUPPORTED, "span attention: %d queries of %d heads", args.n, args.h_q);
   const bool wide = span_wide(args);
   const int d = kv->d, panels = d / 64, box_rows = kv->page_size < kSpanTile ? kv->page_size : kSpanTile;
   SpanPlan p = span_plan(kv, args);
@@ -881,9 +917,13 @@ int span_tc(const ssd_paged_kv *kv, const SpanArgs &args, void *workspace, cudaS
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled (KV pool) failed (%d)", (int)r);
-  for (int b0 = 0; b0 < kv->batch; b0 += kSpanMaxBatch) {
+  // Requests of a launch: their sizes fit shared memory, and their costs 31 bits.
+  const int64_t one = kv->h_kv * p.n_groups * (span_most_tiles(kv, args, p) + kSpanOverhead);
+  if (one >= (int64_t)1 << 31) return fail(SSD_ERR_UNSUPPORTED, "span attention: %d queries of %d heads over %d tokens", args.n, args.h_q, kv->max_seq_len);
+  const int slice = (int)(((int64_t)1 << 31) / (one + 1) < kSpanMaxBatch ? ((int64_t)1 << 31) / (one + 1) : kSpanMaxBatch);
+  for (int b0 = 0; b0 < kv->batch; b0 += slice) {
     SpanArgs a = args;
-    a.kv.batch = kv->batch - b0 < kSpanMaxBatch ? kv->batch - b0 : kSpanMaxBatch;
+    a.kv.batch = kv->batch - b0 < slice ? kv->batch - b0 : slice;
     a.kv.page_table += (int64_t)b0 * kv->max_pages;
     a.kv.seq_lens += b0;
     const int64_t rows = (int64_t)b0 * a.n * a.h_q;
