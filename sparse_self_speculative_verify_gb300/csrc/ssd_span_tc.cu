@@ -10,12 +10,11 @@
 // Roles: warps 0-3 and 4-7 the softmax of a stream (and its O), warp 8 loads (one TMA box per page, 128-byte swizzle),
 // warps 9 and 10 issue a stream's products.
 //
-// Work.  A unit is one (request, KV head); its rows are split into n_groups groups of one block's rows.  n_groups blocks
-// form a team, one group each, that walks the same tokens side by side, so that K and V come from memory once and from L2
-// for the others.  The units' tiles lie end to end and are cut into equal shares, one per team; a cut close to a unit's
-// border moves there.  A unit that several teams share leaves partial results, joined by span_join_kernel.  Where the groups
-// see different tokens and there are many of them (prompts with a window), a team is one block, and the groups lie end to
-// end too.
+// Work.  A unit is one (request, KV head, group of as many queries as a block holds).  The units' tiles lie end to end and are
+// cut into equal shares, one per block (one block per SM); a cut close to a unit's border moves there.  A unit that several
+// blocks share leaves partial results, joined by span_join_kernel.  (Groups of the same head read K and V for themselves: at
+// 256 rows a tile takes longer on the tensor cores than from memory.  Blocks that walked the groups of a head side by side,
+// to read it once, had to do the same work: 8 requests of 33 to 64 nodes with 5 heads a group took 488 us.)
 #include "ssd_sm100.cuh"
 #include "ssd_span.h"
 #include "ssd_tma.h"
@@ -30,17 +29,17 @@ constexpr int kSpanMaxBatch = 1024;     // requests of a launch (their sizes lie
 constexpr int kSpanOverhead = 1;        // what starting and ending a unit costs, in tiles
 constexpr int kSpanSnap = 3;            // a cut this close to a unit's border moves there
 constexpr int kSpanWhole = 6;           // units of so many tiles are not cut
-constexpr int kSpanMinShare = 4;        // least share of a team
+constexpr int kSpanMinShare = 4;        // least share of a block
 constexpr float kSpanLazy = 8.f;        // a row's reference moves when a score exceeds it by this (log2)
 
 struct SpanPlan {
   int n_groups;          // row groups of a unit
   int row_nodes;         // queries of a stream's tile
   int nodes;             // of a group
-  int teams, width;      // teams of blocks: n_groups (a group each) or 1 (a block takes whole groups in turn)
+  int blocks;
   int split;             // whether units are cut; else shares end at their borders and nothing is left to join
-  int32_t *cut_unit;     // [teams]: the unit that team t's share begins inside of, or -1
-  float *o, *lse;        // [teams][2][width][D / 4][rows of a block][4], [teams][2][width][rows] (log2)
+  int32_t *cut_unit;     // [blocks]: the unit that a block's share begins inside of, or -1
+  float *o, *lse;        // [blocks][2][D / 4][rows of a block][4], [blocks][2][rows] (log2)
 };
 
 struct SpanSeg {
@@ -58,11 +57,14 @@ struct SpanCfg {
   static constexpr int kPanels = D / 64;
   static constexpr int kTileBytes = kSpanTile * D * 2;
   static constexpr int kGroup = 1024 * kPanels;  // bytes of 8 tokens: panel after panel of 8 x 128 bytes
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes, kMisc = kV + kStages * kTileBytes;
-  static constexpr int kBars = 4 * kStages + 18 + kSpanRing;
-  // barriers, the requests' prefix, size, length and queries, the streams' maxima and sums
-  static constexpr int kSmem = kMisc + kBars * 8 + (4 * kSpanMaxBatch + 2) * 4 + 1024 * 4 + kSpanRing * (int)sizeof(SpanSeg) + 1024;
+  // Slots of K and of V: V is held through the softmax.  (D = 128: all of the shared memory.)
+  static constexpr int kSlotsK = D == 128 ? 2 : 4, kSlotsV = D == 128 ? (WIDE ? 3 : 2) : 4;
+  static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kSlotsK * kTileBytes, kMisc = kV + kSlotsV * kTileBytes;
+  static constexpr int kBars = 2 * (kSlotsK + kSlotsV) + 16 + kSpanRing;
+  // barriers, segments, the streams' maxima and sums
+  static constexpr int kSmem = kMisc + kBars * 8 + kSpanRing * (int)sizeof(SpanSeg) + (WIDE ? 0 : 512 * 4) + 1024;
+  // before the first copy, in the slots: the requests' prefix, size, length and queries
+  static_assert((kSlotsK + kSlotsV) * kTileBytes >= (4 * kSpanMaxBatch + 1) * 4, "sizes");
   static constexpr int kRows = WIDE ? 256 : 128;
   static constexpr int kColO = 256;  // tensor memory: S (P) of the streams, O of the streams
 };
@@ -71,18 +73,17 @@ struct SpanCfg {
 struct SpanWalk {
   const SpanArgs &a;
   const SpanPlan &pl;
-  const int *pre, *size;      // prefix of the requests' costs; cost of a request's unit (of all its groups, where width is 1)
-  const int *len, *cnt;
+  // Until the first segment: prefix of the requests' costs; cost of a KV head's groups.
+  const int *pre, *size, *len, *cnt;
   int pos, end, u0, u1;       // of the share; the unit at pos
-  int b, g, rg, team;
+  int b, g, rg;
+  int L, c, next_L, next_c;   // of request b, of the one behind it
   bool inside;                // the share begins inside a unit
 
   __device__ SpanWalk(const SpanArgs &a_, const SpanPlan &p_, const int *pre_, const int *size_, const int *len_, const int *cnt_)
-      : a(a_), pl(p_), pre(pre_), size(size_), len(len_), cnt(cnt_), u0(0), u1(0), b(0), g(0) {
-    team = blockIdx.x / pl.width;
-    rg = blockIdx.x % pl.width;
-    if (pl.width > 1 || pl.n_groups == 1) {  // both ends at once, by even and odd lanes
-      const int x = cut(team + (threadIdx.x & 1));
+      : a(a_), pl(p_), pre(pre_), size(size_), len(len_), cnt(cnt_), u0(0), u1(0), b(0), g(0), rg(0) {
+    if (pl.n_groups == 1) {  // both ends at once, by even and odd lanes
+      const int x = cut(blockIdx.x + (threadIdx.x & 1));
       pos = __shfl_sync(0xffffffffu, x, 0);
       end = __shfl_sync(0xffffffffu, x, 1);
       u0 = __shfl_sync(0xffffffffu, u0, 0);
@@ -90,17 +91,22 @@ struct SpanWalk {
       b = __shfl_sync(0xffffffffu, b, 0);
       g = __shfl_sync(0xffffffffu, g, 0);
     } else {
-      end = cut(team + 1);
-      pos = cut(team);
+      end = cut(blockIdx.x + 1);
+      pos = cut(blockIdx.x);
     }
     inside = pos > u0 && pos < u1;
+    L = len[b], c = cnt[b];
+    look_ahead();
   }
-  __device__ SpanTiles tiles_of(int at, int group) const {
-    return span_tiles<kSpanTile>(a, len[at], cnt[at], group * pl.nodes, group * pl.nodes + pl.nodes - 1);
+  __device__ void look_ahead() {
+    if (b + 1 < a.kv.batch) span_sizes(a, b + 1, false, next_L, next_c);
+  }
+  __device__ SpanTiles tiles_of(int len_, int cnt_, int group) const {
+    return span_tiles<kSpanTile>(a, len_, cnt_, group * pl.nodes, group * pl.nodes + pl.nodes - 1);
   }
   // What group `group` of a request costs, in tiles.
-  __device__ int cost(int at, int group) const {
-    const int n = tiles_of(at, group).n_tiles;
+  __device__ int cost(int len_, int cnt_, int group) const {
+    const int n = tiles_of(len_, cnt_, group).n_tiles;
     return n ? n + kSpanOverhead : 0;
   }
   // Sets the unit that position x < pre[batch] lies in (by a converged warp where a unit has groups of its own).
@@ -115,11 +121,11 @@ struct SpanWalk {
     g = rem / sz;
     u0 = pre[lo] + g * sz;
     u1 = u0 + sz;
-    if (pl.width > 1 || pl.n_groups == 1) return;
+    if (pl.n_groups == 1) return;
     const int lane = threadIdx.x & 31;
     int at = u0;
     for (int r0 = 0;; r0 += 32) {  // 32 groups at a time
-      const int mine = r0 + lane < pl.n_groups ? cost(b, r0 + lane) : 0;
+      const int mine = r0 + lane < pl.n_groups ? cost(len[b], cnt[b], r0 + lane) : 0;
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -137,40 +143,44 @@ struct SpanWalk {
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  // Where team t's share begins; sets the unit there, or the one that ends there.
+  // Where block t's share begins; sets the unit there, or the one that ends there.
   __device__ int cut(int t) {
-    const unsigned total = pre[a.kv.batch], n = min((unsigned)pl.teams, max(1u, total / kSpanMinShare));
+    const unsigned total = pre[a.kv.batch], n = min((unsigned)pl.blocks, max(1u, total / kSpanMinShare));
     if (t >= (int)n || total == 0) return total;
     const unsigned per = total / n, x = per * t + (total - per * n) * t / n;
     locate(x);
     if (!pl.split) return 2 * ((int)x - u0) < u1 - u0 ? u0 : u1;
     return (int)x - u0 < kSpanSnap ? u0 : u1 - (int)x < kSpanSnap ? u1 : (int)x;
   }
-  __device__ int unit() const { return pl.width > 1 ? b * a.kv.h_kv + g : (b * a.kv.h_kv + g) * pl.n_groups + rg; }
+  __device__ int unit() const { return (b * a.kv.h_kv + g) * pl.n_groups + rg; }
   __device__ bool next(SpanSeg &s) {
     if (pos >= end) return false;
     if (pos >= u1) {  // the next unit that costs something
+      u0 = u1;
       do {
-        if (pl.width > 1 || ++rg >= pl.n_groups) {
-          if (pl.width == 1) rg = 0;
+        if (++rg * pl.nodes >= c) {  // (groups behind the queries cost nothing)
+          rg = 0;
           if (++g >= a.kv.h_kv) {
             g = 0;
-            do ++b; while (pre[b + 1] <= pos);
+            do {  // a request that sees something
+              ++b;
+              L = next_L, c = next_c;
+              look_ahead();
+            } while (L == 0 || c == 0);
           }
         }
-        u0 = u1;
-        u1 = u0 + (pl.width > 1 ? size[b] : cost(b, rg));
+        u1 = u0 + cost(L, c, rg);
       } while (u1 == u0);
     }
     s.b = b;
     s.g = g;
     s.rg = rg;
-    s.c = cnt[b];
-    s.st = tiles_of(b, rg);
+    s.c = c;
+    s.st = tiles_of(L, c, rg);
     const int stop = min(u1, end);
     s.k0 = min(max(0, pos - u0 - kSpanOverhead), s.st.n_tiles);
     s.k1 = stop == u1 ? s.st.n_tiles : min(max(0, stop - u0 - kSpanOverhead), s.st.n_tiles);
-    s.part = pos == u0 && stop == u1 ? -1 : (team * 2 + (pos == u0)) * pl.width + (pl.width > 1 ? rg : 0);
+    s.part = pos == u0 && stop == u1 ? -1 : blockIdx.x * 2 + (pos == u0);
     pos = stop;
     return true;
   }
@@ -214,16 +224,32 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 8 x 8 pieces of 16 bytes, lane i of eight with row i: afterwards lane i has column i.
+__device__ __forceinline__ void span_transpose(uint4 (&v)[8], int i) {
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1) {
+    const bool upper = (i & s) != 0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      if (p & s) continue;
+      uint4 out = upper ? v[p] : v[p + s], in;
+      in.x = __shfl_xor_sync(0xffffffffu, out.x, s), in.y = __shfl_xor_sync(0xffffffffu, out.y, s);
+      in.z = __shfl_xor_sync(0xffffffffu, out.z, s), in.w = __shfl_xor_sync(0xffffffffu, out.w, s);
+      if (upper) v[p] = in; else v[p + s] = in;
+    }
+  }
+}
+
 template <int V>
 struct SpanInt {
   static constexpr int value = V;
 };
 
-// Joins a row's parts, team `first`'s slot 1 and slot 0 of the parts - 1 teams behind it: weights 2^(lse - max) over their sum.
-// COLS columns from c0 on of row r of the slots' member y, to row `at` of the output.
+// Joins a row's parts, block `first`'s slot 1 and slot 0 of the parts - 1 blocks behind it: weights 2^(lse - max) over their
+// sum.  COLS columns from c0 on of row r of the slots, to row `at` of the output.
 template <int D, int ROWS, int COLS>
-__device__ __forceinline__ void span_join_row(const SpanArgs &a, const SpanPlan &pl, int first, int parts, int y, int r, int c0, int64_t at) {
-  auto slot = [&](int k) { return (int64_t)(k ? (first + k) * 2 : first * 2 + 1) * pl.width + y; };
+__device__ __forceinline__ void span_join_row(const SpanArgs &a, const SpanPlan &pl, int first, int parts, int r, int c0, int64_t at) {
+  auto slot = [&](int k) { return (int64_t)(k ? (first + k) * 2 : first * 2 + 1); };
   float m = -INFINITY, z = 0.f, o[COLS] = {};
 #pragma unroll 4
   for (int k = 0; k < parts; ++k) m = fmaxf(m, __ldcg(pl.lse + slot(k) * ROWS + r));
@@ -254,7 +280,7 @@ template <int D, bool WIDE>
 __global__ void __launch_bounds__(kSpanThreads, 1)
     span_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap, SpanArgs a, SpanPlan pl) {
   using C = SpanCfg<D, WIDE>;
-  constexpr int NS = C::kStages;
+  constexpr int NK = C::kSlotsK, NV = C::kSlotsV;
   extern __shared__ __align__(1024) char smem_raw[];
   char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(sm);
@@ -263,23 +289,20 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
 
   // K and V slots' full / empty, Q buffers' full / empty, the streams' S full, P's halves full, O done, drain
   const uint32_t bars = sbase + C::kMisc;
-  const uint32_t k_full = bars, k_empty = k_full + 8 * NS, v_full = k_empty + 8 * NS, v_empty = v_full + 8 * NS;
-  const uint32_t q_full = v_empty + 8 * NS, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 32,
+  const uint32_t k_full = bars, k_empty = k_full + 8 * NK, v_full = k_empty + 8 * NK, v_empty = v_full + 8 * NV;
+  const uint32_t q_full = v_empty + 8 * NV, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 32,
                  drained = o_done + 16, group = drained + 16, seg_full = group + 8;
-  int *pre = reinterpret_cast<int *>(sm + C::kMisc + C::kBars * 8);
-  int *s_size = pre + kSpanMaxBatch + 2, *s_len = s_size + kSpanMaxBatch, *s_cnt = s_len + kSpanMaxBatch;
-  float *s_m = reinterpret_cast<float *>(s_cnt + kSpanMaxBatch);  // [segment % 2][maxima, sums][stream][row]
-  SpanSeg *ring = reinterpret_cast<SpanSeg *>(s_m + 1024);
+  SpanSeg *ring = reinterpret_cast<SpanSeg *>(sm + C::kMisc + C::kBars * 8);
+  float *s_m = reinterpret_cast<float *>(ring + kSpanRing);  // [maxima, sums][stream][row]
+  int *pre = reinterpret_cast<int *>(sm + C::kK), *s_size = pre + kSpanMaxBatch + 1, *s_len = s_size + kSpanMaxBatch, *s_cnt = s_len + kSpanMaxBatch;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_scan[kSpanThreads / 32];
 
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(k_full + 8 * i, 1), mbar_init(v_full + 8 * i, 1);
-      mbar_init(k_empty + 8 * i, 1), mbar_init(v_empty + 8 * i, 1);
-    }
+    for (int i = 0; i < NK; ++i) mbar_init(k_full + 8 * i, 1), mbar_init(k_empty + 8 * i, 1);
+    for (int i = 0; i < NV; ++i) mbar_init(v_full + 8 * i, 1), mbar_init(v_empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1), mbar_init(q_empty + 8 * i, WIDE ? 1 : 8);
       mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4), mbar_init(p_full + 16 + 8 * i, 4), mbar_init(o_done + 8 * i, 1), mbar_init(drained + 8 * i, 1);
@@ -314,10 +337,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       const int b = (int)(e / pl.n_groups), group = (int)(e - (unsigned)b * pl.n_groups);
       const int n = span_tiles<kSpanTile>(a, s_len[b], s_cnt[b], group * pl.nodes, group * pl.nodes + pl.nodes - 1).n_tiles;
       if (n == 0) continue;
-      if (pl.width > 1)  // a team walks the most tiles of its groups
-        atomicMax(s_size + b, n + kSpanOverhead);
-      else
-        atomicAdd(s_size + b, n + kSpanOverhead);
+      atomicAdd(s_size + b, n + kSpanOverhead);
     }
     __syncthreads();
   }
@@ -347,6 +367,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       off += mine[k];
       if (b == B - 1) pre[B] = off;
     }
+    fence_proxy_async_smem();  // before the copies into this place
     __syncthreads();
   }
   const uint32_t tm = s_tmem;
@@ -368,7 +389,9 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   if (warp == kSpanProducer) {
     // ---------------------------------------------------------------- loads
     SpanWalk walk(a, pl, pre, s_size, s_len, s_cnt);
-    if (blockIdx.x % pl.width == 0 && lane == 0) pl.cut_unit[walk.team] = walk.inside ? walk.unit() : -1;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) pl.cut_unit[blockIdx.x] = walk.inside ? walk.unit() : -1;
     const int box_rows = min(ps, kSpanTile), boxes = kSpanTile / box_rows;
     const uint64_t pol = a.parents && pl.n_groups == 1 ? policy_evict_first() : policy_evict_normal();
     const int oob = (int)((int64_t)a.kv.num_pages * 2 * h_kv * ps / 8);
@@ -400,8 +423,8 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     };
     // K (w = 0) or V of the block's tile f, tile k of segment s.
     auto load_tile = [&](const SpanSeg &s, int k, int32_t pid, uint32_t f, int w) {
-      const uint32_t slot = f % NS, full = (w ? v_full : k_full) + 8 * slot;
-      ok = __all_sync(0xffffffffu, ok & mbar_wait((w ? v_empty : k_empty) + 8 * slot, ((f / NS) & 1) ^ 1, abort));
+      const uint32_t slots = w ? NV : NK, slot = f % slots, full = (w ? v_full : k_full) + 8 * slot;
+      ok = __all_sync(0xffffffffu, ok & mbar_wait((w ? v_empty : k_empty) + 8 * slot, ((f / slots) & 1) ^ 1, abort));
       if (!ok) return;
       const int t = s.st.tile(k) * kSpanTile + lane * box_rows;
       const bool page_ok = pid >= 0 && (int64_t)pid < a.kv.num_pages;
@@ -413,14 +436,11 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
         tma_load_4d(sbase + (w ? C::kV : C::kK) + slot * C::kTileBytes + (lane * box_rows >> 3) * C::kGroup, &kvmap, 0, 0, 0, row8, full, pol);
       __syncwarp();
     };
-    // Publishes the next segment that has tiles.
+    // Publishes the next segment.
     int published = 0;
     auto next_segment = [&]() -> const SpanSeg * {
       SpanSeg x;
-      bool more;
-      while ((more = walk.next(x)) && x.k0 >= x.k1) {  // (a group that sees less than its team walks)
-        for (int r = lane; x.part >= 0 && r < C::kRows; r += 32) pl.lse[(int64_t)x.part * C::kRows + r] = -INFINITY;
-      }
+      const bool more = walk.next(x);
       SpanSeg *to = ring + published % kSpanRing;
       if (!more) x.b = -1;
       if (lane == 0) {
@@ -463,10 +483,8 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     pdl_trigger();
     if (!ok && lane == 0) {  // every copy in flight lands before the block's memory is released
       volatile int never = 0;
-      for (uint32_t i = f > (uint32_t)NS ? f - NS : 0; i <= f; ++i) {
-        mbar_wait(k_full + 8 * (i % NS), (i / NS) & 1, &never, 200000000ll);
-        mbar_wait(v_full + 8 * (i % NS), (i / NS) & 1, &never, 200000000ll);
-      }
+      for (uint32_t i = f > (uint32_t)NK ? f - NK : 0; i <= f; ++i) mbar_wait(k_full + 8 * (i % NK), (i / NK) & 1, &never, 200000000ll);
+      for (uint32_t i = f > (uint32_t)NV ? f - NV : 0; i <= f; ++i) mbar_wait(v_full + 8 * (i % NV), (i / NV) & 1, &never, 200000000ll);
     }
     __syncwarp();
   } else if (warp == kSpanMma || warp == kSpanMma + 1) {
@@ -517,13 +535,27 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     auto clear_unseen = [&](int hi, int sink, int lo, int t0, int slot) {
       if (t0 + kSpanTile <= hi && (t0 + kSpanTile <= sink || t0 >= lo || sink >= lo)) return;
       constexpr int CPR = D / 8;  // 16-byte pieces of a row
-      char *v = sm + C::kV + slot * C::kTileBytes + ((lane % CPR) >> 3) * 1024 + (lane % CPR & 7) * 16;
+      char *v = sm + C::kV + slot * C::kTileBytes;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      auto rows = [&](int r0, int r1) {  // at most a group's
+        const int c = lane % CPR;
+#pragma unroll 1
+        for (int r = r0 + lane / CPR; r < r1; r += 32 / CPR)
+          *reinterpret_cast<uint4 *>(v + (r >> 3) * C::kGroup + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16) = zero;
+      };
+      auto range = [&](int r0, int r1) {
+        if (r0 >= r1) return;
+        const int g0 = (r0 + 7) & ~7, g1 = r1 & ~7;
+        if (g0 > g1) return rows(r0, r1);
+        rows(r0, g0);
+        uint4 *at = reinterpret_cast<uint4 *>(v + (g0 >> 3) * C::kGroup) + lane;  // whole groups lie together
+        for (int g = g0; g < g1; g += 8, at += C::kGroup / 16)
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const int r0 = max(0, (w ? sink : hi) - t0), r1 = w ? min(kSpanTile, min(lo, hi) - t0) : kSpanTile;
-#pragma unroll 4
-        for (int r = r0 + lane / CPR; r < r1; r += 32 / CPR) *reinterpret_cast<uint4 *>(v + (r >> 3) * C::kGroup + (r & 7) * 128) = make_uint4(0, 0, 0, 0);
-      }
+          for (int e = 0; e < C::kGroup / 512; ++e) at[32 * e] = zero;
+        rows(g1, r1);
+      };
+      range(max(0, hi - t0), kSpanTile);
+      range(max(0, sink - t0), min(kSpanTile, min(lo, hi) - t0));
       fence_proxy_async_smem();
       __syncwarp();
     };
@@ -534,21 +566,21 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       for (int j = 0; (sp = segment(j)); ++j) {
         const SpanSeg seg = *sp;
         const int streams = second(seg) ? 2 : 1;
-        mbar_wait(k_full + 8 * (f % NS), (f / NS) & 1, abort);
+        mbar_wait(k_full + 8 * (f % NK), (f / NK) & 1, abort);
         for (int s = 0; s < streams; ++s) {
           mbar_wait(q_full + 8 * s, q_uses[s]++ & 1, abort);
           tc_fence_after();
-          issue_qk(s, s, f % NS, s == streams - 1, seg.k1 - seg.k0 == 1);
+          issue_qk(s, s, f % NK, s == streams - 1, seg.k1 - seg.k0 == 1);
         }
         for (int k = seg.k0; k < seg.k1; ++k, ++f) {
-          const int slot = f % NS, nslot = (f + 1) % NS;
-          mbar_wait(v_full + 8 * slot, (f / NS) & 1, abort);
+          const int slot = f % NV, nslot = (f + 1) % NK;
+          mbar_wait(v_full + 8 * slot, (f / NV) & 1, abort);
           clear_unseen(seg.st.hi, seg.st.sink, seg.st.lo, seg.st.tile(k) * kSpanTile, slot);
           for (int s = 0; s < streams; ++s) {
             issue_pv(s, n[s]++, slot, k == seg.k0, s == streams - 1);
             if (k + 1 < seg.k1) {
               if (s == 0) {
-                mbar_wait(k_full + 8 * nslot, ((f + 1) / NS) & 1, abort);
+                mbar_wait(k_full + 8 * nslot, ((f + 1) / NK) & 1, abort);
                 tc_fence_after();
               }
               issue_qk(s, s, nslot, s == streams - 1, k + 2 == seg.k1);
@@ -567,11 +599,11 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
         bool first = true;
         for (int k = seg.k0; k < seg.k1; ++k, ++f) {
           if ((f & 1) != (uint32_t)s) continue;
-          const int slot = f % NS;
-          mbar_wait(k_full + 8 * slot, (f / NS) & 1, abort);
+          const int slot = f % NV;
+          mbar_wait(k_full + 8 * (f % NK), (f / NK) & 1, abort);
           tc_fence_after();
-          issue_qk(s, j & 1, slot, true, false);
-          mbar_wait(v_full + 8 * slot, (f / NS) & 1, abort);
+          issue_qk(s, j & 1, f % NK, true, false);
+          mbar_wait(v_full + 8 * slot, (f / NV) & 1, abort);
           clear_unseen(seg.st.hi, seg.st.sink, seg.st.lo, seg.st.tile(k) * kSpanTile, slot);
           issue_pv(s, n++, slot, first, true);
           first = false;
@@ -589,7 +621,9 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     // ---------------------------------------------------------------- softmax, O
     // Rows that see nothing; a request's are shared by every B-th block.
     for (int b = blockIdx.x % B; b < B; b += gridDim.x) {
-      const int c = s_cnt[b], below = min(max(0, c - s_len[b]), c);  // queries [0, below) and [c, n)
+      int L, c;
+      span_sizes(a, b, false, L, c);
+      const int below = min(max(0, c - L), c);  // queries [0, below) and [c, n)
       const int rows = below + a.n - c, sharers = max(1, cdiv((int)gridDim.x - b, B));
       for (int64_t e = (blockIdx.x / B) * 256 + tid; e < (int64_t)rows * a.h_q * (D / 8); e += sharers * 256) {
         const int64_t r = e / (D / 8);
@@ -637,10 +671,14 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
           tmem_ld_wait();
           const int t0 = seg.st.tile(k) * kSpanTile, t1 = t0 + kSpanTile;
           if (t1 > all_to || !(t0 >= all_from || t1 <= a.sink)) {
-            uint32_t m[4] = {0u, 0u, 0u, 0u};
+            uint32_t m[4] = {~0u, ~0u, ~0u, ~0u};  // (rows without a query: anything)
             if (valid) span_mask<4>(a, parents, seg.st.base, i, t0, a.status, m);
 #pragma unroll
-            for (int e = 0; e < 128; ++e) x[e] = (m[e >> 5] >> (e & 31) & 1u) ? x[e] : -INFINITY;
+            for (int w = 0; w < 4; ++w)  // (most words of a border's tile are whole for the warp)
+              if (__any_sync(0xffffffffu, m[w] != 0xffffffffu)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[32 * w + e] = (m[w] >> e & 1u) ? x[32 * w + e] : -INFINITY;
+              }
           }
           float mx[4];
 #pragma unroll
@@ -730,7 +768,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       };
       if constexpr (WIDE) {
         const float f = 1.f / l;
-        if (warp_valid) {
+        if (warp_valid && part) {
 #pragma unroll 2
           for (int q = 0; q < D / 32; ++q) {
             float o[32];
@@ -741,18 +779,43 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
             put(o, 32 * q);
             put(o + 16, 32 * q + 16);
           }
+        } else if (warp_valid) {
+          // Eight lanes exchange 16-byte pieces of their rows so that a store covers 128 bytes of four rows (16 bytes of 32
+          // rows took 7300 clocks a segment).
+          const int mine = lane & 7;
+          const unsigned good = __ballot_sync(0xffffffffu, valid);
+          __nv_bfloat16 *rows[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) rows[k] = static_cast<__nv_bfloat16 *>(a.out) + __shfl_sync(0xffffffffu, at, (lane & 24) + k) * D + mine * 8;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 64) {
+            uint4 v[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float o[32];
+              tmem_ld32(col_o + c0 + 32 * q, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[4 * q + e] = make_uint4(pack_bf16(o[8 * e] * f, o[8 * e + 1] * f), pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f),
+                                          pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f), pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f));
+            }
+            span_transpose(v, mine);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (good >> ((lane & 24) + k) & 1) *reinterpret_cast<uint4 *>(rows[k] + c0) = v[k];
+          }
         }
       } else {
         // Each stream ends half of the columns and passes its share of the others on through the segment's Q buffer, whose
         // products are done by then: in one step, or with more than 64 rows in two.
         float *boxes = reinterpret_cast<float *>(sm + C::kQ + (j & 1) * C::kTileBytes);
-        float *my_m = s_m + (j & 1) * 512;  // [stream][row], and the sums behind them
-        my_m[s * 128 + row] = have ? mref : -INFINITY;
-        my_m[256 + s * 128 + row] = have ? l : 0.f;
+        s_m[s * 128 + row] = have ? mref : -INFINITY;
+        s_m[256 + s * 128 + row] = have ? l : 0.f;
         sync_streams();
-        const float m_two = my_m[(1 - s) * 128 + row], m = fmaxf(my_m[s * 128 + row], m_two), ref = m == -INFINITY ? 0.f : m;
+        const float m_two = s_m[(1 - s) * 128 + row], m = fmaxf(s_m[s * 128 + row], m_two), ref = m == -INFINITY ? 0.f : m;
         float f0 = have ? fast_exp2(mref - ref) : 0.f, f1 = fast_exp2(m_two - ref);
-        l = (have ? l : 0.f) * f0 + my_m[256 + (1 - s) * 128 + row] * f1;
+        l = (have ? l : 0.f) * f0 + s_m[256 + (1 - s) * 128 + row] * f1;
         mref = m;
         const float f = 1.f / l;
         f0 *= f, f1 *= f;
@@ -812,25 +875,25 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   if (warp == kSpanMma) tmem_dealloc(tm, 512);
 }
 
-// Joins the parts of the units that teams share.  Blocks (team, group, 32 rows; a warp per D / 8 columns): the one of the first team that begins inside
-// a unit has that unit; its parts are the team before's slot 1 and slot 0 of every team that begins inside it.
+// Joins the parts of the units that blocks share.  Blocks (block, 32 rows; a warp per D / 8 columns): the one of the first that begins inside
+// a unit has that unit; its parts are slot 1 of the block before and slot 0 of every block that begins inside it.
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(256) span_join_kernel(SpanArgs a, SpanPlan pl) {
   using C = SpanCfg<D, WIDE>;
   constexpr int COLS = D / 8;  // of a warp
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = blockIdx.x, r = blockIdx.z * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x, r = blockIdx.y * 32 + lane;
   pdl_wait();
   pdl_trigger();
-  const int unit = pl.cut_unit[team];
-  if (unit < 0 || (team > 0 && pl.cut_unit[team - 1] == unit)) return;
-  int parts = 1;  // the team before's, and those that follow
-  for (int t0 = team;; t0 += 32) {
-    const bool same = t0 + lane < pl.teams && pl.cut_unit[t0 + lane] == unit;
+  const int unit = pl.cut_unit[first];
+  if (unit < 0 || (first > 0 && pl.cut_unit[first - 1] == unit)) return;
+  int parts = 1;  // the block before's, and those that follow
+  for (int t0 = first;; t0 += 32) {
+    const bool same = t0 + lane < pl.blocks && pl.cut_unit[t0 + lane] == unit;
     const unsigned m = __ballot_sync(0xffffffffu, same);
     parts += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
     if (m != 0xffffffffu) break;
   }
-  const int rg = pl.width > 1 ? blockIdx.y : unit % pl.n_groups, bg = pl.width > 1 ? unit : unit / pl.n_groups;
+  const int rg = unit % pl.n_groups, bg = unit / pl.n_groups;
   const int b = bg / a.kv.h_kv, g = bg % a.kv.h_kv;
   int L, c;
   span_sizes(a, b, false, L, c);
@@ -838,7 +901,7 @@ __global__ void __launch_bounds__(256) span_join_kernel(SpanArgs a, SpanPlan pl)
   const int i = rg * pl.nodes + s * row_nodes + node;
   if (node >= row_nodes || i >= c || L - c + i < 0) return;
   const int64_t at = ((int64_t)b * a.n + i) * a.h_q + g * a.G + ((r & 127) - node * a.G);
-  span_join_row<D, C::kRows, COLS>(a, pl, team - 1, parts, blockIdx.y, r, warp * COLS, at);
+  span_join_row<D, C::kRows, COLS>(a, pl, first - 1, parts, r, warp * COLS, at);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -859,16 +922,11 @@ static int64_t span_most_tiles(const ssd_paged_kv *kv, const SpanArgs &a, const 
 
 static SpanPlan span_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
   SpanPlan p = {};
-  const int streams = span_wide(a) ? 2 : 1, sms = sm_count(), batch = kv->batch < kSpanMaxBatch ? kv->batch : kSpanMaxBatch;
-  p.n_groups = cdiv(a.n, streams * (kSpanTile / a.G));
-  p.row_nodes = cdiv(a.n, streams * p.n_groups);  // even groups
+  const int streams = span_wide(a) ? 2 : 1;
+  p.row_nodes = a.n < kSpanTile / a.G ? a.n : kSpanTile / a.G;
   p.nodes = streams * p.row_nodes;
-  // Teams where the groups of a unit see the same long stretch of tokens, or too few units would be left to share out.
-  const bool together = a.window >= 8192 || (int64_t)batch * kv->h_kv * p.n_groups < 2 * sms;
-  p.width = together && p.n_groups <= 32 ? p.n_groups : 1;
-  p.teams = sms / p.width;
-  // A unit's tiles, at most; short ones stay whole, which saves the join's launch (17 requests of up to 33 queries with a window
-  // of 301: 20.1 us cut, 17.1 whole).
+  p.n_groups = cdiv(a.n, p.nodes);
+  p.blocks = sm_count();
   p.split = span_most_tiles(kv, a, p) > kSpanWhole;
   return p;
 }
@@ -876,8 +934,8 @@ static SpanPlan span_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
 static size_t span_carve(const ssd_paged_kv *kv, SpanPlan &p, bool wide, void *ws) {
   Carver c(ws);
   c.take<char>(kCounterBytes);
-  const size_t rows = (size_t)p.teams * 2 * p.width * (wide ? 256 : 128);
-  p.cut_unit = c.take<int32_t>(p.teams);
+  const size_t rows = (size_t)p.blocks * 2 * (wide ? 256 : 128);
+  p.cut_unit = c.take<int32_t>(p.blocks);
   p.o = c.take<float>(rows * kv->d);
   p.lse = c.take<float>(rows);
   return c.off;
@@ -895,9 +953,9 @@ static int span_tc_launch(const CUtensorMap &kvmap, const CUtensorMap &qmap, con
   static_assert(smem <= 227 * 1024, "a block's shared memory");
   int rc = ensure_smem<kernel>(smem);
   if (rc) return rc;
-  if ((rc = launch(kernel, dim3(p.teams * p.width), dim3(kSpanThreads), smem, st, "span_tc_kernel", kvmap, qmap, a, p)) || !p.split || p.teams < 2) return rc;
+  if ((rc = launch(kernel, dim3(p.blocks), dim3(kSpanThreads), smem, st, "span_tc_kernel", kvmap, qmap, a, p)) || !p.split) return rc;
   const int rows = (WIDE ? 128 : 0) + p.row_nodes * a.G;  // (stream 1's behind 128 of stream 0's)
-  return launch(span_join_kernel<D, WIDE>, dim3(p.teams, p.width, cdiv(rows, 32)), dim3(256), 0, st, "span_join_kernel", a, p);
+  return launch(span_join_kernel<D, WIDE>, dim3(p.blocks, cdiv(rows, 32)), dim3(256), 0, st, "span_join_kernel", a, p);
 }
 
 int span_tc(const ssd_paged_kv *kv, const SpanArgs &args, void *workspace, cudaStream_t st) {
