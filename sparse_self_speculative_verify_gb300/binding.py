@@ -671,6 +671,17 @@ class KV4Cache:
         return self._ref
 
 
+_empty = torch.empty
+
+
+def _output(t, name: str, dtype, device: int, shape):
+    """(tensor, address) of an output: the caller's, checked, or a new one."""
+    if t is None:
+        t = _empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _shaped(t, name, dtype, device, shape)
+
+
 _TYPES = {torch.float32: SSD_DTYPE_F32, torch.bfloat16: SSD_DTYPE_BF16}
 _HERE = contextlib.nullcontext()
 _Tensor = torch.Tensor
@@ -994,12 +1005,10 @@ def _span_attn(kv, q, parents, counts, window, sink, scale, out, lse, want_lse, 
     pp = None if window is not None else _shaped(parents, "parents", torch.int32, dev, (B, n))
     pc = _maybe(counts, "counts", torch.int32, dev, (B,))
     with _scope(dev, stream):
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=dev)
-        if lse is None and want_lse:
-            lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
-        po = _shaped(out, "out", dtype, dev, shape)
-        pl = _maybe(lse, "lse", torch.float32, dev, shape[:3])
+        out, po = _output(out, "out", dtype, dev, shape)
+        pl = None
+        if lse is not None or want_lse:
+            lse, pl = _output(lse, "lse", torch.float32, dev, shape[:3])
         if B:
             L = _lib()
             key = (h_q, n, window, sink)
@@ -1060,21 +1069,14 @@ def ssd_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = No
         raise ValueError(f"top_k {top_k} outside [0, {V}]")
     with _scope(dev, stream):
         f32, i32 = torch.float32, torch.int32
-        if logprob is None and tokens is not None:
-            logprob = torch.empty(tokens.shape, dtype=f32, device=dev)
-        if lse is None:
-            lse = torch.empty((N,), dtype=f32, device=dev)
-        if entropy is None:
-            entropy = torch.empty((N,), dtype=f32, device=dev)
-        if top_k and top_ids is None:
-            top_ids = torch.empty((N, top_k), dtype=i32, device=dev)
-        if top_k and top_logprobs is None:
-            top_logprobs = torch.empty((N, top_k), dtype=f32, device=dev)
-        pg = None if tokens is None else _shaped(logprob, "logprob", f32, dev, tokens.shape)
-        pl = _shaped(lse, "lse", f32, dev, (N,))
-        pe = _shaped(entropy, "entropy", f32, dev, (N,))
-        pi = _maybe(top_ids, "top_ids", i32, dev, (N, top_k))
-        pv = _maybe(top_logprobs, "top_logprobs", f32, dev, (N, top_k))
+        pg = pi = pv = None
+        if tokens is not None:
+            logprob, pg = _output(logprob, "logprob", f32, dev, tokens.shape)
+        lse, pl = _output(lse, "lse", f32, dev, (N,))
+        entropy, pe = _output(entropy, "entropy", f32, dev, (N,))
+        if top_k:
+            top_ids, pi = _output(top_ids, "top_ids", i32, dev, (N, top_k))
+            top_logprobs, pv = _output(top_logprobs, "top_logprobs", f32, dev, (N, top_k))
         if N or M:
             _check(_lib().ssd_token_logprobs(logits.data_ptr(), dt, logits.stride(0), N, V, pt, pr, M, pg, pl, pe, pi, pv, top_k,
                                              _raw_stream(dev)))
@@ -1109,16 +1111,10 @@ def ssd_tree_accept(parents: torch.Tensor, tokens: Optional[torch.Tensor], targe
     if m < 1:
         raise ValueError(f"max_path {m} < 1")
     with _scope(dev, stream):
-        if path is None:
-            path = torch.empty((B, m), dtype=i32, device=dev)
-        if cnt is None:
-            cnt = torch.empty((B,), dtype=i32, device=dev)
-        if next is None:
-            next = torch.empty((B,), dtype=i32, device=dev)
-        if advance is None:
-            advance = torch.empty((B,), dtype=i32, device=dev)
-        ph = _shaped(path, "path", i32, dev, (B, m))
-        pk, pn, pa = _shaped(cnt, "cnt", i32, dev, (B,)), _shaped(next, "next", i32, dev, (B,)), _shaped(advance, "advance", i32, dev, (B,))
+        path, ph = _output(path, "path", i32, dev, (B, m))
+        cnt, pk = _output(cnt, "cnt", i32, dev, (B,))
+        next, pn = _output(next, "next", i32, dev, (B,))
+        advance, pa = _output(advance, "advance", i32, dev, (B,))
         if B:
             _check(_lib().ssd_tree_accept(pp, pt, pg, pl, pe, float(epsilon), float(delta), pc, B, n, m, ph, pk, pn, pa, _raw_stream(dev)))
     return {"path": path, "cnt": cnt, "next": next, "advance": advance}

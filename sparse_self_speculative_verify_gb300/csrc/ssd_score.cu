@@ -2,16 +2,33 @@
 //
 // One pass over a row.  Every thread keeps m = max x, s = sum e^(x - m), t = sum (x - m) e^(x - m) of its elements; joined over
 // the row they give  lse = m + ln s  and  entropy = ln s - t / s  (no term is larger than the entropy itself).  The top k
-// need no second pass over the row: the k-th largest of 128 maxima over groups of four threads is a bound that k elements
-// reach, and only the threads whose own maximum reaches it read their elements again (about k of 512, from L2).
+// need no second pass over the row: the k-th largest of 128 to 256 maxima over groups of threads is a bound that k elements
+// reach, and only the threads whose own maximum reaches it read elements again: those of the stage that held it, or all of theirs
+// where another stage's maximum reaches it too.
+// A cluster of 1 to 8 blocks takes a row, by distributed shared memory: sums and group maxima are read by the others, candidates
+// are pushed into the first block's list.
+//
+// What bounds it: the bytes of the logits.  A warp of its own brings them to shared memory by bulk copies, two stages of 8 KB
+// a block and eight blocks an SM (loads into registers, taken and used in turn by the same threads, kept half as much in flight:
+// 512 rows of 151936 bf16 took 44 us, 3.5 TB/s).
+#include <cooperative_groups.h>
+
 #include "ssd_host.h"
+#include "ssd_sm100.cuh"
 
 namespace ssd {
+namespace cg = cooperative_groups;
+using namespace sm100;
 
-constexpr int kScoreThreads = 512;
-constexpr int kScoreGroups = 128;  // maxima that bound the k-th largest from below
+constexpr int kScoreThreads = 128;  // and a warp that loads
+constexpr int kScoreBlocks = 8;     // of an SM
+constexpr int kScoreVectors = 4, kScoreStages = 2, kScoreStage = kScoreThreads * 16 * kScoreVectors;  // vectors of a thread; bytes
+// A thread's reference follows its maximum only when that has grown by this.
+constexpr float kScoreLazy = 4.f;
+constexpr int kScoreGroups = 256;  // most maxima that bound the k-th largest from below
+constexpr int kScoreFused = 4096;  // tokens of chosen rows that the rows' blocks look for themselves
 constexpr int kScoreMaxK = 64;
-constexpr int kScoreCand = 1024;   // candidates for the top k; more: score_ties
+constexpr int kScoreCand = 512;    // candidates for the top k; more: score_ties
 
 struct ScoreArgs {
   const void *logits;
@@ -57,34 +74,76 @@ struct ScoreSums {
   }
 };
 
+// Where m is within this, x - m of any finite x (clamped to kScoreLow) is finite.
+constexpr float kScoreFar = 1e36f, kScoreLow = -3e38f;
+
+template <int V>
+struct ScoreInt {
+  static constexpr int value = V;
+};
+
+// 16 bytes of logits.
 template <typename T>
-struct ScoreVec;  // 16 bytes of logits
+struct ScoreVec;
 template <>
 struct ScoreVec<float> {
   static constexpr int N = 4;
+  __device__ static float max(const uint4 &v) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
   __device__ static void get(const uint4 &v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+  }
+  // with -inf (and what is as far off) as a number, NaN kept
+  __device__ static void get_finite(const uint4 &v, float (&x)[4]) {
+    get(v, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = max_nan(x[i], kScoreLow);
   }
 };
 template <>
 struct ScoreVec<__nv_bfloat16> {
   static constexpr int N = 8;
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ static float max(const uint4 &v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+  }
   __device__ static void get(const uint4 &v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
   }
+  __device__ static void get_finite(const uint4 &v, float (&x)[8]) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(w[i]), "r"(0xff61ff61u));  // about kScoreLow
+    get(make_uint4(w[0], w[1], w[2], w[3]), x);
+  }
 };
 
+// Unsigned keys in the order of the floats.
+__device__ __forceinline__ uint32_t score_key(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
 // (value, index) before (value2, index2) in the order of the top.
 __device__ __forceinline__ bool score_before(float v, int i, float v2, int i2) { return v > v2 || (v == v2 && i < i2); }
 
 struct ScoreSmem {
-  float gmax[kScoreGroups];
+  char stage[kScoreStages][kScoreStage];
+  uint64_t full[kScoreStages], empty[kScoreStages];
+  int abort;
+  float own[kScoreThreads];  // maxima over groups of threads
   float val[kScoreCand];
   int idx[kScoreCand];
   float wm[kScoreThreads / 32], ws[kScoreThreads / 32], wt[kScoreThreads / 32];
-  int count, hits, hit[kScoreThreads];
+  float sums[3];  // of this block's slice
+  int count, hits, full_hits, hit[kScoreThreads];
   float tau, m, lns;
   float best_v[kScoreThreads / 32];
   int best_i[kScoreThreads / 32];
@@ -109,12 +168,15 @@ struct ScoreRow {
 
 // The top k where more than kScoreCand elements reach the bound (ties, or fewer than k above -inf): k times the next
 // largest.  Reads the row up to k times; rows like these hold mostly equal values.
+// Barrier of the threads that are not the loading warp's.
+__device__ __forceinline__ void score_sync() { named_sync(1, kScoreThreads); }
+
 template <typename T>
 __device__ void score_ties(const ScoreArgs &a, const ScoreRow<T> &row, ScoreSmem &sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float pv = INFINITY;
   int pi = -1;
-  __syncthreads();
+  score_sync();
   for (int k = 0; k < a.k; ++k) {
     float bv = 0.f;
     int bi = -1;
@@ -129,19 +191,19 @@ __device__ void score_ties(const ScoreArgs &a, const ScoreRow<T> &row, ScoreSmem
       if (i >= 0 && (bi < 0 || score_before(v, i, bv, bi))) bv = v, bi = i;
     }
     if (lane == 0) sm.best_v[warp] = bv, sm.best_i[warp] = bi;
-    __syncthreads();
+    score_sync();
     bv = sm.best_v[0], bi = sm.best_i[0];
     for (int w = 1; w < kScoreThreads / 32; ++w)
       if (sm.best_i[w] >= 0 && (bi < 0 || score_before(sm.best_v[w], sm.best_i[w], bv, bi))) bv = sm.best_v[w], bi = sm.best_i[w];
     pv = bv, pi = bi;
-    __syncthreads();
+    score_sync();
     if (tid == 0) sm.val[k] = bi < 0 ? -INFINITY : bv, sm.idx[k] = bi;
     if (bi < 0) {  // only NaN is left
       for (int j = k + tid; j < a.k; j += kScoreThreads) sm.val[j] = -INFINITY, sm.idx[j] = -1;
       break;
     }
   }
-  __syncthreads();
+  score_sync();
 }
 
 // ln softmax of x in a row with maximum m and ln of the sum lns (or m = the log-sum-exp and lns = 0).
@@ -149,106 +211,269 @@ __device__ __forceinline__ float score_logprob(float x, float m, float lns) {
   return x == -INFINITY && m + lns == m + lns ? -INFINITY : (x - m) - lns;
 }
 
+// What a token outside the vocabulary or a row outside the logits gets.
+__device__ __forceinline__ bool score_bad(const ScoreArgs &a, int tok) {
+  if (tok >= 0 && tok < a.vocab) return false;
+  atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
+  return true;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
+__global__ void __launch_bounds__(kScoreThreads + 32, kScoreBlocks) score_kernel(ScoreArgs a) {
   constexpr int N = ScoreVec<T>::N;
-  __shared__ ScoreSmem sm;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x;
+  extern __shared__ __align__(16) char smem_raw[];
+  ScoreSmem &sm = *reinterpret_cast<ScoreSmem *>(smem_raw);
+  auto cluster = cg::this_cluster();
+  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x / ranks;
+  if (tid == 0) {
+    sm.count = sm.hits = sm.full_hits = sm.abort = 0, sm.tau = -INFINITY;
+    for (int i = 0; i < kScoreStages; ++i) mbar_init(smem_u32(sm.full + i), 1), mbar_init(smem_u32(sm.empty + i), kScoreThreads / 32);
+    mbar_init_fence();
+  }
+  __syncthreads();
   pdl_wait();
   const ScoreRow<T> row(a, r);
+  const int v0 = (int)((int64_t)row.nv * rank / ranks), v1 = (int)((int64_t)row.nv * (rank + 1) / ranks);
   ScoreSums u = {-3.402823466e38f, 0.f, 0.f};
-  float top = -INFINITY;  // largest element
-  auto take = [&](const uint4 &v) {
-    float x[N];
-    ScoreVec<T>::get(v, x);
-    float mx = x[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) mx = fmaxf(mx, x[i]);
-    if (mx > top) {
-      top = mx;
-      if (mx > u.m) u.move(mx);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) u.add(x[i]);
+  uint64_t s2 = 0, t2 = 0;  // sums of even and odd elements, relative to u.m too
+  float top = -INFINITY, next = -INFINITY;  // largest element, and the largest of the other stages
+  int top_stage = 0;
+  const uint64_t log2e2 = pack2(kLog2e, kLog2e);
+  auto fold = [&]() {
+    float p, q;
+    unpack2(s2, p, q);
+    u.s += p + q;
+    unpack2(t2, p, q);
+    u.t += p + q;
+    s2 = t2 = 0;
   };
-  constexpr int U = 4;
-  int v = tid;
-  for (; v + (U - 1) * kScoreThreads < row.nv; v += U * kScoreThreads) {
-    uint4 w[U];
+  bool near = false;        // |u.m| is within kScoreFar
+  float limit = u.m;        // a maximum above it moves the reference
+  auto far = [&](uint4 v) {  // (the vector turns, so that its words are taken from one place)
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      if (N == 4) {
+        u.add(__uint_as_float(v.x));
+      } else {
+        u.add(bf16_lo(v.x));
+        u.add(bf16_hi(v.x));
+      }
+      v = make_uint4(v.y, v.z, v.w, v.x);
+    }
+  };
+  auto take = [&](const uint4 *v, auto count) {
+    constexpr int C = decltype(count)::value;
+    float mx = ScoreVec<T>::max(v[0]);
 #pragma unroll
-    for (int i = 0; i < U; ++i) w[i] = row.vec(v + i * kScoreThreads);
+    for (int q = 1; q < C; ++q) mx = fmaxf(mx, ScoreVec<T>::max(v[q]));
+    if (mx > limit) {
+      fold();
+      u.move(mx);
+      limit = mx + kScoreLazy;
+      near = fabsf(mx) < kScoreFar;
+    }
+    if (near) {
+      const uint64_t m2 = pack2(-u.m, -u.m);
 #pragma unroll
-    for (int i = 0; i < U; ++i) take(w[i]);
+      for (int q = 0; q < C; ++q) {
+        float x[N];
+        ScoreVec<T>::get_finite(v[q], x);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const uint64_t z = add2(pack2(x[i], x[i + 1]), m2);
+          float y0, y1;
+          unpack2(mul2(z, log2e2), y0, y1);
+          const uint64_t e = pack2(fast_exp2(y0), fast_exp2(y1));
+          s2 = add2(s2, e);
+          t2 = fma2(z, e, t2);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < C; ++q) far(v[q]);
+    }
+    return mx;
+  };
+  // A stage: kScoreStage bytes of the slice's vectors; the loading warp goes to the next barrier at once.
+  constexpr int PER = kScoreStage / 16;
+  const int stages = cdiv(v1 - v0, PER);
+  volatile int *abort = &sm.abort;
+  if (warp == kScoreThreads / 32) {
+    if (lane == 0) {
+      int i = 0;
+      for (; i < stages; ++i) {
+        const int st = i % kScoreStages, bytes = min(PER, v1 - v0 - i * PER) * 16;
+        if (!mbar_wait(smem_u32(sm.empty + st), (i / kScoreStages & 1) ^ 1, abort)) break;
+        mbar_arrive_expect_tx(smem_u32(sm.full + st), bytes);
+        bulk_load(smem_u32(sm.stage[st]), reinterpret_cast<const char *>(row.x + row.head) + ((int64_t)v0 + (int64_t)i * PER) * 16, bytes,
+                  smem_u32(sm.full + st));
+      }
+      volatile int never = 0;  // (a wait ran out: the copies in flight land before the block ends)
+      for (int j = max(0, i - kScoreStages); i < stages && j < i; ++j)
+        mbar_wait(smem_u32(sm.full + j % kScoreStages), j / kScoreStages & 1, &never, 200000000ll);
+    }
+    __syncwarp();
+  } else {
+    for (int i = 0; i < stages; ++i) {
+      const int st = i % kScoreStages, n = min(PER, v1 - v0 - i * PER);
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(sm.full + st), i / kScoreStages & 1, abort))) break;
+      const uint4 *from = reinterpret_cast<const uint4 *>(sm.stage[st]) + tid;
+      uint4 w[kScoreVectors];
+      float mx = -INFINITY;
+      if (n == PER) {
+#pragma unroll
+        for (int q = 0; q < kScoreVectors; ++q) w[q] = from[q * kScoreThreads];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(sm.empty + st));
+        mx = take(w, ScoreInt<kScoreVectors>{});
+      } else {  // (the last stage: nobody waits for its place)
+#pragma unroll 1
+        for (int q = tid; q < n; q += kScoreThreads) {
+          w[0] = reinterpret_cast<const uint4 *>(sm.stage[st])[q];
+          mx = fmaxf(mx, take(w, ScoreInt<1>{}));
+        }
+      }
+      next = fmaxf(next, fminf(top, mx));
+      if (mx > top) top = mx, top_stage = i;
+    }
   }
-  for (; v < row.nv; v += kScoreThreads) take(row.vec(v));
-  const int n_edge = row.head + row.tail;
+  fold();
+  const int n_edge = rank == 0 ? row.head + row.tail : 0;
+  float edge = -INFINITY;
   if (tid < n_edge) {
-    const float x = to_f32<T>(row.x[row.edge(tid)]);
-    top = fmaxf(top, x);
-    if (x > u.m) u.move(x);
-    u.add(x);
+    edge = to_f32<T>(row.x[row.edge(tid)]);
+    if (edge > u.m) u.move(edge);
+    u.add(edge);
   }
   pdl_trigger();
-  // The row's sums.
+  // The slice's sums, and the maxima over groups of `per` threads: 128, 64 or 32 of a block.
   {
     ScoreSums w = u;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       w.join(__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.s, o), __shfl_xor_sync(0xffffffffu, w.t, o));
-    if (lane == 0) sm.wm[warp] = w.m, sm.ws[warp] = w.s, sm.wt[warp] = w.t;
+    if (lane == 0 && warp < kScoreThreads / 32) sm.wm[warp] = w.m, sm.ws[warp] = w.s, sm.wt[warp] = w.t;
   }
-  float g = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-  if ((tid & 3) == 0) sm.gmax[tid >> 2] = g;
-  if (tid == 0) sm.count = sm.hits = 0, sm.tau = -INFINITY;
+  const int per = min(ranks, 4), groups = kScoreThreads / per;
+  float g = fmaxf(top, edge);
+  for (int o = 1; o < per; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+  if (tid < kScoreThreads && tid % per == 0) sm.own[tid / per] = g;
   __syncthreads();
-  if (tid == 0) {
-    ScoreSums w = {sm.wm[0], sm.ws[0], sm.wt[0]};
-    for (int i = 1; i < kScoreThreads / 32; ++i) w.join(sm.wm[i], sm.ws[i], sm.wt[i]);
-    const float lns = logf(w.s);  // -inf: nothing but -inf
-    sm.m = w.m;
-    sm.lns = lns;
-    a.lse[r] = w.m + lns;
-    if (a.entropy) a.entropy[r] = w.s == 0.f ? 0.f : lns - w.t / w.s;
-  }
-  if (a.k && tid < kScoreGroups) {
-    const float mine = sm.gmax[tid];
-    int rank = 0;
-    for (int j = 0; j < kScoreGroups; ++j) rank += score_before(sm.gmax[j], j, mine, tid);
-    if (rank == a.k - 1) sm.tau = mine;
-  }
-  __syncthreads();
-  const float m = sm.m, lns = sm.lns;
-  if (!a.rows)  // the row's own tokens
-    for (int j = tid; j < a.n_tokens / a.n_rows; j += kScoreThreads) {
-      const int64_t at = (int64_t)r * (a.n_tokens / a.n_rows) + j;
-      const int tok = a.tokens[at];
-      if (tok < 0 || tok >= a.vocab) atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
-      a.logprob[at] = tok < 0 || tok >= a.vocab ? NAN : score_logprob(to_f32<T>(row.x[tok]), m, lns);
-    }
-  if (!a.k) return;
-  const float tau = sm.tau;
-  auto offer = [&](float x, int i) {
-    if (x >= tau) {
-      const int at = atomicAdd(&sm.count, 1);
-      if (at < kScoreCand) sm.val[at] = x, sm.idx[at] = i;
-    }
-  };
-  // Threads whose maximum reaches the bound: a warp reads each one's vectors again.
-  if (top >= tau) sm.hit[atomicAdd(&sm.hits, 1)] = tid;
-  if (tid < n_edge) offer(to_f32<T>(row.x[row.edge(tid)]), row.edge(tid));
-  __syncthreads();
-  const int hits = sm.hits;
-  for (int h = warp; h < hits; h += kScoreThreads / 32) {
-    if (*(volatile int *)&sm.count > kScoreCand) break;
-    for (int w = sm.hit[h] + lane * kScoreThreads; w < row.nv; w += 32 * kScoreThreads) {
-      float x[N];
-      ScoreVec<T>::get(row.vec(w), x);
+  if (warp == 0) {
+    ScoreSums w = {-3.402823466e38f, 0.f, 0.f};
+    if (lane < kScoreThreads / 32) w = {sm.wm[lane], sm.ws[lane], sm.wt[lane]};
 #pragma unroll
-      for (int i = 0; i < N; ++i) offer(x[i], row.head + w * N + i);
+    for (int o = 16; o > 0; o >>= 1)
+      w.join(__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.s, o), __shfl_xor_sync(0xffffffffu, w.t, o));
+    if (lane == 0) sm.sums[0] = w.m, sm.sums[1] = w.s, sm.sums[2] = w.t;
+  }
+  if (tid == 0 && sm.abort) atomicOr(a.status, (unsigned)SSD_FAULT_TIMEOUT);
+  if (ranks > 1) cluster.sync(); else __syncthreads();
+  if (rank == 0 && warp == 0) {
+    ScoreSums w = {-3.402823466e38f, 0.f, 0.f};
+    if (lane < ranks) {
+      const float *o = cluster.map_shared_rank(sm.sums, lane);
+      w = {o[0], o[1], o[2]};
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+      w.join(__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.s, o), __shfl_xor_sync(0xffffffffu, w.t, o));
+    if (lane == 0) {
+      const float lns = logf(w.s);  // -inf: nothing but -inf
+      sm.m = w.m;
+      sm.lns = lns;
+      a.lse[r] = w.m + lns;
+      if (a.entropy) a.entropy[r] = w.s == 0.f ? 0.f : lns - w.t / w.s;
     }
   }
-  __syncthreads();
+  if (a.k) {
+    // The bound: bit by bit the largest key, of its upper bits, that k maxima reach.  (Comparing them all with one another took
+    // a third of the call.)
+    if (warp == 0) {
+      uint32_t key[kScoreGroups / 32], t = 0;
+#pragma unroll
+      for (int q = 0; q < kScoreGroups / 32; ++q) {
+        const int j = q * 32 + lane;
+        key[q] = j < ranks * groups ? score_key(cluster.map_shared_rank(sm.own, j / groups)[j % groups]) : 0u;
+      }
+#pragma unroll 1
+      for (uint32_t bit = 1u << 31; bit >= 1u << 12; bit >>= 1) {
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < kScoreGroups / 32; ++q) n += key[q] >= (t | bit);
+        if (__reduce_add_sync(0xffffffffu, n) >= a.k) t |= bit;
+      }
+      if (lane == 0) sm.tau = t <= score_key(-INFINITY) ? -INFINITY : __uint_as_float(t >> 31 ? t ^ 0x80000000u : ~t);
+    }
+    __syncthreads();
+    const float tau = sm.tau;
+    int *count = cluster.map_shared_rank(&sm.count, 0);
+    float *val = cluster.map_shared_rank(sm.val, 0);
+    int *idx = cluster.map_shared_rank(sm.idx, 0);
+    auto offer = [&](float x, int i) {
+      if (x >= tau) {
+        const int at = atomicAdd(count, 1);
+        if (at < kScoreCand) val[at] = x, idx[at] = i;
+      }
+    };
+    // Vectors of the threads whose maximum reaches the bound, read again by everybody and four at a time: of one stage, or all.
+    if (tid < kScoreThreads && top >= tau) {
+      if (next < tau)
+        sm.hit[atomicAdd(&sm.hits, 1)] = top_stage * kScoreThreads + tid;
+      else
+        sm.hit[kScoreThreads - 1 - atomicAdd(&sm.full_hits, 1)] = tid;  // (from the list's other end)
+    }
+    if (tid < n_edge) offer(edge, row.edge(tid));
+    __syncthreads();
+    auto again = [&](int hits, int from, int each, auto vector_of) {
+      const unsigned total = hits * each;
+      constexpr int U = 4;
+      for (unsigned e0 = tid; e0 < total && *(volatile int *)count <= kScoreCand; e0 += U * (kScoreThreads + 32)) {
+        int at[U];
+        uint4 w[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          const unsigned e = e0 + q * (kScoreThreads + 32), h = e / each;
+          at[q] = e < total ? v0 + vector_of(sm.hit[from + h], (int)(e - h * each)) : v1;
+          if (at[q] < v1) w[q] = row.vec(at[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+          if (at[q] < v1 && ScoreVec<T>::max(w[q]) >= tau) {
+            float x[N];
+            ScoreVec<T>::get(w[q], x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) offer(x[i], row.head + at[q] * N + i);
+          }
+      }
+    };
+    again(sm.hits, 0, kScoreVectors, [&](int hit, int q) { return hit / kScoreThreads * PER + hit % kScoreThreads + q * kScoreThreads; });
+    again(sm.full_hits, kScoreThreads - sm.full_hits, cdiv(v1 - v0, kScoreThreads), [&](int hit, int q) { return hit + q * kScoreThreads; });
+  }
+  if (ranks > 1) cluster.sync(); else __syncthreads();
+  if (rank || tid >= kScoreThreads) return;
+  const float m = sm.m, lns = sm.lns;
+  if (!a.rows) {  // the row's own tokens
+    const int each = a.n_tokens / a.n_rows;
+    for (int j = tid; j < each; j += kScoreThreads) {
+      const int64_t at = (int64_t)r * each + j;
+      const int tok = a.tokens[at];
+      a.logprob[at] = score_bad(a, tok) ? NAN : score_logprob(to_f32<T>(row.x[tok]), m, lns);
+    }
+  } else if (a.n_tokens <= kScoreFused) {
+    for (int j = tid; j < a.n_tokens; j += kScoreThreads) {
+      const int of = a.rows[j];
+      if (of == r) {
+        const int tok = a.tokens[j];
+        a.logprob[j] = score_bad(a, tok) ? NAN : score_logprob(to_f32<T>(row.x[tok]), m, lns);
+      } else if (r == 0 && (of < 0 || of >= a.n_rows)) {
+        if (of != -1) atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
+        a.logprob[j] = of == -1 ? 0.f : NAN;
+      }
+    }
+  }
+  if (!a.k) return;
   const int count = sm.count;
   int32_t *ids = a.top_ids + (int64_t)r * a.k;
   float *lps = a.top_logprobs + (int64_t)r * a.k;
@@ -260,13 +485,13 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(ScoreArgs a) {
   for (int c = tid; c < count; c += kScoreThreads) {
     const float x = sm.val[c];
     const int i = sm.idx[c];
-    int rank = 0;
-    for (int j = 0; j < count; ++j) rank += score_before(sm.val[j], sm.idx[j], x, i);
-    if (rank < a.k) ids[rank] = i, lps[rank] = score_logprob(x, m, lns);
+    int before = 0;
+    for (int j = 0; j < count; ++j) before += score_before(sm.val[j], sm.idx[j], x, i);
+    if (before < a.k) ids[before] = i, lps[before] = score_logprob(x, m, lns);
   }
 }
 
-// Tokens looked up in rows of their own choice.
+// Tokens looked up in rows of their own choice, where they are many.
 template <typename T>
 __global__ void __launch_bounds__(128) score_tokens_kernel(ScoreArgs a) {
   const int j = blockIdx.x * 128 + threadIdx.x;
@@ -276,7 +501,7 @@ __global__ void __launch_bounds__(128) score_tokens_kernel(ScoreArgs a) {
   const int r = a.rows[j], tok = a.tokens[j];
   float lp = 0.f;
   if (r != -1) {
-    if (r < 0 || r >= a.n_rows || tok < 0 || tok >= a.vocab) {
+    if (r < 0 || r >= a.n_rows || score_bad(a, tok)) {
       atomicOr(a.status, (unsigned)SSD_FAULT_INDEX);
       lp = NAN;
     } else {
@@ -286,10 +511,38 @@ __global__ void __launch_bounds__(128) score_tokens_kernel(ScoreArgs a) {
   a.logprob[j] = lp;
 }
 
+// Blocks of a row's cluster: so many that six lie on every SM (with fewer the SMs' shares differ too much), with a vector a
+// thread at least.
+static int score_ranks(const ScoreArgs &a, int per_vector) {
+  int ranks = 1;
+  while (ranks < 8 && (int64_t)a.n_rows * ranks < 6 * sm_count() && a.vocab >= 2 * ranks * kScoreThreads * per_vector) ranks *= 2;
+  return ranks;
+}
+
 template <typename T>
 static int score_launch(const ScoreArgs &a, cudaStream_t st) {
-  int rc = launch(score_kernel<T>, dim3(a.n_rows), dim3(kScoreThreads), 0, st, "score_kernel", a);
-  if (rc || !a.rows || a.n_tokens == 0) return rc;
+  const int ranks = score_ranks(a, ScoreVec<T>::N);
+  int rc = ensure_smem<score_kernel<T>>(sizeof(ScoreSmem));
+  if (rc) return rc;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.n_rows * ranks);
+  cfg.blockDim = dim3(kScoreThreads + 32);
+  cfg.dynamicSmemBytes = sizeof(ScoreSmem);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, score_kernel<T>, a);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(SSD_ERR_CUDA, "score_kernel: %s", cudaGetErrorString(e));
+  }
+  rc = check_launch("score_kernel");
+  if (rc || !a.rows || a.n_tokens <= kScoreFused) return rc;
   return launch(score_tokens_kernel<T>, dim3(cdiv(a.n_tokens, 128)), dim3(128), 0, st, "score_tokens_kernel", a);
 }
 
@@ -302,7 +555,7 @@ extern "C" int ssd_token_logprobs(const void *logits, int dtype, int64_t row_str
                                   float *top_logprobs, int top_k, ssd_stream_t stream) {
   const char *who = "ssd_token_logprobs";
   if (dtype != SSD_DTYPE_BF16 && dtype != SSD_DTYPE_F32) return fail(SSD_ERR_UNSUPPORTED, "%s: dtype %d", who, dtype);
-  if (n_rows < 0 || vocab < 1 || n_tokens < 0 || row_stride < 0 || vocab > 1 << 30)
+  if (n_rows < 0 || vocab < 1 || n_tokens < 0 || row_stride < 0 || vocab > 1 << 30 || n_rows > 1 << 27)
     return fail(SSD_ERR_INVALID_ARG, "%s: n_rows %d, vocab %d, n_tokens %d or row_stride out of range", who, n_rows, vocab, n_tokens);
   if (top_k < 0 || top_k > vocab || top_k > kScoreMaxK)
     return fail(SSD_ERR_INVALID_ARG, "%s: top_k %d outside [0, min(vocab, %d)]", who, top_k, kScoreMaxK);
