@@ -1,27 +1,32 @@
 // ssd_span_simt.cu -- span attention on CUDA cores: fp32 caches, and bf16 ones whose pages are below 8 tokens.
 //
-// A block takes up to ROWS query rows of one (request, KV head) and a part of their tiles of 64 tokens.  K and V of a tile
-// are brought to shared memory as fp32; the scores, 64 per row, go there too; the softmax keeps a running maximum and sum
-// per row and O stays in registers.  An element of K and V in shared memory meets 2 or 4 rows of registers in S and in
-// O, so that shared-memory reads and FMAs take about the same time.  Where the (request, head, rows) blocks do not fill
-// the SMs, each is cut into equal parts of its tiles, joined by span_join_kernel.
+// A block of eight warps takes ROWS = 8 RW query rows of one (request, KV head) and a part of their tiles of 64 tokens; a warp
+// has RW rows for itself.  K and V come to shared memory by cp.async, V of a tile while S is computed and K of the next while O
+// is, from row addresses that are looked up one tile ahead.  In S a lane has two tokens and all of the warp's rows: the queries are read by broadcast,
+// and 12 wavefronts of shared memory feed 32 multiply-adds of each lane; in O a lane has four columns (two at d = 64) and all
+// rows.  A row's softmax stays inside its warp.  What bounds it: shared memory and the latencies of
+// a tile's four barriers; 16 requests of 1000 to 4000 tokens, 8 heads of 4 queries, 8 nodes in fp32: 234 us, 22 TFLOP/s (four
+// warps with twice the rows each: 269).  Where the (request, head, rows) blocks do not fill the SMs, each is cut into equal
+// parts of its tiles, joined by span_simt_join_kernel.
 #include "ssd_host.h"
 #include "ssd_span.h"
 
 namespace ssd {
 
 constexpr int kSimtTile = 64;
-constexpr int kSimtThreads = 256;
+constexpr int kSimtWarps = 8;
+constexpr int kSimtThreads = 32 * kSimtWarps;
 
 struct SimtPlan {
   int chunks, parts;  // row chunks of a (request, head), parts of a chunk's tiles
   float *o, *lse;     // [item][ROWS][D], [item][ROWS] (log2), parts > 1
 };
 
-template <int D, int ROWS>
+template <typename T, int D, int ROWS>
 struct SimtSmem {
-  float q[ROWS][D + 4], k[kSimtTile][D + 4], v[kSimtTile][D], s[ROWS][kSimtTile + 4];
-  float m[ROWS], l[ROWS], alpha[ROWS];
+  float q[ROWS][D], p[ROWS][kSimtTile];
+  T kv[2][kSimtTile][D + 16 / sizeof(T)];
+  int64_t row[2][kSimtTile];  // offsets of the K rows of a tile and the next, -1: zeros
 };
 
 template <typename T>
@@ -38,11 +43,23 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v) {
   *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
+__device__ __forceinline__ void load2(const float *p, float &x, float &y) {
+  const float2 v = *reinterpret_cast<const float2 *>(p);
+  x = v.x, y = v.y;
+}
+__device__ __forceinline__ void load2(const __nv_bfloat16 *p, float &x, float &y) {
+  const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
+  x = bf16_lo(v), y = bf16_hi(v);
+}
+__device__ __forceinline__ void store2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) { *reinterpret_cast<uint32_t *>(p) = pack_bf16(x, y); }
+
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(SpanArgs a, SimtPlan pl) {
+__global__ void __launch_bounds__(kSimtThreads, 2) span_simt_kernel(SpanArgs a, SimtPlan pl) {
+  constexpr int RW = ROWS / kSimtWarps, CL = D / 32;  // rows of a warp, columns of a lane
   extern __shared__ __align__(16) char smem_raw[];
-  auto &sm = *reinterpret_cast<SimtSmem<D, ROWS> *>(smem_raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto &sm = *reinterpret_cast<SimtSmem<T, D, ROWS> *>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, w0 = (tid >> 5) * RW;  // the warp's first row
   const int h_kv = a.kv.h_kv, rows = a.n * a.G;
   int64_t x = blockIdx.x;
   const int part = (int)(x % pl.parts);
@@ -58,127 +75,121 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(SpanArgs a, Sim
   const int k0 = (int)((int64_t)st.n_tiles * part / pl.parts), k1 = (int)((int64_t)st.n_tiles * (part + 1) / pl.parts);
   const int32_t *parents = a.parents ? a.parents + (int64_t)b * a.n : nullptr;
 
-  auto row_at = [&](int r) {  // element offset of row r0 + r in q and out
+  auto row_at = [&](int r) {  // row r0 + r of q and out
     const int i = (r0 + r) / a.G;
-    return (((int64_t)b * a.n + i) * a.h_q + g * a.G + (r0 + r - i * a.G)) * D;
+    return ((int64_t)b * a.n + i) * a.h_q + g * a.G + (r0 + r - i * a.G);
   };
   for (int e = tid; e < ROWS * (D / 4); e += kSimtThreads) {
     const int r = e / (D / 4), col = e % (D / 4) * 4;
-    store4(&sm.q[r][col], r < nr ? load4<T>(static_cast<const T *>(a.q) + row_at(r) + col) : make_float4(0.f, 0.f, 0.f, 0.f));
+    store4(&sm.q[r][col], r < nr ? load4<T>(static_cast<const T *>(a.q) + row_at(r) * D + col) : make_float4(0.f, 0.f, 0.f, 0.f));
   }
-  if (tid < ROWS) sm.m[tid] = -INFINITY, sm.l[tid] = 0.f;
-
-  constexpr int TC = D / 4, TR = kSimtThreads / TC, RT = ROWS / TR;  // O: rows per thread, four columns
-  static_assert(RT >= 1 && ROWS % 16 == 0, "tile");
-  const int oc = tid % TC * 4, orow = tid / TC * RT;
-  constexpr int SR = ROWS / 16;  // S: SR rows and tokens st_ + 16 j per thread
-  const int s_t = tid % 16, s_r = tid / 16 * SR;
-  float4 o[RT];
+  float m[RW], l[RW], o[RW][CL];
 #pragma unroll
-  for (int k = 0; k < RT; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-
+  for (int i = 0; i < RW; ++i) {
+    m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < CL; ++j) o[i][j] = 0.f;
+  }
+  auto look_up = [&](int k) {
+    if (k >= k1 || tid >= kSimtTile) return;
+    const int t = st.tile(k) * kSimtTile + tid;
+    const T *row = st.seen(t) ? kv_row<D, T>(a.kv, b, 0, g, t, a.status) : nullptr;
+    sm.row[k & 1][tid] = row ? row - static_cast<const T *>(a.kv.pool) : -1;
+  };
+  // K (which = 0) or V of tile k; a group of its own.
+  auto load = [&](int which, int k) {
+    constexpr int C = D * (int)sizeof(T) / 16;
+    if (k < k1) {
+      const T *pool = static_cast<const T *>(a.kv.pool) + (which ? (int64_t)h_kv * a.kv.page_size * D : 0);
+#pragma unroll
+      for (int e0 = 0; e0 < kSimtTile * C; e0 += kSimtThreads) {
+        const int t = (e0 + tid) / C, col = (e0 + tid) % C * (16 / (int)sizeof(T));
+        const int64_t row = sm.row[k & 1][t];
+        cp_async16(smem_u32(&sm.kv[which][t][col]), row < 0 ? a.kv.pool : pool + row + col, row < 0 ? 0 : 16);
+      }
+    }
+    cp_async_commit();
+  };
+  look_up(k0);
+  __syncthreads();
+  load(0, k0);
+  load(1, k0);
+  look_up(k0 + 1);
   for (int k = k0; k < k1; ++k) {
     const int t0 = st.tile(k) * kSimtTile;
-    __syncthreads();  // the tile before has been used
-    for (int e = tid; e < kSimtTile * TC; e += kSimtThreads) {
-      const int t = e / TC, col = e % TC * 4;
-      float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
-      if (st.seen(t0 + t)) {
-        const T *kr = kv_row<D, T>(a.kv, b, 0, g, t0 + t, a.status);
-        if (kr) {
-          kk = load4<T>(kr + col);
-          vv = load4<T>(kr + (int64_t)h_kv * a.kv.page_size * D + col);
-        }
-      }
-      store4(&sm.k[t][col], kk);
-      store4(&sm.v[t][col], vv);
-    }
+    cp_async_wait<1>();
     __syncthreads();
-    float s[SR][4];
+    float s[RW][2];
 #pragma unroll
-    for (int i = 0; i < SR; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
+    for (int i = 0; i < RW; ++i) s[i][0] = s[i][1] = 0.f;
+#pragma unroll 2
     for (int d = 0; d < D; d += 4) {
-      float4 qv[SR], kv4[4];
+      const float4 ka = load4<T>(&sm.kv[0][lane][d]), kb = load4<T>(&sm.kv[0][lane + 32][d]);
 #pragma unroll
-      for (int i = 0; i < SR; ++i) qv[i] = *reinterpret_cast<const float4 *>(&sm.q[s_r + i][d]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) kv4[j] = *reinterpret_cast<const float4 *>(&sm.k[s_t + 16 * j][d]);
-#pragma unroll
-      for (int i = 0; i < SR; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          s[i][j] = fmaf(qv[i].x, kv4[j].x, fmaf(qv[i].y, kv4[j].y, fmaf(qv[i].z, kv4[j].z, fmaf(qv[i].w, kv4[j].w, s[i][j]))));
-    }
-#pragma unroll
-    for (int i = 0; i < SR; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sm.s[s_r + i][s_t + 16 * j] = s[i][j] * a.scale_log2;
-    __syncthreads();
-    for (int r = warp; r < ROWS; r += kSimtThreads / 32) {  // a warp per row, two tokens per lane
-      const int i = (r0 + r) / a.G;
-      uint32_t m2[2] = {0u, 0u};
-      if (r < nr && i < c && st.base + i >= 0) span_mask<2>(a, parents, st.base, i, t0, a.status, m2);
-      const float x0 = (m2[0] >> lane & 1) ? sm.s[r][lane] : -INFINITY, x1 = (m2[1] >> lane & 1) ? sm.s[r][lane + 32] : -INFINITY;
-      const float m_old = sm.m[r], m_new = fmaxf(m_old, warp_max(fmaxf(x0, x1)));
-      const float ref = m_new == -INFINITY ? 0.f : m_new;
-      const float p0 = exp2f(x0 - ref), p1 = exp2f(x1 - ref), sum = warp_sum(p0 + p1);
-      sm.s[r][lane] = p0;
-      sm.s[r][lane + 32] = p1;
-      __syncwarp();
-      if (lane == 0) {
-        const float f = exp2f(m_old - ref);
-        sm.alpha[r] = f;
-        sm.m[r] = m_new;
-        sm.l[r] = sm.l[r] * f + sum;
+      for (int i = 0; i < RW; ++i) {
+        const float4 q = *reinterpret_cast<const float4 *>(&sm.q[w0 + i][d]);
+        s[i][0] = fmaf(q.x, ka.x, fmaf(q.y, ka.y, fmaf(q.z, ka.z, fmaf(q.w, ka.w, s[i][0]))));
+        s[i][1] = fmaf(q.x, kb.x, fmaf(q.y, kb.y, fmaf(q.z, kb.z, fmaf(q.w, kb.w, s[i][1]))));
       }
     }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const float f = sm.alpha[orow + i];
-      o[i].x *= f, o[i].y *= f, o[i].z *= f, o[i].w *= f;
+    for (int i = 0; i < RW; ++i) {
+      const int node = (r0 + w0 + i) / a.G;
+      uint32_t seen[2] = {0u, 0u};
+      if (w0 + i < nr && node < c && st.base + node >= 0) span_mask<2>(a, parents, st.base, node, t0, a.status, seen);
+      const float x0 = (seen[0] >> lane & 1) ? s[i][0] * a.scale_log2 : -INFINITY, x1 = (seen[1] >> lane & 1) ? s[i][1] * a.scale_log2 : -INFINITY;
+      const float top = fmaxf(m[i], warp_max(fmaxf(x0, x1))), ref = top == -INFINITY ? 0.f : top;
+      const float p0 = exp2f(x0 - ref), p1 = exp2f(x1 - ref), f = exp2f(m[i] - ref);
+      m[i] = top;
+      l[i] = l[i] * f + warp_sum(p0 + p1);
+      sm.p[w0 + i][lane] = p0;
+      sm.p[w0 + i][lane + 32] = p1;
+#pragma unroll
+      for (int j = 0; j < CL; ++j) o[i][j] *= f;
     }
-#pragma unroll 4
+    __syncthreads();
+    load(0, k + 1);
+    cp_async_wait<1>();
+    __syncthreads();
+#pragma unroll 2
     for (int t = 0; t < kSimtTile; t += 4) {
-      float4 pv[RT], vv[4];
+      float v[4][CL];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) pv[i] = *reinterpret_cast<const float4 *>(&sm.s[orow + i][t]);
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) vv[j] = *reinterpret_cast<const float4 *>(&sm.v[t + j][oc]);
+        for (int j = 0; j < CL; j += 2) load2(&sm.kv[1][t + u][lane * CL + j], v[u][j], v[u][j + 1]);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const float p[4] = {pv[i].x, pv[i].y, pv[i].z, pv[i].w};
+      for (int i = 0; i < RW; ++i) {
+        const float4 p = *reinterpret_cast<const float4 *>(&sm.p[w0 + i][t]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          o[i].x = fmaf(p[j], vv[j].x, o[i].x), o[i].y = fmaf(p[j], vv[j].y, o[i].y);
-          o[i].z = fmaf(p[j], vv[j].z, o[i].z), o[i].w = fmaf(p[j], vv[j].w, o[i].w);
-        }
+        for (int j = 0; j < CL; ++j)
+          o[i][j] = fmaf(p.x, v[0][j], fmaf(p.y, v[1][j], fmaf(p.z, v[2][j], fmaf(p.w, v[3][j], o[i][j]))));
       }
     }
+    __syncthreads();
+    load(1, k + 1);
+    look_up(k + 2);
   }
+  cp_async_wait<0>();
   pdl_trigger();
-  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int r = orow + i;
-    if (r >= nr) continue;
-    const float l = sm.l[r], f = l > 0.f || l != l ? 1.f / l : 0.f;
-    const float4 v = make_float4(o[i].x * f, o[i].y * f, o[i].z * f, o[i].w * f);
-    if (pl.parts > 1)
-      store4(pl.o + ((int64_t)blockIdx.x * ROWS + r) * D + oc, v);
-    else
-      store4(static_cast<T *>(a.out) + row_at(r) + oc, v);
-  }
-  if (tid < nr) {
-    const float l = sm.l[tid];
-    const float lse2 = l > 0.f || l != l ? sm.m[tid] + log2f(l) : -INFINITY;
-    if (pl.parts > 1)
-      pl.lse[(int64_t)blockIdx.x * ROWS + tid] = lse2;
-    else if (a.lse)
-      a.lse[row_at(tid) / D] = lse2 * kLn2;
+  for (int i = 0; i < RW; ++i) {
+    const int r = w0 + i;
+    if (r >= nr) break;
+    const bool some = l[i] > 0.f || l[i] != l[i];
+    const float f = some ? 1.f / l[i] : 0.f, lse2 = some ? m[i] + log2f(l[i]) : -INFINITY;
+    const int64_t at = row_at(r), slot = (int64_t)blockIdx.x * ROWS + r;
+    if (pl.parts > 1) {
+#pragma unroll
+      for (int j = 0; j < CL; ++j) o[i][j] *= f;
+#pragma unroll
+      for (int j = 0; j < CL; j += 2) *reinterpret_cast<float2 *>(pl.o + slot * D + lane * CL + j) = make_float2(o[i][j], o[i][j + 1]);
+      if (lane == 0) pl.lse[slot] = lse2;
+    } else {
+#pragma unroll
+      for (int j = 0; j < CL; j += 2) store2(static_cast<T *>(a.out) + at * D + lane * CL + j, o[i][j] * f, o[i][j + 1] * f);
+      if (a.lse && lane == 0) a.lse[at] = lse2 * kLn2;
+    }
   }
 }
 
@@ -216,8 +227,11 @@ __global__ void __launch_bounds__(256) span_simt_join_kernel(SpanArgs a, SimtPla
   if (a.lse && lane == 0) a.lse[at] = z > 0.f || z != z ? (m + log2f(z)) * kLn2 : -INFINITY;
 }
 
-// Row chunks of 16 where that many cover a head's rows, else 32.
-static int simt_rows(const SpanArgs &a) { return (int64_t)a.n * a.G <= 16 ? 16 : 32; }
+// Rows of a block: 8, 16 or 32, as few as cover a head's.
+static int simt_rows(const SpanArgs &a) {
+  const int64_t rows = (int64_t)a.n * a.G;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
 
 static SimtPlan simt_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
   const int rows = simt_rows(a);
@@ -229,10 +243,10 @@ static SimtPlan simt_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
   const int64_t tiles = all < cdiv64(a.sink, kSimtTile) + ((int64_t)a.window + rows / a.G) / kSimtTile + 2
                             ? all
                             : cdiv64(a.sink, kSimtTile) + ((int64_t)a.window + rows / a.G) / kSimtTile + 2;
-  // about four blocks per SM, two tiles each at least
-  const int64_t want = 4 * (int64_t)sm_count();
+  // about eight blocks per SM (one request of 300 tokens, 2 heads, 20 rows in fp32: two tiles a part 22 us, one 12)
+  const int64_t want = 8 * (int64_t)sm_count();
   int64_t parts = units >= want ? 1 : cdiv64(want, units > 0 ? units : 1);
-  if (parts > tiles / 2) parts = tiles / 2;
+  if (parts > tiles) parts = tiles;
   p.parts = parts < 1 ? 1 : (int)parts;
   return p;
 }
@@ -256,7 +270,7 @@ size_t span_simt_workspace(const ssd_paged_kv *kv, const SpanArgs &a) {
 template <typename T, int D, int ROWS>
 static int simt_launch(const ssd_paged_kv *kv, const SpanArgs &a, const SimtPlan &p, cudaStream_t st) {
   constexpr auto kernel = span_simt_kernel<T, D, ROWS>;
-  constexpr int smem = sizeof(SimtSmem<D, ROWS>);
+  constexpr int smem = sizeof(SimtSmem<T, D, ROWS>);
   int rc = ensure_smem<kernel>(smem);
   if (rc) return rc;
   const int64_t items = (int64_t)kv->batch * kv->h_kv * p.chunks * p.parts;
@@ -266,16 +280,18 @@ static int simt_launch(const ssd_paged_kv *kv, const SpanArgs &a, const SimtPlan
   return launch(span_simt_join_kernel<T, D, ROWS>, dim3((unsigned)cdiv64(rows, 8)), dim3(256), 0, st, "span_simt_join_kernel", a, p);
 }
 
+template <typename T, int D>
+static int simt_launch_rows(const ssd_paged_kv *kv, const SpanArgs &a, const SimtPlan &p, cudaStream_t st) {
+  const int rows = simt_rows(a);
+  return rows == 8 ? simt_launch<T, D, 8>(kv, a, p, st) : rows == 16 ? simt_launch<T, D, 16>(kv, a, p, st) : simt_launch<T, D, 32>(kv, a, p, st);
+}
+
 int span_simt(const ssd_paged_kv *kv, const SpanArgs &a, void *workspace, cudaStream_t st) {
   SimtPlan p = simt_plan(kv, a);
   simt_carve(kv, a, p, workspace);
-  const bool few = simt_rows(a) == 16, wide = kv->d == 128;
-  if (kv->dtype == SSD_DTYPE_F32)
-    return wide ? (few ? simt_launch<float, 128, 16>(kv, a, p, st) : simt_launch<float, 128, 32>(kv, a, p, st))
-                : (few ? simt_launch<float, 64, 16>(kv, a, p, st) : simt_launch<float, 64, 32>(kv, a, p, st));
-  using H = __nv_bfloat16;
-  return wide ? (few ? simt_launch<H, 128, 16>(kv, a, p, st) : simt_launch<H, 128, 32>(kv, a, p, st))
-              : (few ? simt_launch<H, 64, 16>(kv, a, p, st) : simt_launch<H, 64, 32>(kv, a, p, st));
+  const bool wide = kv->d == 128;
+  if (kv->dtype == SSD_DTYPE_F32) return wide ? simt_launch_rows<float, 128>(kv, a, p, st) : simt_launch_rows<float, 64>(kv, a, p, st);
+  return wide ? simt_launch_rows<__nv_bfloat16, 128>(kv, a, p, st) : simt_launch_rows<__nv_bfloat16, 64>(kv, a, p, st);
 }
 
 }  // namespace ssd
