@@ -14,9 +14,9 @@ from .binding import (KV4Cache, KVCache, LibraryNotBuilt, PagePool, SSDError, Wo
                       ssd_phase_assign, ssd_phase_fill, ssd_select_topk, ssd_select_topp, ssd_status,
                       ssd_token_logprobs, ssd_tree_accept, ssd_tree_attn, ssd_tree_commit, ssd_unified_attn,
                       ssd_verify_attn, ssd_verify_select, ssd_version, ssd_window_attn)
-from .round import SpecRound
+from .round import SpecRound, TreeRound
 
-__all__ = ["KV4Cache", "KVCache", "LibraryNotBuilt", "PagePool", "SSDError", "SpecRound", "Workspace",
+__all__ = ["KV4Cache", "KVCache", "LibraryNotBuilt", "PagePool", "SSDError", "SpecRound", "TreeRound", "Workspace",
            "ssd_block_sparse_attn", "ssd_block_union", "ssd_combine", "ssd_draft_attn", "ssd_draft_attn_packed",
            "ssd_draft_attn_static", "ssd_draft_pack_bytes", "ssd_kv4_append", "ssd_kv4_draft_attn", "ssd_kv4_read",
            "ssd_kv4_verify_attn", "ssd_kv_advance", "ssd_kv_append", "ssd_kv_compact", "ssd_kv_fork",

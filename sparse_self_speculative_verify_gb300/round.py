@@ -156,3 +156,63 @@ class SpecRound:
         for j in range(k):
             self.draft(q_drafts[j], out=None if draft_outs is None else draft_outs[j], stream=stream,
                        last=j == k - 1)
+
+
+class TreeRound:
+    """One step that drafts trees of tokens, on one attention layer, with every buffer allocated once: the drafts' cheap
+    attention (a window of recent tokens and the first ones), the tree's verify attention, the nodes' log probabilities, the
+    path that stays and its commit to the cache (SpecSA "branch handling"; SparseSpec §2.3 verifies a chain, the tree in which
+    every node hangs on the one before it).
+
+    A step: append the nodes' K and V (``ssd_kv_append``), advance the lengths by the nodes' counts (``ssd_kv_advance``),
+    ``verify``; from the logits ``score`` and ``accept``; ``commit`` on every layer's cache; ``advance`` once.  With caches
+    that share their lengths, one round accepts and advances and the others only ``verify`` and ``commit``."""
+
+    def __init__(self, kv: B.KVCache, h_q: int, n_nodes: int, window: int, sink: int = 4, max_path: Optional[int] = None,
+                 scale: Optional[float] = None, workspace: Optional[B.Workspace] = None):
+        self.kv, self.h_q, self.n, self.window, self.sink = kv, h_q, n_nodes, window, sink
+        self.max_path = min(max_path or n_nodes, n_nodes)
+        self.scale = scale if scale is not None else 1.0 / math.sqrt(kv.d)
+        self.ws = workspace
+        b, dev, dt = kv.batch, kv.device, kv.pool.dtype
+        new = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        self.out_t, self.lse_t = new(b, n_nodes, h_q, kv.d, dtype=dt), new(b, n_nodes, h_q, dtype=torch.float32)
+        self.out_d, self.lse_d = new(b, 1, h_q, kv.d, dtype=dt), new(b, 1, h_q, dtype=torch.float32)
+        self.logprob, self.lse, self.entropy = (new(b, n_nodes, dtype=torch.float32) for _ in range(3))
+        self.path, self.cnt, self.next, self.back = new(b, self.max_path), new(b), new(b), new(b)
+        self._first = (torch.arange(b, dtype=torch.int32, device=dev) * n_nodes)[:, None]  # a tree's first row of logits
+        self._rows = new(b, n_nodes)
+
+    def draft(self, q: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> dict:
+        """Attention of one draft token per request, the last of its cache: q [B, 1, h_q, d]."""
+        return B.ssd_window_attn(self.kv, q, self.window, self.sink, self.scale, out=self.out_d if out is None else out,
+                                 lse=self.lse_d, workspace=self.ws, stream=stream)
+
+    def verify(self, q: torch.Tensor, parents: torch.Tensor, counts: Optional[torch.Tensor] = None, stream=None) -> dict:
+        """Attention of the trees' nodes, the last of their caches: q [B, n, h_q, d]."""
+        return B.ssd_tree_attn(self.kv, q, parents, self.scale, counts=counts, out=self.out_t, lse=self.lse_t, workspace=self.ws,
+                               stream=stream)
+
+    def score(self, logits: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor, top_k: int = 0, stream=None) -> dict:
+        """Every node's log probability under its parent's row (a root's: 0), every row's entropy and top_k alternatives.
+        logits [B * n, vocab]; tokens, parents int32 [B, n]."""
+        with torch.cuda.stream(stream) if stream is not None else _nullcontext():
+            torch.add(parents, self._first, out=self._rows)
+            self._rows.masked_fill_(parents < 0, -1)
+        return B.ssd_token_logprobs(logits, tokens.view(-1), rows=self._rows.view(-1), top_k=top_k, logprob=self.logprob.view(-1),
+                                    lse=self.lse.view(-1), entropy=self.entropy.view(-1), stream=stream)
+
+    def accept(self, parents: torch.Tensor, tokens: torch.Tensor, target: torch.Tensor, counts: Optional[torch.Tensor] = None,
+               epsilon: Optional[float] = None, delta: Optional[float] = None, stream=None) -> dict:
+        """The path that stays, by equality with ``target`` or, with epsilon and delta, by the last ``score``."""
+        more = {} if epsilon is None else dict(logprob=self.logprob, entropy=self.entropy, epsilon=epsilon, delta=delta)
+        return B.ssd_tree_accept(parents, tokens, target, counts=counts, max_path=self.max_path, path=self.path, cnt=self.cnt,
+                                 next=self.next, advance=self.back, stream=stream, **more)
+
+    def commit(self, counts: Optional[torch.Tensor] = None, kv: Optional[B.KVCache] = None, stream=None) -> None:
+        """Moves the accepted rows of this round's cache, or of another layer's, together."""
+        B.ssd_tree_commit(self.kv if kv is None else kv, self.path, self.cnt, self.n, counts=counts, stream=stream)
+
+    def advance(self, stream=None) -> None:
+        """Shortens the lengths to what was accepted."""
+        B.ssd_kv_advance(self.kv.seq_lens, self.back, self.kv.max_seq_len, stream=stream)
