@@ -36,28 +36,30 @@ __device__ __forceinline__ void span_sizes(const SpanArgs &a, int b, bool report
   if (bad && report) atomicOr(a.status, (unsigned)SSD_FAULT_SEQLEN);
 }
 
-// The tokens that the queries [i0, i1] of a request see, as tiles of TILE tokens: tiles [0, first) hold the sinks, tiles
-// [w0, w0 + n_tiles - first) the window.  A token t is seen by one of them iff t < hi and (t < sink or t >= lo).
+// The tokens that the queries [i0, i1] of a request see, in a row: first the sinks, then the window, each from and to a
+// multiple of `grain` (a power of two; what a copy takes at once).  Place v of the row holds token(v); a tile is TILE places.
+// A token t is seen by one of the queries iff t < hi and (t < sink or t >= lo); places without one of these are
+// [sink, lo + off) and those from hi + off on.
 struct SpanTiles {
-  int base, lo, hi, sink, first, w0, n_tiles;
-  __device__ __forceinline__ int tile(int k) const { return k < first ? k : k - first + w0; }
+  int base, lo, hi, sink, split, off, n_tiles;  // from place `split` on token v - off is at place v
+  __device__ __forceinline__ int token(int v) const { return v < split ? v : v - off; }
   __device__ __forceinline__ bool seen(int t) const { return t < hi && (t < sink || t >= lo); }
 };
 
 template <int TILE>
-__device__ __forceinline__ SpanTiles span_tiles(const SpanArgs &a, int L, int c, int i0, int i1) {
+__device__ __forceinline__ SpanTiles span_tiles(const SpanArgs &a, int L, int c, int i0, int i1, int grain) {
   SpanTiles s;
   s.base = L - c;
   i0 = max(i0, -s.base);
   i1 = min(i1, c - 1);
-  s.hi = s.lo = s.sink = s.first = s.w0 = s.n_tiles = 0;
+  s.hi = s.lo = s.sink = s.split = s.off = s.n_tiles = 0;
   if (i0 > i1) return s;
   s.hi = s.base + i1 + 1;
   s.lo = max(0, s.base + i0 - a.window + 1);
   s.sink = min(a.sink, s.hi);
-  s.w0 = s.lo / TILE;
-  s.first = min(cdiv(s.sink, TILE), s.w0);
-  s.n_tiles = s.first + cdiv(s.hi, TILE) - s.w0;
+  const int first = (s.sink + grain - 1) & -grain, from = s.lo & -grain;
+  if (from > first) s.split = first, s.off = first - from;  // (else one stretch from token 0 on)
+  s.n_tiles = cdiv(s.hi + s.off, TILE);
   return s;
 }
 
@@ -68,21 +70,21 @@ __device__ __forceinline__ uint32_t span_bits(int t0, int lo, int hi) {
   return (0xffffffffu >> (32 - (e - a))) << a;
 }
 
-// What row i of the request sees of the W * 32 tokens from t0 on (p = base + i >= 0, i < count).
+// What row i of the request (p = base + i >= 0, i < count) sees of the W * 32 places from v0 on.
 template <int W>
-__device__ __forceinline__ void span_mask(const SpanArgs &a, const int32_t *parents, int base, int i, int t0, unsigned *status,
+__device__ __forceinline__ void span_mask(const SpanArgs &a, const int32_t *parents, int base, int off, int i, int v0, unsigned *status,
                                           uint32_t (&m)[W]) {
   const int p = base + i;
   if (!a.parents) {
 #pragma unroll
     for (int w = 0; w < W; ++w)
-      m[w] = span_bits(t0 + 32 * w, max(0, p - a.window + 1), p + 1) | span_bits(t0 + 32 * w, 0, min(a.sink, p + 1));
+      m[w] = span_bits(v0 + 32 * w, max(0, p - a.window + 1) + off, p + 1 + off) | span_bits(v0 + 32 * w, 0, min(a.sink, p + 1));
     return;
   }
 #pragma unroll
-  for (int w = 0; w < W; ++w) m[w] = span_bits(t0 + 32 * w, 0, base);
-  for (int j = i; j >= 0 && base + j >= t0;) {
-    const int t = base + j - t0;
+  for (int w = 0; w < W; ++w) m[w] = span_bits(v0 + 32 * w, 0, base);
+  for (int j = i; j >= 0 && base + j >= v0;) {
+    const int t = base + j - v0;
 #pragma unroll
     for (int w = 0; w < W; ++w)
       if ((t >> 5) == w) m[w] |= 1u << (t & 31);

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) span_simt_kernel(SpanArgs a, 
   pdl_wait();
   int L, c;
   span_sizes(a, b, g == 0 && chunk == 0 && part == 0 && tid == 0, L, c);
-  const SpanTiles st = span_tiles<kSimtTile>(a, L, c, r0 / a.G, (r0 + nr - 1) / a.G);
+  const SpanTiles st = span_tiles<kSimtTile>(a, L, c, r0 / a.G, (r0 + nr - 1) / a.G, 1);
   const int k0 = (int)((int64_t)st.n_tiles * part / pl.parts), k1 = (int)((int64_t)st.n_tiles * (part + 1) / pl.parts);
   const int32_t *parents = a.parents ? a.parents + (int64_t)b * a.n : nullptr;
 
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) span_simt_kernel(SpanArgs a, 
   }
   auto look_up = [&](int k) {
     if (k >= k1 || tid >= kSimtTile) return;
-    const int t = st.tile(k) * kSimtTile + tid;
+    const int t = st.token(k * kSimtTile + tid);
     const T *row = st.seen(t) ? kv_row<D, T>(a.kv, b, 0, g, t, a.status) : nullptr;
     sm.row[k & 1][tid] = row ? row - static_cast<const T *>(a.kv.pool) : -1;
   };
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) span_simt_kernel(SpanArgs a, 
   load(1, k0);
   look_up(k0 + 1);
   for (int k = k0; k < k1; ++k) {
-    const int t0 = st.tile(k) * kSimtTile;
+    const int t0 = k * kSimtTile;  // its first place
     cp_async_wait<1>();
     __syncthreads();
     float s[RW][2];
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) span_simt_kernel(SpanArgs a, 
     for (int i = 0; i < RW; ++i) {
       const int node = (r0 + w0 + i) / a.G;
       uint32_t seen[2] = {0u, 0u};
-      if (w0 + i < nr && node < c && st.base + node >= 0) span_mask<2>(a, parents, st.base, node, t0, a.status, seen);
+      if (w0 + i < nr && node < c && st.base + node >= 0) span_mask<2>(a, parents, st.base, st.off, node, t0, a.status, seen);
       const float x0 = (seen[0] >> lane & 1) ? s[i][0] * a.scale_log2 : -INFINITY, x1 = (seen[1] >> lane & 1) ? s[i][1] * a.scale_log2 : -INFINITY;
       const float top = fmaxf(m[i], warp_max(fmaxf(x0, x1))), ref = top == -INFINITY ? 0.f : top;
       const float p0 = exp2f(x0 - ref), p1 = exp2f(x1 - ref), f = exp2f(m[i] - ref);

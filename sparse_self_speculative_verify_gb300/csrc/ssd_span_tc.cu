@@ -7,7 +7,7 @@
 // one's softmax runs, the other's products do.
 //   WIDE (more than 128 rows): the streams are two tiles of rows and share every tile of K and V;
 //   else both streams have the same rows and take K / V tiles in turn, their O joined at a segment's end.
-// Roles: warps 0-3 and 4-7 the softmax of a stream (and its O), warp 8 loads (one TMA box per page, 128-byte swizzle),
+// Roles: warps 0-3 and 4-7 the softmax of a stream (and its O), warp 8 loads (TMA boxes of up to 16 tokens of a page, 128-byte swizzle),
 // warps 9 and 10 issue a stream's products.
 //
 // Work.  A unit is one (request, KV head, group of as many queries as a block holds).  The units' tiles lie end to end and are
@@ -37,6 +37,7 @@ struct SpanPlan {
   int row_nodes;         // queries of a stream's tile
   int nodes;             // of a group
   int blocks;
+  int box;               // tokens of a copy: of a page, at most 16
   int split;             // whether units are cut; else shares end at their borders and nothing is left to join
   int32_t *cut_unit;     // [blocks]: the unit that a block's share begins inside of, or -1
   float *o, *lse;        // [blocks][2][D / 4][rows of a block][4], [blocks][2][rows] (log2)
@@ -102,7 +103,7 @@ struct SpanWalk {
     if (b + 1 < a.kv.batch) span_sizes(a, b + 1, false, next_L, next_c);
   }
   __device__ SpanTiles tiles_of(int len_, int cnt_, int group) const {
-    return span_tiles<kSpanTile>(a, len_, cnt_, group * pl.nodes, group * pl.nodes + pl.nodes - 1);
+    return span_tiles<kSpanTile>(a, len_, cnt_, group * pl.nodes, group * pl.nodes + pl.nodes - 1, pl.box);
   }
   // What group `group` of a request costs, in tiles.
   __device__ int cost(int len_, int cnt_, int group) const {
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     int L, c;
     span_sizes(a, b, blockIdx.x == 0, L, c);
     s_len[b] = L, s_cnt[b] = c;
-    const int n = pl.n_groups == 1 ? span_tiles<kSpanTile>(a, L, c, 0, pl.nodes - 1).n_tiles : 0;
+    const int n = pl.n_groups == 1 ? span_tiles<kSpanTile>(a, L, c, 0, pl.nodes - 1, pl.box).n_tiles : 0;
     s_size[b] = n ? n + kSpanOverhead : 0;
   }
   tc_fence_before();
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   if (pl.n_groups > 1) {
     for (unsigned e = tid; e < (unsigned)B * pl.n_groups; e += kSpanThreads) {
       const int b = (int)(e / pl.n_groups), group = (int)(e - (unsigned)b * pl.n_groups);
-      const int n = span_tiles<kSpanTile>(a, s_len[b], s_cnt[b], group * pl.nodes, group * pl.nodes + pl.nodes - 1).n_tiles;
+      const int n = span_tiles<kSpanTile>(a, s_len[b], s_cnt[b], group * pl.nodes, group * pl.nodes + pl.nodes - 1, pl.box).n_tiles;
       if (n == 0) continue;
       atomicAdd(s_size + b, n + kSpanOverhead);
     }
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) pl.cut_unit[blockIdx.x] = walk.inside ? walk.unit() : -1;
-    const int box_rows = min(ps, kSpanTile), boxes = kSpanTile / box_rows;
+    const int box_rows = pl.box, boxes = kSpanTile / box_rows;
     const uint64_t pol = a.parents && pl.n_groups == 1 ? policy_evict_first() : policy_evict_normal();
     const int oob = (int)((int64_t)a.kv.num_pages * 2 * h_kv * ps / 8);
     uint32_t q_uses[2] = {0, 0};
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     bool ok = true;
     // Page of lane's box of tile k, INT32_MIN where nothing of it is seen.
     auto page_of = [&](const SpanSeg &s, int k) -> int32_t {
-      const int t = s.st.tile(k) * kSpanTile + lane * box_rows;
+      const int t = s.st.token(k * kSpanTile + lane * box_rows);
       const bool seen = lane < boxes && t < s.st.hi && (t < s.st.sink || t + box_rows > s.st.lo);
       return seen ? a.kv.page_table[(int64_t)s.b * a.kv.max_pages + (t >> a.kv.log2_ps)] : INT32_MIN;
     };
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       const uint32_t slots = w ? NV : NK, slot = f % slots, full = (w ? v_full : k_full) + 8 * slot;
       ok = __all_sync(0xffffffffu, ok & mbar_wait((w ? v_empty : k_empty) + 8 * slot, ((f / slots) & 1) ^ 1, abort));
       if (!ok) return;
-      const int t = s.st.tile(k) * kSpanTile + lane * box_rows;
+      const int t = s.st.token(k * kSpanTile + lane * box_rows);
       const bool page_ok = pid >= 0 && (int64_t)pid < a.kv.num_pages;
       if (w == 0 && pid != INT32_MIN && !page_ok) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
       const int row8 = page_ok ? (int)((((int64_t)pid * 2 * h_kv + (w ? h_kv : 0) + s.g) * ps + (t & (ps - 1))) >> 3) : oob;
@@ -514,9 +515,9 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
         __syncwarp();
       }
     };
-    // Rows of V that nobody sees may hold anything, and 0 times it has to be 0: those behind `hi` and those from `sink` to `lo`.
-    auto clear_unseen = [&](int hi, int sink, int lo, int t0, int slot) {
-      if (t0 + kSpanTile <= hi && (t0 + kSpanTile <= sink || t0 >= lo || sink >= lo)) return;
+    // Rows of V that nobody sees may hold anything, and 0 times it has to be 0: the places from `end` on and those in [from, to).
+    auto clear_unseen = [&](int end, int from, int to, int t0, int slot) {
+      if (t0 + kSpanTile <= end && (t0 + kSpanTile <= from || t0 >= to || from >= to)) return;
       constexpr int CPR = D / 8;  // 16-byte pieces of a row
       char *v = sm + C::kV + slot * C::kTileBytes;
       const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -537,8 +538,8 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
           for (int e = 0; e < C::kGroup / 512; ++e) at[32 * e] = zero;
         rows(g1, r1);
       };
-      range(max(0, hi - t0), kSpanTile);
-      range(max(0, sink - t0), min(kSpanTile, min(lo, hi) - t0));
+      range(max(0, end - t0), kSpanTile);
+      range(max(0, from - t0), min(kSpanTile, to - t0));
       fence_proxy_async_smem();
       __syncwarp();
     };
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
         for (int k = seg.k0; k < seg.k1; ++k, ++f) {
           const int slot = f % NV, nslot = (f + 1) % NK;
           mbar_wait(v_full + 8 * slot, (f / NV) & 1, abort);
-          clear_unseen(seg.st.hi, seg.st.sink, seg.st.lo, seg.st.tile(k) * kSpanTile, slot);
+          clear_unseen(seg.st.hi + seg.st.off, seg.st.sink, seg.st.lo + seg.st.off, k * kSpanTile, slot);
           for (int s = 0; s < streams; ++s) {
             issue_pv(s, n[s]++, slot, k == seg.k0, s == streams - 1);
             if (k + 1 < seg.k1) {
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
           tc_fence_after();
           issue_qk(s, j & 1, f % NK, true, false);
           mbar_wait(v_full + 8 * slot, (f / NV) & 1, abort);
-          clear_unseen(seg.st.hi, seg.st.sink, seg.st.lo, seg.st.tile(k) * kSpanTile, slot);
+          clear_unseen(seg.st.hi + seg.st.off, seg.st.sink, seg.st.lo + seg.st.off, k * kSpanTile, slot);
           issue_pv(s, n++, slot, first, true);
           first = false;
         }
@@ -637,10 +638,10 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       const int64_t at = ((int64_t)seg.b * a.n + i) * a.h_q + seg.g * a.G + (row - node * a.G);
       const int64_t prow = (int64_t)seg.part * C::kRows + (WIDE ? s * 128 : 0) + row;
       const int32_t *parents = a.parents ? a.parents + (int64_t)seg.b * a.n : nullptr;
-      // Tokens [0, all_to) and, behind lo_all, up to it are seen by every row of the group.
+      // The places [all_from, all_to) and [0, sink) hold tokens that every row of the group sees.
       const int i_first = max(seg.rg * pl.nodes, -seg.st.base), i_last = min(seg.rg * pl.nodes + pl.nodes, seg.c) - 1;
-      const int all_to = a.parents ? max(seg.st.base, 0) : seg.st.base + i_first + 1;
-      const int all_from = a.parents ? 0 : max(0, seg.st.base + i_last - a.window + 1);
+      const int all_to = a.parents ? max(seg.st.base, 0) : seg.st.base + i_first + 1 + seg.st.off;
+      const int all_from = a.parents ? 0 : max(0, seg.st.base + i_last - a.window + 1) + seg.st.off;
       float mref = -INFINITY, l = 0.f;
       bool have = false;  // O holds something
       for (int k = seg.k0; k < seg.k1; ++k, ++f) {
@@ -652,10 +653,10 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(col_s + 32 * q, x + 32 * q);
           tmem_ld_wait();
-          const int t0 = seg.st.tile(k) * kSpanTile, t1 = t0 + kSpanTile;
+          const int t0 = k * kSpanTile, t1 = t0 + kSpanTile;  // places
           if (t1 > all_to || !(t0 >= all_from || t1 <= a.sink)) {
             uint32_t m[4] = {~0u, ~0u, ~0u, ~0u};  // (rows without a query: anything)
-            if (valid) span_mask<4>(a, parents, seg.st.base, i, t0, a.status, m);
+            if (valid) span_mask<4>(a, parents, seg.st.base, seg.st.off, i, t0, a.status, m);
 #pragma unroll
             for (int w = 0; w < 4; ++w)  // (most words of a border's tile are whole for the warp)
               if (__any_sync(0xffffffffu, m[w] != 0xffffffffu)) {
@@ -899,7 +900,7 @@ static bool span_wide(const SpanArgs &a) { return a.n > kSpanTile / a.G; }
 
 // Tiles of a unit's group, at most.
 static int64_t span_most_tiles(const ssd_paged_kv *kv, const SpanArgs &a, const SpanPlan &p) {
-  const int64_t all = cdiv(kv->max_seq_len, kSpanTile), most = cdiv64(a.sink, kSpanTile) + ((int64_t)a.window + p.nodes) / kSpanTile + 2;
+  const int64_t all = cdiv(kv->max_seq_len, kSpanTile), most = cdiv64((int64_t)a.sink + a.window + p.nodes + 2 * p.box, kSpanTile);
   return all < most ? all : most;
 }
 
@@ -910,6 +911,7 @@ static SpanPlan span_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
   p.nodes = streams * p.row_nodes;
   p.n_groups = cdiv(a.n, p.nodes);
   p.blocks = sm_count();
+  p.box = kv->page_size < 16 ? kv->page_size : 16;
   p.split = span_most_tiles(kv, a, p) > kSpanWhole;
   return p;
 }
@@ -945,7 +947,7 @@ int span_tc(const ssd_paged_kv *kv, const SpanArgs &args, void *workspace, cudaS
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   const bool wide = span_wide(args);
-  const int d = kv->d, panels = d / 64, box_rows = kv->page_size < kSpanTile ? kv->page_size : kSpanTile;
+  const int d = kv->d, panels = d / 64;
   SpanPlan p = span_plan(kv, args);
   span_carve(kv, p, wide, workspace);
   // K / V rows as (64 columns, row of 8, panel, group of 8 rows): a box lands as [group][panel][8 rows x 128 B].
@@ -953,7 +955,7 @@ int span_tc(const ssd_paged_kv *kv, const SpanArgs &args, void *workspace, cudaS
   const cuuint32_t es[4] = {1, 1, 1, 1};
   const cuuint64_t dims[4] = {64, 8, (cuuint64_t)panels, (cuuint64_t)kv->num_pages * 2 * kv->h_kv * kv->page_size / 8};
   const cuuint64_t strides[3] = {(cuuint64_t)d * 2, 128, (cuuint64_t)d * 16};
-  const cuuint32_t box[4] = {64, 8, (cuuint32_t)panels, (cuuint32_t)box_rows / 8};
+  const cuuint32_t box[4] = {64, 8, (cuuint32_t)panels, (cuuint32_t)p.box / 8};
   CUresult r = enc(&kvmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(kv->pool), dims, strides, box, es,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
