@@ -7,8 +7,8 @@
 // one's softmax runs, the other's products do.
 //   WIDE (more than 128 rows): the streams are two tiles of rows and share every tile of K and V;
 //   else both streams have the same rows and take K / V tiles in turn, their O joined at a segment's end.
-// Roles: warps 0-3 and 4-7 the softmax of a stream (and its O), warp 8 loads (TMA boxes of up to 16 tokens of a page, 128-byte swizzle),
-// warps 9 and 10 issue a stream's products.
+// Roles: warps 0-3 and 4-7 the softmax of a stream (and its O), warp 8 loads Q and K, warp 11 V (TMA boxes of up to 16 tokens
+// of a page, 128-byte swizzle), warps 9 and 10 issue a stream's products.
 //
 // Work.  A unit is one (request, KV head, group of as many queries as a block holds).  The units' tiles lie end to end and are
 // cut into equal shares, one per block (one block per SM); a cut close to a unit's border moves there.  A unit that several
@@ -23,8 +23,8 @@ namespace ssd {
 using namespace sm100;
 
 constexpr int kSpanTile = 128;          // tokens of a tile, rows of a stream
-constexpr int kSpanThreads = 12 * 32;  // (warp 11 completes the warpgroup whose registers the softmax takes)
-constexpr int kSpanProducer = 8, kSpanMma = 9;
+constexpr int kSpanThreads = 12 * 32;
+constexpr int kSpanProducer = 8, kSpanMma = 9, kSpanLoadV = 11;
 constexpr int kSpanMaxBatch = 1024;     // requests of a launch (their sizes lie in shared memory)
 constexpr int kSpanOverhead = 1;        // what starting and ending a unit costs, in tiles
 constexpr int kSpanSnap = 3;            // a cut this close to a unit's border moves there
@@ -181,7 +181,7 @@ struct SpanWalk {
     const int stop = min(u1, end);
     s.k0 = min(max(0, pos - u0 - kSpanOverhead), s.st.n_tiles);
     s.k1 = stop == u1 ? s.st.n_tiles : min(max(0, stop - u0 - kSpanOverhead), s.st.n_tiles);
-    s.part = pos == u0 && stop == u1 ? -1 : blockIdx.x * 2 + (pos == u0);
+    s.part = pos == u0 && stop == u1 ? -1 : (int)blockIdx.x * 2 + (pos == u0);
     pos = stop;
     return true;
   }
@@ -370,17 +370,11 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   // Registers: 256 x 208 + 128 x 88 are the launch's 384 x 168.
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == kSpanProducer) {
+  if (warp == kSpanProducer || warp == kSpanLoadV) {
     // ---------------------------------------------------------------- loads
-    SpanWalk walk(a, pl, pre, s_size, s_len, s_cnt);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) pl.cut_unit[blockIdx.x] = walk.inside ? walk.unit() : -1;
     const int box_rows = pl.box, boxes = kSpanTile / box_rows;
     const uint64_t pol = a.parents && pl.n_groups == 1 ? policy_evict_first() : policy_evict_normal();
     const int oob = (int)((int64_t)a.kv.num_pages * 2 * h_kv * ps / 8);
-    uint32_t q_uses[2] = {0, 0};
-    int j = 0;  // segments so far
     bool ok = true;
     // Page of lane's box of tile k, INT32_MIN where nothing of it is seen.
     auto page_of = [&](const SpanSeg &s, int k) -> int32_t {
@@ -388,6 +382,44 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       const bool seen = lane < boxes && t < s.st.hi && (t < s.st.sink || t + box_rows > s.st.lo);
       return seen ? a.kv.page_table[(int64_t)s.b * a.kv.max_pages + (t >> a.kv.log2_ps)] : INT32_MIN;
     };
+    // K (w = 0) or V of the block's tile f, tile k of segment s.
+    auto load_tile = [&](const SpanSeg &s, int k, int32_t pid, uint32_t f, int w) {
+      const uint32_t slots = w ? NV : NK, slot = f % slots, full = (w ? v_full : k_full) + 8 * slot;
+      ok = __all_sync(0xffffffffu, ok & mbar_wait((w ? v_empty : k_empty) + 8 * slot, ((f / slots) & 1) ^ 1, abort));
+      if (!ok) return;
+      const int t = s.st.token(k * kSpanTile + lane * box_rows);
+      const bool page_ok = pid >= 0 && (int64_t)pid < a.kv.num_pages;
+      if (w == 0 && pid != INT32_MIN && !page_ok) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
+      const int row8 = page_ok ? (int)((((int64_t)pid * 2 * h_kv + (w ? h_kv : 0) + s.g) * ps + (t & (ps - 1))) >> 3) : oob;
+      if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
+      __syncwarp();
+      if (lane < boxes)
+        tma_load_4d(sbase + (w ? C::kV : C::kK) + slot * C::kTileBytes + (lane * box_rows >> 3) * C::kGroup, &kvmap, 0, 0, 0, row8, full, pol);
+      __syncwarp();
+    };
+    uint32_t f = 0;
+    if (warp == kSpanLoadV) {
+      const SpanSeg *sp;
+      for (int j = 0; ok && (sp = segment(j)); ++j) {
+        const SpanSeg seg = *sp;
+        int32_t pid = page_of(seg, seg.k0);
+        for (int k = seg.k0; ok && k < seg.k1; ++k, ++f) {
+          const int32_t next = k + 1 < seg.k1 ? page_of(seg, k + 1) : 0;
+          load_tile(seg, k, pid, f, 1);
+          pid = next;
+        }
+      }
+      if (!ok) {  // every copy in flight lands before the block's memory is released
+        volatile int never = 0;
+        for (uint32_t i = f > (uint32_t)NV ? f - NV : 0; i < f; ++i) mbar_wait(v_full + 8 * (i % NV), (i / NV) & 1, &never, 200000000ll);
+      }
+    } else {
+    SpanWalk walk(a, pl, pre, s_size, s_len, s_cnt);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) pl.cut_unit[blockIdx.x] = walk.inside ? walk.unit() : -1;
+    uint32_t q_uses[2] = {0, 0};
+    int j = 0;  // segments so far
     auto load_q = [&](const SpanSeg &s) {
 #pragma unroll
       for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
@@ -405,21 +437,6 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       }
       ++j;
     };
-    // K (w = 0) or V of the block's tile f, tile k of segment s.
-    auto load_tile = [&](const SpanSeg &s, int k, int32_t pid, uint32_t f, int w) {
-      const uint32_t slots = w ? NV : NK, slot = f % slots, full = (w ? v_full : k_full) + 8 * slot;
-      ok = __all_sync(0xffffffffu, ok & mbar_wait((w ? v_empty : k_empty) + 8 * slot, ((f / slots) & 1) ^ 1, abort));
-      if (!ok) return;
-      const int t = s.st.token(k * kSpanTile + lane * box_rows);
-      const bool page_ok = pid >= 0 && (int64_t)pid < a.kv.num_pages;
-      if (w == 0 && pid != INT32_MIN && !page_ok) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
-      const int row8 = page_ok ? (int)((((int64_t)pid * 2 * h_kv + (w ? h_kv : 0) + s.g) * ps + (t & (ps - 1))) >> 3) : oob;
-      if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
-      __syncwarp();
-      if (lane < boxes)
-        tma_load_4d(sbase + (w ? C::kV : C::kK) + slot * C::kTileBytes + (lane * box_rows >> 3) * C::kGroup, &kvmap, 0, 0, 0, row8, full, pol);
-      __syncwarp();
-    };
     // Publishes the next segment.
     int published = 0;
     auto next_segment = [&]() -> const SpanSeg * {
@@ -435,8 +452,6 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       ++published;
       return more ? to : nullptr;
     };
-    // K runs one tile ahead of V.  At a segment's end its last V goes first: the next queries may have to wait for their buffer.
-    uint32_t f = 0;
     const SpanSeg *seg = next_segment();
     int k = 0;
     int32_t pid = 0;
@@ -444,31 +459,30 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       k = seg->k0;
       pid = page_of(*seg, k);
       load_q(*seg);
-      load_tile(*seg, k, pid, 0, 0);
     }
     while (seg && ok) {
+      // What follows, its page ids on their way.
       const SpanSeg *ns = seg;
       int nk = k + 1;
       const bool turn = nk == seg->k1;
       if (turn) {
-        load_tile(*seg, k, pid, f, 1);
+        load_tile(*seg, k, pid, f, 0);
         ns = next_segment();
         nk = ns ? ns->k0 : 0;
       }
       const int32_t npid = ns ? page_of(*ns, nk) : 0;
+      if (!turn) load_tile(*seg, k, pid, f, 0);
       if (turn && ns) load_q(*ns);
-      if (ns) load_tile(*ns, nk, npid, f + 1, 0);
-      if (!turn) load_tile(*seg, k, pid, f, 1);
       ++f;
       seg = ns;
       k = nk;
       pid = npid;
     }
     pdl_trigger();
-    if (!ok && lane == 0) {  // every copy in flight lands before the block's memory is released
+    if (!ok) {
       volatile int never = 0;
-      for (uint32_t i = f > (uint32_t)NK ? f - NK : 0; i <= f; ++i) mbar_wait(k_full + 8 * (i % NK), (i / NK) & 1, &never, 200000000ll);
-      for (uint32_t i = f > (uint32_t)NV ? f - NV : 0; i <= f; ++i) mbar_wait(v_full + 8 * (i % NV), (i / NV) & 1, &never, 200000000ll);
+      for (uint32_t i = f > (uint32_t)NK ? f - NK : 0; i < f; ++i) mbar_wait(k_full + 8 * (i % NK), (i / NK) & 1, &never, 200000000ll);
+    }
     }
     __syncwarp();
   } else if (warp == kSpanMma || warp == kSpanMma + 1) {
