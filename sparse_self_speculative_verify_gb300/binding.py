@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -672,12 +673,13 @@ class KV4Cache:
 
 
 _empty = torch.empty
+_devices = functools.lru_cache(None)(lambda index: torch.device("cuda", index))  # (an index costs torch.empty 2 us more)
 
 
 def _output(t, name: str, dtype, device: int, shape):
     """(tensor, address) of an output: the caller's, checked, or a new one."""
     if t is None:
-        t = _empty(shape, dtype=dtype, device=device)
+        t = _empty(shape, dtype=dtype, device=_devices(device))
         return t, t.data_ptr()
     return t, _shaped(t, name, dtype, device, shape)
 
