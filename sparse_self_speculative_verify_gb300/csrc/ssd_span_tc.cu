@@ -229,37 +229,6 @@ struct SpanInt {
   static constexpr int value = V;
 };
 
-// Joins a row's parts, block `first`'s slot 1 and slot 0 of the parts - 1 blocks behind it: weights 2^(lse - max) over their
-// sum.  COLS columns from c0 on of row r of the slots, to row `at` of the output.
-template <int D, int ROWS, int COLS>
-__device__ __forceinline__ void span_join_row(const SpanArgs &a, const SpanPlan &pl, int first, int parts, int r, int c0, int64_t at) {
-  auto slot = [&](int k) { return (int64_t)(k ? (first + k) * 2 : first * 2 + 1); };
-  float m = -INFINITY, z = 0.f, o[COLS] = {};
-#pragma unroll 4
-  for (int k = 0; k < parts; ++k) m = fmaxf(m, __ldcg(pl.lse + slot(k) * ROWS + r));
-  const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 2
-  for (int k = 0; k < parts; ++k) {
-    const float w = fast_exp2(__ldcg(pl.lse + slot(k) * ROWS + r) - ref);
-    const float4 *src = reinterpret_cast<const float4 *>(pl.o) + (slot(k) * (D / 4) + c0 / 4) * ROWS + r;
-    z += w;
-#pragma unroll
-    for (int e = 0; e < COLS / 4; ++e) {
-      const float4 v = __ldcg(src + e * ROWS);
-      if (w == 0.f) continue;  // a part that this row sees nothing of left no O
-      o[4 * e] = fmaf(w, v.x, o[4 * e]), o[4 * e + 1] = fmaf(w, v.y, o[4 * e + 1]);
-      o[4 * e + 2] = fmaf(w, v.z, o[4 * e + 2]), o[4 * e + 3] = fmaf(w, v.w, o[4 * e + 3]);
-    }
-  }
-  const float f = 1.f / z;
-  uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + c0);
-#pragma unroll
-  for (int e = 0; e < COLS / 8; ++e)
-    dst[e] = make_uint4(pack_bf16(o[8 * e] * f, o[8 * e + 1] * f), pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f),
-                        pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f), pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f));
-  if (a.lse && c0 == 0) a.lse[at] = (m + log2f(z)) * kLn2;
-}
-
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kSpanThreads, 1)
     span_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap, SpanArgs a, SpanPlan pl) {
@@ -873,33 +842,73 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   if (warp == kSpanMma) tmem_dealloc(tm, 512);
 }
 
-// Joins the parts of the units that blocks share.  Blocks (block, 32 rows; a warp per D / 8 columns): the one of the first that begins inside
-// a unit has that unit; its parts are slot 1 of the block before and slot 0 of every block that begins inside it.
+// Joins the parts of the units that blocks share: weights 2^(lse - max) over their sum.  Blocks (block, 32 rows; a warp per
+// D / 8 columns): the one of the first that begins inside a unit has that unit; its parts are slot 1 of the block before and
+// slot 0 of every block that begins inside it.  What bounds it: latency, three loads that wait for one another.
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(256) span_join_kernel(SpanArgs a, SpanPlan pl) {
   using C = SpanCfg<D, WIDE>;
-  constexpr int COLS = D / 8;  // of a warp
+  constexpr int COLS = D / 8, U = 4;  // columns of a warp, parts in flight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x, r = blockIdx.y * 32 + lane;
   pdl_wait();
   pdl_trigger();
-  const int unit = pl.cut_unit[first];
-  if (unit < 0 || (first > 0 && pl.cut_unit[first - 1] == unit)) return;
-  int parts = 1;  // the block before's, and those that follow
-  for (int t0 = first;; t0 += 32) {
-    const bool same = t0 + lane < pl.blocks && pl.cut_unit[t0 + lane] == unit;
-    const unsigned m = __ballot_sync(0xffffffffu, same);
-    parts += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-    if (m != 0xffffffffu) break;
+  // Lane i: what block first - 1 + i begins inside.
+  const int seen = first - 1 + lane, cut = seen >= 0 && seen < pl.blocks ? pl.cut_unit[seen] : -1;
+  const int unit = __shfl_sync(0xffffffffu, cut, 1);
+  if (unit < 0 || __shfl_sync(0xffffffffu, cut, 0) == unit) return;
+  unsigned others = ~(__ballot_sync(0xffffffffu, cut == unit) | 1u);
+  int parts = others ? __ffs(others) - 1 : 32;
+  for (int t0 = first + 31; !others; t0 += 32) {
+    others = ~__ballot_sync(0xffffffffu, t0 + lane < pl.blocks && pl.cut_unit[t0 + lane] == unit);
+    parts += others ? __ffs(others) - 1 : 32;
   }
-  const int rg = unit % pl.n_groups, bg = unit / pl.n_groups;
-  const int b = bg / a.kv.h_kv, g = bg % a.kv.h_kv;
+  const int rg = unit % pl.n_groups, bg = unit / pl.n_groups, b = bg / a.kv.h_kv, g = bg % a.kv.h_kv;
   int L, c;
   span_sizes(a, b, false, L, c);
-  const int row_nodes = pl.row_nodes, s = r >> 7, node = (r & 127) / a.G;
-  const int i = rg * pl.nodes + s * row_nodes + node;
-  if (node >= row_nodes || i >= c || L - c + i < 0) return;
+  const int s = r >> 7, node = (r & 127) / a.G, i = rg * pl.nodes + s * pl.row_nodes + node;
+  float m = -INFINITY, z = 0.f, o[COLS] = {};
+  for (int k0 = 0; k0 < parts; k0 += U) {
+    float lse[U];
+    float4 v[U][COLS / 4];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t slot = (int64_t)(first - 1 + k0 + k) * 2 + (k0 + k == 0);
+      lse[k] = -INFINITY;
+      if (k0 + k >= parts) continue;
+      lse[k] = pl.lse[slot * C::kRows + r];
+      const float4 *src = reinterpret_cast<const float4 *>(pl.o) + (slot * (D / 4) + warp * (COLS / 4)) * C::kRows + r;
+#pragma unroll
+      for (int e = 0; e < COLS / 4; ++e) v[k][e] = src[e * C::kRows];
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < U; ++k) top = fmaxf(top, lse[k]);
+    const float ref = top == -INFINITY ? 0.f : top, f = fast_exp2(m - ref);
+    m = top;
+    z *= f;
+#pragma unroll
+    for (int e = 0; e < COLS; ++e) o[e] *= f;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const float w = fast_exp2(lse[k] - ref);
+      if (w == 0.f) continue;  // a part that this row sees nothing of left no O
+      z += w;
+#pragma unroll
+      for (int e = 0; e < COLS / 4; ++e) {
+        o[4 * e] = fmaf(w, v[k][e].x, o[4 * e]), o[4 * e + 1] = fmaf(w, v[k][e].y, o[4 * e + 1]);
+        o[4 * e + 2] = fmaf(w, v[k][e].z, o[4 * e + 2]), o[4 * e + 3] = fmaf(w, v[k][e].w, o[4 * e + 3]);
+      }
+    }
+  }
+  if (node >= pl.row_nodes || i >= c || L - c + i < 0) return;
   const int64_t at = ((int64_t)b * a.n + i) * a.h_q + g * a.G + ((r & 127) - node * a.G);
-  span_join_row<D, C::kRows, COLS>(a, pl, first - 1, parts, r, warp * COLS, at);
+  const float f = 1.f / z;
+  uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + warp * COLS);
+#pragma unroll
+  for (int e = 0; e < COLS / 8; ++e)
+    dst[e] = make_uint4(pack_bf16(o[8 * e] * f, o[8 * e + 1] * f), pack_bf16(o[8 * e + 2] * f, o[8 * e + 3] * f),
+                        pack_bf16(o[8 * e + 4] * f, o[8 * e + 5] * f), pack_bf16(o[8 * e + 6] * f, o[8 * e + 7] * f));
+  if (a.lse && warp == 0) a.lse[at] = (m + log2f(z)) * kLn2;
 }
 
 // ------------------------------------------------------------------------------------------------
