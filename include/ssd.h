@@ -485,9 +485,9 @@ int ssd_kv_compact(const ssd_paged_kv *kv, const ssd_paged_kv *to, const int32_t
  *                    most 2^30): the last `window` ones and the request's first `sink`.  Pages that hold no token
  *                    of these are not read; their entries of the page table may be free.
  *   q     device [batch][n][h_q][d] of kv->dtype, 16-byte aligned; h_q / h_kv at most 128.
- *   scale softmax scale, positive and finite.
+ *   scale softmax scale, positive and finite (in units of log2 too).
  *   out   device [batch][n][h_q][d] of kv->dtype, 16-byte aligned; lse device float [batch][n][h_q] or NULL.
- *         Products and sums are held in fp32; over a bf16 cache probabilities are rounded to bf16 (2^-9 of each) before
+ *         Products and sums are held in fp32; over a bf16 cache probabilities are rounded to bf16 (2^-8 of each) before
  *         they meet V.  Rows i >= counts[b], and queries whose position would be negative, get out = 0, lse = -inf.
  *   workspace  device, >= the matching query's bytes, 256-byte aligned.
  * A length outside [counts[b], max_seq_len] and a count outside [0, n] raise SSD_FAULT_SEQLEN and are clamped.  K and V

@@ -672,6 +672,14 @@ class KV4Cache:
         return self._ref
 
 
+def _c_int(v, name: str) -> int:
+    """A whole number that a C int holds (ctypes would keep its low 32 bits)."""
+    v = int(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} {v} out of range")
+    return v
+
+
 _empty = torch.empty
 _devices = functools.lru_cache(None)(lambda index: torch.device("cuda", index))  # (an index costs torch.empty 2 us more)
 
@@ -734,11 +742,11 @@ _STREAM_WS = {}  # (device, stream, name): buffer, aligned address, bytes from t
 _WS_LOCK = threading.RLock()
 
 
-def _stream_ws(device: int, name: str, nbytes: int, workspace: Optional[Workspace]):
+def _stream_ws(device: int, name: str, nbytes: int, workspace: Optional[Workspace], counters: bool = True):
     """Workspace of a call on the current stream: the caller's, or one kept for (device, stream), so that
     calls on different streams never share one; a call under stream capture without a workspace, or with one that an
     earlier call has not made large enough, takes a buffer of its graph's own memory, whose counters a node of the
-    graph clears.  A caller's workspace that graphs were captured with must outlive them, and
+    graph clears (calls without counters need none).  A caller's workspace that graphs were captured with must outlive them, and
     they run one after the other.  Under _WS_LOCK."""
     capturing = _capturing()
     if workspace is not None:
@@ -750,7 +758,8 @@ def _stream_ws(device: int, name: str, nbytes: int, workspace: Optional[Workspac
             return _ws(at, name, nbytes, workspace)
     if capturing:
         buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
-        buf[:COUNTER_BYTES + 256].zero_()
+        if counters:
+            buf[:COUNTER_BYTES + 256].zero_()
         return Workspace.aligned(buf), nbytes
     key = (device, _raw_stream(device), name)
     kept = _STREAM_WS.get(key)
@@ -1019,7 +1028,7 @@ def _span_attn(kv, q, parents, counts, window, sink, scale, out, lse, want_lse, 
                 need = kv._need[key] = L.ssd_tree_workspace_bytes(kv.ref(), h_q, n) if window is None else \
                     L.ssd_window_workspace_bytes(kv.ref(), h_q, n, window, sink)
             with _WS_LOCK:
-                ws, avail = _stream_ws(dev, "span", need, workspace)
+                ws, avail = _stream_ws(dev, "span", need, workspace, False)
                 st = _raw_stream(dev)
                 _check(L.ssd_tree_attn(kv.ref(), pq, h_q, n, pp, pc, scale, po, pl, ws, avail, st) if window is None else
                        L.ssd_window_attn(kv.ref(), pq, h_q, n, pc, window, sink, scale, po, pl, ws, avail, st))
@@ -1040,7 +1049,7 @@ def ssd_window_attn(kv: KVCache, q: torch.Tensor, window: int, sink: int, scale:
     """Attention of each request's last counts[b] (int32 [B]; None: n) tokens, a decoding step's one or a prompt's many, with
     a sliding window: position p sees the tokens t <= p with t > p - window or t < sink.  q [B, n, h_q, d] and out have the
     cache's type.  Rows behind counts[b]: out 0, lse -inf."""
-    return _span_attn(kv, q, None, counts, int(window), int(sink), float(scale), out, lse, want_lse, workspace, stream)
+    return _span_attn(kv, q, None, counts, _c_int(window, "window"), _c_int(sink, "sink"), float(scale), out, lse, want_lse, workspace, stream)
 
 
 def ssd_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, rows: Optional[torch.Tensor] = None, top_k: int = 0,
@@ -1109,7 +1118,7 @@ def ssd_tree_accept(parents: torch.Tensor, tokens: Optional[torch.Tensor], targe
         raise ValueError("logprob and entropy go together")
     pl = _maybe(logprob, "logprob", f32, dev, (B, n))
     pe = _maybe(entropy, "entropy", f32, dev, (B, n))
-    m = n if max_path is None else int(max_path)
+    m = n if max_path is None else _c_int(max_path, "max_path")
     if m < 1:
         raise ValueError(f"max_path {m} < 1")
     with _scope(dev, stream):
@@ -1138,4 +1147,4 @@ def ssd_tree_commit(kv: KVCache, path: torch.Tensor, cnt: torch.Tensor, n: int, 
     if B == 0:
         return
     with _scope(dev, stream):
-        _check(_lib().ssd_tree_commit(kv.ref(), int(n), pc, pp, m, pk, _raw_stream(dev)))
+        _check(_lib().ssd_tree_commit(kv.ref(), _c_int(n, "n"), pc, pp, m, pk, _raw_stream(dev)))

@@ -35,7 +35,7 @@ static int span_attn(const char *who, const ssd_paged_kv *kv, const void *q, int
   SpanArgs a = {};
   int rc = span_args(who, kv, h_q, n, window, sink, tree, &a);
   if (rc) return rc;
-  if (!(scale > 0.f) || isinf(scale)) return fail(SSD_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+  if (!(scale > 0.f) || isinf(scale * kLog2e)) return fail(SSD_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
   if (kv->batch == 0) return SSD_OK;
   if (!q || !out || (tree && !parents)) return fail(SSD_ERR_INVALID_ARG, "%s: a required pointer is NULL", who);
   if (!aligned16(q) || !aligned16(out)) return fail(SSD_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", who);

@@ -28,9 +28,14 @@ constexpr int kSpanProducer = 8, kSpanMma = 9, kSpanLoadV = 11;
 constexpr int kSpanMaxBatch = 1024;     // requests of a launch (their sizes lie in shared memory)
 constexpr int kSpanOverhead = 1;        // what starting and ending a unit costs, in tiles
 constexpr int kSpanSnap = 3;            // a cut this close to a unit's border moves there
-constexpr int kSpanWhole = 6;           // units of so many tiles are not cut
+// Units of more than kSpanWhole tiles are cut; shorter ones where equal shares save more than kSpanJoin tiles, what leaving
+// parts and joining them costs.  (32 requests, 8 heads, 10 tiles: whole 34.9 us, cut 37.5; 100 requests: 87.6 and 84.4; one of
+// 6 tiles: 14.6 and 15.9, of 8: 15 and 14; of 64 requests of up to 12 tiles each their own number, 60 and 63.3.)
+constexpr int kSpanWhole = 12, kSpanJoin = 5;
 // Least share of a block: one request of 1000 tokens, 64 rows, 15.5 us with 4 and 13.5 with 3; 8000 tokens, 256 rows, 28.3 and 30.1.
 constexpr int kSpanLeast = 3, kSpanLeastWide = 4;
+// Every part of a unit has tiles: a cut inside lies behind the overhead, and two of one unit are a share apart.
+static_assert(kSpanSnap > kSpanOverhead && kSpanLeast >= 1 && kSpanLeastWide >= 1, "parts without tiles");
 constexpr float kSpanLazy = 8.f;        // a row's reference moves when a score exceeds it by this (log2)
 
 struct SpanPlan {
@@ -188,7 +193,7 @@ struct SpanWalk {
   }
 };
 
-// 16 columns of this thread's lane of tensor memory (one of the 32-bit registers each).
+// 16 columns of this thread's lane of tensor memory, a register each.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]),
@@ -339,251 +344,251 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
 
   // Registers: 256 x 208 + 128 x 88 are the launch's 384 x 168.
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == kSpanProducer || warp == kSpanLoadV) {
-    // ---------------------------------------------------------------- loads
-    const int box_rows = pl.box, boxes = kSpanTile / box_rows;
-    const uint64_t pol = a.parents && pl.n_groups == 1 ? policy_evict_first() : policy_evict_normal();
-    const int oob = (int)((int64_t)a.kv.num_pages * 2 * h_kv * ps / 8);
-    bool ok = true;
-    // Page of lane's box of tile k, INT32_MIN where nothing of it is seen.
-    auto page_of = [&](const SpanSeg &s, int k) -> int32_t {
-      const int t = s.st.token(k * kSpanTile + lane * box_rows);
-      const bool seen = lane < boxes && t < s.st.hi && (t < s.st.sink || t + box_rows > s.st.lo);
-      return seen ? a.kv.page_table[(int64_t)s.b * a.kv.max_pages + (t >> a.kv.log2_ps)] : INT32_MIN;
-    };
-    // K (w = 0) or V of the block's tile f, tile k of segment s.
-    auto load_tile = [&](const SpanSeg &s, int k, int32_t pid, uint32_t f, int w) {
-      const uint32_t slots = w ? NV : NK, slot = f % slots, full = (w ? v_full : k_full) + 8 * slot;
-      ok = __all_sync(0xffffffffu, ok & mbar_wait((w ? v_empty : k_empty) + 8 * slot, ((f / slots) & 1) ^ 1, abort));
-      if (!ok) return;
-      const int t = s.st.token(k * kSpanTile + lane * box_rows);
-      const bool page_ok = pid >= 0 && (int64_t)pid < a.kv.num_pages;
-      if (w == 0 && pid != INT32_MIN && !page_ok) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
-      const int row8 = page_ok ? (int)((((int64_t)pid * 2 * h_kv + (w ? h_kv : 0) + s.g) * ps + (t & (ps - 1))) >> 3) : oob;
-      if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
-      __syncwarp();
-      if (lane < boxes)
-        tma_load_4d(sbase + (w ? C::kV : C::kK) + slot * C::kTileBytes + (lane * box_rows >> 3) * C::kGroup, &kvmap, 0, 0, 0, row8, full, pol);
-      __syncwarp();
-    };
-    uint32_t f = 0;
-    if (warp == kSpanLoadV) {
-      const SpanSeg *sp;
-      for (int j = 0; ok && (sp = segment(j)); ++j) {
-        const SpanSeg seg = *sp;
-        int32_t pid = page_of(seg, seg.k0);
-        for (int k = seg.k0; ok && k < seg.k1; ++k, ++f) {
-          const int32_t next = k + 1 < seg.k1 ? page_of(seg, k + 1) : 0;
-          load_tile(seg, k, pid, f, 1);
-          pid = next;
-        }
-      }
-      if (!ok) {  // every copy in flight lands before the block's memory is released
-        volatile int never = 0;
-        for (uint32_t i = f > (uint32_t)NV ? f - NV : 0; i < f; ++i) mbar_wait(v_full + 8 * (i % NV), (i / NV) & 1, &never, 200000000ll);
-      }
-    } else {
-    SpanWalk walk(a, pl, pre, s_size, s_len, s_cnt);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) pl.cut_unit[blockIdx.x] = walk.inside ? walk.unit() : -1;
-    uint32_t q_uses[2] = {0, 0};
-    int j = 0;  // segments so far
-    auto load_q = [&](const SpanSeg &s) {
-#pragma unroll
-      for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
-        const int buf = WIDE ? w : j & 1;
-        if (WIDE && w && !second(s)) continue;
-        ok = __all_sync(0xffffffffu, ok & mbar_wait(q_empty + 8 * buf, (q_uses[buf] & 1) ^ 1, abort));
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(q_full + 8 * buf, row_nodes * a.G * D * 2);
-          for (int p = 0; p < C::kPanels; ++p)
-            tma_load_4d(sbase + C::kQ + buf * C::kTileBytes + p * (kSpanTile * 128), &qmap, p * 64, s.g * a.G, s.rg * pl.nodes + w * row_nodes,
-                        s.b, q_full + 8 * buf);
-        }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kSpanProducer || warp == kSpanLoadV) {
+      // ---------------------------------------------------------------- loads
+      const int box_rows = pl.box, boxes = kSpanTile / box_rows;
+      const uint64_t pol = a.parents && pl.n_groups == 1 ? policy_evict_first() : policy_evict_normal();
+      const int oob = (int)((int64_t)a.kv.num_pages * 2 * h_kv * ps / 8);
+      bool ok = true;
+      // Page of lane's box of tile k, INT32_MIN where nothing of it is seen.
+      auto page_of = [&](const SpanSeg &s, int k) -> int32_t {
+        const int t = s.st.token(k * kSpanTile + lane * box_rows);
+        const bool seen = lane < boxes && t < s.st.hi && (t < s.st.sink || t + box_rows > s.st.lo);
+        return seen ? a.kv.page_table[(int64_t)s.b * a.kv.max_pages + (t >> a.kv.log2_ps)] : INT32_MIN;
+      };
+      // K (w = 0) or V of the block's tile f, tile k of segment s.
+      auto load_tile = [&](const SpanSeg &s, int k, int32_t pid, uint32_t f, int w) {
+        const uint32_t slots = w ? NV : NK, slot = f % slots, full = (w ? v_full : k_full) + 8 * slot;
+        ok = __all_sync(0xffffffffu, ok & mbar_wait((w ? v_empty : k_empty) + 8 * slot, ((f / slots) & 1) ^ 1, abort));
+        if (!ok) return;
+        const int t = s.st.token(k * kSpanTile + lane * box_rows);
+        const bool page_ok = pid >= 0 && (int64_t)pid < a.kv.num_pages;
+        if (w == 0 && pid != INT32_MIN && !page_ok) atomicOr(a.status, (unsigned)SSD_FAULT_PAGE);
+        const int row8 = page_ok ? (int)((((int64_t)pid * 2 * h_kv + (w ? h_kv : 0) + s.g) * ps + (t & (ps - 1))) >> 3) : oob;
+        if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
         __syncwarp();
-        ++q_uses[buf];
-      }
-      ++j;
-    };
-    // Publishes the next segment.
-    int published = 0;
-    auto next_segment = [&]() -> const SpanSeg * {
-      SpanSeg x;
-      const bool more = walk.next(x);
-      SpanSeg *to = ring + published % kSpanRing;
-      if (!more) x.b = -1;
-      if (lane == 0) {
-        *to = x;
-        mbar_arrive(seg_full + 8 * (published % kSpanRing));
-      }
-      __syncwarp();
-      ++published;
-      return more ? to : nullptr;
-    };
-    const SpanSeg *seg = next_segment();
-    int k = 0;
-    int32_t pid = 0;
-    if (seg) {
-      k = seg->k0;
-      pid = page_of(*seg, k);
-      load_q(*seg);
-    }
-    while (seg && ok) {
-      // What follows, its page ids on their way.
-      const SpanSeg *ns = seg;
-      int nk = k + 1;
-      const bool turn = nk == seg->k1;
-      if (turn) {
-        load_tile(*seg, k, pid, f, 0);
-        ns = next_segment();
-        nk = ns ? ns->k0 : 0;
-      }
-      const int32_t npid = ns ? page_of(*ns, nk) : 0;
-      if (!turn) load_tile(*seg, k, pid, f, 0);
-      if (turn && ns) load_q(*ns);
-      ++f;
-      seg = ns;
-      k = nk;
-      pid = npid;
-    }
-    pdl_trigger();
-    if (!ok) {
-      volatile int never = 0;
-      for (uint32_t i = f > (uint32_t)NK ? f - NK : 0; i < f; ++i) mbar_wait(k_full + 8 * (i % NK), (i / NK) & 1, &never, 200000000ll);
-    }
-    }
-    __syncwarp();
-  } else if (warp == kSpanMma || warp == kSpanMma + 1) {
-    // ---------------------------------------------------------------- products
-    // WIDE: warp 9 issues for both streams in turn, O += P V of a tile and at once S of the next, so that one stream's
-    // softmax always has the other's products beside it (issued by two warps they fell into step, and the tensor cores idled
-    // during both softmaxes).  Else a warp per stream, which waits for its own tiles only.
-    const int mine = warp - kSpanMma;
-    const uint32_t id_qk = idesc_bf16_f32(128, 128, 0, 0), id_pv = idesc_bf16_f32(128, D, 0, 1);
-    // One elected lane of a converged warp issues, so that the operands stay warp-uniform: from a lane chosen by its number an
-    // instruction took 95 clocks.
-    const uint64_t qd = smem_desc(sbase + C::kQ, 16, 1024), kd = smem_desc(sbase + C::kK, 16, C::kGroup), vd = smem_desc(sbase + C::kV, 1024, C::kGroup);
-    const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
-    auto issue_qk = [&](int s, int buf, int slot, bool free_k, bool free_q) {
-      const uint64_t q = qd + (uint64_t)(buf * C::kTileBytes >> 4), k = kd + (uint64_t)(slot * C::kTileBytes >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_ss(tmu + s * 128, q + (uint64_t)(((kk >> 2) * (kSpanTile * 128) + (kk & 3) * 32) >> 4),
-                      k + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0 ? 1u : 0u);
-        mma_commit(s_full + 8 * s);
-        if (free_k) mma_commit(k_empty + 8 * slot);
-        if (free_q) mma_commit(q_empty + 8 * buf);
-      }
-      __syncwarp();
-    };
-    // O += P V of stream s's tile n, a half of the tokens as soon as its half of P is there.
-    auto issue_pv = [&](int s, uint32_t n, int slot, bool first, bool free_v) {
-      const uint64_t v = vd + (uint64_t)(slot * C::kTileBytes >> 4);
-      const uint32_t acc = first ? 0u : 1u;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mbar_wait(p_full + 16 * h + 8 * s, n & 1, abort);
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-            mma_bf16_ts(tmu + C::kColO + s * 128, tmu + s * 128 + kk * 8, v + (uint64_t)((kk * 2 * C::kGroup) >> 4), id_pv, kk > 0 ? 1u : acc);
-          if (h) {
-            mma_commit(o_done + 8 * s);
-            if (free_v) mma_commit(v_empty + 8 * slot);
+        if (lane < boxes)
+          tma_load_4d(sbase + (w ? C::kV : C::kK) + slot * C::kTileBytes + (lane * box_rows >> 3) * C::kGroup, &kvmap, 0, 0, 0, row8, full, pol);
+        __syncwarp();
+      };
+      uint32_t f = 0;
+      if (warp == kSpanLoadV) {
+        const SpanSeg *sp;
+        for (int j = 0; ok && (sp = segment(j)); ++j) {
+          const SpanSeg seg = *sp;
+          int32_t pid = page_of(seg, seg.k0);
+          for (int k = seg.k0; ok && k < seg.k1; ++k, ++f) {
+            const int32_t next = k + 1 < seg.k1 ? page_of(seg, k + 1) : 0;
+            load_tile(seg, k, pid, f, 1);
+            pid = next;
           }
         }
-        __syncwarp();
-      }
-    };
-    // Rows of V that nobody sees may hold anything, and 0 times it has to be 0: the places from `end` on and those in [from, to).
-    auto clear_unseen = [&](int end, int from, int to, int t0, int slot) {
-      if (t0 + kSpanTile <= end && (t0 + kSpanTile <= from || t0 >= to || from >= to)) return;
-      constexpr int CPR = D / 8;  // 16-byte pieces of a row
-      char *v = sm + C::kV + slot * C::kTileBytes;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      auto rows = [&](int r0, int r1) {  // at most a group's
-        const int c = lane % CPR;
-#pragma unroll 1
-        for (int r = r0 + lane / CPR; r < r1; r += 32 / CPR)
-          *reinterpret_cast<uint4 *>(v + (r >> 3) * C::kGroup + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16) = zero;
-      };
-      auto range = [&](int r0, int r1) {
-        if (r0 >= r1) return;
-        const int g0 = (r0 + 7) & ~7, g1 = r1 & ~7;
-        if (g0 > g1) return rows(r0, r1);
-        rows(r0, g0);
-        uint4 *at = reinterpret_cast<uint4 *>(v + (g0 >> 3) * C::kGroup) + lane;  // whole groups lie together
-        for (int g = g0; g < g1; g += 8, at += C::kGroup / 16)
-#pragma unroll
-          for (int e = 0; e < C::kGroup / 512; ++e) at[32 * e] = zero;
-        rows(g1, r1);
-      };
-      range(max(0, end - t0), kSpanTile);
-      range(max(0, from - t0), min(kSpanTile, to - t0));
-      fence_proxy_async_smem();
-      __syncwarp();
-    };
-    uint32_t f = 0;  // tiles of the block
-    if (WIDE && mine == 0) {
-      uint32_t n[2] = {0, 0}, q_uses[2] = {0, 0};
-      const SpanSeg *sp;
-      for (int j = 0; (sp = segment(j)); ++j) {
-        const SpanSeg seg = *sp;
-        const int streams = second(seg) ? 2 : 1;
-        mbar_wait(k_full + 8 * (f % NK), (f / NK) & 1, abort);
-        for (int s = 0; s < streams; ++s) {
-          mbar_wait(q_full + 8 * s, q_uses[s]++ & 1, abort);
-          tc_fence_after();
-          issue_qk(s, s, f % NK, s == streams - 1, seg.k1 - seg.k0 == 1);
+        if (!ok) {  // every copy in flight lands before the block's memory is released
+          volatile int never = 0;
+          for (uint32_t i = f > (uint32_t)NV ? f - NV : 0; i < f; ++i) mbar_wait(v_full + 8 * (i % NV), (i / NV) & 1, &never, 200000000ll);
         }
-        for (int k = seg.k0; k < seg.k1; ++k, ++f) {
-          const int slot = f % NV, nslot = (f + 1) % NK;
-          mbar_wait(v_full + 8 * slot, (f / NV) & 1, abort);
-          clear_unseen(seg.st.hi + seg.st.off, seg.st.sink, seg.st.lo + seg.st.off, k * kSpanTile, slot);
+      } else {
+        SpanWalk walk(a, pl, pre, s_size, s_len, s_cnt);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) pl.cut_unit[blockIdx.x] = walk.inside ? walk.unit() : -1;
+        uint32_t q_uses[2] = {0, 0};
+        int j = 0;  // segments so far
+        auto load_q = [&](const SpanSeg &s) {
+#pragma unroll
+          for (int w = 0; w < (WIDE ? 2 : 1); ++w) {
+            const int buf = WIDE ? w : j & 1;
+            if (WIDE && w && !second(s)) continue;
+            ok = __all_sync(0xffffffffu, ok & mbar_wait(q_empty + 8 * buf, (q_uses[buf] & 1) ^ 1, abort));
+            if (ok && lane == 0) {
+              mbar_arrive_expect_tx(q_full + 8 * buf, row_nodes * a.G * D * 2);
+              for (int p = 0; p < C::kPanels; ++p)
+                tma_load_4d(sbase + C::kQ + buf * C::kTileBytes + p * (kSpanTile * 128), &qmap, p * 64, s.g * a.G, s.rg * pl.nodes + w * row_nodes,
+                            s.b, q_full + 8 * buf);
+            }
+            __syncwarp();
+            ++q_uses[buf];
+          }
+          ++j;
+        };
+        // Publishes the next segment.
+        int published = 0;
+        auto next_segment = [&]() -> const SpanSeg * {
+          SpanSeg x;
+          const bool more = walk.next(x);
+          SpanSeg *to = ring + published % kSpanRing;
+          if (!more) x.b = -1;
+          if (lane == 0) {
+            *to = x;
+            mbar_arrive(seg_full + 8 * (published % kSpanRing));
+          }
+          __syncwarp();
+          ++published;
+          return more ? to : nullptr;
+        };
+        const SpanSeg *seg = next_segment();
+        int k = 0;
+        int32_t pid = 0;
+        if (seg) {
+          k = seg->k0;
+          pid = page_of(*seg, k);
+          load_q(*seg);
+        }
+        while (seg && ok) {
+          // What follows, its page ids on their way.
+          const SpanSeg *ns = seg;
+          int nk = k + 1;
+          const bool turn = nk == seg->k1;
+          if (turn) {
+            load_tile(*seg, k, pid, f, 0);
+            ns = next_segment();
+            nk = ns ? ns->k0 : 0;
+          }
+          const int32_t npid = ns ? page_of(*ns, nk) : 0;
+          if (!turn) load_tile(*seg, k, pid, f, 0);
+          if (turn && ns) load_q(*ns);
+          ++f;
+          seg = ns;
+          k = nk;
+          pid = npid;
+        }
+        pdl_trigger();
+        if (!ok) {
+          volatile int never = 0;
+          for (uint32_t i = f > (uint32_t)NK ? f - NK : 0; i < f; ++i) mbar_wait(k_full + 8 * (i % NK), (i / NK) & 1, &never, 200000000ll);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kSpanMma || warp == kSpanMma + 1) {
+      // ---------------------------------------------------------------- products
+      // WIDE: warp 9 issues for both streams in turn, O += P V of a tile and at once S of the next, so that one stream's
+      // softmax always has the other's products beside it (issued by two warps they fell into step, and the tensor cores idled
+      // during both softmaxes).  Else a warp per stream, which waits for its own tiles only.
+      const int mine = warp - kSpanMma;
+      const uint32_t id_qk = idesc_bf16_f32(128, 128, 0, 0), id_pv = idesc_bf16_f32(128, D, 0, 1);
+      // One elected lane of a converged warp issues, so that the operands stay warp-uniform: from a lane chosen by its number an
+      // instruction took 95 clocks.
+      const uint64_t qd = smem_desc(sbase + C::kQ, 16, 1024), kd = smem_desc(sbase + C::kK, 16, C::kGroup), vd = smem_desc(sbase + C::kV, 1024, C::kGroup);
+      const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
+      auto issue_qk = [&](int s, int buf, int slot, bool free_k, bool free_q) {
+        const uint64_t q = qd + (uint64_t)(buf * C::kTileBytes >> 4), k = kd + (uint64_t)(slot * C::kTileBytes >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16_ss(tmu + s * 128, q + (uint64_t)(((kk >> 2) * (kSpanTile * 128) + (kk & 3) * 32) >> 4),
+                        k + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0 ? 1u : 0u);
+          mma_commit(s_full + 8 * s);
+          if (free_k) mma_commit(k_empty + 8 * slot);
+          if (free_q) mma_commit(q_empty + 8 * buf);
+        }
+        __syncwarp();
+      };
+      // O += P V of stream s's tile n, a half of the tokens as soon as its half of P is there.
+      auto issue_pv = [&](int s, uint32_t n, int slot, bool first, bool free_v) {
+        const uint64_t v = vd + (uint64_t)(slot * C::kTileBytes >> 4);
+        const uint32_t acc = first ? 0u : 1u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mbar_wait(p_full + 16 * h + 8 * s, n & 1, abort);
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              mma_bf16_ts(tmu + C::kColO + s * 128, tmu + s * 128 + kk * 8, v + (uint64_t)((kk * 2 * C::kGroup) >> 4), id_pv, kk > 0 ? 1u : acc);
+            if (h) {
+              mma_commit(o_done + 8 * s);
+              if (free_v) mma_commit(v_empty + 8 * slot);
+            }
+          }
+          __syncwarp();
+        }
+      };
+      // Rows of V that nobody sees may hold anything, and 0 times it has to be 0: the places from `end` on and those in [from, to).
+      auto clear_unseen = [&](int end, int from, int to, int t0, int slot) {
+        if (t0 + kSpanTile <= end && (t0 + kSpanTile <= from || t0 >= to || from >= to)) return;
+        constexpr int CPR = D / 8;  // 16-byte pieces of a row
+        char *v = sm + C::kV + slot * C::kTileBytes;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        auto rows = [&](int r0, int r1) {  // at most a group's
+          const int c = lane % CPR;
+#pragma unroll 1
+          for (int r = r0 + lane / CPR; r < r1; r += 32 / CPR)
+            *reinterpret_cast<uint4 *>(v + (r >> 3) * C::kGroup + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16) = zero;
+        };
+        auto range = [&](int r0, int r1) {
+          if (r0 >= r1) return;
+          const int g0 = (r0 + 7) & ~7, g1 = r1 & ~7;
+          if (g0 > g1) return rows(r0, r1);
+          rows(r0, g0);
+          uint4 *at = reinterpret_cast<uint4 *>(v + (g0 >> 3) * C::kGroup) + lane;  // whole groups lie together
+          for (int g = g0; g < g1; g += 8, at += C::kGroup / 16)
+#pragma unroll
+            for (int e = 0; e < C::kGroup / 512; ++e) at[32 * e] = zero;
+          rows(g1, r1);
+        };
+        range(max(0, end - t0), kSpanTile);
+        range(max(0, from - t0), min(kSpanTile, to - t0));
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      uint32_t f = 0;  // tiles of the block
+      if (WIDE && mine == 0) {
+        uint32_t n[2] = {0, 0}, q_uses[2] = {0, 0};
+        const SpanSeg *sp;
+        for (int j = 0; (sp = segment(j)); ++j) {
+          const SpanSeg seg = *sp;
+          const int streams = second(seg) ? 2 : 1;
+          mbar_wait(k_full + 8 * (f % NK), (f / NK) & 1, abort);
           for (int s = 0; s < streams; ++s) {
-            issue_pv(s, n[s]++, slot, k == seg.k0, s == streams - 1);
-            if (k + 1 < seg.k1) {
-              if (s == 0) {
-                mbar_wait(k_full + 8 * nslot, ((f + 1) / NK) & 1, abort);
-                tc_fence_after();
+            mbar_wait(q_full + 8 * s, q_uses[s]++ & 1, abort);
+            tc_fence_after();
+            issue_qk(s, s, f % NK, s == streams - 1, seg.k1 - seg.k0 == 1);
+          }
+          for (int k = seg.k0; k < seg.k1; ++k, ++f) {
+            const int slot = f % NV, nslot = (f + 1) % NK;
+            mbar_wait(v_full + 8 * slot, (f / NV) & 1, abort);
+            clear_unseen(seg.st.hi + seg.st.off, seg.st.sink, seg.st.lo + seg.st.off, k * kSpanTile, slot);
+            for (int s = 0; s < streams; ++s) {
+              issue_pv(s, n[s]++, slot, k == seg.k0, s == streams - 1);
+              if (k + 1 < seg.k1) {
+                if (s == 0) {
+                  mbar_wait(k_full + 8 * nslot, ((f + 1) / NK) & 1, abort);
+                  tc_fence_after();
+                }
+                issue_qk(s, s, nslot, s == streams - 1, k + 2 == seg.k1);
               }
-              issue_qk(s, s, nslot, s == streams - 1, k + 2 == seg.k1);
             }
           }
         }
       }
-    }
-    if (!WIDE) {
-      const int s = mine;
-      uint32_t n = 0;
-      const SpanSeg *sp;
-      for (int j = 0; (sp = segment(j)); ++j) {
-        const SpanSeg seg = *sp;
-        mbar_wait(q_full + 8 * (j & 1), (j >> 1) & 1, abort);
-        bool first = true;
-        for (int k = seg.k0; k < seg.k1; ++k, ++f) {
-          if ((f & 1) != (uint32_t)s) continue;
-          const int slot = f % NV;
-          mbar_wait(k_full + 8 * (f % NK), (f / NK) & 1, abort);
-          tc_fence_after();
-          issue_qk(s, j & 1, f % NK, true, false);
-          mbar_wait(v_full + 8 * slot, (f / NV) & 1, abort);
-          clear_unseen(seg.st.hi + seg.st.off, seg.st.sink, seg.st.lo + seg.st.off, k * kSpanTile, slot);
-          issue_pv(s, n++, slot, first, true);
-          first = false;
+      if (!WIDE) {
+        const int s = mine;
+        uint32_t n = 0;
+        const SpanSeg *sp;
+        for (int j = 0; (sp = segment(j)); ++j) {
+          const SpanSeg seg = *sp;
+          mbar_wait(q_full + 8 * (j & 1), (j >> 1) & 1, abort);
+          bool first = true;
+          for (int k = seg.k0; k < seg.k1; ++k, ++f) {
+            if ((f & 1) != (uint32_t)s) continue;
+            const int slot = f % NV;
+            mbar_wait(k_full + 8 * (f % NK), (f / NK) & 1, abort);
+            tc_fence_after();
+            issue_qk(s, j & 1, f % NK, true, false);
+            mbar_wait(v_full + 8 * slot, (f / NV) & 1, abort);
+            clear_unseen(seg.st.hi + seg.st.off, seg.st.sink, seg.st.lo + seg.st.off, k * kSpanTile, slot);
+            issue_pv(s, n++, slot, first, true);
+            first = false;
+          }
         }
       }
+      if (elect_one()) mma_commit(drained + 8 * mine);
+      __syncwarp();
+      volatile int never = 0;
+      mbar_wait(drained + 8 * mine, 0, &never);
+      __syncwarp();
     }
-    if (elect_one()) mma_commit(drained + 8 * mine);
-    __syncwarp();
-    volatile int never = 0;
-    mbar_wait(drained + 8 * mine, 0, &never);
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------------------------------------------------------- softmax, O
@@ -937,7 +942,9 @@ static SpanPlan span_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
   p.blocks = sm_count();
   p.least = span_wide(a) ? kSpanLeastWide : kSpanLeast;
   p.box = kv->page_size < 16 ? kv->page_size : 16;
-  p.split = span_most_tiles(kv, a, p) > kSpanWhole;
+  const int64_t unit = span_most_tiles(kv, a, p) + kSpanOverhead, units = (int64_t)kv->batch * kv->h_kv * p.n_groups;
+  const int64_t share = units * unit / p.blocks, longest = cdiv64(units, p.blocks) * unit;
+  p.split = unit - kSpanOverhead > kSpanWhole || longest > (share > p.least ? share : p.least) + kSpanJoin;
   return p;
 }
 

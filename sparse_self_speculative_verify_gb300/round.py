@@ -195,7 +195,7 @@ class TreeRound:
 
     def score(self, logits: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor, top_k: int = 0, stream=None) -> dict:
         """Every node's log probability under its parent's row (a root's: 0), every row's entropy and top_k alternatives.
-        logits [B * n, vocab]; tokens, parents int32 [B, n]."""
+        logits [B * n, vocab]; tokens, parents int32 [B, n], a parent of -1 behind a tree's counts."""
         with torch.cuda.stream(stream) if stream is not None else _nullcontext():
             torch.add(parents, self._first, out=self._rows)
             self._rows.masked_fill_(parents < 0, -1)
@@ -205,6 +205,8 @@ class TreeRound:
     def accept(self, parents: torch.Tensor, tokens: torch.Tensor, target: torch.Tensor, counts: Optional[torch.Tensor] = None,
                epsilon: Optional[float] = None, delta: Optional[float] = None, stream=None) -> dict:
         """The path that stays, by equality with ``target`` or, with epsilon and delta, by the last ``score``."""
+        if (epsilon is None) != (delta is None):
+            raise ValueError("epsilon and delta go together")
         more = {} if epsilon is None else dict(logprob=self.logprob, entropy=self.entropy, epsilon=epsilon, delta=delta)
         return B.ssd_tree_accept(parents, tokens, target, counts=counts, max_path=self.max_path, path=self.path, cnt=self.cnt,
                                  next=self.next, advance=self.back, stream=stream, **more)

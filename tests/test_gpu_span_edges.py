@@ -52,6 +52,14 @@ def test_few_long_requests_that_many_blocks_share(n, h_q):
     check(c, run(c))
 
 
+@pytest.mark.parametrize("B,n", [(1, 1), (9, 3), (40, 1), (110, 2)])
+@pytest.mark.parametrize("window", [900, 1300, 2000])
+def test_units_around_the_size_that_is_cut(B, n, window):
+    """Units of 8 to 17 tiles, fewer and more of them than blocks."""
+    lens = [n + (97 * b) % 2100 if b % 5 else 2150 for b in range(B)]
+    check(c := Case(lens, [n] * B, n, 8, 4, 64, 16, BF, seed=B, window=window, sink=6), run(c))
+
+
 def test_scores_that_grow_along_the_cache():
     """The reference of a row moves many times, by more than the exponent of a half."""
     c = Case([3000], [4], 4, 4, 1, 128, 16, BF, seed=3)
@@ -188,12 +196,40 @@ def test_other_streams_and_threads():
     assert all(torch.equal(o, want[i]["out"]) for i in range(2) for o in results[i])
 
 
+def test_two_graphs_replayed_at_once():
+    """Each has its own workspace, captured without a call before it on that stream."""
+    cases = [Case([5000 + 900 * i, 60], [6, 5 + i], 6, 8, 2, 128, 16, BF, seed=30 + i) for i in range(2)]
+    want = [run(c) for c in cases]
+    kvs = [kv_of(c) for c in cases]
+    q, par = [c.q.to(DEV) for c in cases], [torch.from_numpy(c.parents).to(DEV) for c in cases]
+    cnt = [torch.tensor(c.counts, dtype=torch.int32, device=DEV) for c in cases]
+    streams, graphs, outs = [torch.cuda.Stream() for _ in cases], [torch.cuda.CUDAGraph() for _ in cases], []
+    torch.cuda.synchronize()
+    for i in range(2):
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            outs.append(F.ssd_tree_attn(kvs[i], q[i], par[i], cases[i].scale, counts=cnt[i]))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for o in outs:
+            o["out"].zero_()
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                for _ in range(5):
+                    graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o["out"], w["out"]) and torch.equal(o["lse"], w["lse"]) for o, w in zip(outs, want))
+    assert F.ssd_status() == 0
+
+
 def test_refusals_name_what_is_wrong():
     c = Case([40], [3], 3, 4, 2, 64, 8, BF, seed=11)
     kv, q, par = kv_of(c), c.q.to(DEV), torch.from_numpy(c.parents).to(DEV)
     for what, match in ((lambda: F.ssd_tree_attn(kv, q.float(), par, 0.1), "q must be"), (lambda: F.ssd_tree_attn(kv, q[:, :2], par, 0.1), "contiguous|must be"),
                         (lambda: F.ssd_tree_attn(kv, q, par.long(), 0.1), "parents must be"), (lambda: F.ssd_tree_attn(kv, q, par[:, :2].contiguous(), 0.1), "parents must be"),
                         (lambda: F.ssd_tree_attn(kv, q, par, -1.0), "scale"), (lambda: F.ssd_window_attn(kv, q, 0, 0, 0.1), "window"),
+                        (lambda: F.ssd_window_attn(kv, q, (1 << 32) + 8, 0, 0.1), "window"), (lambda: F.ssd_window_attn(kv, q, 8, 1 << 32, 0.1), "sink"),
+                        (lambda: F.TreeRound(kv, 4, 3, 8).accept(par, par, par, epsilon=0.1), "go together"),
                         (lambda: F.ssd_window_attn(kv, q, 5, 0, 0.1, out=torch.empty(q.shape, device=DEV)), "out must be"),
                         (lambda: F.ssd_window_attn(kv, q, 5, 0, 0.1, counts=par), "counts must be"),
                         (lambda: F.ssd_window_attn(kv, q[0], 5, 0, 0.1), "q must be"),

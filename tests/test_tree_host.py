@@ -38,7 +38,7 @@ def _window(lib, kv, **o):
 
 BAD = [(dict(q=None), E), (dict(out=None), E), (dict(q=4104), E), (dict(out=8200), E), (dict(h_q=30), E), (dict(h_q=0), E), (dict(n=0), E),
        (dict(n=-3), E), (dict(h_q=8 * 129), U), (dict(scale=0.0), E), (dict(scale=-0.5), E), (dict(scale=float("nan")), E),
-       (dict(scale=float("inf")), E), (dict(ws=None), W), (dict(wsb=100), W), (dict(ws=(1 << 20) + 16), E)]
+       (dict(scale=float("inf")), E), (dict(scale=3e38), E), (dict(ws=None), W), (dict(wsb=100), W), (dict(ws=(1 << 20) + 16), E)]
 
 
 @pytest.mark.parametrize("dtype", [binding.SSD_DTYPE_BF16, binding.SSD_DTYPE_F32])
@@ -117,3 +117,10 @@ def test_binding_refuses_what_is_not_on_the_device():
         F.ssd_tree_attn(None, i32, i32, 0.1)
     with pytest.raises(TypeError):
         F.ssd_tree_commit(None, i32, i32[:, 0], 4)
+
+
+def test_binding_refuses_what_an_int_does_not_hold():
+    assert binding._c_int(-(1 << 31), "x") == -(1 << 31) and binding._c_int((1 << 31) - 1, "x") == (1 << 31) - 1
+    for v in (1 << 31, (1 << 32) + 5, -(1 << 31) - 1):
+        with pytest.raises(ValueError, match="x .* out of range"):
+            binding._c_int(v, "x")
