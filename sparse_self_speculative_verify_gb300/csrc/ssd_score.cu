@@ -76,8 +76,8 @@ struct ScoreSums {
   }
 };
 
-// Where m is within this, x - m of any finite x (clamped to kScoreLow) is finite.
-constexpr float kScoreFar = 1e36f, kScoreLow = -3e38f;
+// Where m is within kScoreFar, (x - m) log2 e of every x, raised to kScoreLow, is finite.
+constexpr float kScoreFar = 1e36f, kScoreLow = -1e38f;
 
 template <int V>
 struct ScoreInt {
@@ -90,8 +90,13 @@ struct ScoreVec;
 template <>
 struct ScoreVec<float> {
   static constexpr int N = 4;
-  __device__ static float max(const uint4 &v) {
-    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  template <int C = 1>
+  __device__ static float max(const uint4 *v) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < C; ++q)
+      m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(v[q].x), __uint_as_float(v[q].y))), fmaxf(__uint_as_float(v[q].z), __uint_as_float(v[q].w)));
+    return m;
   }
   __device__ static void get(const uint4 &v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
@@ -111,8 +116,11 @@ struct ScoreVec<__nv_bfloat16> {
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
-  __device__ static float max(const uint4 &v) {
-    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+  template <int C = 1>
+  __device__ static float max(const uint4 *v) {
+    uint32_t m = max2(max2(v[0].x, v[0].y), max2(v[0].z, v[0].w));
+#pragma unroll
+    for (int q = 1; q < C; ++q) m = max2(m, max2(max2(v[q].x, v[q].y), max2(v[q].z, v[q].w)));
     return fmaxf(bf16_lo(m), bf16_hi(m));
   }
   __device__ static void get(const uint4 &v, float (&x)[8]) {
@@ -123,7 +131,7 @@ struct ScoreVec<__nv_bfloat16> {
   __device__ static void get_finite(const uint4 &v, float (&x)[8]) {
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(w[i]), "r"(0xff61ff61u));  // about kScoreLow
+    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(w[i]), "r"(0xfe96fe96u));  // about kScoreLow
     get(make_uint4(w[0], w[1], w[2], w[3]), x);
   }
 };
@@ -238,19 +246,24 @@ __global__ void __launch_bounds__(kScoreThreads + 32, kScoreBlocks) score_kernel
   const ScoreRow<T> row(a, r);
   const int v0 = (int)((int64_t)row.nv * rank / ranks), v1 = (int)((int64_t)row.nv * (rank + 1) / ranks);
   ScoreSums u = {-3.402823466e38f, 0.f, 0.f};
-  uint64_t s2 = 0, t2 = 0;  // sums of even and odd elements, relative to u.m too
+  // Sums of even and odd elements, in log2 and relative to `ref`, u.m log2 e rounded: one instruction gives (x - m) log2 e.
+  uint64_t s2 = 0, t2 = 0;
+  float ref = 0.f;
+  bool near = false;  // |u.m| is within kScoreFar
   float top = -INFINITY, next = -INFINITY;  // largest element, and the largest of the other stages
   int top_stage = 0;
   const uint64_t log2e2 = pack2(kLog2e, kLog2e);
   auto fold = [&]() {
-    float p, q;
+    if (!near) return;
+    float p, q, d = fmaf(-u.m, kLog2e, ref) * kLn2;  // what the rounding moved the reference by, |m| / 2^24 at most
     unpack2(s2, p, q);
-    u.s += p + q;
+    const float s = p + q;
     unpack2(t2, p, q);
-    u.t += p + q;
+    const float t = fmaf(s, d, (p + q) * kLn2);
+    u.s += fmaf(s, d, s);
+    u.t += fmaf(t, d, t);
     s2 = t2 = 0;
   };
-  bool near = false;        // |u.m| is within kScoreFar
   float limit = u.m;        // a maximum above it moves the reference
   auto far = [&](uint4 v) {  // (the vector turns, so that its words are taken from one place)
 #pragma unroll 1
@@ -266,26 +279,25 @@ __global__ void __launch_bounds__(kScoreThreads + 32, kScoreBlocks) score_kernel
   };
   auto take = [&](const uint4 *v, auto count) {
     constexpr int C = decltype(count)::value;
-    float mx = ScoreVec<T>::max(v[0]);
-#pragma unroll
-    for (int q = 1; q < C; ++q) mx = fmaxf(mx, ScoreVec<T>::max(v[q]));
+    const float mx = ScoreVec<T>::template max<C>(v);
     if (mx > limit) {
       fold();
       u.move(mx);
       limit = mx + kScoreLazy;
       near = fabsf(mx) < kScoreFar;
+      ref = mx * kLog2e;
     }
     if (near) {
-      const uint64_t m2 = pack2(-u.m, -u.m);
+      const uint64_t ref2 = pack2(-ref, -ref);
 #pragma unroll
       for (int q = 0; q < C; ++q) {
         float x[N];
         ScoreVec<T>::get_finite(v[q], x);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-          const uint64_t z = add2(pack2(x[i], x[i + 1]), m2);
+          const uint64_t z = fma2(pack2(x[i], x[i + 1]), log2e2, ref2);
           float y0, y1;
-          unpack2(mul2(z, log2e2), y0, y1);
+          unpack2(z, y0, y1);
           const uint64_t e = pack2(fast_exp2(y0), fast_exp2(y1));
           s2 = add2(s2, e);
           t2 = fma2(z, e, t2);
@@ -442,7 +454,7 @@ __global__ void __launch_bounds__(kScoreThreads + 32, kScoreBlocks) score_kernel
         }
 #pragma unroll
         for (int q = 0; q < U; ++q)
-          if (at[q] < v1 && ScoreVec<T>::max(w[q]) >= tau) {
+          if (at[q] < v1 && ScoreVec<T>::max(w + q) >= tau) {
             float x[N];
             ScoreVec<T>::get(w[q], x);
 #pragma unroll
