@@ -30,6 +30,7 @@
 
 #include "ssd_kv4_attn.cuh"
 #include "ssd_sm100.cuh"
+#include "ssd_sm100_pairs.cuh"
 
 namespace ssd {
 

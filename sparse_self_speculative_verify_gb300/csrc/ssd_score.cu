@@ -8,13 +8,16 @@
 // A cluster of 1 to 8 blocks takes a row, by distributed shared memory: sums and group maxima are read by the others, candidates
 // are pushed into the first block's list.
 //
-// What bounds it: the bytes of the logits.  A warp of its own brings them to shared memory by bulk copies, two stages of 8 KB
-// a block and eight blocks an SM (loads into registers, taken and used in turn by the same threads, kept half as much in flight:
-// 512 rows of 151936 bf16 took 44 us, 3.5 TB/s).
+// What bounds it: the bytes of the logits where they are many (1000 rows of 151936 bf16: 50 us, 6.0 TB/s), else what comes before
+// and behind them: 512 rows 38.3 us (4.1 TB/s), of which the top 20 are 6 and the start, the ends and the cluster's barriers 6
+// more; one row 8.6.  A warp of its own brings the logits to shared memory by bulk copies, two stages of 8 KB a block and eight
+// blocks an SM (loads into registers, taken and used in turn by the same threads, kept half as much in flight: 44 us where this
+// first took 40).
 #include <cooperative_groups.h>
 
 #include "ssd_host.h"
 #include "ssd_sm100.cuh"
+#include "ssd_sm100_pairs.cuh"
 
 namespace ssd {
 namespace cg = cooperative_groups;

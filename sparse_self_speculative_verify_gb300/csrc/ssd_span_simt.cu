@@ -2,12 +2,12 @@
 //
 // A block of eight warps takes ROWS = 8 RW query rows of one (request, KV head) and a part of their tiles of 64 tokens; a warp
 // has RW rows for itself.  K and V come to shared memory by cp.async, V of a tile while S is computed and K of the next while O
-// is, from row addresses that are looked up one tile ahead.  In S a lane has two tokens and all of the warp's rows: the queries are read by broadcast,
-// and 12 wavefronts of shared memory feed 32 multiply-adds of each lane; in O a lane has four columns (two at d = 64) and all
-// rows.  A row's softmax stays inside its warp.  What bounds it: shared memory and the latencies of
-// a tile's four barriers; 16 requests of 1000 to 4000 tokens, 8 heads of 4 queries, 8 nodes in fp32: 234 us, 22 TFLOP/s (four
-// warps with twice the rows each: 269).  Where the (request, head, rows) blocks do not fill the SMs, each is cut into equal
-// parts of its tiles, joined by span_simt_join_kernel.
+// is, from row addresses that are looked up one tile ahead.  In S a lane has two tokens and all of the warp's rows: the queries
+// are read by broadcast, and 12 wavefronts of shared memory feed 32 multiply-adds of each lane; in O a lane has four columns
+// (two at d = 64) and all rows.  A row's softmax stays inside its warp.  What bounds it: shared memory (69 % busy) and the
+// latencies of a tile's four barriers; 16 requests of 1000 to 4000 tokens, 8 heads of 4 queries, 8 nodes in fp32: 221 us, 23
+// TFLOP/s (four warps with twice the rows each: 269); one request of 300 tokens: 11.4, latency.  Where the (request, head, rows)
+// blocks do not fill the SMs, each is cut into equal parts of its tiles, joined by span_simt_join_kernel.
 #include "ssd_host.h"
 #include "ssd_span.h"
 

@@ -10,14 +10,27 @@
 // Roles: warps 0-3 and 4-7 the softmax of a stream (and its O), warp 8 loads Q and K, warp 11 V (TMA boxes of up to 16 tokens
 // of a page, 128-byte swizzle), warps 9 and 10 issue a stream's products.
 //
+// Softmax.  A row's reference follows its maximum only when that has grown by 2^8, so that O is seldom rescaled; sums, O and
+// references are fp32.  P is rounded to bf16 for the second product (half a step, 2^-8 of each term, whose signs differ: 0.0023
+// of the outputs' 2-norm beside the output type's own 0.0017); the row's sum takes the unrounded P.
+//
+// What bounds it, one GB300, 8 heads of 128 (us a call, launch and join included):
+//   decoding, 128 requests of 8192 tokens: HBM, 612 (7.0 TB/s of K and V);
+//   trees of 16 nodes, 4 heads a group (64 rows), 32 requests of 2048 to 8192 tokens: HBM, 106 to 116 by the draw (5.9 TB/s);
+//   trees of up to 64 nodes, 5 heads a group (3 tiles of rows), 8 requests of 16384 to 65536: 290 to 376 by the draw, the
+//     tensor cores half busy, 3.6 TB/s: groups of 256 rows read K and V for themselves, and the softmax of a tile (128 exponents
+//     a thread) takes as long as the products of the other stream;
+//   4 chunks of up to 4096 prompt tokens, window 2048: 320 to 370 by the draw, 1.33 PFLOP/s, as above; whole prompts 1.36;
+//   one window of 1024 tokens for each of 32 requests: 35, start and the units' ends around 20 us of HBM; one request: 11 to 14.
+//
 // Work.  A unit is one (request, KV head, group of as many queries as a block holds).  The units' tiles lie end to end and are
 // cut into equal shares, one per block (one block per SM); a cut close to a unit's border moves there.  A unit that several
 // blocks share leaves partial results, joined by span_join_kernel.  (Groups of the same head read K and V for themselves: at
 // 256 rows a tile takes longer on the tensor cores than from memory.  Blocks that walked the groups of a head side by side,
 // to read it once, had to do the same work: 8 requests of 33 to 64 nodes with 5 heads a group took 488 us.)
 #include "ssd_sm100.cuh"
+#include "ssd_sm100_pairs.cuh"
 #include "ssd_span.h"
-#include "ssd_tma.h"
 
 namespace ssd {
 using namespace sm100;
@@ -850,7 +863,8 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
 
 // Joins the parts of the units that blocks share: weights 2^(lse - max) over their sum.  Blocks (block, 32 rows; a warp per
 // D / 8 columns): the one of the first that begins inside a unit has that unit; its parts are slot 1 of the block before and
-// slot 0 of every block that begins inside it.  What bounds it: latency, three loads that wait for one another.
+// slot 0 of every block that begins inside it.  What bounds it: latency, three loads that wait for one another, and its launch:
+// 2 to 4 us of a call.  (The last block to arrive joining the parts in the attention kernel took 47 us where this takes 43.)
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(256) span_join_kernel(SpanArgs a, SpanPlan pl) {
   using C = SpanCfg<D, WIDE>;
@@ -921,6 +935,17 @@ __global__ void __launch_bounds__(256) span_join_kernel(SpanArgs a, SpanPlan pl)
 // Host side.
 // ------------------------------------------------------------------------------------------------
 
+// The driver's tensor-map encoder, looked up once; nullptr where it has none.
+static decltype(&cuTensorMapEncodeTiled) span_encoder() {
+  static decltype(&cuTensorMapEncodeTiled) const found = [] {
+    void *at = nullptr;
+    cudaDriverEntryPointQueryResult how = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &at, 12000, cudaEnableDefault, &how) != cudaSuccess) cudaGetLastError();
+    return how == cudaDriverEntryPointSuccess ? reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(at) : nullptr;
+  }();
+  return found;
+}
+
 bool span_tc_takes(const ssd_paged_kv *kv) {
   return kv->dtype == SSD_DTYPE_BF16 && kv->page_size >= 8 && kv->h_kv <= 4096 && (int64_t)kv->num_pages * 2 * kv->h_kv * kv->page_size / 8 < (int64_t)1 << 31;
 }
@@ -976,7 +1001,7 @@ static int span_tc_launch(const CUtensorMap &kvmap, const CUtensorMap &qmap, con
 }
 
 int span_tc(const ssd_paged_kv *kv, const SpanArgs &args, void *workspace, cudaStream_t st) {
-  EncodeTiledFn enc = encode_fn();
+  const auto enc = span_encoder();
   if (!enc) return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   const bool wide = span_wide(args);
   const int d = kv->d, panels = d / 64;

@@ -38,7 +38,6 @@
 //    hardware named barriers.
 #include "ssd_host.h"
 #include "ssd_sm100.cuh"
-#include "ssd_tma.h"
 #include "ssd_verify_tile.cuh"
 
 namespace ssd {
@@ -1013,7 +1012,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // ------------------------------------------------------------------------------------------------
 // Host side.
 // ------------------------------------------------------------------------------------------------
-EncodeTiledFn encode_fn() {
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
   if (!fn) {
     void *p = nullptr;
