@@ -5,13 +5,16 @@
 // is, from row addresses that are looked up one tile ahead.  In S a lane has two tokens and all of the warp's rows: the queries
 // are read by broadcast, and 12 wavefronts of shared memory feed 32 multiply-adds of each lane; in O a lane has four columns
 // (two at d = 64) and all rows.  A row's softmax stays inside its warp.  What bounds it: shared memory (69 % busy) and the
-// latencies of a tile's four barriers; 16 requests of 1000 to 4000 tokens, 8 heads of 4 queries, 8 nodes in fp32: 221 us, 23
-// TFLOP/s (four warps with twice the rows each: 269); one request of 300 tokens: 11.4, latency.  Where the (request, head, rows)
-// blocks do not fill the SMs, each is cut into equal parts of its tiles, joined by span_simt_join_kernel.
+// latencies of a tile's four barriers; 16 requests of 1000 to 4000 tokens, 8 heads of 4 queries, 8 nodes in fp32: 224 us, 23
+// TFLOP/s (231 with unpaired multiply-adds; four warps with twice the rows each: 269; about two blocks an SM instead of eight:
+// 293); one request of 300 tokens: 11.4, latency.  Where the (request, head, rows) blocks do not fill the SMs, each is cut into
+// equal parts of its tiles, joined by span_simt_join_kernel.
 #include "ssd_host.h"
+#include "ssd_sm100_pairs.cuh"
 #include "ssd_span.h"
 
 namespace ssd {
+using namespace sm100;
 
 constexpr int kSimtTile = 64;
 constexpr int kSimtWarps = 8;
@@ -119,25 +122,34 @@ __global__ void __launch_bounds__(kSimtThreads, 2) span_simt_kernel(SpanArgs a, 
     const int t0 = k * kSimtTile;  // its first place
     cp_async_wait<1>();
     __syncthreads();
-    float s[RW][2];
+    uint64_t s2[RW][2];  // sums over even and odd columns
 #pragma unroll
-    for (int i = 0; i < RW; ++i) s[i][0] = s[i][1] = 0.f;
+    for (int i = 0; i < RW; ++i) s2[i][0] = s2[i][1] = 0;
 #pragma unroll 2
     for (int d = 0; d < D; d += 4) {
       const float4 ka = load4<T>(&sm.kv[0][lane][d]), kb = load4<T>(&sm.kv[0][lane + 32][d]);
+      const uint64_t a0 = pack2(ka.x, ka.y), a1 = pack2(ka.z, ka.w), b0 = pack2(kb.x, kb.y), b1 = pack2(kb.z, kb.w);
 #pragma unroll
       for (int i = 0; i < RW; ++i) {
         const float4 q = *reinterpret_cast<const float4 *>(&sm.q[w0 + i][d]);
-        s[i][0] = fmaf(q.x, ka.x, fmaf(q.y, ka.y, fmaf(q.z, ka.z, fmaf(q.w, ka.w, s[i][0]))));
-        s[i][1] = fmaf(q.x, kb.x, fmaf(q.y, kb.y, fmaf(q.z, kb.z, fmaf(q.w, kb.w, s[i][1]))));
+        const uint64_t q0 = pack2(q.x, q.y), q1 = pack2(q.z, q.w);
+        s2[i][0] = fma2(q0, a0, fma2(q1, a1, s2[i][0]));
+        s2[i][1] = fma2(q0, b0, fma2(q1, b1, s2[i][1]));
       }
     }
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
       const int node = (r0 + w0 + i) / a.G;
+      float s[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float even, odd;
+        unpack2(s2[i][h], even, odd);
+        s[h] = even + odd;
+      }
       uint32_t seen[2] = {0u, 0u};
       if (w0 + i < nr && node < c && st.base + node >= 0) span_mask<2>(a, parents, st.base, st.off, node, t0, a.status, seen);
-      const float x0 = (seen[0] >> lane & 1) ? s[i][0] * a.scale_log2 : -INFINITY, x1 = (seen[1] >> lane & 1) ? s[i][1] * a.scale_log2 : -INFINITY;
+      const float x0 = (seen[0] >> lane & 1) ? s[0] * a.scale_log2 : -INFINITY, x1 = (seen[1] >> lane & 1) ? s[1] * a.scale_log2 : -INFINITY;
       const float top = fmaxf(m[i], warp_max(fmaxf(x0, x1))), ref = top == -INFINITY ? 0.f : top;
       const float p0 = exp2f(x0 - ref), p1 = exp2f(x1 - ref), f = exp2f(m[i] - ref);
       m[i] = top;
@@ -153,17 +165,24 @@ __global__ void __launch_bounds__(kSimtThreads, 2) span_simt_kernel(SpanArgs a, 
     __syncthreads();
 #pragma unroll 2
     for (int t = 0; t < kSimtTile; t += 4) {
-      float v[4][CL];
+      uint64_t v[4][CL / 2];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int j = 0; j < CL; j += 2) load2(&sm.kv[1][t + u][lane * CL + j], v[u][j], v[u][j + 1]);
+        for (int j = 0; j < CL; j += 2) {
+          float x, y;
+          load2(&sm.kv[1][t + u][lane * CL + j], x, y);
+          v[u][j / 2] = pack2(x, y);
+        }
 #pragma unroll
       for (int i = 0; i < RW; ++i) {
         const float4 p = *reinterpret_cast<const float4 *>(&sm.p[w0 + i][t]);
+        const uint64_t px = pack2(p.x, p.x), py = pack2(p.y, p.y), pz = pack2(p.z, p.z), pw = pack2(p.w, p.w);
 #pragma unroll
-        for (int j = 0; j < CL; ++j)
-          o[i][j] = fmaf(p.x, v[0][j], fmaf(p.y, v[1][j], fmaf(p.z, v[2][j], fmaf(p.w, v[3][j], o[i][j]))));
+        for (int j = 0; j < CL; j += 2) {
+          const uint64_t sum = fma2(px, v[0][j / 2], fma2(py, v[1][j / 2], fma2(pz, v[2][j / 2], fma2(pw, v[3][j / 2], pack2(o[i][j], o[i][j + 1])))));
+          unpack2(sum, o[i][j], o[i][j + 1]);
+        }
       }
     }
     __syncthreads();
@@ -247,6 +266,8 @@ static SimtPlan simt_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
   const int64_t want = 8 * (int64_t)sm_count();
   int64_t parts = units >= want ? 1 : cdiv64(want, units > 0 ? units : 1);
   if (parts > tiles) parts = tiles;
+  // of two tiles at least where the units fill the SMs (7 requests of 64 tokens, 8 heads, 264 rows: 34 us; of one tile: 42)
+  if (units >= 2 * (int64_t)sm_count() && parts > tiles / 2) parts = tiles / 2;
   p.parts = parts < 1 ? 1 : (int)parts;
   return p;
 }
