@@ -9,6 +9,8 @@
 // TFLOP/s (231 with unpaired multiply-adds; four warps with twice the rows each: 269; about two blocks an SM instead of eight:
 // 293); one request of 300 tokens: 11.4, latency.  Where the (request, head, rows) blocks do not fill the SMs, each is cut into
 // equal parts of its tiles, joined by span_simt_join_kernel.
+#include <type_traits>
+
 #include "ssd_host.h"
 #include "ssd_sm100_pairs.cuh"
 #include "ssd_span.h"
@@ -120,23 +122,33 @@ __global__ void __launch_bounds__(kSimtThreads, 2) span_simt_kernel(SpanArgs a, 
   look_up(k0 + 1);
   for (int k = k0; k < k1; ++k) {
     const int t0 = k * kSimtTile;  // its first place
+    const int end = st.hi + st.off - t0;  // nothing is seen from this place of the tile on
     cp_async_wait<1>();
     __syncthreads();
     uint64_t s2[RW][2];  // sums over even and odd columns
 #pragma unroll
     for (int i = 0; i < RW; ++i) s2[i][0] = s2[i][1] = 0;
+    auto products = [&](auto both) {
 #pragma unroll 2
-    for (int d = 0; d < D; d += 4) {
-      const float4 ka = load4<T>(&sm.kv[0][lane][d]), kb = load4<T>(&sm.kv[0][lane + 32][d]);
-      const uint64_t a0 = pack2(ka.x, ka.y), a1 = pack2(ka.z, ka.w), b0 = pack2(kb.x, kb.y), b1 = pack2(kb.z, kb.w);
+      for (int d = 0; d < D; d += 4) {
+        const float4 ka = load4<T>(&sm.kv[0][lane][d]);
+        const uint64_t a0 = pack2(ka.x, ka.y), a1 = pack2(ka.z, ka.w);
+        float4 kb = {};
+        if (decltype(both)::value) kb = load4<T>(&sm.kv[0][lane + 32][d]);
+        const uint64_t b0 = pack2(kb.x, kb.y), b1 = pack2(kb.z, kb.w);
 #pragma unroll
-      for (int i = 0; i < RW; ++i) {
-        const float4 q = *reinterpret_cast<const float4 *>(&sm.q[w0 + i][d]);
-        const uint64_t q0 = pack2(q.x, q.y), q1 = pack2(q.z, q.w);
-        s2[i][0] = fma2(q0, a0, fma2(q1, a1, s2[i][0]));
-        s2[i][1] = fma2(q0, b0, fma2(q1, b1, s2[i][1]));
+        for (int i = 0; i < RW; ++i) {
+          const float4 q = *reinterpret_cast<const float4 *>(&sm.q[w0 + i][d]);
+          const uint64_t q0 = pack2(q.x, q.y), q1 = pack2(q.z, q.w);
+          s2[i][0] = fma2(q0, a0, fma2(q1, a1, s2[i][0]));
+          if (decltype(both)::value) s2[i][1] = fma2(q0, b0, fma2(q1, b1, s2[i][1]));
+        }
       }
-    }
+    };
+    if (end > 32)
+      products(std::true_type());
+    else
+      products(std::false_type());
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
       const int node = (r0 + w0 + i) / a.G;
@@ -164,7 +176,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) span_simt_kernel(SpanArgs a, 
     cp_async_wait<1>();
     __syncthreads();
 #pragma unroll 2
-    for (int t = 0; t < kSimtTile; t += 4) {
+    for (int t = 0; t < min(end, kSimtTile); t += 4) {
       uint64_t v[4][CL / 2];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
