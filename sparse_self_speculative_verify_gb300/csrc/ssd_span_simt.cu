@@ -7,7 +7,7 @@
 // (two at d = 64) and all rows.  A row's softmax stays inside its warp.  What bounds it: shared memory (69 % busy) and the
 // latencies of a tile's four barriers; 16 requests of 1000 to 4000 tokens, 8 heads of 4 queries, 8 nodes in fp32: 224 us, 23
 // TFLOP/s (231 with unpaired multiply-adds; four warps with twice the rows each: 269; about two blocks an SM instead of eight:
-// 293); one request of 300 tokens: 11.4, latency.  Where the (request, head, rows) blocks do not fill the SMs, each is cut into
+// 293); one request of 300 tokens: 10, latency.  Where the (request, head, rows) blocks do not fill the SMs, each is cut into
 // equal parts of its tiles, joined by span_simt_join_kernel.
 #include <type_traits>
 
@@ -258,22 +258,27 @@ __global__ void __launch_bounds__(256) span_simt_join_kernel(SpanArgs a, SimtPla
   if (a.lse && lane == 0) a.lse[at] = z > 0.f || z != z ? (m + log2f(z)) * kLn2 : -INFINITY;
 }
 
-// Rows of a block: 8, 16 or 32, as few as cover a head's.
-static int simt_rows(const SpanArgs &a) {
+// Tiles of a chunk of `rows` rows, at most: the sinks', the window's and those that its ends cut.
+static int64_t simt_tiles(const ssd_paged_kv *kv, const SpanArgs &a, int rows) {
+  const int64_t all = cdiv(kv->max_seq_len, kSimtTile);
+  const int64_t most = cdiv64(a.sink, kSimtTile) + ((int64_t)a.window + rows / a.G) / kSimtTile + 2;
+  return all < most ? all : most;
+}
+
+// Rows of a block: 32, or 8 or 16 where these cover a head's or where all tiles of such chunks are on the SMs at once.  (One
+// request of 300 tokens, 2 heads of 64, 20 rows: 10 us by 8 rows, 11.2 by 32; of 400 tokens, 8 heads of 128, 32 rows: 11.5 and 14.6.)
+static int simt_rows(const ssd_paged_kv *kv, const SpanArgs &a) {
   const int64_t rows = (int64_t)a.n * a.G;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  for (int r = 8; r < 32; r *= 2)
+    if (rows <= r || (int64_t)kv->batch * kv->h_kv * cdiv64(rows, r) * simt_tiles(kv, a, r) <= 2 * sm_count()) return r;
+  return 32;
 }
 
 static SimtPlan simt_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
-  const int rows = simt_rows(a);
+  const int rows = simt_rows(kv, a);
   SimtPlan p = {};
   p.chunks = (int)cdiv64((int64_t)a.n * a.G, rows);
-  const int64_t units = (int64_t)kv->batch * kv->h_kv * p.chunks;
-  // tiles of a chunk, at most: the sinks', the window's and those that its ends cut
-  const int64_t all = cdiv(kv->max_seq_len, kSimtTile);
-  const int64_t tiles = all < cdiv64(a.sink, kSimtTile) + ((int64_t)a.window + rows / a.G) / kSimtTile + 2
-                            ? all
-                            : cdiv64(a.sink, kSimtTile) + ((int64_t)a.window + rows / a.G) / kSimtTile + 2;
+  const int64_t units = (int64_t)kv->batch * kv->h_kv * p.chunks, tiles = simt_tiles(kv, a, rows);
   // about eight blocks per SM (one request of 300 tokens, 2 heads, 20 rows in fp32: two tiles a part 22 us, one 12)
   const int64_t want = 8 * (int64_t)sm_count();
   int64_t parts = units >= want ? 1 : cdiv64(want, units > 0 ? units : 1);
@@ -288,7 +293,7 @@ static size_t simt_carve(const ssd_paged_kv *kv, const SpanArgs &a, SimtPlan &p,
   Carver c(ws);
   c.take<char>(kCounterBytes);
   if (p.parts > 1) {
-    const size_t items = (size_t)kv->batch * kv->h_kv * p.chunks * p.parts, rows = simt_rows(a);
+    const size_t items = (size_t)kv->batch * kv->h_kv * p.chunks * p.parts, rows = simt_rows(kv, a);
     p.o = c.take<float>(items * rows * kv->d);
     p.lse = c.take<float>(items * rows);
   }
@@ -315,7 +320,7 @@ static int simt_launch(const ssd_paged_kv *kv, const SpanArgs &a, const SimtPlan
 
 template <typename T, int D>
 static int simt_launch_rows(const ssd_paged_kv *kv, const SpanArgs &a, const SimtPlan &p, cudaStream_t st) {
-  const int rows = simt_rows(a);
+  const int rows = simt_rows(kv, a);
   return rows == 8 ? simt_launch<T, D, 8>(kv, a, p, st) : rows == 16 ? simt_launch<T, D, 16>(kv, a, p, st) : simt_launch<T, D, 32>(kv, a, p, st);
 }
 
