@@ -265,12 +265,14 @@ static int64_t simt_tiles(const ssd_paged_kv *kv, const SpanArgs &a, int rows) {
   return all < most ? all : most;
 }
 
-// Rows of a block: 32, or 8 or 16 where these cover a head's or where all tiles of such chunks are on the SMs at once.  (One
-// request of 300 tokens, 2 heads of 64, 20 rows: 10 us by 8 rows, 11.2 by 32; of 400 tokens, 8 heads of 128, 32 rows: 11.5 and 14.6.)
+// Rows of a block: 32, or 8 or 16 where these cover a head's or where all tiles of such chunks are on the SMs at once, two an SM or
+// four at d = 64.  (One request of 300 tokens, 2 heads of 64, 20 rows: 10 us by 8 rows, 11.2 by 32; of 400 tokens, 8 heads of
+// 128, 32 rows: 11.5 and 14.6.  Up to twice as many blocks, d = 64 with 256 rows: 12.5, else 13.7; d = 128, two of 800 tokens:
+// 25.3, else 20.8.)
 static int simt_rows(const ssd_paged_kv *kv, const SpanArgs &a) {
   const int64_t rows = (int64_t)a.n * a.G;
   for (int r = 8; r < 32; r *= 2)
-    if (rows <= r || (int64_t)kv->batch * kv->h_kv * cdiv64(rows, r) * simt_tiles(kv, a, r) <= 2 * sm_count()) return r;
+    if (rows <= r || (int64_t)kv->batch * kv->h_kv * cdiv64(rows, r) * simt_tiles(kv, a, r) <= 256 / kv->d * sm_count()) return r;
   return 32;
 }
 
