@@ -265,7 +265,8 @@ static int64_t simt_tiles(const ssd_paged_kv *kv, const SpanArgs &a, int rows) {
   return all < most ? all : most;
 }
 
-// Rows of a block: 32, or 8 or 16 where these cover a head's or where all tiles of such chunks are on the SMs at once, two an SM or
+// Rows of a block: 32; 48, which take 1.45 times as long, where that saves one of two or three chunks (36 rows 166 us, by 32 218; 72 rows
+// 621 and 664; 256 rows 235 and 217, so not there); or 8 or 16 where these cover a head's or where all tiles of such chunks are on the SMs at once, two an SM or
 // four at d = 64.  (One request of 300 tokens, 2 heads of 64, 20 rows: 10 us by 8 rows, 11.2 by 32; of 400 tokens, 8 heads of
 // 128, 32 rows: 11.5 and 14.6.  Up to twice as many blocks, d = 64 with 256 rows: 12.5, else 13.7; d = 128, two of 800 tokens:
 // 25.3, else 20.8.)
@@ -273,7 +274,7 @@ static int simt_rows(const ssd_paged_kv *kv, const SpanArgs &a) {
   const int64_t rows = (int64_t)a.n * a.G;
   for (int r = 8; r < 32; r *= 2)
     if (rows <= r || (int64_t)kv->batch * kv->h_kv * cdiv64(rows, r) * simt_tiles(kv, a, r) <= 256 / kv->d * sm_count()) return r;
-  return 32;
+  return rows > 32 && rows <= 96 && cdiv64(rows, 48) < cdiv64(rows, 32) ? 48 : 32;
 }
 
 static SimtPlan simt_plan(const ssd_paged_kv *kv, const SpanArgs &a) {
@@ -322,8 +323,12 @@ static int simt_launch(const ssd_paged_kv *kv, const SpanArgs &a, const SimtPlan
 
 template <typename T, int D>
 static int simt_launch_rows(const ssd_paged_kv *kv, const SpanArgs &a, const SimtPlan &p, cudaStream_t st) {
-  const int rows = simt_rows(kv, a);
-  return rows == 8 ? simt_launch<T, D, 8>(kv, a, p, st) : rows == 16 ? simt_launch<T, D, 16>(kv, a, p, st) : simt_launch<T, D, 32>(kv, a, p, st);
+  switch (simt_rows(kv, a)) {
+    case 8: return simt_launch<T, D, 8>(kv, a, p, st);
+    case 16: return simt_launch<T, D, 16>(kv, a, p, st);
+    case 32: return simt_launch<T, D, 32>(kv, a, p, st);
+    default: return simt_launch<T, D, 48>(kv, a, p, st);
+  }
 }
 
 int span_simt(const ssd_paged_kv *kv, const SpanArgs &a, void *workspace, cudaStream_t st) {

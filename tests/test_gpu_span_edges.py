@@ -52,6 +52,16 @@ def test_few_long_requests_that_many_blocks_share(n, h_q):
     check(c, run(c))
 
 
+@pytest.mark.parametrize("dtype,d,page", [(F32, 128, 16), (F32, 64, 8), (BF, 128, 4), (BF, 64, 2)])
+@pytest.mark.parametrize("n", [3, 5, 9, 18, 33])
+def test_row_blocks_of_every_size_on_cuda_cores(dtype, d, page, n):
+    """12, 20, 36, 72 and 132 rows a head, more units than fit the SMs at once."""
+    lens = [n + (61 * b) % 280 for b in range(40)]
+    counts = [n - b % 3 for b in range(40)]
+    check(c := Case(lens, counts, n, 8, 2, d, page, dtype, seed=n), run(c))
+    check(c := Case(lens, counts, n, 8, 2, d, page, dtype, seed=n, window=70, sink=2), run(c))
+
+
 @pytest.mark.parametrize("B,n", [(1, 1), (9, 3), (40, 1), (110, 2)])
 @pytest.mark.parametrize("window", [900, 1300, 2000])
 def test_units_around_the_size_that_is_cut(B, n, window):
