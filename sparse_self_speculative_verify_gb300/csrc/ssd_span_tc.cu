@@ -20,7 +20,7 @@
 //   trees of up to 64 nodes, 5 heads a group (3 tiles of rows), 8 requests of 16384 to 65536: 290 to 376 by the draw, the
 //     tensor cores half busy, 3.6 TB/s: groups of 256 rows read K and V for themselves, and the softmax of a tile (128 exponents
 //     a thread) takes as long as the products of the other stream;
-//   4 chunks of up to 4096 prompt tokens, window 2048: 320 to 370 by the draw, 1.33 PFLOP/s, as above; whole prompts 1.36;
+//   4 chunks of up to 4096 prompt tokens, window 2048: 320 to 382 by the draw, 1.33 PFLOP/s, as above; whole prompts 1.36;
 //   one window of 1024 tokens for each of 32 requests: 35, start and the units' ends around 20 us of HBM; one request: 11 to 14.
 //
 // Work.  A unit is one (request, KV head, group of as many queries as a block holds).  The units' tiles lie end to end and are
