@@ -79,8 +79,10 @@ struct ScoreSums {
   }
 };
 
-// Where m is within kScoreFar, (x - m) log2 e of every x, raised to kScoreLow, is finite.
-constexpr float kScoreFar = 1e36f, kScoreLow = -1e38f;
+// Where m is within kScoreFar, m log2 e rounded lies within 1/4 of itself (2^-24 of less than 2^23), so that exponents relative to it are as
+// good as those relative to m; they are finite for every x raised to kScoreLow.  Larger m, and m of banned tokens that hold a large
+// negative number: x - m itself.
+constexpr float kScoreFar = 4194304.f, kScoreLow = -1e38f;
 
 template <int V>
 struct ScoreInt {
@@ -258,13 +260,13 @@ __global__ void __launch_bounds__(kScoreThreads + 32, kScoreBlocks) score_kernel
   const uint64_t log2e2 = pack2(kLog2e, kLog2e);
   auto fold = [&]() {
     if (!near) return;
-    float p, q, d = fmaf(-u.m, kLog2e, ref) * kLn2;  // what the rounding moved the reference by, |m| / 2^24 at most
+    const float d = fmaf(-u.m, kLog2e, ref), f = fast_exp2(d);  // what the rounding moved the reference by, 1/4 at most
+    float p, q;
     unpack2(s2, p, q);
     const float s = p + q;
     unpack2(t2, p, q);
-    const float t = fmaf(s, d, (p + q) * kLn2);
-    u.s += fmaf(s, d, s);
-    u.t += fmaf(t, d, t);
+    u.s = fmaf(s, f, u.s);
+    u.t = fmaf((p + q + s * d) * kLn2, f, u.t);
     s2 = t2 = 0;
   };
   float limit = u.m;        // a maximum above it moves the reference
