@@ -69,8 +69,10 @@ struct SpanSeg {
   int c;              // the request's queries
   SpanTiles st;
 };
-constexpr int kSpanRing = 8;  // segments handed from the producer to the other warps
-// (It is at most kStages tiles ahead of the products, they at most one ahead of the softmax, and every segment has a tile.)
+// Segments handed from the producer to the other warps.  A slot is written again once every warp that reads it has arrived: the loads
+// of V, the products, and the softmax of both streams, of which a WIDE block's second passes over segments without rows for it
+// and is held back by nothing else there.
+constexpr int kSpanRing = 8;
 
 template <int D, bool WIDE>
 struct SpanCfg {
@@ -80,7 +82,8 @@ struct SpanCfg {
   // Slots of K and of V: V is held through the softmax.  (D = 128: all of the shared memory.)
   static constexpr int kSlotsK = D == 128 ? 2 : 4, kSlotsV = D == 128 ? (WIDE ? 3 : 2) : 4;
   static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kSlotsK * kTileBytes, kMisc = kV + kSlotsV * kTileBytes;
-  static constexpr int kBars = 2 * (kSlotsK + kSlotsV) + 16 + kSpanRing;
+  static constexpr int kBars = 2 * (kSlotsK + kSlotsV) + 16 + 2 * kSpanRing;
+  static constexpr int kReaders = 8 + 1 + (WIDE ? 1 : 2);  // warps that read a segment
   // barriers, segments, the streams' maxima and sums
   static constexpr int kSmem = kMisc + kBars * 8 + kSpanRing * (int)sizeof(SpanSeg) + (WIDE ? 0 : 512 * 4) + 1024;
   // before the first copy, in the slots: the requests' prefix, size, length and queries
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
   const uint32_t bars = sbase + C::kMisc;
   const uint32_t k_full = bars, k_empty = k_full + 8 * NK, v_full = k_empty + 8 * NK, v_empty = v_full + 8 * NV;
   const uint32_t q_full = v_empty + 8 * NV, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 32,
-                 drained = o_done + 16, group = drained + 16, seg_full = group + 8;
+                 drained = o_done + 16, group = drained + 16, seg_full = group + 8, seg_empty = seg_full + 8 * kSpanRing;
   SpanSeg *ring = reinterpret_cast<SpanSeg *>(sm + C::kMisc + C::kBars * 8);
   float *s_m = reinterpret_cast<float *>(ring + kSpanRing);  // [maxima, sums][stream][row]
   int *pre = reinterpret_cast<int *>(sm + C::kK), *s_size = pre + kSpanMaxBatch + 1, *s_len = s_size + kSpanMaxBatch, *s_cnt = s_len + kSpanMaxBatch;
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
       mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, 4), mbar_init(p_full + 16 + 8 * i, 4), mbar_init(o_done + 8 * i, 1), mbar_init(drained + 8 * i, 1);
     }
     mbar_init(group, 8);
-    for (int i = 0; i < kSpanRing; ++i) mbar_init(seg_full + 8 * i, 1);
+    for (int i = 0; i < kSpanRing; ++i) mbar_init(seg_full + 8 * i, 1), mbar_init(seg_empty + 8 * i, C::kReaders);
     mbar_init_fence();
   }
   if (warp == kSpanMma) {
@@ -352,6 +355,11 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     const SpanSeg *x = ring + j % kSpanRing;
     return __all_sync(0xffffffffu, ok) && x->b >= 0 ? x : nullptr;
   };
+  // This warp is done with segment j's slot.
+  auto release = [&](int j) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_empty + 8 * (j % kSpanRing));
+  };
   // Whether stream 1 of a WIDE block has rows in a segment.
   auto second = [&](const SpanSeg &x) { return x.rg * pl.nodes + row_nodes < x.c; };
 
@@ -390,6 +398,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
         const SpanSeg *sp;
         for (int j = 0; ok && (sp = segment(j)); ++j) {
           const SpanSeg seg = *sp;
+          release(j);
           int32_t pid = page_of(seg, seg.k0);
           for (int k = seg.k0; ok && k < seg.k1; ++k, ++f) {
             const int32_t next = k + 1 < seg.k1 ? page_of(seg, k + 1) : 0;
@@ -425,9 +434,13 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
           }
           ++j;
         };
-        // Publishes the next segment.
+        // Publishes the next segment, nullptr behind the last one (and where a wait ran out).
         int published = 0;
         auto next_segment = [&]() -> const SpanSeg * {
+          if (published >= kSpanRing) {
+            ok = __all_sync(0xffffffffu, ok & mbar_wait(seg_empty + 8 * (published % kSpanRing), (published / kSpanRing & 1) ^ 1, abort));
+            if (!ok) return nullptr;
+          }
           SpanSeg x;
           const bool more = walk.next(x);
           SpanSeg *to = ring + published % kSpanRing;
@@ -551,6 +564,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
         const SpanSeg *sp;
         for (int j = 0; (sp = segment(j)); ++j) {
           const SpanSeg seg = *sp;
+          release(j);
           const int streams = second(seg) ? 2 : 1;
           mbar_wait(k_full + 8 * (f % NK), (f / NK) & 1, abort);
           for (int s = 0; s < streams; ++s) {
@@ -581,6 +595,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
         const SpanSeg *sp;
         for (int j = 0; (sp = segment(j)); ++j) {
           const SpanSeg seg = *sp;
+          release(j);
           mbar_wait(q_full + 8 * (j & 1), (j >> 1) & 1, abort);
           bool first = true;
           for (int k = seg.k0; k < seg.k1; ++k, ++f) {
@@ -633,7 +648,10 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
     const SpanSeg *sp;
     for (int j = 0; (sp = segment(j)); ++j) {
       const SpanSeg &seg = *sp;
-      if (WIDE && s && !second(seg)) continue;
+      if (WIDE && s && !second(seg)) {
+        release(j);
+        continue;
+      }
       const int i = seg.rg * pl.nodes + (WIDE ? s * row_nodes : 0) + node;
       const bool valid = node < row_nodes && i < seg.c && seg.st.base + i >= 0;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
@@ -852,6 +870,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1)
           a.lse[at] = lse2 * kLn2;
       }
       tc_fence_before();
+      release(j);
     }
   }
   tc_fence_before();
