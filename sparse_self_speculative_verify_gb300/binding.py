@@ -1061,7 +1061,7 @@ def ssd_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = No
     dt = _typed(logits, "logits")
     if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be a CUDA tensor [rows, vocab] with its last dimension dense")
-    N, V = logits.shape
+    N, V = _c_int(logits.shape[0], "rows"), _c_int(logits.shape[1], "vocab")
     dev = logits.get_device()
     M = 0
     pt = pr = None
@@ -1069,7 +1069,7 @@ def ssd_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = No
         if not isinstance(tokens, _Tensor):
             raise TypeError("tokens must be a torch.Tensor")
         pt = _shaped(tokens, "tokens", torch.int32, dev, tokens.shape)
-        M = tokens.numel()
+        M = _c_int(tokens.numel(), "tokens")
         if rows is not None:
             pr = _shaped(rows, "rows", torch.int32, dev, tokens.shape)
         elif tokens.dim() not in (1, 2) or tokens.shape[0] != N:
@@ -1105,7 +1105,7 @@ def ssd_tree_accept(parents: torch.Tensor, tokens: Optional[torch.Tensor], targe
     cnt - counts for ``ssd_kv_advance``."""
     if not isinstance(parents, _Tensor) or parents.dim() != 2 or not parents.is_cuda:
         raise ValueError("parents must be a CUDA tensor [batch, n]")
-    B, n = parents.shape
+    B, n = _c_int(parents.shape[0], "batch"), _c_int(parents.shape[1], "n")
     dev = parents.get_device()
     i32, f32 = torch.int32, torch.float32
     pp = _shaped(parents, "parents", i32, dev, (B, n))
@@ -1140,7 +1140,7 @@ def ssd_tree_commit(kv: KVCache, path: torch.Tensor, cnt: torch.Tensor, n: int, 
     dev, B = kv._geometry[:2]
     if not isinstance(path, _Tensor) or path.dim() != 2:
         raise ValueError("path must be a torch.Tensor [batch, max_path]")
-    m = path.shape[1]
+    m = _c_int(path.shape[1], "max_path")
     pp = _shaped(path, "path", torch.int32, dev, (B, m))
     pk = _shaped(cnt, "cnt", torch.int32, dev, (B,))
     pc = _maybe(counts, "counts", torch.int32, dev, (B,))
