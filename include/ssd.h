@@ -485,7 +485,8 @@ int ssd_kv_compact(const ssd_paged_kv *kv, const ssd_paged_kv *to, const int32_t
  *                    most 2^30): the last `window` ones and the request's first `sink`.  Pages that hold no token
  *                    of these are not read; their entries of the page table may be free.
  *   q     device [batch][n][h_q][d] of kv->dtype, 16-byte aligned; h_q / h_kv at most 128.
- *   scale softmax scale, positive and finite (in units of log2 too).
+ *   scale softmax scale, positive and finite (in units of log2 too).  Over a bf16 cache scores, scale * q.k * log2 e, lie
+ *         within 2^30 of 0.
  *   out   device [batch][n][h_q][d] of kv->dtype, 16-byte aligned; lse device float [batch][n][h_q] or NULL.
  *         Products and sums are held in fp32; over a bf16 cache probabilities are rounded to bf16 (2^-8 of each) before
  *         they meet V.  Rows i >= counts[b], and queries whose position would be negative, get out = 0, lse = -inf.
@@ -514,8 +515,9 @@ int ssd_window_attn(const ssd_paged_kv *kv, const void *q, int h_q, int n, const
  *   lse, entropy  device float [n_rows] (lse is required, entropy may be NULL): ln sum exp x; -sum p ln p.
  *   top_ids, top_logprobs  device int32 / float [n_rows][top_k]: the top_k largest logits of each row, descending, equal
  *            ones in the order of their index.  0 <= top_k <= min(vocab, 64).
- * Sums are held in fp32 relative to the row's maximum.  -inf is a token that cannot occur; a row of nothing else has
- * lse = -inf, entropy 0 and log probabilities -inf.  A row with NaN or +inf has lse, entropy and log probabilities NaN;
+ * Sums are held in fp32 relative to the row's maximum m, whatever finite numbers the row holds (a large negative one may ban a
+ * token); log probabilities are (x - m) - ln sum, but with more than 4096 tokens of chosen rows x - lse, which is up to 2^-23 of |lse|
+ * farther off.  -inf is a token that cannot occur; a row of nothing else has lse = -inf, entropy 0 and log probabilities -inf.  A row with NaN or +inf has lse, entropy and log probabilities NaN;
  * NaN is never among the top, and where a row has fewer than top_k others the rest of top_ids is -1.
  */
 int ssd_token_logprobs(const void *logits, int dtype, int64_t row_stride, int n_rows, int vocab, const int32_t *tokens,

@@ -9,10 +9,12 @@
 // are pushed into the first block's list.
 //
 // What bounds it: the bytes of the logits where they are many (1000 rows of 151936 bf16: 50 us, 6.0 TB/s), else what comes before
-// and behind them: 512 rows 38.3 us (4.1 TB/s), of which the top 20 are 6 and the start, the ends and the cluster's barriers 6
+// and behind them: 512 rows 38.0 us (4.1 TB/s), of which the top 20 are 6 and the start, the ends and the cluster's barriers 6
 // more; one row 8.6.  A warp of its own brings the logits to shared memory by bulk copies, two stages of 8 KB a block and eight
 // blocks an SM (loads into registers, taken and used in turn by the same threads, kept half as much in flight: 44 us where this
-// first took 40).
+// first took 40).  Threads that have met nothing but banned tokens (-inf, or beyond kScoreFar) take element after element: 512 rows in which 99 % are
+// banned 53 us without a top, else 32.  Where no more than about k tokens are allowed, the top k is score_ties' work: 512 rows with 5
+// allowed 2.9 ms for the top 5, 11.6 for the top 20.
 #include <cooperative_groups.h>
 
 #include "ssd_host.h"

@@ -7,7 +7,10 @@
 // (two at d = 64) and all rows.  A row's softmax stays inside its warp.  What bounds it: shared memory (69 % busy) and the
 // latencies of a tile's four barriers; 16 requests of 1000 to 4000 tokens, 8 heads of 4 queries, 8 nodes in fp32: 224 us, 23
 // TFLOP/s (231 with unpaired multiply-adds; four warps with twice the rows each: 269; about two blocks an SM instead of eight:
-// 293); one request of 300 tokens: 10, latency.  Where the (request, head, rows) blocks do not fill the SMs, each is cut into
+// 293); one request of 300 tokens: 10, latency.  A long request of one
+// head and a deep tree are far from that: 8 nodes, 4 queries a head, over 16000 / 131072 tokens 57 / 326 us (8 heads 144 / 670, the last
+// at 26 TFLOP/s): the join reads up to eight parts an SM one after the other; 512 nodes in a chain over 4000 tokens, 2 heads, 1.56 ms, side
+// by side 0.17: the mask walks a row's ancestors in every tile.  Where the (request, head, rows) blocks do not fill the SMs, each is cut into
 // equal parts of its tiles, joined by span_simt_join_kernel.
 #include <type_traits>
 

@@ -5,7 +5,8 @@
 //   O [128 rows x D]         += P V        (P from tensor memory, in the place of S; V as it lies, token-major)
 // so that a row's softmax belongs to one thread.  A block runs two such streams, which take turns on the tensor cores: while
 // one's softmax runs, the other's products do.
-//   WIDE (more than 128 rows): the streams are two tiles of rows and share every tile of K and V;
+//   WIDE (n queries of more than 128 rows, whatever a request's own number): the streams are two tiles of rows and share every tile
+//   of K and V;
 //   else both streams have the same rows and take K / V tiles in turn, their O joined at a segment's end.
 // Roles: warps 0-3 and 4-7 the softmax of a stream (and its O), warp 8 loads Q and K, warp 11 V (TMA boxes of up to 16 tokens
 // of a page, 128-byte swizzle), warps 9 and 10 issue a stream's products.
@@ -18,8 +19,8 @@
 //   decoding, 128 requests of 8192 tokens: HBM, 612 (7.0 TB/s of K and V);
 //   trees of 16 nodes, 4 heads a group (64 rows), 32 requests of 2048 to 8192 tokens: HBM, 106 to 116 by the draw (5.9 TB/s);
 //   trees of up to 64 nodes, 5 heads a group (3 tiles of rows), 8 requests of 16384 to 65536: 290 to 376 by the draw, the
-//     tensor cores half busy, 3.6 TB/s: groups of 256 rows read K and V for themselves, and the softmax of a tile (128 exponents
-//     a thread) takes as long as the products of the other stream;
+//     tensor cores half busy, 3.6 TB/s: groups of 256 rows read K and V for themselves, S of a stream's next tile waits for the
+//     softmax and O += P V of this one (P lies in S's place), and a last group of up to 128 rows has one stream alone;
 //   4 chunks of up to 4096 prompt tokens, window 2048: 320 to 382 by the draw, 1.33 PFLOP/s, as above; whole prompts 1.36;
 //   one window of 1024 tokens for each of 32 requests: 35, start and the units' ends around 20 us of HBM; one request: 11 to 14.
 //

@@ -159,10 +159,11 @@ class SpecRound:
 
 
 class TreeRound:
-    """One step that drafts trees of tokens, on one attention layer, with every buffer allocated once: the drafts' cheap
-    attention (a window of recent tokens and the first ones), the tree's verify attention, the nodes' log probabilities, the
+    """One step that verifies a drafted tree of tokens, on one attention layer, with every buffer allocated once: a draft token's
+    cheap attention (a window of recent tokens and the first ones), the tree's verify attention, the nodes' log probabilities, the
     path that stays and its commit to the cache (SpecSA "branch handling"; SparseSpec §2.3 verifies a chain, the tree in which
-    every node hangs on the one before it).
+    every node hangs on the one before it).  ``draft`` is for a request's last token, a tree's root or a chain's; trees grow from
+    the alternatives that ``score`` gives (``draft`` of an inner node would see its siblings, which lie beside it in the cache).
 
     A step: append the nodes' K and V (``ssd_kv_append``), advance the lengths by the nodes' counts (``ssd_kv_advance``),
     ``verify``; from the logits ``score`` and ``accept``; ``commit`` on every layer's cache; ``advance`` once.  With caches
